@@ -485,6 +485,185 @@ int smoe_experts_ffn_routed_q2(int n_experts, int k,
                                void *workspace, size_t workspace_bytes,
                                void *stream);
 
+/* Element types of the rows that the many-token calls move and multiply. */
+#define SMOE_F32 0
+#define SMOE_BF16 1
+
+/* Most slots (tokens x k) of one many-token call, most rows of one 8-bit
+ * product, and most rows of its weights over all experts. */
+#define SMOE_MAX_SLOTS (1 << 30)
+
+/*
+ * Many tokens: from a batch's router logits to its experts and back.
+ *
+ * smoe_topk_rows -> smoe_dispatch_tokens -> the experts' products on the
+ * sorted rows -> smoe_combine_tokens is a whole MoE layer for a batch, with
+ * no host round trip; every step has a gradient.  Slot a = t k + s is token
+ * t's s-th selection.  None of these calls uses atomics on sums: the same
+ * inputs give the same bits.  Sizes that the host cannot check (indices,
+ * places, offsets: device data) are checked on the device before they
+ * address memory; a place, order or offset outside its range is reported by
+ * smoe_last_device_status as SMOE_ERR_ROUTE and its slot counts as one
+ * without an expert.  1 <= k <= SMOE_MAX_TOP_K, n_experts <=
+ * SMOE_MAX_ROUTE_EXPERTS, n_tokens k <= SMOE_MAX_SLOTS, d_model >= 0 (any
+ * number; rows whose pitch and base are multiples of 16 bytes move as
+ * 16-byte vectors).  Index arrays are aligned to 4 bytes, rows to their
+ * element.  n_tokens == 0 is a no-op (offsets become zeros).
+ */
+
+/*
+ * The k largest of each row of logits and their weights, as
+ * smoe_route_topk_bf16 selects for one token (descending, ties to the lower
+ * expert, NaN below every number):
+ *
+ *   top_w[t][r] = exp(l_r - l_0) / sum over r' < k of exp(l_r' - l_0).
+ *
+ * A logit of -infinity is an expert that is off for the token: selected, it
+ * gives index -1 and weight 0, and a row of nothing else is all -1 and 0.
+ * logits: f32 [n_tokens x n_experts] with row pitch ld >= n_experts (in
+ * floats); top_idx: int32 [n_tokens x k], top_w: f32 [n_tokens x k], written.
+ * One launch.
+ */
+int smoe_topk_rows(const float *logits, int n_tokens, int n_experts, int ld,
+                   int k, int *top_idx, float *top_w, void *stream);
+
+/*
+ * Gradient of top_w to the logits (the selection itself is constant):
+ *
+ *   d_logits[t][top_idx[t][r]] = w_r (dw_r - sum over q of w_q dw_q),
+ *
+ * 0 for every other logit.  d_logits: f32 [n_tokens x n_experts], 16-byte
+ * aligned, written whole.
+ */
+int smoe_topk_rows_backward(const int *top_idx, const float *top_w,
+                            const float *d_top_w, int n_tokens, int n_experts,
+                            int k, float *d_logits, void *stream);
+
+/*
+ * Bytes of workspace smoe_dispatch_tokens needs; (size_t)-1 for sizes it
+ * would refuse, 0 for n_tokens == 0.
+ */
+size_t smoe_dispatch_workspace_bytes(int n_tokens, int k, int n_experts);
+
+/*
+ * Sorts a batch's slots by expert, stably, and brings the tokens' rows into
+ * that order.  Of the R = n_tokens k rows, [offsets[e], offsets[e + 1]) are
+ * expert e's, in slot order; the rows from offsets[n_experts] on belong to
+ * the slots whose index is outside [0, n_experts) (-1: no expert).
+ *
+ *   order[row] = the slot of a row,
+ *   place[slot] = its row, or -1 - row for a slot without an expert,
+ *   xs[row] = x[order[row] / k], zeros for a slot without an expert.
+ *
+ * top_idx: int32 [n_tokens x k]; x: [n_tokens x d_model] of dtype (SMOE_F32
+ * or SMOE_BF16); offsets: int32 [n_experts + 1], order and place: int32 [R],
+ * xs: [R x d_model], written.  x and xs both NULL: the sort alone.
+ * workspace: smoe_dispatch_workspace_bytes(...) bytes, 16-byte aligned,
+ * contents unspecified before and after.
+ */
+int smoe_dispatch_tokens(const int *top_idx, int n_tokens, int k,
+                         int n_experts, const void *x, int dtype, int d_model,
+                         int *offsets, int *order, int *place, void *xs,
+                         void *workspace, size_t workspace_bytes,
+                         void *stream);
+
+/*
+ * Gradient of xs to x: d_x[t] = sum over s, in order, of d_xs[place[t][s]]
+ * (f32 sums, rounded once), slots without an expert adding nothing.
+ */
+int smoe_dispatch_tokens_backward(const void *d_xs, int dtype,
+                                  const int *place, int n_tokens, int k,
+                                  int d_model, void *d_x, void *stream);
+
+/*
+ * The experts' rows back in token order, weighted:
+ *
+ *   out[t] = sum over s, in order, of top_w[t][s] ys[place[t][s]]
+ *
+ * (f32 sums, rounded once), slots without an expert adding nothing; a token
+ * without any gives zeros.  ys: [R x d_model], out: [n_tokens x d_model] of
+ * dtype; top_w: f32 [n_tokens x k].
+ */
+int smoe_combine_tokens(const void *ys, int dtype, const int *place,
+                        const float *top_w, int n_tokens, int k, int d_model,
+                        void *out, void *stream);
+
+/*
+ * Gradient of out to ys and top_w:
+ *
+ *   d_ys[place[t][s]] = top_w[t][s] d_out[t]   (zeros: rows without an expert)
+ *   d_top_w[t][s] = sum over j of d_out[t][j] ys[place[t][s]][j]   (0 there)
+ */
+int smoe_combine_tokens_backward(const void *d_out, const void *ys, int dtype,
+                                 const int *place, const float *top_w,
+                                 int n_tokens, int k, int d_model, void *d_ys,
+                                 float *d_top_w, void *stream);
+
+/*
+ * 8-bit weights and activations ("Q8").  A row of activations is held as
+ * int8 codes with one f32 scale per row (token), a matrix of weights as int8
+ * codes with one f32 scale per output row (channel).
+ */
+#define SMOE_Q8_PLAIN 0
+#define SMOE_Q8_SILU_MUL 1
+
+/*
+ * Quantises rows of v = x (act SMOE_Q8_PLAIN; x: [rows x cols]) or of
+ * v = SiLU(gate) * up (SMOE_Q8_SILU_MUL; x: [rows x 2 cols], gate the first
+ * cols of a row and up the last), in f32:
+ *
+ *   top = max |v|,  scales[r] = top / 127,
+ *   q[r][c] = v (127 / top) rounded to the nearest integer, ties to even.
+ *
+ * A row of zeros has scale 0 and codes 0; a row that holds a NaN or an
+ * infinity has scale NaN and codes 0, so that every product of it is NaN.
+ * cols <= SMOE_MAX_COLS; q 16-byte aligned.
+ */
+int smoe_quantize_rows_q8(const void *x, int dtype, int act, int rows,
+                          int cols, int8_t *q, float *scales, void *stream);
+
+/*
+ * Product of 8-bit rows with one 8-bit matrix:
+ *
+ *   y[r][n] = x_scales[r] w_scales[n] sum over c of xq[r][c] wq[n][c].
+ *
+ * xq: int8 [n_rows x n_in], wq: int8 [n_out x n_in], both 16-byte aligned,
+ * n_in a multiple of 16 (any n_out); y: [n_rows x n_out] of dtype, w_scales
+ * and y 16-byte aligned.  The integer products are exact; their sums are
+ * taken in 32 bits (integer, or f32 on the tensor cores: exact up to 2^24).
+ * workspace: smoe_matmul_q8_workspace_bytes(...) bytes, 16-byte aligned,
+ * contents unspecified before and after.
+ */
+size_t smoe_matmul_q8_workspace_bytes(int n_rows, int n_out, int n_in);
+int smoe_matmul_q8(const int8_t *xq, const float *x_scales, int n_rows,
+                   const int8_t *wq, const float *w_scales, int n_out,
+                   int n_in, void *y, int dtype, void *workspace,
+                   size_t workspace_bytes, void *stream);
+
+/*
+ * The same product over the experts of a sorted batch: row r of
+ * [offsets[e], offsets[e + 1]) is multiplied by expert e's matrix,
+ *
+ *   y[r][n] = x_scales[i] w_scales[e][n] sum over c of xq[i][c] wq[e][n][c],
+ *
+ * where i = order[r] / k (the row's token: the gather is part of the
+ * product, the tokens are quantised once), or i = r when order is NULL (xq
+ * already sorted).  Rows from offsets[n_experts] on are zeros.
+ * offsets and order: device arrays as smoe_dispatch_tokens writes them;
+ * xq: int8 [n_src x n_in]; wq: int8 [n_experts x n_out x n_in] and w_scales:
+ * f32 [n_experts x n_out], the experts one after another; y: [n_rows x
+ * n_out].  workspace: smoe_experts_matmul_q8_workspace_bytes(...) bytes.
+ */
+size_t smoe_experts_matmul_q8_workspace_bytes(int n_src, int n_rows,
+                                              int n_experts, int n_out,
+                                              int n_in);
+int smoe_experts_matmul_q8(const int8_t *xq, const float *x_scales, int n_src,
+                           const int *order, int k, const int *offsets,
+                           int n_rows, int n_experts, const int8_t *wq,
+                           const float *w_scales, int n_out, int n_in,
+                           void *y, int dtype, void *workspace,
+                           size_t workspace_bytes, void *stream);
+
 /* Size of the device array ffn_batch_q4_noalloc uses as its workspace. */
 #define SMOE_NOALLOC_SCRATCH_BYTES (32u << 20)
 

@@ -90,6 +90,18 @@ _SIGS = {
     "smoe_experts_ffn_batch_q4": ([_I, _P, _P, _P, _P, _P, _P, _P, _P, _P, _I, _I, _I, _P, _SZ, _P], _I),
     "smoe_experts_ffn_batch_q2": ([_I, _P, _P, _P, _P, _P, _P, _P, _P, _P, _I, _I, _I, _P, _SZ, _P], _I),
     "ffn_batch_q4_noalloc": ([_P, _P, _P, _P, _P, _P, _P, _P, _I, _I, _I, _I, _P], _I),
+    "smoe_topk_rows": ([_P, _I, _I, _I, _I, _P, _P, _P], _I),
+    "smoe_topk_rows_backward": ([_P, _P, _P, _I, _I, _I, _P, _P], _I),
+    "smoe_dispatch_workspace_bytes": ([_I, _I, _I], _SZ),
+    "smoe_dispatch_tokens": ([_P, _I, _I, _I, _P, _I, _I, _P, _P, _P, _P, _P, _SZ, _P], _I),
+    "smoe_dispatch_tokens_backward": ([_P, _I, _P, _I, _I, _I, _P, _P], _I),
+    "smoe_combine_tokens": ([_P, _I, _P, _P, _I, _I, _I, _P, _P], _I),
+    "smoe_combine_tokens_backward": ([_P, _P, _I, _P, _P, _I, _I, _I, _P, _P, _P], _I),
+    "smoe_quantize_rows_q8": ([_P, _I, _I, _I, _I, _P, _P, _P], _I),
+    "smoe_matmul_q8_workspace_bytes": ([_I, _I, _I], _SZ),
+    "smoe_matmul_q8": ([_P, _P, _I, _P, _P, _I, _I, _P, _I, _P, _SZ, _P], _I),
+    "smoe_experts_matmul_q8_workspace_bytes": ([_I, _I, _I, _I, _I], _SZ),
+    "smoe_experts_matmul_q8": ([_P, _P, _I, _P, _I, _P, _I, _I, _P, _P, _I, _I, _P, _I, _P, _SZ, _P], _I),
     "smoe_last_device_status": ([_P], _I),
     "smoe_selftest_bounded_wait": ([_I, _P], _I),
     "smoe_copy": ([_P, _P, ctypes.c_size_t, _P], _I),
@@ -365,6 +377,88 @@ def ffn_batch_q4_noalloc(gate_codes, gate_scales, up_codes, up_scales, down_code
                                      _ptr(up_scales), _ptr(down_codes), _ptr(down_scales), _ptr(X),
                                      _ptr(Y), T, d_model, d_ff, group, _stream(stream)),
            "ffn_batch_q4_noalloc")
+
+
+# ---- many tokens, and experts in 8 bits
+
+SMOE_F32 = 0
+SMOE_BF16 = 1
+SMOE_MAX_SLOTS = 1 << 30
+SMOE_Q8_PLAIN = 0
+SMOE_Q8_SILU_MUL = 1
+
+
+def smoe_topk_rows(logits, n_tokens, n_experts, ld, k, top_idx, top_w, stream=None):
+    """The k largest logits of each row (pitch ld floats) and their softmax
+    weights; -inf is an expert that is off (index -1, weight 0)."""
+    _check(_lib.smoe_topk_rows(_ptr(logits), n_tokens, n_experts, ld, k, _ptr(top_idx), _ptr(top_w),
+                               _stream(stream)), "smoe_topk_rows")
+
+
+def smoe_topk_rows_backward(top_idx, top_w, d_top_w, n_tokens, n_experts, k, d_logits, stream=None):
+    _check(_lib.smoe_topk_rows_backward(_ptr(top_idx), _ptr(top_w), _ptr(d_top_w), n_tokens, n_experts, k,
+                                        _ptr(d_logits), _stream(stream)), "smoe_topk_rows_backward")
+
+
+def smoe_dispatch_workspace_bytes(n_tokens, k, n_experts):
+    return _lib.smoe_dispatch_workspace_bytes(n_tokens, k, n_experts)
+
+
+def smoe_dispatch_tokens(top_idx, n_tokens, k, n_experts, x, dtype, d_model, offsets, order, place, xs,
+                         workspace, workspace_bytes, stream=None):
+    """Sorts the slots by expert (offsets, order, place) and brings the rows
+    of x into that order (x and xs None: the sort alone).  dtype: SMOE_F32 or
+    SMOE_BF16, of x and xs."""
+    _check(_lib.smoe_dispatch_tokens(_ptr(top_idx), n_tokens, k, n_experts, _ptr(x), dtype, d_model,
+                                     _ptr(offsets), _ptr(order), _ptr(place), _ptr(xs), _ptr(workspace),
+                                     workspace_bytes, _stream(stream)), "smoe_dispatch_tokens")
+
+
+def smoe_dispatch_tokens_backward(d_xs, dtype, place, n_tokens, k, d_model, d_x, stream=None):
+    _check(_lib.smoe_dispatch_tokens_backward(_ptr(d_xs), dtype, _ptr(place), n_tokens, k, d_model, _ptr(d_x),
+                                              _stream(stream)), "smoe_dispatch_tokens_backward")
+
+
+def smoe_combine_tokens(ys, dtype, place, top_w, n_tokens, k, d_model, out, stream=None):
+    _check(_lib.smoe_combine_tokens(_ptr(ys), dtype, _ptr(place), _ptr(top_w), n_tokens, k, d_model, _ptr(out),
+                                    _stream(stream)), "smoe_combine_tokens")
+
+
+def smoe_combine_tokens_backward(d_out, ys, dtype, place, top_w, n_tokens, k, d_model, d_ys, d_top_w,
+                                 stream=None):
+    _check(_lib.smoe_combine_tokens_backward(_ptr(d_out), _ptr(ys), dtype, _ptr(place), _ptr(top_w), n_tokens, k,
+                                             d_model, _ptr(d_ys), _ptr(d_top_w), _stream(stream)),
+           "smoe_combine_tokens_backward")
+
+
+def smoe_quantize_rows_q8(x, dtype, act, rows, cols, q, scales, stream=None):
+    """int8 codes and one scale per row of x, or (SMOE_Q8_SILU_MUL) of
+    SiLU(gate) * up of rows [gate | up] of 2 cols."""
+    _check(_lib.smoe_quantize_rows_q8(_ptr(x), dtype, act, rows, cols, _ptr(q), _ptr(scales), _stream(stream)),
+           "smoe_quantize_rows_q8")
+
+
+def smoe_matmul_q8_workspace_bytes(n_rows, n_out, n_in):
+    return _lib.smoe_matmul_q8_workspace_bytes(n_rows, n_out, n_in)
+
+
+def smoe_matmul_q8(xq, x_scales, n_rows, wq, w_scales, n_out, n_in, y, dtype, workspace, workspace_bytes,
+                   stream=None):
+    _check(_lib.smoe_matmul_q8(_ptr(xq), _ptr(x_scales), n_rows, _ptr(wq), _ptr(w_scales), n_out, n_in, _ptr(y),
+                               dtype, _ptr(workspace), workspace_bytes, _stream(stream)), "smoe_matmul_q8")
+
+
+def smoe_experts_matmul_q8_workspace_bytes(n_src, n_rows, n_experts, n_out, n_in):
+    return _lib.smoe_experts_matmul_q8_workspace_bytes(n_src, n_rows, n_experts, n_out, n_in)
+
+
+def smoe_experts_matmul_q8(xq, x_scales, n_src, order, k, offsets, n_rows, n_experts, wq, w_scales, n_out, n_in,
+                           y, dtype, workspace, workspace_bytes, stream=None):
+    """order None: xq is already in the sorted order."""
+    _check(_lib.smoe_experts_matmul_q8(_ptr(xq), _ptr(x_scales), n_src, _ptr(order), k, _ptr(offsets), n_rows,
+                                       n_experts, _ptr(wq), _ptr(w_scales), n_out, n_in, _ptr(y), dtype,
+                                       _ptr(workspace), workspace_bytes, _stream(stream)),
+           "smoe_experts_matmul_q8")
 
 
 def smoe_last_device_status(stream=None):

@@ -2,7 +2,7 @@
 // on the host, then the kernel launches.  Nothing here allocates memory.
 #include <mutex>
 
-#include "internal.h"
+#include "internal_tokens.h"
 #include "smoe.h"
 
 namespace smoe {
@@ -720,6 +720,241 @@ int smoe_combine(int k, const float *expert_out, const float *top_w, float *out,
                          {top_w, static_cast<size_t>(k) * sizeof(float)}};
     if (any_alias(o, 1, ins, k > 0 ? 2 : 0)) return SMOE_ERR_ALIAS;
     return to_status(smoe::launch_combine(k, expert_out, top_w, out, d_model, static_cast<cudaStream_t>(stream)));
+}
+
+// ---- many tokens
+
+static bool aligned_to(const void *p, size_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
+
+static size_t elem_bytes(int dtype) { return dtype == SMOE_BF16 ? 2u : 4u; }
+
+// Sizes shared by the calls over T tokens' k slots: T k slots are counted in
+// 32 bits.
+static int check_slots(int n_tokens, int k)
+{
+    if (n_tokens < 0 || k < 1 || k > SMOE_MAX_TOP_K) return SMOE_ERR_SHAPE;
+    if (static_cast<long long>(n_tokens) * k > SMOE_MAX_SLOTS) return SMOE_ERR_SHAPE;
+    return SMOE_OK;
+}
+
+static int check_rows(int dtype, int d_model)
+{
+    if (dtype != SMOE_F32 && dtype != SMOE_BF16) return SMOE_ERR_SHAPE;
+    return d_model < 0 ? SMOE_ERR_SHAPE : SMOE_OK;
+}
+
+int smoe_topk_rows(const float *logits, int n_tokens, int n_experts, int ld, int k, int *top_idx, float *top_w,
+                   void *stream)
+{
+    const int st = check_slots(n_tokens, k);
+    if (st != SMOE_OK) return st;
+    if (n_experts < 1 || n_experts > SMOE_MAX_ROUTE_EXPERTS || k > n_experts || ld < n_experts) return SMOE_ERR_SHAPE;
+    if (n_tokens == 0) return SMOE_OK;
+    if (!logits || !top_idx || !top_w) return SMOE_ERR_NULL;
+    if (!aligned_to(logits, 4) || !aligned_to(top_idx, 4) || !aligned_to(top_w, 4)) return SMOE_ERR_ALIGN;
+    const size_t slots = static_cast<size_t>(n_tokens) * k;
+    const Span outs[2] = {{top_idx, slots * sizeof(int)}, {top_w, slots * sizeof(float)}};
+    const Span ins[1] = {
+        {logits, (static_cast<size_t>(n_tokens - 1) * ld + static_cast<size_t>(n_experts)) * sizeof(float)}};
+    if (any_alias(outs, 2, ins, 1)) return SMOE_ERR_ALIAS;
+    return to_status(smoe::launch_topk_rows(logits, n_tokens, n_experts, ld, k, top_idx, top_w,
+                                            static_cast<cudaStream_t>(stream)));
+}
+
+int smoe_topk_rows_backward(const int *top_idx, const float *top_w, const float *d_top_w, int n_tokens, int n_experts,
+                            int k, float *d_logits, void *stream)
+{
+    const int st = check_slots(n_tokens, k);
+    if (st != SMOE_OK) return st;
+    if (n_experts < 1 || n_experts > SMOE_MAX_ROUTE_EXPERTS || k > n_experts) return SMOE_ERR_SHAPE;
+    if (n_tokens == 0) return SMOE_OK;
+    if (!top_idx || !top_w || !d_top_w || !d_logits) return SMOE_ERR_NULL;
+    if (!aligned_to(top_idx, 4) || !aligned_to(top_w, 4) || !aligned_to(d_top_w, 4) || !aligned16(d_logits))
+        return SMOE_ERR_ALIGN;
+    const size_t slots = static_cast<size_t>(n_tokens) * k;
+    const Span outs[1] = {{d_logits, static_cast<size_t>(n_tokens) * n_experts * sizeof(float)}};
+    const Span ins[3] = {{top_idx, slots * sizeof(int)}, {top_w, slots * sizeof(float)}, {d_top_w, slots * sizeof(float)}};
+    if (any_alias(outs, 1, ins, 3)) return SMOE_ERR_ALIAS;
+    return to_status(smoe::launch_topk_rows_grad(top_idx, top_w, d_top_w, n_tokens, n_experts, k, d_logits,
+                                                 static_cast<cudaStream_t>(stream)));
+}
+
+size_t smoe_dispatch_workspace_bytes(int n_tokens, int k, int n_experts)
+{
+    if (check_slots(n_tokens, k) != SMOE_OK || n_experts < 1 || n_experts > SMOE_MAX_ROUTE_EXPERTS)
+        return static_cast<size_t>(-1);
+    return n_tokens == 0 ? 0 : smoe::dispatch_workspace(n_tokens, k, n_experts);
+}
+
+int smoe_dispatch_tokens(const int *top_idx, int n_tokens, int k, int n_experts, const void *x, int dtype, int d_model,
+                         int *offsets, int *order, int *place, void *xs, void *workspace, size_t workspace_bytes,
+                         void *stream)
+{
+    int st = check_slots(n_tokens, k);
+    if (st == SMOE_OK) st = check_rows(dtype, d_model);
+    if (st != SMOE_OK) return st;
+    if (n_experts < 1 || n_experts > SMOE_MAX_ROUTE_EXPERTS) return SMOE_ERR_SHAPE;
+    if (!offsets) return SMOE_ERR_NULL;
+    if (!aligned_to(offsets, 4)) return SMOE_ERR_ALIGN;
+    const cudaStream_t s = static_cast<cudaStream_t>(stream);
+    if (n_tokens == 0) return to_status(smoe::launch_zero_words(offsets, n_experts + 1, s));
+    if (!top_idx || !order || !place) return SMOE_ERR_NULL;
+    const bool rows = (x || xs) && d_model > 0;
+    if (rows && (!x || !xs)) return SMOE_ERR_NULL;
+    const size_t e = elem_bytes(dtype);
+    if (!aligned_to(top_idx, 4) || !aligned_to(order, 4) || !aligned_to(place, 4)) return SMOE_ERR_ALIGN;
+    if (rows && (!aligned_to(x, e) || !aligned_to(xs, e))) return SMOE_ERR_ALIGN;
+    const size_t need = smoe::dispatch_workspace(n_tokens, k, n_experts);
+    if (!workspace || workspace_bytes < need) return SMOE_ERR_WORKSPACE;
+    if (!aligned16(workspace)) return SMOE_ERR_ALIGN;
+    const size_t slots = static_cast<size_t>(n_tokens) * k;
+    const Span outs[5] = {{offsets, (static_cast<size_t>(n_experts) + 1) * sizeof(int)},
+                          {order, slots * sizeof(int)},
+                          {place, slots * sizeof(int)},
+                          {workspace, need},
+                          {xs, rows ? slots * d_model * e : 0}};
+    const Span ins[2] = {{top_idx, slots * sizeof(int)}, {x, rows ? static_cast<size_t>(n_tokens) * d_model * e : 0}};
+    if (any_alias(outs, 5, ins, 2)) return SMOE_ERR_ALIAS;
+    cudaError_t err = smoe::launch_sort_tokens(top_idx, static_cast<int>(slots), n_experts, offsets, order, place, workspace, s);
+    if (err == cudaSuccess && rows) err = smoe::launch_gather_tokens(x, dtype, place, n_tokens, k, d_model, xs, s);
+    return to_status(err);
+}
+
+// out[t] = sum over s of w[t, s] rows[place[t, s]], w null: of the rows.
+static int sum_impl(const void *rows, int dtype, const int *place, const float *w, bool weighted, int n_tokens, int k,
+                    int d_model, void *out, void *stream)
+{
+    int st = check_slots(n_tokens, k);
+    if (st == SMOE_OK) st = check_rows(dtype, d_model);
+    if (st != SMOE_OK) return st;
+    if (n_tokens == 0 || d_model == 0) return SMOE_OK;
+    if (!rows || !place || !out || (weighted && !w)) return SMOE_ERR_NULL;
+    const size_t e = elem_bytes(dtype), slots = static_cast<size_t>(n_tokens) * k;
+    if (!aligned_to(rows, e) || !aligned_to(out, e) || !aligned_to(place, 4) || (weighted && !aligned_to(w, 4)))
+        return SMOE_ERR_ALIGN;
+    const Span outs[1] = {{out, static_cast<size_t>(n_tokens) * d_model * e}};
+    const Span ins[3] = {{rows, slots * d_model * e}, {place, slots * sizeof(int)}, {w, weighted ? slots * sizeof(float) : 0}};
+    if (any_alias(outs, 1, ins, 3)) return SMOE_ERR_ALIAS;
+    return to_status(smoe::launch_sum_tokens(rows, dtype, place, weighted ? w : nullptr, n_tokens, k, d_model, out,
+                                             static_cast<cudaStream_t>(stream)));
+}
+
+int smoe_dispatch_tokens_backward(const void *d_xs, int dtype, const int *place, int n_tokens, int k, int d_model,
+                                  void *d_x, void *stream)
+{
+    return sum_impl(d_xs, dtype, place, nullptr, false, n_tokens, k, d_model, d_x, stream);
+}
+
+int smoe_combine_tokens(const void *ys, int dtype, const int *place, const float *top_w, int n_tokens, int k, int d_model,
+                        void *out, void *stream)
+{
+    return sum_impl(ys, dtype, place, top_w, true, n_tokens, k, d_model, out, stream);
+}
+
+int smoe_combine_tokens_backward(const void *d_out, const void *ys, int dtype, const int *place, const float *top_w,
+                                 int n_tokens, int k, int d_model, void *d_ys, float *d_top_w, void *stream)
+{
+    int st = check_slots(n_tokens, k);
+    if (st == SMOE_OK) st = check_rows(dtype, d_model);
+    if (st != SMOE_OK) return st;
+    if (n_tokens == 0) return SMOE_OK;
+    if (!place || !top_w || !d_top_w || (d_model > 0 && (!d_out || !ys || !d_ys))) return SMOE_ERR_NULL;
+    const size_t e = elem_bytes(dtype), slots = static_cast<size_t>(n_tokens) * k;
+    if (!aligned_to(place, 4) || !aligned_to(top_w, 4) || !aligned_to(d_top_w, 4)) return SMOE_ERR_ALIGN;
+    if (d_model > 0 && (!aligned_to(d_out, e) || !aligned_to(ys, e) || !aligned_to(d_ys, e))) return SMOE_ERR_ALIGN;
+    const Span outs[2] = {{d_ys, slots * d_model * e}, {d_top_w, slots * sizeof(float)}};
+    const Span ins[4] = {{d_out, static_cast<size_t>(n_tokens) * d_model * e},
+                         {ys, slots * d_model * e},
+                         {place, slots * sizeof(int)},
+                         {top_w, slots * sizeof(float)}};
+    if (any_alias(outs, 2, ins, 4)) return SMOE_ERR_ALIAS;
+    return to_status(smoe::launch_combine_tokens_grad(d_out, ys, dtype, place, top_w, n_tokens, k, d_model, d_ys, d_top_w,
+                                                      static_cast<cudaStream_t>(stream)));
+}
+
+// ---- 8-bit weights and activations
+
+int smoe_quantize_rows_q8(const void *x, int dtype, int act, int rows, int cols, int8_t *q, float *scales, void *stream)
+{
+    const int st = check_rows(dtype, cols);
+    if (st != SMOE_OK) return st;
+    if (rows < 0 || cols > SMOE_MAX_COLS || (act != SMOE_Q8_PLAIN && act != SMOE_Q8_SILU_MUL)) return SMOE_ERR_SHAPE;
+    if (rows == 0) return SMOE_OK;
+    if (!scales || (cols > 0 && (!x || !q))) return SMOE_ERR_NULL;
+    const size_t e = elem_bytes(dtype), n = static_cast<size_t>(rows) * cols;
+    if (!aligned_to(scales, 4) || (cols > 0 && (!aligned_to(x, e) || !aligned16(q)))) return SMOE_ERR_ALIGN;
+    const Span outs[2] = {{q, n}, {scales, static_cast<size_t>(rows) * sizeof(float)}};
+    const Span ins[1] = {{x, n * e * (act == SMOE_Q8_SILU_MUL ? 2 : 1)}};
+    if (any_alias(outs, 2, ins, 1)) return SMOE_ERR_ALIAS;
+    return to_status(smoe::launch_quantize_rows(x, dtype, act == SMOE_Q8_SILU_MUL, rows, cols, q, scales,
+                                                static_cast<cudaStream_t>(stream)));
+}
+
+// Sizes of an 8-bit product: rows of whole 16-byte vectors; the weights' rows
+// are counted in 32 bits.
+static int check_q8(int n_src, int n_rows, int n_experts, int n_out, int n_in)
+{
+    if (n_src < 0 || n_rows < 0 || n_rows > SMOE_MAX_SLOTS || n_out < 0 || n_in < 0) return SMOE_ERR_SHAPE;
+    if (n_experts < 1 || n_experts > SMOE_MAX_ROUTE_EXPERTS) return SMOE_ERR_SHAPE;
+    if (n_in % 16 != 0 || n_in > SMOE_MAX_COLS) return SMOE_ERR_SHAPE;
+    if (static_cast<long long>(n_experts) * n_out > SMOE_MAX_SLOTS) return SMOE_ERR_SHAPE;
+    return SMOE_OK;
+}
+
+size_t smoe_experts_matmul_q8_workspace_bytes(int n_src, int n_rows, int n_experts, int n_out, int n_in)
+{
+    if (check_q8(n_src, n_rows, n_experts, n_out, n_in) != SMOE_OK) return static_cast<size_t>(-1);
+    return n_rows == 0 || n_out == 0 ? 0 : smoe::q8_workspace(n_src, n_rows, n_experts, n_out, n_in);
+}
+
+size_t smoe_matmul_q8_workspace_bytes(int n_rows, int n_out, int n_in)
+{
+    return smoe_experts_matmul_q8_workspace_bytes(n_rows, n_rows, 1, n_out, n_in);
+}
+
+static int q8_impl(const int8_t *xq, const float *x_scales, int n_src, const int *order, int k, const int *offsets,
+                   bool sorted, int n_rows, int n_experts, const int8_t *wq, const float *w_scales, int n_out, int n_in,
+                   void *y, int dtype, void *workspace, size_t workspace_bytes, void *stream)
+{
+    int st = check_q8(n_src, n_rows, n_experts, n_out, n_in);
+    if (st == SMOE_OK) st = check_rows(dtype, 0);
+    if (st != SMOE_OK) return st;
+    if (order ? (k < 1 || k > SMOE_MAX_TOP_K) : n_src < n_rows) return SMOE_ERR_SHAPE;
+    if (n_rows == 0 || n_out == 0) return SMOE_OK;
+    if (!x_scales || !w_scales || !y || (sorted && !offsets) || (n_in > 0 && (!xq || !wq))) return SMOE_ERR_NULL;
+    const size_t e = elem_bytes(dtype);
+    if (!aligned_to(x_scales, 4) || !aligned16(w_scales) || !aligned16(y) || (order && !aligned_to(order, 4)) ||
+        (sorted && !aligned_to(offsets, 4)) || (n_in > 0 && (!aligned16(xq) || !aligned16(wq))))
+        return SMOE_ERR_ALIGN;
+    const size_t need = smoe::q8_workspace(n_src, n_rows, n_experts, n_out, n_in);
+    if (!workspace || workspace_bytes < need) return SMOE_ERR_WORKSPACE;
+    if (!aligned16(workspace)) return SMOE_ERR_ALIGN;
+    const size_t wrows = static_cast<size_t>(n_experts) * n_out;
+    const Span outs[2] = {{y, static_cast<size_t>(n_rows) * n_out * e}, {workspace, need}};
+    const Span ins[6] = {{xq, static_cast<size_t>(n_src) * n_in},
+                         {x_scales, static_cast<size_t>(n_src) * sizeof(float)},
+                         {wq, wrows * n_in},
+                         {w_scales, wrows * sizeof(float)},
+                         {order, order ? static_cast<size_t>(n_rows) * sizeof(int) : 0},
+                         {offsets, sorted ? (static_cast<size_t>(n_experts) + 1) * sizeof(int) : 0}};
+    if (any_alias(outs, 2, ins, 6)) return SMOE_ERR_ALIAS;
+    return to_status(smoe::launch_q8(xq, x_scales, n_src, order, k, sorted ? offsets : nullptr, n_rows, n_experts, wq,
+                                     w_scales, n_out, n_in, y, dtype, workspace, static_cast<cudaStream_t>(stream)));
+}
+
+int smoe_matmul_q8(const int8_t *xq, const float *x_scales, int n_rows, const int8_t *wq, const float *w_scales, int n_out,
+                   int n_in, void *y, int dtype, void *workspace, size_t workspace_bytes, void *stream)
+{
+    return q8_impl(xq, x_scales, n_rows, nullptr, 1, nullptr, false, n_rows, 1, wq, w_scales, n_out, n_in, y, dtype,
+                   workspace, workspace_bytes, stream);
+}
+
+int smoe_experts_matmul_q8(const int8_t *xq, const float *x_scales, int n_src, const int *order, int k,
+                           const int *offsets, int n_rows, int n_experts, const int8_t *wq, const float *w_scales,
+                           int n_out, int n_in, void *y, int dtype, void *workspace, size_t workspace_bytes, void *stream)
+{
+    return q8_impl(xq, x_scales, n_src, order, k, offsets, true, n_rows, n_experts, wq, w_scales, n_out, n_in, y, dtype,
+                   workspace, workspace_bytes, stream);
 }
 
 int smoe_copy(void *dst, const void *src, size_t bytes, void *stream)

@@ -1,0 +1,290 @@
+// 8-bit weights and activations: the row quantiser and the products
+//   y[r][n] = x_scale[src(r)] w_scale[e][n] sum_k xq[src(r)][k] wq[e][n][k]
+// over one matrix, or over the experts of a sorted batch (rows
+// [offsets[e], offsets[e + 1]) by expert e's matrix, src(r) = order[r] / k).
+//
+// plan_tiles turns the experts' row counts, which only the device knows,
+// into a list of tiles of at most `step` rows of one expert each; rows past
+// the last expert's are tiles of expert -1, whose outputs are zeros.
+#include "common.cuh"
+#include "internal_tokens.h"
+#include "rowvec.cuh"
+#include "smoe.h"
+
+namespace smoe {
+namespace {
+
+// ---------------------------------------------------------------- quantiser
+
+constexpr int QUANT_THREADS = 256;
+
+// The VE values at column c of row r: x itself, or silu(gate) * up of a row
+// [gate | up] of 2 cols.
+template <typename T, int VE, bool ACT>
+__device__ __forceinline__ void quant_values(const T *row, int cols, int c, float (&v)[VE])
+{
+    RowVec<T, VE> a;
+    a.load(row + c);
+    a.get(v);
+    if (ACT) {
+        RowVec<T, VE> b;
+        float u[VE];
+        b.load(row + cols + c);
+        b.get(u);
+#pragma unroll
+        for (int i = 0; i < VE; ++i) v[i] = silu_f32(v[i]) * u[i];
+    }
+}
+
+// One CTA per row: the largest magnitude, then the rounding.
+template <typename T, int VE, bool ACT>
+__global__ void __launch_bounds__(QUANT_THREADS) quantize_rows(const T *__restrict__ x, int cols, int8_t *__restrict__ q,
+                                                               float *__restrict__ scales)
+{
+    __shared__ float warp_max[QUANT_THREADS / 32];
+    pdl_launch_dependents();
+    pdl_wait();
+    const size_t r = blockIdx.x;
+    const T *row = x + r * cols * (ACT ? 2 : 1);
+    float top = 0.f;
+    bool bad = false;
+    for (int c = threadIdx.x * VE; c < cols; c += QUANT_THREADS * VE) {
+        float v[VE];
+        quant_values<T, VE, ACT>(row, cols, c, v);
+#pragma unroll
+        for (int i = 0; i < VE; ++i) {
+            bad |= !isfinite(v[i]);
+            top = fmaxf(top, fabsf(v[i]));
+        }
+    }
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1) top = fmaxf(top, __shfl_xor_sync(FULL_MASK, top, off));
+    if ((threadIdx.x & 31) == 0) warp_max[threadIdx.x >> 5] = top;
+    bad = __syncthreads_or(bad);
+    for (int i = 0; i < QUANT_THREADS / 32; ++i) top = fmaxf(top, warp_max[i]);
+    // a row of zeros has scale 0; a row that is not finite scale NaN and
+    // codes 0, so that every product of it is NaN
+    const float up = bad || top == 0.f ? 0.f : __fdiv_rn(127.f, top);
+    if (threadIdx.x == 0) scales[r] = bad ? __int_as_float(0x7fffffff) : __fdiv_rn(top, 127.f);
+    for (int c = threadIdx.x * VE; c < cols; c += QUANT_THREADS * VE) {
+        float v[VE];
+        quant_values<T, VE, ACT>(row, cols, c, v);
+#pragma unroll
+        for (int i = 0; i < VE; ++i)
+            q[r * cols + c + i] = bad ? 0 : static_cast<int8_t>(max(-127, min(127, __float2int_rn(__fmul_rn(v[i], up)))));
+    }
+}
+
+// ---------------------------------------------------------------- tiles
+
+struct Tile {
+    int expert, row0, rows, pad;
+};
+
+constexpr int PLAN_THREADS = 1024;
+
+// tiles[0 .. *ntiles): every expert's rows in steps of `step`, then the rows
+// past the last expert's.  offsets null: one matrix, R rows.
+__global__ void __launch_bounds__(PLAN_THREADS) plan_tiles(const int *__restrict__ offsets, int n, int R, int step,
+                                                           int max_tiles, int *__restrict__ ntiles,
+                                                           Tile *__restrict__ tiles, unsigned *status)
+{
+    __shared__ int warp_sums[PLAN_THREADS / 32];
+    __shared__ int run_s;
+    pdl_launch_dependents();
+    pdl_wait();
+    const int tid = threadIdx.x, lane = tid & 31, wi = tid >> 5;
+    int run = 0;
+    for (int b = 0; b <= n; b += PLAN_THREADS) {
+        const int e = b + tid;
+        int lo = 0, hi = 0;
+        if (e <= n) {
+            lo = offsets ? offsets[e] : (e == 0 ? 0 : R);
+            hi = e < n ? (offsets ? offsets[e + 1] : R) : R;
+            if (lo < 0 || hi < lo || hi > R) {
+                atomicExch(status, kStatusRoute);
+                lo = hi = 0;
+            }
+        }
+        const int cnt = (hi - lo + step - 1) / step;
+        int inc = cnt;
+#pragma unroll
+        for (int off = 1; off < 32; off <<= 1) {
+            const int o = __shfl_up_sync(FULL_MASK, inc, off);
+            if (lane >= off) inc += o;
+        }
+        if (lane == 31) warp_sums[wi] = inc;
+        __syncthreads();
+        int before = run;
+        for (int i = 0; i < wi; ++i) before += warp_sums[i];
+        if (tid == PLAN_THREADS - 1) run_s = before + inc;
+        const int t0 = before + inc - cnt;
+        for (int i = 0; i < cnt && t0 + i < max_tiles; ++i)
+            tiles[t0 + i] = Tile{e < n ? e : -1, lo + i * step, min(step, hi - lo - i * step), 0};
+        __syncthreads();
+        run = run_s;
+    }
+    if (tid == 0) *ntiles = min(run, max_tiles);
+}
+
+// ---------------------------------------------------------------- products
+
+constexpr int DOT_WARPS = 8;
+constexpr int DOT_ROWS = 8;   // activation rows per tile
+constexpr int DOT_OUTS = 4;   // weight rows per warp
+
+struct Q8Args {
+    const int8_t *xq;
+    const float *xs;
+    const int *order;  // null: row r is its own source
+    const int8_t *wq;
+    const float *ws;
+    void *y;
+    const int *ntiles;
+    const Tile *tiles;
+    unsigned *status;
+    int k, nsrc, N, K;
+};
+
+// Source row of sorted row r, or -1 (reported) where order says nonsense.
+__device__ __forceinline__ int source_row(const Q8Args &a, int r)
+{
+    if (!a.order) return r;
+    const int s = a.order[r];
+    if (s < 0 || s / a.k >= a.nsrc) {
+        atomicExch(a.status, kStatusRoute);
+        return -1;
+    }
+    return s / a.k;
+}
+
+__device__ __forceinline__ void put(float *p, float v) { *p = v; }
+__device__ __forceinline__ void put(__nv_bfloat16 *p, float v) { *p = __float2bfloat16_rn(v); }
+
+// Integer dot products on the CUDA cores, exact in 32 bits (K <= 32768): a
+// warp holds 4 weight rows against the tile's up to 8 activation rows, 16
+// columns of each per lane and step.
+template <typename T>
+__global__ void __launch_bounds__(DOT_WARPS * 32) q8_dot(const Q8Args a)
+{
+    pdl_launch_dependents();
+    pdl_wait();
+    if (static_cast<int>(blockIdx.x) >= *a.ntiles) return;
+    const Tile tile = a.tiles[blockIdx.x];
+    const int lane = threadIdx.x & 31;
+    const int n0 = (blockIdx.y * DOT_WARPS + (threadIdx.x >> 5)) * DOT_OUTS;
+    if (n0 >= a.N) return;
+    T *y = static_cast<T *>(a.y);
+    if (tile.expert < 0) {
+        for (int i = lane; i < tile.rows * DOT_OUTS; i += 32)
+            if (n0 + i % DOT_OUTS < a.N)
+                put(y + static_cast<size_t>(tile.row0 + i / DOT_OUTS) * a.N + n0 + i % DOT_OUTS, 0.f);
+        return;
+    }
+    int src[DOT_ROWS];
+#pragma unroll
+    for (int r = 0; r < DOT_ROWS; ++r) src[r] = r < tile.rows ? source_row(a, tile.row0 + r) : -1;
+    int acc[DOT_OUTS][DOT_ROWS];
+#pragma unroll
+    for (int o = 0; o < DOT_OUTS; ++o)
+#pragma unroll
+        for (int r = 0; r < DOT_ROWS; ++r) acc[o][r] = 0;
+    const int8_t *w = a.wq + (static_cast<size_t>(tile.expert) * a.N + n0) * a.K;
+    for (int c = lane * 16; c < a.K; c += 512) {
+        uint4 wv[DOT_OUTS];
+#pragma unroll
+        for (int o = 0; o < DOT_OUTS; ++o)
+            wv[o] = n0 + o < a.N ? ldg_stream(w + static_cast<size_t>(o) * a.K + c) : make_uint4(0u, 0u, 0u, 0u);
+#pragma unroll
+        for (int r = 0; r < DOT_ROWS; ++r) {
+            if (r >= tile.rows) break;
+            if (src[r] < 0) continue;
+            const uint4 xv = *reinterpret_cast<const uint4 *>(a.xq + static_cast<size_t>(src[r]) * a.K + c);
+#pragma unroll
+            for (int o = 0; o < DOT_OUTS; ++o) {
+                acc[o][r] = __dp4a(static_cast<int>(wv[o].x), static_cast<int>(xv.x), acc[o][r]);
+                acc[o][r] = __dp4a(static_cast<int>(wv[o].y), static_cast<int>(xv.y), acc[o][r]);
+                acc[o][r] = __dp4a(static_cast<int>(wv[o].z), static_cast<int>(xv.z), acc[o][r]);
+                acc[o][r] = __dp4a(static_cast<int>(wv[o].w), static_cast<int>(xv.w), acc[o][r]);
+            }
+        }
+    }
+#pragma unroll
+    for (int r = 0; r < DOT_ROWS; ++r) {
+        if (r >= tile.rows) break;
+        const float xs = src[r] >= 0 ? a.xs[src[r]] : 0.f;
+#pragma unroll
+        for (int o = 0; o < DOT_OUTS; ++o) {
+            const int sum = __reduce_add_sync(FULL_MASK, acc[o][r]);
+            if (lane == o && n0 + o < a.N)
+                put(y + static_cast<size_t>(tile.row0 + r) * a.N + n0 + o,
+                    static_cast<float>(sum) * xs * a.ws[static_cast<size_t>(tile.expert) * a.N + n0 + o]);
+        }
+    }
+}
+
+template <typename T, int VE, bool ACT>
+cudaError_t quant_t(const void *x, int rows, int cols, int8_t *q, float *scales, cudaStream_t stream)
+{
+    return launch_pdl(quantize_rows<T, VE, ACT>, dim3(static_cast<unsigned>(rows)), dim3(QUANT_THREADS), 0, stream,
+                      static_cast<const T *>(x), cols, q, scales);
+}
+
+template <typename T, int VE>
+cudaError_t quant_a(bool act, const void *x, int rows, int cols, int8_t *q, float *scales, cudaStream_t stream)
+{
+    return act ? quant_t<T, VE, true>(x, rows, cols, q, scales, stream)
+               : quant_t<T, VE, false>(x, rows, cols, q, scales, stream);
+}
+
+size_t up256(size_t v) { return (v + 255) & ~static_cast<size_t>(255); }
+
+// Most tiles of `step` rows that R rows of n experts (and the rows of none) give.
+int most_tiles(int R, int n, int step)
+{
+    return R / step + (n + 1 < R ? n + 1 : R);
+}
+
+}  // namespace
+
+cudaError_t launch_quantize_rows(const void *x, int dtype, bool act, int rows, int cols, int8_t *q, float *scales,
+                                 cudaStream_t stream)
+{
+    const bool bf = dtype == SMOE_BF16;
+    const size_t pitch = static_cast<size_t>(cols) * (bf ? 2 : 4);
+    const bool v = ((reinterpret_cast<uintptr_t>(x) | pitch) & 15u) == 0;
+    if (bf)
+        return v ? quant_a<__nv_bfloat16, 8>(act, x, rows, cols, q, scales, stream)
+                 : quant_a<__nv_bfloat16, 1>(act, x, rows, cols, q, scales, stream);
+    return v ? quant_a<float, 4>(act, x, rows, cols, q, scales, stream)
+             : quant_a<float, 1>(act, x, rows, cols, q, scales, stream);
+}
+
+size_t q8_workspace(int nsrc, int R, int n, int N, int K)
+{
+    (void)nsrc;
+    (void)N;
+    (void)K;
+    return up256(16 + static_cast<size_t>(most_tiles(R, n, DOT_ROWS)) * sizeof(Tile));
+}
+
+cudaError_t launch_q8(const int8_t *xq, const float *xs, int nsrc, const int *order, int k, const int *offsets, int R,
+                      int n, const int8_t *wq, const float *ws, int N, int K, void *y, int dtype, void *workspace,
+                      cudaStream_t stream)
+{
+    unsigned *status = device_status_word();
+    if (!status) return cudaErrorInvalidDevice;
+    const int max_tiles = most_tiles(R, n, DOT_ROWS);
+    int *ntiles = static_cast<int *>(workspace);
+    Tile *tiles = reinterpret_cast<Tile *>(static_cast<char *>(workspace) + 16);
+    cudaError_t e = launch_pdl(plan_tiles, dim3(1), dim3(PLAN_THREADS), 0, stream, offsets, n, R, DOT_ROWS, max_tiles,
+                               ntiles, tiles, status);
+    if (e != cudaSuccess) return e;
+    const Q8Args a = {xq, xs, order, wq, ws, y, ntiles, tiles, status, k, nsrc, N, K};
+    const dim3 grid(static_cast<unsigned>(max_tiles),
+                    static_cast<unsigned>((N + DOT_WARPS * DOT_OUTS - 1) / (DOT_WARPS * DOT_OUTS)));
+    if (dtype == SMOE_BF16) return launch_pdl(q8_dot<__nv_bfloat16>, grid, dim3(DOT_WARPS * 32), 0, stream, a);
+    return launch_pdl(q8_dot<float>, grid, dim3(DOT_WARPS * 32), 0, stream, a);
+}
+
+}  // namespace smoe

@@ -1,0 +1,545 @@
+// Many tokens between the router and the experts: the top-k selection of
+// every row of logits, the stable sort of the tokens' slots by expert with
+// the gather of their rows, the weighted sum of the experts' rows back into
+// token order, and the gradients of all three.
+//
+// A slot a = t k + s is the s-th selection of token t.  The sort gives every
+// slot a row: rows [offsets[e], offsets[e + 1]) belong to expert e, in slot
+// order; slots without an expert take the rows past offsets[E] and their
+// place is written as -1 - row.
+#include "common.cuh"
+#include "internal_tokens.h"
+#include "rowvec.cuh"
+#include "smoe.h"
+
+namespace smoe {
+namespace {
+
+constexpr uint32_t kKeyNegInf = 0x007FFFFFu;  // value_key(-inf)
+
+// Order-preserving 32-bit key of a logit: larger = ranks first, NaN below
+// every number (1), 0 = retired.
+__device__ __forceinline__ uint32_t value_key(float v)
+{
+    const uint32_t u = __float_as_uint(v == 0.f ? 0.f : v);  // -0 ranks with +0
+    if (isnan(v)) return 1u;
+    return (u & 0x80000000u) ? ~u : (u | 0x80000000u);
+}
+
+__device__ __forceinline__ float value_of_key(uint32_t u)
+{
+    if (u <= 1u) return __int_as_float(0x7fffffff);
+    return __uint_as_float((u & 0x80000000u) ? (u & 0x7fffffffu) : ~u);
+}
+
+// Softmax over the k selected values of one row, by one warp: lane l holds
+// ranks l and l + 32 (keys ka, kb; indices ea, eb).  A selected -inf is a
+// masked expert: index -1, weight 0, and a row of nothing else is all that.
+__device__ __forceinline__ void write_row(uint32_t ka, uint32_t kb, int ea, int eb, int k, int *__restrict__ idx,
+                                          float *__restrict__ w)
+{
+    const int lane = threadIdx.x & 31;
+    const uint32_t k0 = __shfl_sync(FULL_MASK, ka, 0);
+    const float v0 = value_of_key(k0);
+    const bool ha = lane < k && ka != kKeyNegInf, hb = lane + 32 < k && kb != kKeyNegInf;
+    const float xa = ha ? expf(value_of_key(ka) - v0) : 0.f;
+    const float xb = hb ? expf(value_of_key(kb) - v0) : 0.f;
+    float sum = xa + xb;
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1) sum += __shfl_xor_sync(FULL_MASK, sum, off);
+    if (lane < k) {
+        idx[lane] = ha ? ea : -1;
+        w[lane] = ha ? xa / sum : 0.f;
+    }
+    if (lane + 32 < k) {
+        idx[lane + 32] = hb ? eb : -1;
+        w[lane + 32] = hb ? xb / sum : 0.f;
+    }
+}
+
+constexpr int TOPK_WARPS = 8;
+
+// n <= 32 V: one warp per row, V keys per lane (expert j 32 + lane), k
+// rounds of a warp-wide maximum; among equal values the lowest expert wins.
+template <int V>
+__global__ void __launch_bounds__(TOPK_WARPS * 32) topk_rows_warp(const float *__restrict__ logits, int T, int n, int ld,
+                                                                  int k, int *__restrict__ idx, float *__restrict__ w)
+{
+    const int t = blockIdx.x * TOPK_WARPS + (threadIdx.x >> 5);
+    const int lane = threadIdx.x & 31;
+    pdl_launch_dependents();
+    pdl_wait();
+    if (t >= T) return;
+    const float *row = logits + static_cast<size_t>(t) * ld;
+    uint32_t key[V];
+#pragma unroll
+    for (int j = 0; j < V; ++j) key[j] = j * 32 + lane < n ? value_key(row[j * 32 + lane]) : 0u;
+    uint32_t ka = 0u, kb = 0u;
+    int ea = -1, eb = -1;
+    for (int r = 0; r < k; ++r) {
+        uint32_t best = key[0];
+        int bj = 0;
+#pragma unroll
+        for (int j = 1; j < V; ++j)
+            if (key[j] > best) {
+                best = key[j];
+                bj = j;
+            }
+        const uint32_t top = __reduce_max_sync(FULL_MASK, best);
+        const unsigned e = __reduce_min_sync(FULL_MASK, best == top ? static_cast<unsigned>(bj * 32 + lane) : 0xFFFFFFFFu);
+        if ((e & 31u) == static_cast<unsigned>(lane)) {
+            const int oj = static_cast<int>(e >> 5);
+#pragma unroll
+            for (int j = 0; j < V; ++j)
+                if (j == oj) key[j] = 0u;
+        }
+        if ((r & 31) == lane) {
+            if (r < 32) {
+                ka = top;
+                ea = static_cast<int>(e);
+            } else {
+                kb = top;
+                eb = static_cast<int>(e);
+            }
+        }
+    }
+    write_row(ka, kb, ea, eb, k, idx + static_cast<size_t>(t) * k, w + static_cast<size_t>(t) * k);
+}
+
+constexpr int TOPK_BLOCK = 256;
+
+// Any n: one CTA per row, the keys in shared memory.
+__global__ void __launch_bounds__(TOPK_BLOCK) topk_rows_block(const float *__restrict__ logits, int n, int ld, int k,
+                                                              int *__restrict__ idx, float *__restrict__ w)
+{
+    extern __shared__ uint32_t keys[];  // [n]
+    __shared__ unsigned long long warp_best[TOPK_BLOCK / 32];
+    __shared__ uint32_t sel_k[SMOE_MAX_TOP_K];
+    __shared__ int sel_e[SMOE_MAX_TOP_K];
+    const int tid = threadIdx.x;
+    pdl_launch_dependents();
+    pdl_wait();
+    const size_t t = blockIdx.x;
+    const float *row = logits + t * ld;
+    for (int e = tid; e < n; e += TOPK_BLOCK) keys[e] = value_key(row[e]);
+    __syncthreads();
+    for (int r = 0; r < k; ++r) {
+        unsigned long long best = 0;
+        for (int e = tid; e < n; e += TOPK_BLOCK) {
+            const unsigned long long c =
+                (static_cast<unsigned long long>(keys[e]) << 32) | (0xFFFFFFFFu - static_cast<uint32_t>(e));
+            best = c > best ? c : best;
+        }
+#pragma unroll
+        for (int off = 16; off > 0; off >>= 1) {
+            const unsigned long long o = __shfl_xor_sync(FULL_MASK, best, off);
+            best = o > best ? o : best;
+        }
+        if ((tid & 31) == 0) warp_best[tid >> 5] = best;
+        __syncthreads();
+        if (tid == 0) {
+            for (int i = 1; i < TOPK_BLOCK / 32; ++i) best = warp_best[i] > best ? warp_best[i] : best;
+            const int e = static_cast<int>(0xFFFFFFFFu - static_cast<uint32_t>(best));
+            sel_k[r] = static_cast<uint32_t>(best >> 32);
+            sel_e[r] = e;
+            keys[e] = 0u;  // retired
+        }
+        __syncthreads();
+    }
+    if (tid < 32) {
+        const uint32_t ka = tid < k ? sel_k[tid] : 0u, kb = tid + 32 < k ? sel_k[tid + 32] : 0u;
+        const int ea = tid < k ? sel_e[tid] : -1, eb = tid + 32 < k ? sel_e[tid + 32] : -1;
+        write_row(ka, kb, ea, eb, k, idx + t * k, w + t * k);
+    }
+}
+
+// dl[idx[r]] = w[r] (dw[r] - sum_q w[q] dw[q]), every other logit's gradient
+// is 0.  One warp per row: zeros first, then the selected ones.
+__global__ void __launch_bounds__(TOPK_WARPS * 32) topk_rows_grad(const int *__restrict__ idx, const float *__restrict__ w,
+                                                                  const float *__restrict__ dw, int T, int n, int k,
+                                                                  float *__restrict__ dl)
+{
+    const int t = blockIdx.x * TOPK_WARPS + (threadIdx.x >> 5);
+    const int lane = threadIdx.x & 31;
+    pdl_launch_dependents();
+    pdl_wait();
+    if (t >= T) return;
+    const size_t a = static_cast<size_t>(t) * k;
+    const bool ina = lane < k, inb = lane + 32 < k;
+    const int ea = ina ? idx[a + lane] : -1, eb = inb ? idx[a + lane + 32] : -1;
+    const float wa = ea >= 0 ? w[a + lane] : 0.f, wb = eb >= 0 ? w[a + lane + 32] : 0.f;
+    const float ga = ea >= 0 ? dw[a + lane] : 0.f, gb = eb >= 0 ? dw[a + lane + 32] : 0.f;
+    float c = fmaf(wa, ga, wb * gb);
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1) c += __shfl_xor_sync(FULL_MASK, c, off);
+    float *row = dl + static_cast<size_t>(t) * n;
+    if ((n & 3) == 0) {
+        for (int e = lane; e < (n >> 2); e += 32) reinterpret_cast<float4 *>(row)[e] = make_float4(0.f, 0.f, 0.f, 0.f);
+    } else {
+        for (int e = lane; e < n; e += 32) row[e] = 0.f;
+    }
+    __syncwarp();
+    if (ea >= 0 && ea < n) row[ea] = wa * (ga - c);
+    if (eb >= 0 && eb < n) row[eb] = wb * (gb - c);
+}
+
+// ---------------------------------------------------------------- the sort
+
+constexpr int SORT_THREADS = 256;  // = slots per chunk
+
+// An index outside [0, n) goes to the bucket n: no expert.
+__device__ __forceinline__ int bucket(int e, int n) { return e >= 0 && e < n ? e : n; }
+
+// hist[c][e] = slots of chunk c in bucket e <= n.
+__global__ void __launch_bounds__(SORT_THREADS) sort_hist(const int *__restrict__ top_idx, int R, int n,
+                                                          int *__restrict__ hist)
+{
+    extern __shared__ int cnt[];  // [n + 1]
+    pdl_launch_dependents();
+    for (int e = threadIdx.x; e <= n; e += SORT_THREADS) cnt[e] = 0;
+    __syncthreads();
+    pdl_wait();
+    const long long a = static_cast<long long>(blockIdx.x) * SORT_THREADS + threadIdx.x;
+    if (a < R) atomicAdd(&cnt[bucket(top_idx[a], n)], 1);
+    __syncthreads();
+    int *h = hist + static_cast<size_t>(blockIdx.x) * (n + 1);
+    for (int e = threadIdx.x; e <= n; e += SORT_THREADS) h[e] = cnt[e];
+}
+
+// hist[c][e] becomes the sum over earlier chunks, total[e] the sum over all.
+// A CTA takes 32 buckets; its 32 warps take equal runs of chunks.
+__global__ void __launch_bounds__(1024) sort_scan(int *__restrict__ hist, int *__restrict__ total, int nchunks, int n)
+{
+    __shared__ int part[32][33];
+    pdl_launch_dependents();
+    pdl_wait();
+    const int lane = threadIdx.x & 31, wi = threadIdx.x >> 5;
+    const int e = blockIdx.x * 32 + lane;
+    const int per = (nchunks + 31) / 32;
+    const int c0 = min(nchunks, wi * per), c1 = min(nchunks, c0 + per);
+    int sum = 0;
+    if (e <= n)
+        for (int c = c0; c < c1; ++c) sum += hist[static_cast<size_t>(c) * (n + 1) + e];
+    part[wi][lane] = sum;
+    __syncthreads();
+    int before = 0;
+    for (int i = 0; i < wi; ++i) before += part[i][lane];
+    if (e <= n) {
+        for (int c = c0; c < c1; ++c) {
+            int *h = hist + static_cast<size_t>(c) * (n + 1) + e;
+            const int v = *h;
+            *h = before;
+            before += v;
+        }
+        if (wi == 31) total[e] = before;
+    }
+}
+
+// Exclusive prefix sum of v over the block's threads (blockDim.x <= 1024).
+__device__ __forceinline__ int block_exclusive(int v, int *warp_sums)
+{
+    const int lane = threadIdx.x & 31, wi = threadIdx.x >> 5;
+    int inc = v;
+#pragma unroll
+    for (int off = 1; off < 32; off <<= 1) {
+        const int o = __shfl_up_sync(FULL_MASK, inc, off);
+        if (lane >= off) inc += o;
+    }
+    if (lane == 31) warp_sums[wi] = inc;
+    __syncthreads();
+    int before = 0;
+    for (int i = 0; i < wi; ++i) before += warp_sums[i];
+    __syncthreads();
+    return before + inc - v;
+}
+
+// Row of every slot: the bucket's first row, the bucket's slots in earlier
+// chunks, and the equal slots before it in its own chunk.
+__global__ void __launch_bounds__(SORT_THREADS) sort_place(const int *__restrict__ top_idx, int R, int n,
+                                                           const int *__restrict__ hist, const int *__restrict__ total,
+                                                           int *__restrict__ offsets, int *__restrict__ order,
+                                                           int *__restrict__ place)
+{
+    extern __shared__ int first[];  // [n + 1]
+    __shared__ __align__(16) int mine[SORT_THREADS];
+    __shared__ int warp_sums[SORT_THREADS / 32];
+    const int tid = threadIdx.x;
+    pdl_launch_dependents();
+    pdl_wait();
+    const long long a = static_cast<long long>(blockIdx.x) * SORT_THREADS + tid;
+    const int e = a < R ? bucket(top_idx[a], n) : n + 1;
+    mine[tid] = e;
+    int run = 0;
+    for (int b = 0; b <= n; b += SORT_THREADS) {
+        const int v = b + tid <= n ? total[b + tid] : 0;
+        const int ex = run + block_exclusive(v, warp_sums);
+        if (b + tid <= n) first[b + tid] = ex;
+        if (tid == SORT_THREADS - 1) warp_sums[0] = ex + v;
+        __syncthreads();
+        run = warp_sums[0];
+        __syncthreads();
+    }
+    if (blockIdx.x == 0)
+        for (int i = tid; i <= n; i += SORT_THREADS) offsets[i] = first[i];
+    if (a >= R) return;
+    int rank = 0;
+    for (int i = 0; i < tid; ++i) rank += mine[i] == e;
+    const int row = first[e] + hist[static_cast<size_t>(blockIdx.x) * (n + 1) + e] + rank;
+    order[row] = static_cast<int>(a);
+    place[a] = e < n ? row : -1 - row;
+}
+
+// ---------------------------------------------------------------- rows
+
+constexpr int ROW_THREADS = 256;
+
+// A place read from device memory, checked: the row (>= 0) of a slot with an
+// expert, or -1.  A row outside [0, R) is reported and treated as none.
+__device__ __forceinline__ int checked_place(int p, int R, unsigned *status)
+{
+    if (p >= R || p < -R) {
+        atomicExch(status, kStatusRoute);
+        return -1;
+    }
+    return p;
+}
+
+// xs[place[t, s]] = x[t]; the rows of slots without an expert are zeros.
+// One CTA per token and column block: x is read once and written k times.
+template <typename T, int VE>
+__global__ void __launch_bounds__(ROW_THREADS) gather_rows(const T *__restrict__ x, const int *__restrict__ place, int k,
+                                                           int d, T *__restrict__ xs)
+{
+    pdl_launch_dependents();
+    pdl_wait();
+    const size_t t = blockIdx.x;
+    for (int c = (blockIdx.y * ROW_THREADS + threadIdx.x) * VE; c < d; c += gridDim.y * ROW_THREADS * VE) {
+        RowVec<T, VE> v, z;
+        v.load(x + t * d + c);
+        z.zero();
+        for (int s = 0; s < k; ++s) {
+            const int p = place[t * k + s];
+            if (p >= 0) v.store(xs + static_cast<size_t>(p) * d + c);
+            else z.store(xs + static_cast<size_t>(-1 - p) * d + c);
+        }
+    }
+}
+
+// out[t] = sum over s, in order, of w[t, s] ys[place[t, s]] (w null: of the
+// rows themselves), f32 sums.
+template <typename T, int VE>
+__global__ void __launch_bounds__(ROW_THREADS) sum_rows(const T *__restrict__ ys, const int *__restrict__ place,
+                                                        const float *__restrict__ w, int R, int k, int d,
+                                                        T *__restrict__ out, unsigned *status)
+{
+    pdl_launch_dependents();
+    pdl_wait();
+    const size_t t = blockIdx.x;
+    for (int c = (blockIdx.y * ROW_THREADS + threadIdx.x) * VE; c < d; c += gridDim.y * ROW_THREADS * VE) {
+        float acc[VE];
+#pragma unroll
+        for (int i = 0; i < VE; ++i) acc[i] = 0.f;
+        for (int s = 0; s < k; ++s) {
+            const int p = checked_place(place[t * k + s], R, status);
+            if (p < 0) continue;
+            const float ws = w ? w[t * k + s] : 1.f;
+            RowVec<T, VE> v;
+            v.load(ys + static_cast<size_t>(p) * d + c);
+            float f[VE];
+            v.get(f);
+#pragma unroll
+            for (int i = 0; i < VE; ++i) acc[i] = fmaf(ws, f[i], acc[i]);
+        }
+        RowVec<T, VE> o;
+        o.set(acc);
+        o.store(out + t * d + c);
+    }
+}
+
+// d_ys[place[t, s]] = w[t, s] d_out[t] (zeros in the rows of slots without an
+// expert) and d_w[t, s] = <d_out[t], ys[place[t, s]]>: one warp per slot.
+template <typename T, int VE>
+__global__ void __launch_bounds__(ROW_THREADS) combine_grad(const T *__restrict__ d_out, const T *__restrict__ ys,
+                                                            const int *__restrict__ place, const float *__restrict__ w,
+                                                            int R, int k, int d, T *__restrict__ d_ys,
+                                                            float *__restrict__ d_w, unsigned *status)
+{
+    pdl_launch_dependents();
+    pdl_wait();
+    const size_t t = blockIdx.x;
+    const int lane = threadIdx.x & 31;
+    const T *g = d_out + t * d;
+    for (int s = threadIdx.x >> 5; s < k; s += ROW_THREADS / 32) {
+        const int raw = place[t * k + s];
+        const int p = checked_place(raw, R, status);
+        if (p < 0) {
+            if (raw < 0 && raw >= -R) {
+                RowVec<T, VE> z;
+                z.zero();
+                for (int c = lane * VE; c < d; c += 32 * VE) z.store(d_ys + static_cast<size_t>(-1 - raw) * d + c);
+            }
+            if (lane == 0) d_w[t * k + s] = 0.f;
+            continue;
+        }
+        const float ws = w[t * k + s];
+        float dot = 0.f;
+        for (int c = lane * VE; c < d; c += 32 * VE) {
+            RowVec<T, VE> gv, yv;
+            gv.load(g + c);
+            yv.load(ys + static_cast<size_t>(p) * d + c);
+            float gf[VE], yf[VE];
+            gv.get(gf);
+            yv.get(yf);
+#pragma unroll
+            for (int i = 0; i < VE; ++i) {
+                dot = fmaf(gf[i], yf[i], dot);
+                gf[i] *= ws;
+            }
+            gv.set(gf);
+            gv.store(d_ys + static_cast<size_t>(p) * d + c);
+        }
+#pragma unroll
+        for (int off = 16; off > 0; off >>= 1) dot += __shfl_xor_sync(FULL_MASK, dot, off);
+        if (lane == 0) d_w[t * k + s] = dot;
+    }
+}
+
+__global__ void __launch_bounds__(ROW_THREADS) zero_words(int *__restrict__ p, int n)
+{
+    pdl_launch_dependents();
+    pdl_wait();
+    const int i = blockIdx.x * ROW_THREADS + threadIdx.x;
+    if (i < n) p[i] = 0;
+}
+
+bool vec16(const void *p, size_t row_bytes)
+{
+    return ((reinterpret_cast<uintptr_t>(p) | row_bytes) & 15u) == 0;
+}
+
+}  // namespace
+
+cudaError_t launch_topk_rows(const float *logits, int T, int n, int ld, int k, int *idx, float *w, cudaStream_t stream)
+{
+    const dim3 grid(static_cast<unsigned>((T + TOPK_WARPS - 1) / TOPK_WARPS)), block(TOPK_WARPS * 32);
+    if (n <= 64) return launch_pdl(topk_rows_warp<2>, grid, block, 0, stream, logits, T, n, ld, k, idx, w);
+    if (n <= 128) return launch_pdl(topk_rows_warp<4>, grid, block, 0, stream, logits, T, n, ld, k, idx, w);
+    if (n <= 256) return launch_pdl(topk_rows_warp<8>, grid, block, 0, stream, logits, T, n, ld, k, idx, w);
+    if (n <= 512) return launch_pdl(topk_rows_warp<16>, grid, block, 0, stream, logits, T, n, ld, k, idx, w);
+    const size_t smem = static_cast<size_t>(n) * sizeof(uint32_t);
+    return launch_pdl(topk_rows_block, dim3(static_cast<unsigned>(T)), dim3(TOPK_BLOCK), smem, stream, logits, n, ld, k,
+                      idx, w);
+}
+
+cudaError_t launch_topk_rows_grad(const int *idx, const float *w, const float *dw, int T, int n, int k, float *dl,
+                                  cudaStream_t stream)
+{
+    return launch_pdl(topk_rows_grad, dim3(static_cast<unsigned>((T + TOPK_WARPS - 1) / TOPK_WARPS)),
+                      dim3(TOPK_WARPS * 32), 0, stream, idx, w, dw, T, n, k, dl);
+}
+
+cudaError_t launch_zero_words(int *p, int n, cudaStream_t stream)
+{
+    return launch_pdl(zero_words, dim3(static_cast<unsigned>((n + ROW_THREADS - 1) / ROW_THREADS)), dim3(ROW_THREADS), 0,
+                      stream, p, n);
+}
+
+size_t dispatch_workspace(int T, int k, int n)
+{
+    const size_t R = static_cast<size_t>(T) * k;
+    const size_t chunks = (R + SORT_THREADS - 1) / SORT_THREADS;
+    return ((chunks + 1) * (static_cast<size_t>(n) + 1) * sizeof(int) + 255) & ~static_cast<size_t>(255);
+}
+
+cudaError_t launch_sort_tokens(const int *top_idx, int R, int n, int *offsets, int *order, int *place, void *workspace,
+                               cudaStream_t stream)
+{
+    const int chunks = (R + SORT_THREADS - 1) / SORT_THREADS;
+    int *hist = static_cast<int *>(workspace);
+    int *total = hist + static_cast<size_t>(chunks) * (n + 1);
+    const size_t smem = (static_cast<size_t>(n) + 1) * sizeof(int);
+    cudaError_t e = launch_pdl(sort_hist, dim3(static_cast<unsigned>(chunks)), dim3(SORT_THREADS), smem, stream, top_idx,
+                               R, n, hist);
+    if (e != cudaSuccess) return e;
+    e = launch_pdl(sort_scan, dim3(static_cast<unsigned>((n + 32) / 32)), dim3(1024), 0, stream, hist, total, chunks, n);
+    if (e != cudaSuccess) return e;
+    return launch_pdl(sort_place, dim3(static_cast<unsigned>(chunks)), dim3(SORT_THREADS), smem, stream, top_idx, R, n,
+                      hist, total, offsets, order, place);
+}
+
+namespace {
+
+template <typename T, int VE>
+dim3 row_grid(int tokens, int d)
+{
+    const unsigned cols = static_cast<unsigned>((d + ROW_THREADS * VE - 1) / (ROW_THREADS * VE));
+    return dim3(static_cast<unsigned>(tokens), cols < 64u ? cols : 64u);
+}
+
+template <typename T, int VE>
+cudaError_t gather_t(const void *x, const int *place, int tokens, int k, int d, void *xs, cudaStream_t stream)
+{
+    return launch_pdl(gather_rows<T, VE>, row_grid<T, VE>(tokens, d), dim3(ROW_THREADS), 0, stream,
+                      static_cast<const T *>(x), place, k, d, static_cast<T *>(xs));
+}
+
+template <typename T, int VE>
+cudaError_t sum_t(const void *ys, const int *place, const float *w, int tokens, int k, int d, void *out, unsigned *status,
+                  cudaStream_t stream)
+{
+    return launch_pdl(sum_rows<T, VE>, row_grid<T, VE>(tokens, d), dim3(ROW_THREADS), 0, stream,
+                      static_cast<const T *>(ys), place, w, tokens * k, k, d, static_cast<T *>(out), status);
+}
+
+template <typename T, int VE>
+cudaError_t grad_t(const void *d_out, const void *ys, const int *place, const float *w, int tokens, int k, int d,
+                   void *d_ys, float *d_w, unsigned *status, cudaStream_t stream)
+{
+    return launch_pdl(combine_grad<T, VE>, dim3(static_cast<unsigned>(tokens)), dim3(ROW_THREADS), 0, stream,
+                      static_cast<const T *>(d_out), static_cast<const T *>(ys), place, w, tokens * k, k, d,
+                      static_cast<T *>(d_ys), d_w, status);
+}
+
+}  // namespace
+
+cudaError_t launch_gather_tokens(const void *x, int dtype, const int *place, int tokens, int k, int d, void *xs,
+                                 cudaStream_t stream)
+{
+    const size_t pitch = static_cast<size_t>(d) * (dtype == SMOE_BF16 ? 2 : 4);
+    const bool v = vec16(x, pitch) && vec16(xs, pitch);
+    if (dtype == SMOE_BF16)
+        return v ? gather_t<__nv_bfloat16, 8>(x, place, tokens, k, d, xs, stream)
+                 : gather_t<__nv_bfloat16, 1>(x, place, tokens, k, d, xs, stream);
+    return v ? gather_t<float, 4>(x, place, tokens, k, d, xs, stream)
+             : gather_t<float, 1>(x, place, tokens, k, d, xs, stream);
+}
+
+cudaError_t launch_sum_tokens(const void *ys, int dtype, const int *place, const float *w, int tokens, int k, int d,
+                              void *out, cudaStream_t stream)
+{
+    unsigned *status = device_status_word();
+    if (!status) return cudaErrorInvalidDevice;
+    const size_t pitch = static_cast<size_t>(d) * (dtype == SMOE_BF16 ? 2 : 4);
+    const bool v = vec16(ys, pitch) && vec16(out, pitch);
+    if (dtype == SMOE_BF16)
+        return v ? sum_t<__nv_bfloat16, 8>(ys, place, w, tokens, k, d, out, status, stream)
+                 : sum_t<__nv_bfloat16, 1>(ys, place, w, tokens, k, d, out, status, stream);
+    return v ? sum_t<float, 4>(ys, place, w, tokens, k, d, out, status, stream)
+             : sum_t<float, 1>(ys, place, w, tokens, k, d, out, status, stream);
+}
+
+cudaError_t launch_combine_tokens_grad(const void *d_out, const void *ys, int dtype, const int *place, const float *w,
+                                       int tokens, int k, int d, void *d_ys, float *d_w, cudaStream_t stream)
+{
+    unsigned *status = device_status_word();
+    if (!status) return cudaErrorInvalidDevice;
+    const size_t pitch = static_cast<size_t>(d) * (dtype == SMOE_BF16 ? 2 : 4);
+    const bool v = vec16(d_out, pitch) && vec16(ys, pitch) && vec16(d_ys, pitch);
+    if (dtype == SMOE_BF16)
+        return v ? grad_t<__nv_bfloat16, 8>(d_out, ys, place, w, tokens, k, d, d_ys, d_w, status, stream)
+                 : grad_t<__nv_bfloat16, 1>(d_out, ys, place, w, tokens, k, d, d_ys, d_w, status, stream);
+    return v ? grad_t<float, 4>(d_out, ys, place, w, tokens, k, d, d_ys, d_w, status, stream)
+             : grad_t<float, 1>(d_out, ys, place, w, tokens, k, d, d_ys, d_w, status, stream);
+}
+
+}  // namespace smoe
