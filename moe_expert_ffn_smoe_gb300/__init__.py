@@ -128,12 +128,30 @@ def _ptr(a):
     return a.data_ptr()
 
 
-def _stream(s):
-    if s is None:
+_current = None  # () -> cudaStream_t of torch's current stream on the current device
+
+
+def _current_stream():
+    """torch's current stream; the lookup is settled by the first call that
+    finds a device (asking torch.cuda.is_available() and building a Stream
+    object on every call cost as much as a small call's launch)."""
+    global _current
+    if _current is None:
         import torch
         if not torch.cuda.is_available():
             return None
-        return torch.cuda.current_stream().cuda_stream
+        torch.cuda.current_stream()  # initialises CUDA
+        raw, device = getattr(torch._C, "_cuda_getCurrentRawStream", None), getattr(torch._C, "_cuda_getDevice", None)
+        if raw is not None and device is not None:
+            _current = lambda: raw(device())  # noqa: E731
+        else:
+            _current = lambda: torch.cuda.current_stream().cuda_stream  # noqa: E731
+    return _current()
+
+
+def _stream(s):
+    if s is None:
+        return _current_stream()
     if isinstance(s, int):
         return s
     return s.cuda_stream
