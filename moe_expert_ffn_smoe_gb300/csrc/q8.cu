@@ -6,8 +6,7 @@
 // plan_tiles turns the experts' row counts, which only the device knows,
 // into a list of tiles of at most `step` rows of one expert each; rows past
 // the last expert's are tiles of expert -1, whose outputs are zeros.
-#include "common.cuh"
-#include "internal_tokens.h"
+#include "q8.cuh"
 #include "rowvec.cuh"
 #include "smoe.h"
 
@@ -77,10 +76,6 @@ __global__ void __launch_bounds__(QUANT_THREADS) quantize_rows(const T *__restri
 
 // ---------------------------------------------------------------- tiles
 
-struct Tile {
-    int expert, row0, rows, pad;
-};
-
 constexpr int PLAN_THREADS = 1024;
 
 // tiles[0 .. *ntiles): every expert's rows in steps of `step`, then the rows
@@ -146,21 +141,6 @@ struct Q8Args {
     int k, nsrc, N, K;
 };
 
-// Source row of sorted row r, or -1 (reported) where order says nonsense.
-__device__ __forceinline__ int source_row(const Q8Args &a, int r)
-{
-    if (!a.order) return r;
-    const int s = a.order[r];
-    if (s < 0 || s / a.k >= a.nsrc) {
-        atomicExch(a.status, kStatusRoute);
-        return -1;
-    }
-    return s / a.k;
-}
-
-__device__ __forceinline__ void put(float *p, float v) { *p = v; }
-__device__ __forceinline__ void put(__nv_bfloat16 *p, float v) { *p = __float2bfloat16_rn(v); }
-
 // Integer dot products on the CUDA cores, exact in 32 bits (K <= 32768): a
 // warp holds 4 weight rows against the tile's up to 8 activation rows, 16
 // columns of each per lane and step.
@@ -183,7 +163,7 @@ __global__ void __launch_bounds__(DOT_WARPS * 32) q8_dot(const Q8Args a)
     }
     int src[DOT_ROWS];
 #pragma unroll
-    for (int r = 0; r < DOT_ROWS; ++r) src[r] = r < tile.rows ? source_row(a, tile.row0 + r) : -1;
+    for (int r = 0; r < DOT_ROWS; ++r) src[r] = r < tile.rows ? source_row(a.order, a.k, a.nsrc, tile.row0 + r, a.status) : -1;
     int acc[DOT_OUTS][DOT_ROWS];
 #pragma unroll
     for (int o = 0; o < DOT_OUTS; ++o)
@@ -237,14 +217,6 @@ cudaError_t quant_a(bool act, const void *x, int rows, int cols, int8_t *q, floa
                : quant_t<T, VE, false>(x, rows, cols, q, scales, stream);
 }
 
-size_t up256(size_t v) { return (v + 255) & ~static_cast<size_t>(255); }
-
-// Most tiles of `step` rows that R rows of n experts (and the rows of none) give.
-int most_tiles(int R, int n, int step)
-{
-    return R / step + (n + 1 < R ? n + 1 : R);
-}
-
 }  // namespace
 
 cudaError_t launch_quantize_rows(const void *x, int dtype, bool act, int rows, int cols, int8_t *q, float *scales,
@@ -260,11 +232,19 @@ cudaError_t launch_quantize_rows(const void *x, int dtype, bool act, int rows, i
              : quant_a<float, 1>(act, x, rows, cols, q, scales, stream);
 }
 
+#ifndef Q8_TC_MIN
+#define Q8_TC_MIN 16
+#endif
+static bool on_tensor_cores(int R, int n, int K)
+{
+    return K > 0 && R > static_cast<long long>(Q8_TC_MIN) * n;
+}
+
 size_t q8_workspace(int nsrc, int R, int n, int N, int K)
 {
     (void)nsrc;
     (void)N;
-    (void)K;
+    if (on_tensor_cores(R, n, K)) return q8_tc_workspace(R, n, K);
     return up256(16 + static_cast<size_t>(most_tiles(R, n, DOT_ROWS)) * sizeof(Tile));
 }
 
@@ -272,6 +252,8 @@ cudaError_t launch_q8(const int8_t *xq, const float *xs, int nsrc, const int *or
                       int n, const int8_t *wq, const float *ws, int N, int K, void *y, int dtype, void *workspace,
                       cudaStream_t stream)
 {
+    if (on_tensor_cores(R, n, K))
+        return launch_q8_tc(Q8Call{xq, xs, nsrc, order, k, offsets, R, n, wq, ws, N, K, y, dtype}, workspace, stream);
     unsigned *status = device_status_word();
     if (!status) return cudaErrorInvalidDevice;
     const int max_tiles = most_tiles(R, n, DOT_ROWS);
