@@ -20,7 +20,8 @@
 // take neighbouring weight tiles of the same rows and each loads half of the
 // row tile for both (multicast), which halves the activation traffic from
 // L2.  Roles (warps): 0-7 epilogue, 8-15 widen weights (two groups, alternate
-// K tiles), 16 issues the MMAs, 17 streams the weights, 18 the rows.
+// K tiles), 16 issues the MMAs, 17 streams the weights, 18 and 19
+// the rows.
 // Every wait is bounded.
 #include <cuda_fp16.h>
 
@@ -41,17 +42,19 @@ constexpr int CONV_WARP0 = 8;
 constexpr int MMA_WARP = 16, W_WARP = 17, X_WARP = 18;
 constexpr int TC_THREADS = 20 * 32;
 
-// Shapes of the two forms: row tile NT, cluster CL, and the rings of A
-// stages (tensor memory), row stages and weight chunks (shared memory).
+// Shapes of the two forms: row tile NT, cluster CL, the rings of A stages
+// (tensor memory), row stages and weight chunks (shared memory), and the rows
+// of one tensor copy of activations (a copy costs its issuer about 100 clocks
+// whatever its size: 16-row boxes made the issuing warp pace the K loop).
 template <int NT>
 struct Form;
 template <>
 struct Form<192> {
-    static constexpr int CL = 2, AS = 4, XS = 6, WS = 4;
+    static constexpr int CL = 2, AS = 4, XS = 6, WS = 4, BOX = 48;
 };
 template <>
 struct Form<64> {
-    static constexpr int CL = 1, AS = 8, XS = 8, WS = 8;
+    static constexpr int CL = 1, AS = 8, XS = 8, WS = 8, BOX = 16;
 };
 
 template <int NT>
@@ -118,6 +121,20 @@ __device__ __forceinline__ void mma_commit_mc(uint32_t bar, uint16_t mask)
                  : "memory");
 }
 
+// Whether phase `parity` of an mbarrier has completed, without waiting.
+__device__ __forceinline__ bool mbar_test(uint32_t bar, uint32_t parity)
+{
+    uint32_t done;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.test_wait.parity.acquire.cta.shared::cta.b64 p, [%1], %2;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(done)
+        : "r"(bar), "r"(parity)
+        : "memory");
+    return done != 0;
+}
+
 __device__ __forceinline__ Tile tile_at(const TcArgs &a, int i, int ntiles)
 {
     if (i >= ntiles) return Tile{0, 0, 0, 0};
@@ -131,7 +148,7 @@ __global__ void __launch_bounds__(TC_THREADS, 1) q8_tc(const __grid_constant__ T
     using F = Form<NT>;
     constexpr int CL = F::CL, AS = F::AS, XS = F::XS, WS = F::WS;
     constexpr uint32_t XB = NT * 128u, ACOL0 = 2u * NT;
-    static_assert(2 * NT + AS * 32 <= 512 && AS % 2 == 0, "tensor memory");
+    static_assert(2 * NT + AS * 32 <= 512 && AS % 2 == 0 && XS % 2 == 0, "tensor memory; two issuers");
     extern __shared__ uint8_t smem_raw[];
     const uint32_t raw = smem_addr(smem_raw);
     const uint32_t base = (raw + 1023u) & ~1023u;
@@ -185,77 +202,111 @@ __global__ void __launch_bounds__(TC_THREADS, 1) q8_tc(const __grid_constant__ T
     bool failed = false;
 
     if (warp == W_WARP) {
-        if (lane == 0) {
-            uint32_t g = 0;
+        if (elect_one()) {
+            uint32_t s = 0, p = 1;  // parity of the release before this round; none waited for in the first
+            bool round0 = true;
             for (long long it = first; it < nitems && !failed; it += stride) {
                 const Tile t = tile_at(a, static_cast<int>(it / mgroups), ntiles);
                 const int row = t.expert * a.N + (static_cast<int>(it % mgroups) * CL + rank) * MT;
-                for (int c = 0; c < nch; ++c, ++g) {
-                    const uint32_t s = g % WS;
-                    if (g >= WS && !mbar_wait_bounded(wempty + 8 * s, (g / WS - 1) & 1, a.status, 7u)) {
+                for (int c = 0; c < nch; ++c) {
+                    if (!round0 && !mbar_wait_bounded(wempty + 8 * s, p, a.status, 7u)) {
                         failed = true;
                         break;
                     }
                     mbar_arrive_expect_tx(wfull + 8 * s, W_BYTES);
                     tma_load_2d(w0 + s * W_BYTES, &a.wmap, c * 128, row, wfull + 8 * s);
+                    if (++s == WS) {
+                        s = 0;
+                        p ^= 1u;
+                        round0 = false;
+                    }
                 }
             }
         }
-    } else if (warp == X_WARP) {
-        uint32_t g = 0;
-        for (long long it = first; it < nitems && !failed; it += stride) {
-            const Tile t = tile_at(a, static_cast<int>(it / mgroups), ntiles);
-            const int boxes = (t.rows + 15) >> 4;
-            for (int kt = 0; kt < nkt; ++kt, ++g) {
-                const uint32_t s = g % XS;
-                if (lane == 0) {
-                    if (g >= XS && !mbar_wait_bounded(xempty + 8 * s, (g / XS - 1) & 1, a.status, 8u)) failed = true;
-                    else mbar_arrive_expect_tx(xfull + 8 * s, static_cast<uint32_t>(boxes) * 2048u);
+        __syncwarp();
+    } else if (warp == X_WARP || warp == X_WARP + 1) {
+        // the two warps take alternate K tiles: a tensor copy costs its
+        // issuer 100 to 200 clocks, and one issuer paced the K loop
+        if (elect_one()) {
+            uint32_t s = warp - X_WARP, p = 1;
+            bool round0 = true;
+            for (long long it = first; it < nitems && !failed; it += stride) {
+                const Tile t = tile_at(a, static_cast<int>(it / mgroups), ntiles);
+                const int boxes = (t.rows + F::BOX - 1) / F::BOX;
+                for (int kt = warp - X_WARP; kt < nkt; kt += 2) {
+                    if (!round0 && !mbar_wait_bounded(xempty + 8 * s, p, a.status, 8u)) {
+                        failed = true;
+                        break;
+                    }
+                    mbar_arrive_expect_tx(xfull + 8 * s, static_cast<uint32_t>(boxes) * (F::BOX * 128u));
+                    for (int b = rank; b < boxes; b += CL) {
+                        const uint32_t dst = x0 + s * XB + static_cast<uint32_t>(b) * (F::BOX * 128u);
+                        if (CL > 1)
+                            tma_load_2d_mc(dst, &a.xmap, kt * KT, t.row0 + b * F::BOX, xfull + 8 * s, (1u << CL) - 1);
+                        else tma_load_2d(dst, &a.xmap, kt * KT, t.row0 + b * F::BOX, xfull + 8 * s);
+                    }
+                    s += 2;
+                    if (s >= XS) {
+                        s -= XS;
+                        p ^= 1u;
+                        round0 = false;
+                    }
                 }
-                failed = __shfl_sync(FULL_MASK, failed, 0);
-                if (failed) break;
-                if (lane < boxes && lane % CL == rank) {
-                    const uint32_t dst = x0 + s * XB + static_cast<uint32_t>(lane) * 2048u;
-                    if (CL > 1) tma_load_2d_mc(dst, &a.xmap, kt * KT, t.row0 + lane * 16, xfull + 8 * s, (1u << CL) - 1);
-                    else tma_load_2d(dst, &a.xmap, kt * KT, t.row0 + lane * 16, xfull + 8 * s);
+            }
+            // the other CTA's last releases of this warp's stages arrive
+            // here: they must have before this CTA may leave
+            if (CL > 1 && !failed) {
+                for (int j = 0; j < XS / 2; ++j) {
+                    if (!round0 && !mbar_wait_bounded(xempty + 8 * s, p, a.status, 8u)) failed = true;
+                    s += 2;
+                    if (s >= XS) {
+                        s -= XS;
+                        p ^= 1u;
+                        round0 = false;
+                    }
                 }
             }
         }
-        // the other CTA's last releases of these stages arrive here: they
-        // must have before this CTA may leave
-        if (CL > 1 && !failed && lane == 0)
-            for (uint32_t j = g > XS ? g - XS : 0; j < g; ++j)
-                if (!mbar_wait_bounded(xempty + 8 * (j % XS), (j / XS) & 1, a.status, 8u)) failed = true;
+        __syncwarp();
     } else if (warp == MMA_WARP) {
-        if (lane == 0) {
-            uint32_t g = 0, d = 0;
+        // one thread issues; it looks at both barriers of a stage before it
+        // waits for either, so that two stages that are ready cost one look
+        if (elect_one()) {
+            uint32_t sa = 0, pa = 0, sx = 0, px = 0, d = 0;
             for (long long it = first; it < nitems && !failed; it += stride, ++d) {
                 const Tile t = tile_at(a, static_cast<int>(it / mgroups), ntiles);
                 const uint32_t idesc = idesc_f16((t.rows + 15) & ~15);
                 const uint32_t acc = tmem + (d & 1) * NT;
-                if (d >= 2 && !mbar_wait_bounded(dempty + 8 * (d & 1), (d / 2 - 1) & 1, a.status, 4u)) {
-                    failed = true;
-                    break;
-                }
-                for (int kt = 0; kt < nkt; ++kt, ++g) {
-                    const uint32_t sa = g % AS, sx = g % XS;
-                    if (!mbar_wait_bounded(xfull + 8 * sx, (g / XS) & 1, a.status, 3u) ||
-                        !mbar_wait_bounded(afull + 8 * sa, (g / AS) & 1, a.status, 3u)) {
+                if (d >= 2 && !mbar_wait_bounded(dempty + 8 * (d & 1), (d / 2 - 1) & 1, a.status, 4u)) failed = true;
+                for (int kt = 0; kt < nkt && !failed; ++kt) {
+                    const bool rx = mbar_test(xfull + 8 * sx, px), ra = mbar_test(afull + 8 * sa, pa);
+                    if (!(rx && ra) && !(mbar_wait_bounded(xfull + 8 * sx, px, a.status, 3u) &&
+                                         mbar_wait_bounded(afull + 8 * sa, pa, a.status, 3u))) {
                         failed = true;
                         break;
                     }
                     tc_fence_after();
+                    const uint32_t at = tmem + ACOL0 + sa * 32;
+                    const uint64_t xd = desc_sw128(x0 + sx * XB);
 #pragma unroll
                     for (int kk = 0; kk < KT / 16; ++kk)
-                        mma_f16_ta(acc, tmem + ACOL0 + sa * 32 + kk * 8, desc_sw128(x0 + sx * XB + kk * 32), idesc,
-                                   kt + kk != 0);
+                        mma_f16_ta(acc, at + kk * 8, xd + kk * 2, idesc, kt + kk != 0);
                     mma_commit(aempty + 8 * sa);
                     if (CL > 1) mma_commit_mc(xempty + 8 * sx, (1u << CL) - 1);
                     else mma_commit(xempty + 8 * sx);
+                    if (kt == nkt - 1) mma_commit(dfull + 8 * (d & 1));
+                    if (++sa == AS) {
+                        sa = 0;
+                        pa ^= 1u;
+                    }
+                    if (++sx == XS) {
+                        sx = 0;
+                        px ^= 1u;
+                    }
                 }
-                if (!failed) mma_commit(dfull + 8 * (d & 1));
             }
         }
+        __syncwarp();
     } else if (warp >= CONV_WARP0 && warp < MMA_WARP) {
         // thread = one weight row; group grp widens the K tiles 2 c + grp
         const int ct = threadIdx.x - CONV_WARP0 * 32;
@@ -554,7 +605,7 @@ cudaError_t launch_q8_tc(const Q8Call &c, void *workspace, cudaStream_t stream)
 
     TcArgs a = {};
     if (!encode(&a.wmap, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, c.wq, c.K, static_cast<long long>(c.n) * c.N, 128, MT) ||
-        !encode(&a.xmap, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 2, x16, c.K, c.R, KT, 16))
+        !encode(&a.xmap, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 2, x16, c.K, c.R, KT, nt == 192 ? Form<192>::BOX : Form<64>::BOX))
         return cudaErrorInvalidValue;
     const PrepArgs p = {c.xq, c.xs, c.order, c.offsets, x16, xss, c.y, ntiles, tiles, status, c.nsrc, c.k, c.R, c.n, c.K,
                         c.N, nt, max_tiles, c.dtype == SMOE_BF16 ? 2 : 4};
