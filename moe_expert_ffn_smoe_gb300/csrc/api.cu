@@ -815,9 +815,8 @@ int smoe_dispatch_tokens(const int *top_idx, int n_tokens, int k, int n_experts,
                           {xs, rows ? slots * d_model * e : 0}};
     const Span ins[2] = {{top_idx, slots * sizeof(int)}, {x, rows ? static_cast<size_t>(n_tokens) * d_model * e : 0}};
     if (any_alias(outs, 5, ins, 2)) return SMOE_ERR_ALIAS;
-    cudaError_t err = smoe::launch_sort_tokens(top_idx, static_cast<int>(slots), n_experts, offsets, order, place, workspace, s);
-    if (err == cudaSuccess && rows) err = smoe::launch_gather_tokens(x, dtype, place, n_tokens, k, d_model, xs, s);
-    return to_status(err);
+    return to_status(smoe::launch_dispatch(top_idx, n_tokens, k, n_experts, rows ? x : nullptr, dtype, d_model, offsets,
+                                           order, place, rows ? xs : nullptr, workspace, s));
 }
 
 // out[t] = sum over s of w[t, s] rows[place[t, s]], w null: of the rows.

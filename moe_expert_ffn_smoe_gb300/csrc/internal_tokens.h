@@ -13,10 +13,8 @@ cudaError_t launch_topk_rows_grad(const int *idx, const float *w, const float *d
 // into that order, their weighted sum back (w null: plain sum) and its
 // gradient.  dtype: SMOE_F32 or SMOE_BF16.
 size_t dispatch_workspace(int T, int k, int n);
-cudaError_t launch_sort_tokens(const int *top_idx, int R, int n, int *offsets, int *order, int *place, void *workspace,
-                               cudaStream_t stream);
-cudaError_t launch_gather_tokens(const void *x, int dtype, const int *place, int tokens, int k, int d, void *xs,
-                                 cudaStream_t stream);
+cudaError_t launch_dispatch(const int *top_idx, int tokens, int k, int n, const void *x, int dtype, int d, int *offsets,
+                            int *order, int *place, void *xs, void *workspace, cudaStream_t stream);
 cudaError_t launch_sum_tokens(const void *ys, int dtype, const int *place, const float *w, int tokens, int k, int d,
                               void *out, cudaStream_t stream);
 cudaError_t launch_combine_tokens_grad(const void *d_out, const void *ys, int dtype, const int *place, const float *w,

@@ -35,42 +35,91 @@ __device__ __forceinline__ void quant_values(const T *row, int cols, int c, floa
     }
 }
 
-// One CTA per row: the largest magnitude, then the rounding.
+// VE codes of one vector as one store.
+__device__ __forceinline__ void put_codes(int8_t *q, const int (&c)[8])
+{
+    uint2 w;
+    w.x = (c[0] & 0xff) | (c[1] & 0xff) << 8 | (c[2] & 0xff) << 16 | static_cast<uint32_t>(c[3]) << 24;
+    w.y = (c[4] & 0xff) | (c[5] & 0xff) << 8 | (c[6] & 0xff) << 16 | static_cast<uint32_t>(c[7]) << 24;
+    *reinterpret_cast<uint2 *>(q) = w;
+}
+__device__ __forceinline__ void put_codes(int8_t *q, const int (&c)[4])
+{
+    *reinterpret_cast<uint32_t *>(q) =
+        (c[0] & 0xff) | (c[1] & 0xff) << 8 | (c[2] & 0xff) << 16 | static_cast<uint32_t>(c[3]) << 24;
+}
+__device__ __forceinline__ void put_codes(int8_t *q, const int (&c)[1]) { *q = static_cast<int8_t>(c[0]); }
+
+// One CTA per row: the largest magnitude, then the rounding.  A thread keeps
+// its first NV vectors in registers, so that a row of up to NV x 256 vectors
+// is read (and its activation computed) once; what is beyond is read again.
+// Bound by reading x; measured against reading every row twice: 2047 rows of
+// 4096 bf16 (table in the design notes).
 template <typename T, int VE, bool ACT>
 __global__ void __launch_bounds__(QUANT_THREADS) quantize_rows(const T *__restrict__ x, int cols, int8_t *__restrict__ q,
                                                                float *__restrict__ scales)
 {
+    constexpr int NV = 32 / VE < 8 ? 32 / VE : 8;
     __shared__ float warp_max[QUANT_THREADS / 32];
     pdl_launch_dependents();
     pdl_wait();
     const size_t r = blockIdx.x;
     const T *row = x + r * cols * (ACT ? 2 : 1);
+    const int c0 = threadIdx.x * VE;
+    float held[NV][VE];
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+        if (c0 + i * QUANT_THREADS * VE < cols) quant_values<T, VE, ACT>(row, cols, c0 + i * QUANT_THREADS * VE, held[i]);
+        else {
+#pragma unroll
+            for (int j = 0; j < VE; ++j) held[i][j] = 0.f;
+        }
+    }
     float top = 0.f;
     bool bad = false;
-    for (int c = threadIdx.x * VE; c < cols; c += QUANT_THREADS * VE) {
+#pragma unroll
+    for (int i = 0; i < NV; ++i)
+#pragma unroll
+        for (int j = 0; j < VE; ++j) {
+            bad |= !isfinite(held[i][j]);
+            top = fmaxf(top, fabsf(held[i][j]));
+        }
+    for (int c = c0 + NV * QUANT_THREADS * VE; c < cols; c += QUANT_THREADS * VE) {
         float v[VE];
         quant_values<T, VE, ACT>(row, cols, c, v);
 #pragma unroll
-        for (int i = 0; i < VE; ++i) {
-            bad |= !isfinite(v[i]);
-            top = fmaxf(top, fabsf(v[i]));
+        for (int j = 0; j < VE; ++j) {
+            bad |= !isfinite(v[j]);
+            top = fmaxf(top, fabsf(v[j]));
         }
     }
 #pragma unroll
     for (int off = 16; off > 0; off >>= 1) top = fmaxf(top, __shfl_xor_sync(FULL_MASK, top, off));
     if ((threadIdx.x & 31) == 0) warp_max[threadIdx.x >> 5] = top;
     bad = __syncthreads_or(bad);
+#pragma unroll
     for (int i = 0; i < QUANT_THREADS / 32; ++i) top = fmaxf(top, warp_max[i]);
     // a row of zeros has scale 0; a row that is not finite scale NaN and
     // codes 0, so that every product of it is NaN
     const float up = bad || top == 0.f ? 0.f : __fdiv_rn(127.f, top);
     if (threadIdx.x == 0) scales[r] = bad ? __int_as_float(0x7fffffff) : __fdiv_rn(top, 127.f);
-    for (int c = threadIdx.x * VE; c < cols; c += QUANT_THREADS * VE) {
+    auto code = [&](float v) { return bad ? 0 : max(-127, min(127, __float2int_rn(__fmul_rn(v, up)))); };
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+        const int c = c0 + i * QUANT_THREADS * VE;
+        if (c >= cols) break;
+        int k[VE];
+#pragma unroll
+        for (int j = 0; j < VE; ++j) k[j] = code(held[i][j]);
+        put_codes(q + r * cols + c, k);
+    }
+    for (int c = c0 + NV * QUANT_THREADS * VE; c < cols; c += QUANT_THREADS * VE) {
         float v[VE];
+        int k[VE];
         quant_values<T, VE, ACT>(row, cols, c, v);
 #pragma unroll
-        for (int i = 0; i < VE; ++i)
-            q[r * cols + c + i] = bad ? 0 : static_cast<int8_t>(max(-127, min(127, __float2int_rn(__fmul_rn(v[i], up)))));
+        for (int j = 0; j < VE; ++j) k[j] = code(v[j]);
+        put_codes(q + r * cols + c, k);
     }
 }
 
@@ -79,7 +128,7 @@ __global__ void __launch_bounds__(QUANT_THREADS) quantize_rows(const T *__restri
 constexpr int PLAN_THREADS = 1024;
 
 // tiles[0 .. *ntiles): every expert's rows in steps of `step`, then the rows
-// past the last expert's.  offsets null: one matrix, R rows.
+// past the last expert's.
 __global__ void __launch_bounds__(PLAN_THREADS) plan_tiles(const int *__restrict__ offsets, int n, int R, int step,
                                                            int max_tiles, int *__restrict__ ntiles,
                                                            Tile *__restrict__ tiles, unsigned *status)
@@ -94,8 +143,8 @@ __global__ void __launch_bounds__(PLAN_THREADS) plan_tiles(const int *__restrict
         const int e = b + tid;
         int lo = 0, hi = 0;
         if (e <= n) {
-            lo = offsets ? offsets[e] : (e == 0 ? 0 : R);
-            hi = e < n ? (offsets ? offsets[e + 1] : R) : R;
+            lo = offsets[e];
+            hi = e < n ? offsets[e + 1] : R;
             if (lo < 0 || hi < lo || hi > R) {
                 atomicExch(status, kStatusRoute);
                 lo = hi = 0;
@@ -138,22 +187,26 @@ struct Q8Args {
     const int *ntiles;
     const Tile *tiles;
     unsigned *status;
-    int k, nsrc, N, K;
+    int k, nsrc, N, K, R;
 };
 
 // Integer dot products on the CUDA cores, exact in 32 bits (K <= 32768): a
 // warp holds 4 weight rows against the tile's up to 8 activation rows, 16
-// columns of each per lane and step.
+// columns of each per lane and step, two steps of weights in flight.  Bound
+// by streaming the weights; for one matrix (tiles null) they are asked for
+// before the previous kernel is waited for.
 template <typename T>
-__global__ void __launch_bounds__(DOT_WARPS * 32) q8_dot(const Q8Args a)
+__global__ void __launch_bounds__(DOT_WARPS * 32, 2) q8_dot(const Q8Args a)
 {
     pdl_launch_dependents();
-    pdl_wait();
-    if (static_cast<int>(blockIdx.x) >= *a.ntiles) return;
-    const Tile tile = a.tiles[blockIdx.x];
     const int lane = threadIdx.x & 31;
     const int n0 = (blockIdx.y * DOT_WARPS + (threadIdx.x >> 5)) * DOT_OUTS;
-    if (n0 >= a.N) return;
+    if (a.tiles) {
+        pdl_wait();
+        if (static_cast<int>(blockIdx.x) >= *a.ntiles) return;
+    }
+    const int row0 = blockIdx.x * DOT_ROWS;
+    const Tile tile = a.tiles ? a.tiles[blockIdx.x] : Tile{0, row0, min(DOT_ROWS, a.R - row0), 0};
     T *y = static_cast<T *>(a.y);
     if (tile.expert < 0) {
         for (int i = lane; i < tile.rows * DOT_OUTS; i += 32)
@@ -161,33 +214,48 @@ __global__ void __launch_bounds__(DOT_WARPS * 32) q8_dot(const Q8Args a)
                 put(y + static_cast<size_t>(tile.row0 + i / DOT_OUTS) * a.N + n0 + i % DOT_OUTS, 0.f);
         return;
     }
+    const int8_t *w = a.wq + (static_cast<size_t>(tile.expert) * a.N + n0) * a.K;
+    uint4 wv[2][DOT_OUTS];
+    auto fetch = [&](uint4 (&v)[DOT_OUTS], int c) {
+#pragma unroll
+        for (int o = 0; o < DOT_OUTS; ++o)
+            v[o] = n0 + o < a.N && c < a.K ? ldg_stream(w + static_cast<size_t>(o) * a.K + c) : make_uint4(0u, 0u, 0u, 0u);
+    };
+    int c = lane * 16;
+    fetch(wv[0], c);
+    fetch(wv[1], c + 512);
+    if (!a.tiles) pdl_wait();
+    if (n0 >= a.N) return;
     int src[DOT_ROWS];
 #pragma unroll
-    for (int r = 0; r < DOT_ROWS; ++r) src[r] = r < tile.rows ? source_row(a.order, a.k, a.nsrc, tile.row0 + r, a.status) : -1;
+    for (int r = 0; r < DOT_ROWS; ++r)
+        src[r] = r < tile.rows ? source_row(a.order, a.k, a.nsrc, tile.row0 + r, a.status) : -1;
     int acc[DOT_OUTS][DOT_ROWS];
 #pragma unroll
     for (int o = 0; o < DOT_OUTS; ++o)
 #pragma unroll
         for (int r = 0; r < DOT_ROWS; ++r) acc[o][r] = 0;
-    const int8_t *w = a.wq + (static_cast<size_t>(tile.expert) * a.N + n0) * a.K;
-    for (int c = lane * 16; c < a.K; c += 512) {
-        uint4 wv[DOT_OUTS];
-#pragma unroll
-        for (int o = 0; o < DOT_OUTS; ++o)
-            wv[o] = n0 + o < a.N ? ldg_stream(w + static_cast<size_t>(o) * a.K + c) : make_uint4(0u, 0u, 0u, 0u);
+    auto dot = [&](const uint4 (&v)[DOT_OUTS], int at) {
+        if (at >= a.K) return;
 #pragma unroll
         for (int r = 0; r < DOT_ROWS; ++r) {
             if (r >= tile.rows) break;
             if (src[r] < 0) continue;
-            const uint4 xv = *reinterpret_cast<const uint4 *>(a.xq + static_cast<size_t>(src[r]) * a.K + c);
+            const uint4 xv = *reinterpret_cast<const uint4 *>(a.xq + static_cast<size_t>(src[r]) * a.K + at);
 #pragma unroll
             for (int o = 0; o < DOT_OUTS; ++o) {
-                acc[o][r] = __dp4a(static_cast<int>(wv[o].x), static_cast<int>(xv.x), acc[o][r]);
-                acc[o][r] = __dp4a(static_cast<int>(wv[o].y), static_cast<int>(xv.y), acc[o][r]);
-                acc[o][r] = __dp4a(static_cast<int>(wv[o].z), static_cast<int>(xv.z), acc[o][r]);
-                acc[o][r] = __dp4a(static_cast<int>(wv[o].w), static_cast<int>(xv.w), acc[o][r]);
+                acc[o][r] = __dp4a(static_cast<int>(v[o].x), static_cast<int>(xv.x), acc[o][r]);
+                acc[o][r] = __dp4a(static_cast<int>(v[o].y), static_cast<int>(xv.y), acc[o][r]);
+                acc[o][r] = __dp4a(static_cast<int>(v[o].z), static_cast<int>(xv.z), acc[o][r]);
+                acc[o][r] = __dp4a(static_cast<int>(v[o].w), static_cast<int>(xv.w), acc[o][r]);
             }
         }
+    };
+    for (; c - lane * 16 < a.K; c += 1024) {
+        dot(wv[0], c);
+        fetch(wv[0], c + 1024);
+        dot(wv[1], c + 512);
+        fetch(wv[1], c + 1536);
     }
 #pragma unroll
     for (int r = 0; r < DOT_ROWS; ++r) {
@@ -256,13 +324,16 @@ cudaError_t launch_q8(const int8_t *xq, const float *xs, int nsrc, const int *or
         return launch_q8_tc(Q8Call{xq, xs, nsrc, order, k, offsets, R, n, wq, ws, N, K, y, dtype}, workspace, stream);
     unsigned *status = device_status_word();
     if (!status) return cudaErrorInvalidDevice;
-    const int max_tiles = most_tiles(R, n, DOT_ROWS);
+    // one matrix: tiles of consecutive rows, no list needed
+    const int max_tiles = offsets ? most_tiles(R, n, DOT_ROWS) : (R + DOT_ROWS - 1) / DOT_ROWS;
     int *ntiles = static_cast<int *>(workspace);
-    Tile *tiles = reinterpret_cast<Tile *>(static_cast<char *>(workspace) + 16);
-    cudaError_t e = launch_pdl(plan_tiles, dim3(1), dim3(PLAN_THREADS), 0, stream, offsets, n, R, DOT_ROWS, max_tiles,
-                               ntiles, tiles, status);
-    if (e != cudaSuccess) return e;
-    const Q8Args a = {xq, xs, order, wq, ws, y, ntiles, tiles, status, k, nsrc, N, K};
+    Tile *tiles = offsets ? reinterpret_cast<Tile *>(static_cast<char *>(workspace) + 16) : nullptr;
+    if (offsets) {
+        const cudaError_t e = launch_pdl(plan_tiles, dim3(1), dim3(PLAN_THREADS), 0, stream, offsets, n, R, DOT_ROWS,
+                                         max_tiles, ntiles, tiles, status);
+        if (e != cudaSuccess) return e;
+    }
+    const Q8Args a = {xq, xs, order, wq, ws, y, ntiles, tiles, status, k, nsrc, N, K, R};
     const dim3 grid(static_cast<unsigned>(max_tiles),
                     static_cast<unsigned>((N + DOT_WARPS * DOT_OUTS - 1) / (DOT_WARPS * DOT_OUTS)));
     if (dtype == SMOE_BF16) return launch_pdl(q8_dot<__nv_bfloat16>, grid, dim3(DOT_WARPS * 32), 0, stream, a);

@@ -289,6 +289,80 @@ __global__ void __launch_bounds__(SORT_THREADS) sort_place(const int *__restrict
     place[a] = e < n ? row : -1 - row;
 }
 
+// ---------------------------------------------------------------- small sorts
+
+constexpr int SMALL_THREADS = 256;
+
+// The whole dispatch of a small batch in one launch: every CTA finds the
+// rows of its own token's slots by counting, over all R slots, those that
+// sort before them, then copies its share of the token's row; one CTA more
+// counts the buckets and writes the offsets.  R^2 / 32 warp steps in all:
+// cheaper than three more launches up to SMALL_SLOTS.
+constexpr int SMALL_SLOTS = 4096;
+
+template <typename T, int VE>
+__global__ void __launch_bounds__(SMALL_THREADS) dispatch_small(const int *__restrict__ top_idx, int tokens, int k, int n,
+                                                                const T *__restrict__ x, int d, int *__restrict__ offsets,
+                                                                int *__restrict__ order, int *__restrict__ place,
+                                                                T *__restrict__ xs)
+{
+    extern __shared__ int cnt[];  // [n + 1]; the gathering CTAs use [0, k) for their rows
+    __shared__ int warp_sums[SMALL_THREADS / 32];
+    const int tid = threadIdx.x, lane = tid & 31;
+    const int R = tokens * k;
+    pdl_launch_dependents();
+    if (static_cast<int>(blockIdx.x) == tokens) {
+        if (blockIdx.y != 0) return;
+        for (int e = tid; e <= n; e += SMALL_THREADS) cnt[e] = 0;
+        __syncthreads();
+        pdl_wait();
+        for (int a = tid; a < R; a += SMALL_THREADS) atomicAdd(&cnt[bucket(top_idx[a], n)], 1);
+        __syncthreads();
+        int run = 0;
+        for (int b = 0; b <= n; b += SMALL_THREADS) {
+            const int v = b + tid <= n ? cnt[b + tid] : 0;
+            const int ex = run + block_exclusive(v, warp_sums);
+            if (b + tid <= n) offsets[b + tid] = ex;
+            if (tid == SMALL_THREADS - 1) warp_sums[0] = ex + v;
+            __syncthreads();
+            run = warp_sums[0];
+            __syncthreads();
+        }
+        return;
+    }
+    pdl_wait();
+    const int t = blockIdx.x;
+    for (int s = tid >> 5; s < k; s += SMALL_THREADS / 32) {
+        const int a = t * k + s;
+        const int e = bucket(top_idx[a], n);
+        int before = 0;
+        for (int b = lane; b < R; b += 32) {
+            const int o = bucket(top_idx[b], n);
+            before += o < e || (o == e && b < a);
+        }
+        const int row = __reduce_add_sync(FULL_MASK, before);
+        if (lane == 0) {
+            cnt[s] = e < n ? row : -1 - row;
+            if (blockIdx.y == 0) {
+                order[row] = a;
+                place[a] = e < n ? row : -1 - row;
+            }
+        }
+    }
+    if (!xs) return;
+    __syncthreads();
+    for (int c = (blockIdx.y * SMALL_THREADS + tid) * VE; c < d; c += gridDim.y * SMALL_THREADS * VE) {
+        RowVec<T, VE> v, z;
+        v.load(x + static_cast<size_t>(t) * d + c);
+        z.zero();
+        for (int s = 0; s < k; ++s) {
+            const int p = cnt[s];
+            if (p >= 0) v.store(xs + static_cast<size_t>(p) * d + c);
+            else z.store(xs + static_cast<size_t>(-1 - p) * d + c);
+        }
+    }
+}
+
 // ---------------------------------------------------------------- rows
 
 constexpr int ROW_THREADS = 256;
@@ -451,6 +525,8 @@ size_t dispatch_workspace(int T, int k, int n)
     return ((chunks + 1) * (static_cast<size_t>(n) + 1) * sizeof(int) + 255) & ~static_cast<size_t>(255);
 }
 
+namespace {
+
 cudaError_t launch_sort_tokens(const int *top_idx, int R, int n, int *offsets, int *order, int *place, void *workspace,
                                cudaStream_t stream)
 {
@@ -466,8 +542,6 @@ cudaError_t launch_sort_tokens(const int *top_idx, int R, int n, int *offsets, i
     return launch_pdl(sort_place, dim3(static_cast<unsigned>(chunks)), dim3(SORT_THREADS), smem, stream, top_idx, R, n,
                       hist, total, offsets, order, place);
 }
-
-namespace {
 
 template <typename T, int VE>
 dim3 row_grid(int tokens, int d)
@@ -500,13 +574,34 @@ cudaError_t grad_t(const void *d_out, const void *ys, const int *place, const fl
                       static_cast<T *>(d_ys), d_w, status);
 }
 
+template <typename T, int VE>
+cudaError_t small_t(const int *top_idx, int tokens, int k, int n, const void *x, int d, int *offsets, int *order,
+                    int *place, void *xs, cudaStream_t stream)
+{
+    dim3 grid = row_grid<T, VE>(tokens, xs ? d : 1);
+    grid.x += 1;
+    const size_t words = static_cast<size_t>(n) + 1 > SMOE_MAX_TOP_K ? static_cast<size_t>(n) + 1 : SMOE_MAX_TOP_K;
+    return launch_pdl(dispatch_small<T, VE>, grid, dim3(SMALL_THREADS), words * sizeof(int), stream, top_idx, tokens, k, n,
+                      static_cast<const T *>(x), d, offsets, order, place, static_cast<T *>(xs));
+}
+
 }  // namespace
 
-cudaError_t launch_gather_tokens(const void *x, int dtype, const int *place, int tokens, int k, int d, void *xs,
-                                 cudaStream_t stream)
+cudaError_t launch_dispatch(const int *top_idx, int tokens, int k, int n, const void *x, int dtype, int d, int *offsets,
+                            int *order, int *place, void *xs, void *workspace, cudaStream_t stream)
 {
     const size_t pitch = static_cast<size_t>(d) * (dtype == SMOE_BF16 ? 2 : 4);
     const bool v = vec16(x, pitch) && vec16(xs, pitch);
+    const int R = tokens * k;
+    if (R <= SMALL_SLOTS) {
+        if (dtype == SMOE_BF16)
+            return v ? small_t<__nv_bfloat16, 8>(top_idx, tokens, k, n, x, d, offsets, order, place, xs, stream)
+                     : small_t<__nv_bfloat16, 1>(top_idx, tokens, k, n, x, d, offsets, order, place, xs, stream);
+        return v ? small_t<float, 4>(top_idx, tokens, k, n, x, d, offsets, order, place, xs, stream)
+                 : small_t<float, 1>(top_idx, tokens, k, n, x, d, offsets, order, place, xs, stream);
+    }
+    const cudaError_t e = launch_sort_tokens(top_idx, R, n, offsets, order, place, workspace, stream);
+    if (e != cudaSuccess || !xs) return e;
     if (dtype == SMOE_BF16)
         return v ? gather_t<__nv_bfloat16, 8>(x, place, tokens, k, d, xs, stream)
                  : gather_t<__nv_bfloat16, 1>(x, place, tokens, k, d, xs, stream);
