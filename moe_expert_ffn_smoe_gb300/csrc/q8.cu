@@ -35,20 +35,24 @@ __device__ __forceinline__ void quant_values(const T *row, int cols, int c, floa
     }
 }
 
-// VE codes of one vector as one store.
-__device__ __forceinline__ void put_codes(int8_t *q, const int (&c)[8])
+// The code of a scaled value |p| <= 127.5 in the low byte: adding 1.5 2^23
+// rounds p to an integer, ties to even, in the lowest mantissa bits.
+__device__ __forceinline__ uint32_t code_bits(float v, float up)
 {
-    uint2 w;
-    w.x = (c[0] & 0xff) | (c[1] & 0xff) << 8 | (c[2] & 0xff) << 16 | static_cast<uint32_t>(c[3]) << 24;
-    w.y = (c[4] & 0xff) | (c[5] & 0xff) << 8 | (c[6] & 0xff) << 16 | static_cast<uint32_t>(c[7]) << 24;
-    *reinterpret_cast<uint2 *>(q) = w;
+    return __float_as_uint(__fadd_rn(__fmul_rn(v, up), 12582912.f));
 }
-__device__ __forceinline__ void put_codes(int8_t *q, const int (&c)[4])
+
+// VE codes (the low bytes of c) as one store.
+__device__ __forceinline__ uint32_t pack4(const uint32_t *c)
 {
-    *reinterpret_cast<uint32_t *>(q) =
-        (c[0] & 0xff) | (c[1] & 0xff) << 8 | (c[2] & 0xff) << 16 | static_cast<uint32_t>(c[3]) << 24;
+    return __byte_perm(__byte_perm(c[0], c[1], 0x0040), __byte_perm(c[2], c[3], 0x0040), 0x5410);
 }
-__device__ __forceinline__ void put_codes(int8_t *q, const int (&c)[1]) { *q = static_cast<int8_t>(c[0]); }
+__device__ __forceinline__ void put_codes(int8_t *q, const uint32_t (&c)[8])
+{
+    *reinterpret_cast<uint2 *>(q) = make_uint2(pack4(c), pack4(c + 4));
+}
+__device__ __forceinline__ void put_codes(int8_t *q, const uint32_t (&c)[4]) { *reinterpret_cast<uint32_t *>(q) = pack4(c); }
+__device__ __forceinline__ void put_codes(int8_t *q, const uint32_t (&c)[1]) { *q = static_cast<int8_t>(c[0]); }
 
 // One CTA per row: the largest magnitude, then the rounding.  A thread keeps
 // its first NV vectors in registers, so that a row of up to NV x 256 vectors
@@ -60,7 +64,7 @@ __global__ void __launch_bounds__(QUANT_THREADS) quantize_rows(const T *__restri
                                                                float *__restrict__ scales)
 {
     constexpr int NV = 32 / VE < 8 ? 32 / VE : 8;
-    __shared__ float warp_max[QUANT_THREADS / 32];
+    __shared__ uint32_t warp_max[QUANT_THREADS / 32];
     pdl_launch_dependents();
     pdl_wait();
     const size_t r = blockIdx.x;
@@ -75,50 +79,54 @@ __global__ void __launch_bounds__(QUANT_THREADS) quantize_rows(const T *__restri
             for (int j = 0; j < VE; ++j) held[i][j] = 0.f;
         }
     }
-    float top = 0.f;
-    bool bad = false;
+    // magnitudes as bit patterns: their order is the integers', and a NaN or
+    // an infinity is above every finite one
+    uint32_t most = 0u;
 #pragma unroll
     for (int i = 0; i < NV; ++i)
 #pragma unroll
-        for (int j = 0; j < VE; ++j) {
-            bad |= !isfinite(held[i][j]);
-            top = fmaxf(top, fabsf(held[i][j]));
-        }
+        for (int j = 0; j < VE; ++j) most = max(most, __float_as_uint(held[i][j]) & 0x7fffffffu);
     for (int c = c0 + NV * QUANT_THREADS * VE; c < cols; c += QUANT_THREADS * VE) {
         float v[VE];
         quant_values<T, VE, ACT>(row, cols, c, v);
 #pragma unroll
-        for (int j = 0; j < VE; ++j) {
-            bad |= !isfinite(v[j]);
-            top = fmaxf(top, fabsf(v[j]));
-        }
+        for (int j = 0; j < VE; ++j) most = max(most, __float_as_uint(v[j]) & 0x7fffffffu);
     }
+    most = __reduce_max_sync(FULL_MASK, most);
+    if ((threadIdx.x & 31) == 0) warp_max[threadIdx.x >> 5] = most;
+    __syncthreads();
 #pragma unroll
-    for (int off = 16; off > 0; off >>= 1) top = fmaxf(top, __shfl_xor_sync(FULL_MASK, top, off));
-    if ((threadIdx.x & 31) == 0) warp_max[threadIdx.x >> 5] = top;
-    bad = __syncthreads_or(bad);
-#pragma unroll
-    for (int i = 0; i < QUANT_THREADS / 32; ++i) top = fmaxf(top, warp_max[i]);
+    for (int i = 0; i < QUANT_THREADS / 32; ++i) most = max(most, warp_max[i]);
     // a row of zeros has scale 0; a row that is not finite scale NaN and
     // codes 0, so that every product of it is NaN
-    const float up = bad || top == 0.f ? 0.f : __fdiv_rn(127.f, top);
+    const bool bad = most >= 0x7f800000u;
+    const float top = __uint_as_float(most);
+    const float up = bad || most == 0u ? 0.f : __fdiv_rn(127.f, top);
     if (threadIdx.x == 0) scales[r] = bad ? __int_as_float(0x7fffffff) : __fdiv_rn(top, 127.f);
-    auto code = [&](float v) { return bad ? 0 : max(-127, min(127, __float2int_rn(__fmul_rn(v, up)))); };
+    const bool plain = !bad && up < INFINITY;  // 127 / top overflows below 4e-37: those codes saturate
+    auto codes = [&](const float (&v)[VE], uint32_t (&k)[VE]) {
+        if (plain) {
+#pragma unroll
+            for (int j = 0; j < VE; ++j) k[j] = code_bits(v[j], up);
+        } else {
+#pragma unroll
+            for (int j = 0; j < VE; ++j)
+                k[j] = bad || v[j] == 0.f ? 0u : static_cast<uint32_t>(v[j] > 0.f ? 127 : -127);
+        }
+    };
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
         const int c = c0 + i * QUANT_THREADS * VE;
         if (c >= cols) break;
-        int k[VE];
-#pragma unroll
-        for (int j = 0; j < VE; ++j) k[j] = code(held[i][j]);
+        uint32_t k[VE];
+        codes(held[i], k);
         put_codes(q + r * cols + c, k);
     }
     for (int c = c0 + NV * QUANT_THREADS * VE; c < cols; c += QUANT_THREADS * VE) {
         float v[VE];
-        int k[VE];
+        uint32_t k[VE];
         quant_values<T, VE, ACT>(row, cols, c, v);
-#pragma unroll
-        for (int j = 0; j < VE; ++j) k[j] = code(v[j]);
+        codes(v, k);
         put_codes(q + r * cols + c, k);
     }
 }
@@ -192,15 +200,18 @@ struct Q8Args {
 
 // Integer dot products on the CUDA cores, exact in 32 bits (K <= 32768): a
 // warp holds 4 weight rows against the tile's up to 8 activation rows, 16
-// columns of each per lane and step, two steps of weights in flight.  Bound
-// by streaming the weights; for one matrix (tiles null) they are asked for
-// before the previous kernel is waited for.
+// columns of each per lane and step.  A warp walks its groups of 4 rows as
+// one sequence of steps, the weights of the next DEPTH steps in flight
+// across the groups' ends.  Bound by streaming the weights; for one matrix
+// (tiles null) they are asked for before the previous kernel is waited for.
 template <typename T>
 __global__ void __launch_bounds__(DOT_WARPS * 32, 2) q8_dot(const Q8Args a)
 {
+    constexpr int DEPTH = 3;
     pdl_launch_dependents();
     const int lane = threadIdx.x & 31;
-    const int n0 = (blockIdx.y * DOT_WARPS + (threadIdx.x >> 5)) * DOT_OUTS;
+    int n0 = (blockIdx.y * DOT_WARPS + (threadIdx.x >> 5)) * DOT_OUTS;  // the group being summed
+    const int stride = gridDim.y * DOT_WARPS * DOT_OUTS;
     if (a.tiles) {
         pdl_wait();
         if (static_cast<int>(blockIdx.x) >= *a.ntiles) return;
@@ -209,23 +220,28 @@ __global__ void __launch_bounds__(DOT_WARPS * 32, 2) q8_dot(const Q8Args a)
     const Tile tile = a.tiles ? a.tiles[blockIdx.x] : Tile{0, row0, min(DOT_ROWS, a.R - row0), 0};
     T *y = static_cast<T *>(a.y);
     if (tile.expert < 0) {
-        for (int i = lane; i < tile.rows * DOT_OUTS; i += 32)
-            if (n0 + i % DOT_OUTS < a.N)
-                put(y + static_cast<size_t>(tile.row0 + i / DOT_OUTS) * a.N + n0 + i % DOT_OUTS, 0.f);
+        for (; n0 < a.N; n0 += stride)
+            for (int i = lane; i < tile.rows * DOT_OUTS; i += 32)
+                if (n0 + i % DOT_OUTS < a.N)
+                    put(y + static_cast<size_t>(tile.row0 + i / DOT_OUTS) * a.N + n0 + i % DOT_OUTS, 0.f);
         return;
     }
-    const int8_t *w = a.wq + (static_cast<size_t>(tile.expert) * a.N + n0) * a.K;
-    uint4 wv[2][DOT_OUTS];
-    auto fetch = [&](uint4 (&v)[DOT_OUTS], int c) {
+    const int8_t *w = a.wq + static_cast<size_t>(tile.expert) * a.N * a.K;
+    uint4 wv[DEPTH][DOT_OUTS];
+    int fn = n0, fc = lane * 16;  // the next step to fetch
+    auto fetch = [&](uint4 (&v)[DOT_OUTS]) {
 #pragma unroll
         for (int o = 0; o < DOT_OUTS; ++o)
-            v[o] = n0 + o < a.N && c < a.K ? ldg_stream(w + static_cast<size_t>(o) * a.K + c) : make_uint4(0u, 0u, 0u, 0u);
+            v[o] = fn + o < a.N && fc < a.K ? ldg_stream(w + static_cast<size_t>(fn + o) * a.K + fc) : make_uint4(0u, 0u, 0u, 0u);
+        fc += 512;
+        if (fc - lane * 16 >= a.K) {
+            fc = lane * 16;
+            fn += stride;
+        }
     };
-    int c = lane * 16;
-    fetch(wv[0], c);
-    fetch(wv[1], c + 512);
+#pragma unroll
+    for (int i = 0; i < DEPTH; ++i) fetch(wv[i]);
     if (!a.tiles) pdl_wait();
-    if (n0 >= a.N) return;
     int src[DOT_ROWS];
 #pragma unroll
     for (int r = 0; r < DOT_ROWS; ++r)
@@ -235,38 +251,45 @@ __global__ void __launch_bounds__(DOT_WARPS * 32, 2) q8_dot(const Q8Args a)
     for (int o = 0; o < DOT_OUTS; ++o)
 #pragma unroll
         for (int r = 0; r < DOT_ROWS; ++r) acc[o][r] = 0;
-    auto dot = [&](const uint4 (&v)[DOT_OUTS], int at) {
-        if (at >= a.K) return;
+    int c = lane * 16;
+    while (n0 < a.N) {
 #pragma unroll
-        for (int r = 0; r < DOT_ROWS; ++r) {
-            if (r >= tile.rows) break;
-            if (src[r] < 0) continue;
-            const uint4 xv = *reinterpret_cast<const uint4 *>(a.xq + static_cast<size_t>(src[r]) * a.K + at);
+        for (int i = 0; i < DEPTH; ++i) {
+            if (n0 >= a.N) break;
+            if (c < a.K) {
 #pragma unroll
-            for (int o = 0; o < DOT_OUTS; ++o) {
-                acc[o][r] = __dp4a(static_cast<int>(v[o].x), static_cast<int>(xv.x), acc[o][r]);
-                acc[o][r] = __dp4a(static_cast<int>(v[o].y), static_cast<int>(xv.y), acc[o][r]);
-                acc[o][r] = __dp4a(static_cast<int>(v[o].z), static_cast<int>(xv.z), acc[o][r]);
-                acc[o][r] = __dp4a(static_cast<int>(v[o].w), static_cast<int>(xv.w), acc[o][r]);
+                for (int r = 0; r < DOT_ROWS; ++r) {
+                    if (r >= tile.rows) break;
+                    if (src[r] < 0) continue;
+                    const uint4 xv = *reinterpret_cast<const uint4 *>(a.xq + static_cast<size_t>(src[r]) * a.K + c);
+#pragma unroll
+                    for (int o = 0; o < DOT_OUTS; ++o) {
+                        acc[o][r] = __dp4a(static_cast<int>(wv[i][o].x), static_cast<int>(xv.x), acc[o][r]);
+                        acc[o][r] = __dp4a(static_cast<int>(wv[i][o].y), static_cast<int>(xv.y), acc[o][r]);
+                        acc[o][r] = __dp4a(static_cast<int>(wv[i][o].z), static_cast<int>(xv.z), acc[o][r]);
+                        acc[o][r] = __dp4a(static_cast<int>(wv[i][o].w), static_cast<int>(xv.w), acc[o][r]);
+                    }
+                }
             }
-        }
-    };
-    for (; c - lane * 16 < a.K; c += 1024) {
-        dot(wv[0], c);
-        fetch(wv[0], c + 1024);
-        dot(wv[1], c + 512);
-        fetch(wv[1], c + 1536);
-    }
+            fetch(wv[i]);
+            c += 512;
+            if (c - lane * 16 >= a.K) {  // the group is summed
 #pragma unroll
-    for (int r = 0; r < DOT_ROWS; ++r) {
-        if (r >= tile.rows) break;
-        const float xs = src[r] >= 0 ? a.xs[src[r]] : 0.f;
+                for (int r = 0; r < DOT_ROWS; ++r) {
+                    if (r >= tile.rows) break;
+                    const float xs = src[r] >= 0 ? a.xs[src[r]] : 0.f;
 #pragma unroll
-        for (int o = 0; o < DOT_OUTS; ++o) {
-            const int sum = __reduce_add_sync(FULL_MASK, acc[o][r]);
-            if (lane == o && n0 + o < a.N)
-                put(y + static_cast<size_t>(tile.row0 + r) * a.N + n0 + o,
-                    static_cast<float>(sum) * xs * a.ws[static_cast<size_t>(tile.expert) * a.N + n0 + o]);
+                    for (int o = 0; o < DOT_OUTS; ++o) {
+                        const int sum = __reduce_add_sync(FULL_MASK, acc[o][r]);
+                        acc[o][r] = 0;
+                        if (lane == o && n0 + o < a.N)
+                            put(y + static_cast<size_t>(tile.row0 + r) * a.N + n0 + o,
+                                static_cast<float>(sum) * xs * a.ws[static_cast<size_t>(tile.expert) * a.N + n0 + o]);
+                    }
+                }
+                c = lane * 16;
+                n0 += stride;
+            }
         }
     }
 }
@@ -334,8 +357,18 @@ cudaError_t launch_q8(const int8_t *xq, const float *xs, int nsrc, const int *or
         if (e != cudaSuccess) return e;
     }
     const Q8Args a = {xq, xs, order, wq, ws, y, ntiles, tiles, status, k, nsrc, N, K, R};
-    const dim3 grid(static_cast<unsigned>(max_tiles),
-                    static_cast<unsigned>((N + DOT_WARPS * DOT_OUTS - 1) / (DOT_WARPS * DOT_OUTS)));
+    // CTAs per tile: enough for about two waves of the device (two CTAs an
+    // SM) when every row has an expert of its own
+    const DeviceInfo *dev = device_info();
+    if (!dev) return cudaErrorInvalidDevice;
+    const int likely = offsets ? (R < n ? R : n) : max_tiles;
+    const int blocks = (N + DOT_WARPS * DOT_OUTS - 1) / (DOT_WARPS * DOT_OUTS);
+#ifndef DOT_WAVES
+#define DOT_WAVES 16
+#endif
+    int per_tile = (DOT_WAVES * dev->sm_count + likely - 1) / likely;
+    if (per_tile > blocks) per_tile = blocks;
+    const dim3 grid(static_cast<unsigned>(max_tiles), static_cast<unsigned>(per_tile));
     if (dtype == SMOE_BF16) return launch_pdl(q8_dot<__nv_bfloat16>, grid, dim3(DOT_WARPS * 32), 0, stream, a);
     return launch_pdl(q8_dot<float>, grid, dim3(DOT_WARPS * 32), 0, stream, a);
 }

@@ -18,12 +18,12 @@ namespace {
 constexpr uint32_t kKeyNegInf = 0x007FFFFFu;  // value_key(-inf)
 
 // Order-preserving 32-bit key of a logit: larger = ranks first, NaN below
-// every number (1), 0 = retired.
+// every number (1), 0 = retired.  -0 ranks with +0 (v + 0).
 __device__ __forceinline__ uint32_t value_key(float v)
 {
-    const uint32_t u = __float_as_uint(v == 0.f ? 0.f : v);  // -0 ranks with +0
-    if (isnan(v)) return 1u;
-    return (u & 0x80000000u) ? ~u : (u | 0x80000000u);
+    const uint32_t u = __float_as_uint(v + 0.f);
+    const uint32_t key = u ^ (static_cast<uint32_t>(static_cast<int>(u) >> 31) | 0x80000000u);
+    return v != v ? 1u : key;
 }
 
 __device__ __forceinline__ float value_of_key(uint32_t u)
@@ -39,11 +39,10 @@ __device__ __forceinline__ void write_row(uint32_t ka, uint32_t kb, int ea, int 
                                           float *__restrict__ w)
 {
     const int lane = threadIdx.x & 31;
-    const uint32_t k0 = __shfl_sync(FULL_MASK, ka, 0);
-    const float v0 = value_of_key(k0);
+    const float v0 = value_of_key(__shfl_sync(FULL_MASK, ka, 0));
     const bool ha = lane < k && ka != kKeyNegInf, hb = lane + 32 < k && kb != kKeyNegInf;
     const float xa = ha ? expf(value_of_key(ka) - v0) : 0.f;
-    const float xb = hb ? expf(value_of_key(kb) - v0) : 0.f;
+    const float xb = k > 32 && hb ? expf(value_of_key(kb) - v0) : 0.f;
     float sum = xa + xb;
 #pragma unroll
     for (int off = 16; off > 0; off >>= 1) sum += __shfl_xor_sync(FULL_MASK, sum, off);
@@ -59,40 +58,27 @@ __device__ __forceinline__ void write_row(uint32_t ka, uint32_t kb, int ea, int 
 
 constexpr int TOPK_WARPS = 8;
 
-// n <= 32 V: one warp per row, V keys per lane (expert j 32 + lane), k
-// rounds of a warp-wide maximum; among equal values the lowest expert wins.
+// k rounds of a warp-wide maximum over V keys per lane (expert i 32 + lane);
+// among equal values the lowest expert wins.  Lane l ends with ranks l and
+// l + 32.  Any k, any ties.
 template <int V>
-__global__ void __launch_bounds__(TOPK_WARPS * 32) topk_rows_warp(const float *__restrict__ logits, int T, int n, int ld,
-                                                                  int k, int *__restrict__ idx, float *__restrict__ w)
+__device__ __forceinline__ void select_by_rounds(uint32_t (&key)[V], int k, uint32_t &ka, uint32_t &kb, int &ea, int &eb)
 {
-    const int t = blockIdx.x * TOPK_WARPS + (threadIdx.x >> 5);
     const int lane = threadIdx.x & 31;
-    pdl_launch_dependents();
-    pdl_wait();
-    if (t >= T) return;
-    const float *row = logits + static_cast<size_t>(t) * ld;
-    uint32_t key[V];
-#pragma unroll
-    for (int j = 0; j < V; ++j) key[j] = j * 32 + lane < n ? value_key(row[j * 32 + lane]) : 0u;
-    uint32_t ka = 0u, kb = 0u;
-    int ea = -1, eb = -1;
     for (int r = 0; r < k; ++r) {
         uint32_t best = key[0];
-        int bj = 0;
+        int bi = 0;
 #pragma unroll
-        for (int j = 1; j < V; ++j)
-            if (key[j] > best) {
-                best = key[j];
-                bj = j;
+        for (int i = 1; i < V; ++i)
+            if (key[i] > best) {
+                best = key[i];
+                bi = i;
             }
         const uint32_t top = __reduce_max_sync(FULL_MASK, best);
-        const unsigned e = __reduce_min_sync(FULL_MASK, best == top ? static_cast<unsigned>(bj * 32 + lane) : 0xFFFFFFFFu);
-        if ((e & 31u) == static_cast<unsigned>(lane)) {
-            const int oj = static_cast<int>(e >> 5);
+        const unsigned e = __reduce_min_sync(FULL_MASK, best == top ? static_cast<unsigned>(bi * 32 + lane) : 0xFFFFFFFFu);
 #pragma unroll
-            for (int j = 0; j < V; ++j)
-                if (j == oj) key[j] = 0u;
-        }
+        for (int i = 0; i < V; ++i)
+            if (e == static_cast<unsigned>(i * 32 + lane)) key[i] = 0u;  // retired
         if ((r & 31) == lane) {
             if (r < 32) {
                 ka = top;
@@ -103,7 +89,85 @@ __global__ void __launch_bounds__(TOPK_WARPS * 32) topk_rows_warp(const float *_
             }
         }
     }
-    write_row(ka, kb, ea, eb, k, idx + static_cast<size_t>(t) * k, w + static_cast<size_t>(t) * k);
+}
+
+// n <= 32 V: one warp per row, V logits per lane.  Up to k = 16 the row is
+// first cut down: the k-th largest of the lanes' maxima is a lower bound of
+// the k-th largest logit, and the few logits not below it (k and one or two
+// more, as a rule) are gathered one to a lane in expert order, where counting
+// the larger ones before and after gives each its rank.  That takes half the
+// instructions of k rounds over the whole row, which is what bounds this
+// kernel (32,768 rows of 128, k = 8).  Where more than 32 logits are left
+// (ties) or k > 16 the rounds select.
+template <int V>
+__global__ void __launch_bounds__(TOPK_WARPS * 32) topk_rows_warp(const float *__restrict__ logits, int T, int n, int ld,
+                                                                  int k, int *__restrict__ idx, float *__restrict__ w)
+{
+    __shared__ uint2 left[TOPK_WARPS][32];  // key, expert
+    const int wi = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int t = blockIdx.x * TOPK_WARPS + wi;
+    pdl_launch_dependents();
+    pdl_wait();
+    if (t >= T) return;
+    const float *row = logits + static_cast<size_t>(t) * ld;
+    idx += static_cast<size_t>(t) * k;
+    w += static_cast<size_t>(t) * k;
+    uint32_t key[V];
+#pragma unroll
+    for (int i = 0; i < V; ++i) key[i] = i * 32 + lane < n ? value_key(row[i * 32 + lane]) : 0u;
+    if (k <= 16) {
+        uint32_t most = key[0];
+#pragma unroll
+        for (int i = 1; i < V; ++i) most = max(most, key[i]);
+        uint32_t bound = 0u, first = 0u;
+        for (int r = 0; r < k; ++r) {
+            const uint32_t top = __reduce_max_sync(FULL_MASK, most);
+            if (top == 0u) break;  // every lane's maximum is among them
+            if (r == 0) first = top;
+            bound = top;
+            if (most == top) most = 0u;
+        }
+        if (first == kKeyNegInf) {  // nothing but masked experts
+            if (lane < k) {
+                idx[lane] = -1;
+                w[lane] = 0.f;
+            }
+            return;
+        }
+        int count = 0;
+        const uint32_t before = (1u << lane) - 1u;
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+            const bool in = key[i] >= bound;
+            const uint32_t m = __ballot_sync(FULL_MASK, in);
+            const int at = count + __popc(m & before);
+            if (in && at < 32) left[wi][at] = make_uint2(key[i], static_cast<uint32_t>(i * 32 + lane));
+            count += __popc(m);
+        }
+        if (count <= 32) {
+            __syncwarp();
+            const uint2 mine = lane < count ? left[wi][lane] : make_uint2(0u, 0u);
+            int rank = lane < count ? 0 : 32;
+            for (int c = 0; c < count; ++c) {
+                const uint32_t o = left[wi][c].x;
+                rank += c < lane ? o >= mine.x : o > mine.x;
+            }
+            const bool sel = rank < k, there = sel && mine.x != kKeyNegInf;
+            const float x = there ? expf(value_of_key(mine.x) - value_of_key(first)) : 0.f;
+            float sum = x;
+#pragma unroll
+            for (int off = 16; off > 0; off >>= 1) sum += __shfl_xor_sync(FULL_MASK, sum, off);
+            if (sel) {
+                idx[rank] = there ? static_cast<int>(mine.y) : -1;
+                w[rank] = there ? x / sum : 0.f;
+            }
+            return;
+        }
+    }
+    uint32_t ka = 0u, kb = 0u;
+    int ea = -1, eb = -1;
+    select_by_rounds<V>(key, k, ka, kb, ea, eb);
+    write_row(ka, kb, ea, eb, k, idx, w);
 }
 
 constexpr int TOPK_BLOCK = 256;
@@ -153,34 +217,53 @@ __global__ void __launch_bounds__(TOPK_BLOCK) topk_rows_block(const float *__res
     }
 }
 
+constexpr int GRAD_ROWS = 2;  // rows per warp, whose loads are in flight together
+
 // dl[idx[r]] = w[r] (dw[r] - sum_q w[q] dw[q]), every other logit's gradient
-// is 0.  One warp per row: zeros first, then the selected ones.
+// is 0.  A warp writes its rows' zeros while their few inputs are on their
+// way, then the selected ones.
 __global__ void __launch_bounds__(TOPK_WARPS * 32) topk_rows_grad(const int *__restrict__ idx, const float *__restrict__ w,
                                                                   const float *__restrict__ dw, int T, int n, int k,
                                                                   float *__restrict__ dl)
 {
-    const int t = blockIdx.x * TOPK_WARPS + (threadIdx.x >> 5);
+    const int t0 = (blockIdx.x * TOPK_WARPS + (threadIdx.x >> 5)) * GRAD_ROWS;
     const int lane = threadIdx.x & 31;
     pdl_launch_dependents();
     pdl_wait();
-    if (t >= T) return;
-    const size_t a = static_cast<size_t>(t) * k;
-    const bool ina = lane < k, inb = lane + 32 < k;
-    const int ea = ina ? idx[a + lane] : -1, eb = inb ? idx[a + lane + 32] : -1;
-    const float wa = ea >= 0 ? w[a + lane] : 0.f, wb = eb >= 0 ? w[a + lane + 32] : 0.f;
-    const float ga = ea >= 0 ? dw[a + lane] : 0.f, gb = eb >= 0 ? dw[a + lane + 32] : 0.f;
-    float c = fmaf(wa, ga, wb * gb);
+    if (t0 >= T) return;
+    int e[GRAD_ROWS][2];
+    float wr[GRAD_ROWS][2], g[GRAD_ROWS][2];
 #pragma unroll
-    for (int off = 16; off > 0; off >>= 1) c += __shfl_xor_sync(FULL_MASK, c, off);
-    float *row = dl + static_cast<size_t>(t) * n;
+    for (int i = 0; i < GRAD_ROWS; ++i)
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            const bool in = t0 + i < T && lane + 32 * h < k;
+            const size_t a = static_cast<size_t>(t0 + i) * k + lane + 32 * h;
+            e[i][h] = in ? idx[a] : -1;
+            wr[i][h] = in ? w[a] : 0.f;
+            g[i][h] = in ? dw[a] : 0.f;
+        }
+    float *row = dl + static_cast<size_t>(t0) * n;
+    const int words = min(GRAD_ROWS, T - t0) * n;
     if ((n & 3) == 0) {
-        for (int e = lane; e < (n >> 2); e += 32) reinterpret_cast<float4 *>(row)[e] = make_float4(0.f, 0.f, 0.f, 0.f);
+        for (int c = lane; c < (words >> 2); c += 32) reinterpret_cast<float4 *>(row)[c] = make_float4(0.f, 0.f, 0.f, 0.f);
     } else {
-        for (int e = lane; e < n; e += 32) row[e] = 0.f;
+        for (int c = lane; c < words; c += 32) row[c] = 0.f;
     }
     __syncwarp();
-    if (ea >= 0 && ea < n) row[ea] = wa * (ga - c);
-    if (eb >= 0 && eb < n) row[eb] = wb * (gb - c);
+#pragma unroll
+    for (int i = 0; i < GRAD_ROWS; ++i) {
+        // a slot without an expert has no weight, and its gradient is nothing
+        float c = 0.f;
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+            if (e[i][h] >= 0) c = fmaf(wr[i][h], g[i][h], c);
+#pragma unroll
+        for (int off = 16; off > 0; off >>= 1) c += __shfl_xor_sync(FULL_MASK, c, off);
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+            if (e[i][h] >= 0 && e[i][h] < n) row[static_cast<size_t>(i) * n + e[i][h]] = wr[i][h] * (g[i][h] - c);
+    }
 }
 
 // ---------------------------------------------------------------- the sort
@@ -508,7 +591,8 @@ cudaError_t launch_topk_rows(const float *logits, int T, int n, int ld, int k, i
 cudaError_t launch_topk_rows_grad(const int *idx, const float *w, const float *dw, int T, int n, int k, float *dl,
                                   cudaStream_t stream)
 {
-    return launch_pdl(topk_rows_grad, dim3(static_cast<unsigned>((T + TOPK_WARPS - 1) / TOPK_WARPS)),
+    constexpr int rows = TOPK_WARPS * GRAD_ROWS;
+    return launch_pdl(topk_rows_grad, dim3(static_cast<unsigned>((T + rows - 1) / rows)),
                       dim3(TOPK_WARPS * 32), 0, stream, idx, w, dw, T, n, k, dl);
 }
 
