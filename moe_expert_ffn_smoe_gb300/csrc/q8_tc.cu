@@ -14,15 +14,16 @@
 // the MMA reads its A operand; the activations, reused by every weight tile,
 // are widened once by q8_prep into the workspace.
 //
-// q8_tc is persistent: clusters walk the items (tile of rows, group of
+// q8_tc is persistent: CTAs, or pairs of them, walk the items (tile of rows,
 // weight tiles), accumulators double-buffered so that the store of one item
-// runs under the products of the next.  With clusters of two, the two CTAs
-// take neighbouring weight tiles of the same rows and each loads half of the
-// row tile for both (multicast), which halves the activation traffic from
-// L2.  Roles (warps): 0-7 epilogue, 8-15 widen weights (two groups, alternate
-// K tiles), 16 issues the MMAs, 17 streams the weights, 18 and 19
-// the rows.
-// Every wait is bounded.
+// runs under the products of the next.  A pair (cta_group::2) multiplies 256
+// weight rows at once, each CTA widening its own 128 and holding half of the
+// activation rows, so that a row tile crosses from L2 once for 256 weight
+// rows and its stages take half the shared memory: twice as many are in
+// flight.
+// Roles (warps): 0-7 epilogue, 8-23 widen weights (four groups, every
+// fourth K tile each), 24 issues the MMAs (of the pair: the even CTA's), 25
+// streams the weights, 26-29 the rows.  Every wait is bounded.
 #include <cuda_fp16.h>
 
 #include <atomic>
@@ -38,30 +39,29 @@ constexpr int KT = 64;                  // columns per K tile
 constexpr int MT = 128;                 // weight rows per CTA tile
 constexpr uint32_t W_BYTES = MT * 128;  // one weight chunk: 128 rows x 128 columns (two K tiles)
 constexpr int EPI_WARPS = 8;
-constexpr int CONV_WARP0 = 8;
-constexpr int MMA_WARP = 16, W_WARP = 17, X_WARP = 18;
-constexpr int TC_THREADS = 20 * 32;
+constexpr int CONV_WARP0 = 8, CONV_GROUPS = 4;  // groups of four warps: a row each thread
+constexpr int MMA_WARP = CONV_WARP0 + 4 * CONV_GROUPS, W_WARP = MMA_WARP + 1, X_WARP = MMA_WARP + 2, X_WARPS = 4;
+constexpr int TC_THREADS = (X_WARP + X_WARPS) * 32;
 
-// Shapes of the two forms: row tile NT, cluster CL, the rings of A stages
-// (tensor memory), row stages and weight chunks (shared memory), and the rows
-// of one tensor copy of activations (a copy costs its issuer about 100 clocks
-// whatever its size: 16-row boxes made the issuing warp pace the K loop).
+// Shapes of the two forms: row tile NT, CTAs per tile CL, and the rings of A
+// stages (tensor memory, a K tile each), row stages (a CTA's share of the
+// rows x two K tiles) and weight chunks (shared memory).
 template <int NT>
 struct Form;
 template <>
 struct Form<192> {
-    static constexpr int CL = 2, AS = 4, XS = 6, WS = 4, BOX = 48;
+    static constexpr int CL = 2, AS = 4, XS = 6, WS = 4;
 };
 template <>
 struct Form<64> {
-    static constexpr int CL = 1, AS = 8, XS = 8, WS = 8, BOX = 16;
+    static constexpr int CL = 1, AS = 8, XS = 4, WS = 8;
 };
 
 template <int NT>
 constexpr size_t tc_smem()
 {
     using F = Form<NT>;
-    return 1024 + static_cast<size_t>(F::WS) * W_BYTES + static_cast<size_t>(F::XS) * NT * 128 + 512;
+    return 1024 + static_cast<size_t>(F::WS) * W_BYTES + static_cast<size_t>(F::XS) * (NT / F::CL) * 256 + 512;
 }
 
 struct alignas(128) TcArgs {
@@ -71,7 +71,7 @@ struct alignas(128) TcArgs {
     const int *ntiles;
     const Tile *tiles;     // null: one matrix, tiles of `step` rows
     unsigned *status;
-    int R, N, K, step, mtiles;
+    int R, N, K, step, mtiles, box;  // box: rows of one copy
 };
 
 // Four int8 in a word as two f16 pairs: byte b + 128 in the mantissa of
@@ -96,43 +96,107 @@ __device__ __forceinline__ uint64_t desc_sw128(uint32_t addr)
 }
 
 // Instruction descriptor, kind::f16: f32 accumulate, A and B f16, K-major.
-__device__ __forceinline__ uint32_t idesc_f16(int n)
+__device__ __forceinline__ uint32_t idesc_f16(int m, int n)
 {
-    return (1u << 4) | (static_cast<uint32_t>(n >> 3) << 17) | (static_cast<uint32_t>(MT >> 4) << 24);
+    return (1u << 4) | (static_cast<uint32_t>(n >> 3) << 17) | (static_cast<uint32_t>(m >> 4) << 24);
 }
 
-// 2-D tensor copy of one box into the same place of every CTA of `mask`,
-// completing on the barrier at the same place.
-__device__ __forceinline__ void tma_load_2d_mc(uint32_t dst, const CUtensorMap *map, int x, int y, uint32_t bar,
-                                               uint16_t mask)
+// The pair's form of mma_f16_ta: 256 rows of A, 128 in each CTA's tensor
+// memory, B's rows split between the CTAs' shared memory at one address.
+__device__ __forceinline__ void mma_f16_ta_pair(uint32_t tmem, uint32_t a_tmem, uint64_t b, uint32_t idesc, uint32_t acc)
 {
     asm volatile(
-        "cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes.multicast::cluster [%0], [%1, {%2, "
-        "%3}], [%4], %5;" ::"r"(dst),
-        "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(bar), "h"(mask)
+        "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::2.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(tmem),
+        "r"(a_tmem), "l"(b), "r"(idesc), "r"(acc)
         : "memory");
 }
 
-__device__ __forceinline__ void mma_commit_mc(uint32_t bar, uint16_t mask)
+// Arrives on the barrier at this place in both CTAs of the pair.
+__device__ __forceinline__ void mma_commit_pair(uint32_t bar)
 {
-    asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(
-                     bar),
-                 "h"(mask)
-                 : "memory");
+    asm volatile(
+        "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(bar),
+        "h"(static_cast<uint16_t>(3))
+        : "memory");
 }
 
-// Whether phase `parity` of an mbarrier has completed, without waiting.
-__device__ __forceinline__ bool mbar_test(uint32_t bar, uint32_t parity)
+// Copies into this CTA that complete on a barrier of either CTA of the pair.
+__device__ __forceinline__ void tma_load_2d_pair(uint32_t dst, const CUtensorMap *map, int x, int y, uint32_t bar)
+{
+    asm volatile(
+        "cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes.cta_group::2 [%0], [%1, {%2, %3}], "
+        "[%4];" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(bar)
+        : "memory");
+}
+
+// Arrives on a barrier of either CTA of the cluster (a shared::cluster
+// address).  What it hands over is tensor memory, ordered by the tcgen05
+// fences and waits around it; a release at cluster scope would also wait for
+// this thread's earlier reads and writes elsewhere (1,700 clocks a K tile
+// against 500).
+__device__ __forceinline__ void mbar_arrive_cluster(uint32_t bar)
+{
+    asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+
+// mbar_wait_bounded for barriers that the other CTA's threads arrive on:
+// acquires at cluster scope.
+__device__ __forceinline__ bool mbar_try_wait_cluster(uint32_t bar, uint32_t parity)
 {
     uint32_t done;
     asm volatile(
         "{\n\t.reg .pred p;\n\t"
-        "mbarrier.test_wait.parity.acquire.cta.shared::cta.b64 p, [%1], %2;\n\t"
+        "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2, 20000;\n\t"
         "selp.u32 %0, 1, 0, p;\n\t}"
         : "=r"(done)
         : "r"(bar), "r"(parity)
         : "memory");
     return done != 0;
+}
+template <int CL>
+__device__ __forceinline__ bool wait_pair(uint32_t bar, uint32_t parity, unsigned *status, unsigned code)
+{
+    if (CL == 1) return mbar_wait_bounded(bar, parity, status, code);
+    if (mbar_try_wait_cluster(bar, parity)) return true;
+    const long long t0 = clock64();
+    for (uint32_t i = 0; i < (1u << 24); ++i) {
+        __nanosleep(64);
+        if (mbar_try_wait_cluster(bar, parity)) return true;
+        if (clock64() - t0 > 4000000000LL) break;
+    }
+    atomicExch(status, code);
+    return false;
+}
+
+// Whether phase `parity` has completed, without waiting.
+template <int CL>
+__device__ __forceinline__ bool mbar_test(uint32_t bar, uint32_t parity)
+{
+    uint32_t done;
+    if (CL > 1)
+        asm volatile(
+            "{\n\t.reg .pred p;\n\tmbarrier.test_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
+            "selp.u32 %0, 1, 0, p;\n\t}"
+            : "=r"(done)
+            : "r"(bar), "r"(parity)
+            : "memory");
+    else
+        asm volatile(
+            "{\n\t.reg .pred p;\n\tmbarrier.test_wait.parity.acquire.cta.shared::cta.b64 p, [%1], %2;\n\t"
+            "selp.u32 %0, 1, 0, p;\n\t}"
+            : "=r"(done)
+            : "r"(bar), "r"(parity)
+            : "memory");
+    return done != 0;
+}
+
+// Columns of the MMA for a tile of `rows`: a pair's come in 32s.
+template <int CL>
+__device__ __forceinline__ int mma_cols(int rows)
+{
+    return (rows + 16 * CL - 1) & ~(16 * CL - 1);
 }
 
 __device__ __forceinline__ Tile tile_at(const TcArgs &a, int i, int ntiles)
@@ -147,12 +211,14 @@ __global__ void __launch_bounds__(TC_THREADS, 1) q8_tc(const __grid_constant__ T
 {
     using F = Form<NT>;
     constexpr int CL = F::CL, AS = F::AS, XS = F::XS, WS = F::WS;
-    constexpr uint32_t XB = NT * 128u, ACOL0 = 2u * NT;
-    static_assert(2 * NT + AS * 32 <= 512 && AS % 2 == 0 && XS % 2 == 0, "tensor memory; two issuers");
+    constexpr int XR = NT / CL;                            // rows of a CTA's share of a tile, at most
+    constexpr uint32_t XB = XR * 128u, ACOL0 = 2u * NT;    // XB: one K tile of them; a row stage is two
+    static_assert(2 * NT + AS * 32 <= 512 && AS % CONV_GROUPS == 0 && WS % (CONV_GROUPS / 2) == 0,
+                  "tensor memory; stages of one group of widening warps");
     extern __shared__ uint8_t smem_raw[];
     const uint32_t raw = smem_addr(smem_raw);
     const uint32_t base = (raw + 1023u) & ~1023u;
-    const uint32_t w0 = base, x0 = w0 + WS * W_BYTES, bars = x0 + XS * XB;
+    const uint32_t w0 = base, x0 = w0 + WS * W_BYTES, bars = x0 + XS * 2 * XB;
     const uint32_t wfull = bars, wempty = wfull + 8 * WS, xfull = wempty + 8 * WS, xempty = xfull + 8 * XS,
                    afull = xempty + 8 * XS, aempty = afull + 8 * AS, dfull = aempty + 8 * AS, dempty = dfull + 16,
                    tslot = dempty + 16;
@@ -166,33 +232,37 @@ __global__ void __launch_bounds__(TC_THREADS, 1) q8_tc(const __grid_constant__ T
             mbar_init(wempty + 8 * i, 8);  // the eight widening warps
         }
         for (int i = 0; i < XS; ++i) {
-            mbar_init(xfull + 8 * i, 1);
-            mbar_init(xempty + 8 * i, CL);  // every CTA that the stage's boxes go to
+            mbar_init(xfull + 8 * i, 2);  // the two row-loading warps of the stage; used in the issuing CTA
+            mbar_init(xempty + 8 * i, 1);
         }
         for (int i = 0; i < AS; ++i) {
-            mbar_init(afull + 8 * i, 4);  // one group of widening warps
+            mbar_init(afull + 8 * i, 4 * CL);  // one group of widening warps of every CTA; used in the issuing CTA
             mbar_init(aempty + 8 * i, 1);
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(dfull + 8 * i, 1);
-            mbar_init(dempty + 8 * i, EPI_WARPS);
+            mbar_init(dempty + 8 * i, EPI_WARPS * CL);  // used in the issuing CTA
         }
         fence_mbar_init();
     }
     if (warp == MMA_WARP) {
-        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(tslot) : "memory");
-        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+        if (CL > 1) {
+            asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(tslot) : "memory");
+            asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+        } else {
+            asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(tslot) : "memory");
+            asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+        }
     }
     tc_fence_before();
-    if (CL > 1) cluster_sync();  // no copy may reach a CTA whose barriers are not there yet
     __syncthreads();
+    if (CL > 1) cluster_sync();  // nothing may reach a CTA whose barriers are not there yet
     tc_fence_after();
     uint32_t tmem;
     asm volatile("ld.shared.u32 %0, [%1];" : "=r"(tmem) : "r"(tslot));
     if (threadIdx.x == 0) pdl_launch_dependents();
 
     const int nch = (a.K + 127) / 128;  // weight chunks, two K tiles each (columns past K are zeros)
-    const int nkt = 2 * nch;
     const int mgroups = (a.mtiles + CL - 1) / CL;
     // the tile list comes from the previous kernel; without one the weights,
     // which no kernel of this call writes, are asked for at once
@@ -224,26 +294,33 @@ __global__ void __launch_bounds__(TC_THREADS, 1) q8_tc(const __grid_constant__ T
             }
         }
         __syncwarp();
-    } else if (warp == X_WARP || warp == X_WARP + 1) {
-        // the two warps take alternate K tiles: a tensor copy costs its
-        // issuer 100 to 200 clocks, and one issuer paced the K loop
+    } else if (warp >= X_WARP) {
+        // A stage is two K tiles.  Each of the four warps loads one K tile of
+        // every other stage: a copy costs its issuer hundreds of clocks, and
+        // fewer issuers paced the K loop.  The bytes of both CTAs complete on
+        // the issuing CTA's barrier, which alone expects them.
+        const uint32_t half = (warp - X_WARP) & 1, part = (warp - X_WARP) >> 1;
+        const uint32_t lead = CL > 1 ? mapa_shared(xfull, 0) : xfull;
         if (elect_one()) {
-            uint32_t s = warp - X_WARP, p = 1;
+            uint32_t s = part, p = 1, step = 0;  // step: the ring's steps so far, mod 2
             bool round0 = true;
             for (long long it = first; it < nitems && !failed; it += stride) {
                 const Tile t = tile_at(a, static_cast<int>(it / mgroups), ntiles);
-                const int boxes = (t.rows + F::BOX - 1) / F::BOX;
-                for (int kt = warp - X_WARP; kt < nkt; kt += 2) {
+                const int share = mma_cols<CL>(t.rows) / CL;  // rows of this CTA's share, a multiple of 16
+                const int row0 = t.row0 + rank * share;
+                const int copies = (share + a.box - 1) / a.box;
+                for (int c = static_cast<int>(step ^ part); c < nch; c += 2) {
                     if (!round0 && !mbar_wait_bounded(xempty + 8 * s, p, a.status, 8u)) {
                         failed = true;
                         break;
                     }
-                    mbar_arrive_expect_tx(xfull + 8 * s, static_cast<uint32_t>(boxes) * (F::BOX * 128u));
-                    for (int b = rank; b < boxes; b += CL) {
-                        const uint32_t dst = x0 + s * XB + static_cast<uint32_t>(b) * (F::BOX * 128u);
-                        if (CL > 1)
-                            tma_load_2d_mc(dst, &a.xmap, kt * KT, t.row0 + b * F::BOX, xfull + 8 * s, (1u << CL) - 1);
-                        else tma_load_2d(dst, &a.xmap, kt * KT, t.row0 + b * F::BOX, xfull + 8 * s);
+                    if (rank == 0) mbar_arrive_expect_tx(xfull + 8 * s, static_cast<uint32_t>(copies * a.box) * (128u * CL));
+                    const int x = (2 * c + static_cast<int>(half)) * KT;
+                    const uint32_t dst = x0 + (2 * s + half) * XB, bar = lead + 8 * s;
+                    for (int b = 0; b < copies; ++b) {
+                        const uint32_t to = dst + static_cast<uint32_t>(b * a.box) * 128u;
+                        if (CL > 1) tma_load_2d_pair(to, &a.xmap, x, row0 + b * a.box, bar);
+                        else tma_load_2d(to, &a.xmap, x, row0 + b * a.box, bar);
                     }
                     s += 2;
                     if (s >= XS) {
@@ -252,9 +329,10 @@ __global__ void __launch_bounds__(TC_THREADS, 1) q8_tc(const __grid_constant__ T
                         round0 = false;
                     }
                 }
+                step ^= static_cast<uint32_t>(nch & 1);
             }
-            // the other CTA's last releases of this warp's stages arrive
-            // here: they must have before this CTA may leave
+            // the last releases of this warp's stages arrive here from the
+            // other CTA's issue: they must have before this CTA may leave
             if (CL > 1 && !failed) {
                 for (int j = 0; j < XS / 2; ++j) {
                     if (!round0 && !mbar_wait_bounded(xempty + 8 * s, p, a.status, 8u)) failed = true;
@@ -269,35 +347,49 @@ __global__ void __launch_bounds__(TC_THREADS, 1) q8_tc(const __grid_constant__ T
         }
         __syncwarp();
     } else if (warp == MMA_WARP) {
-        // one thread issues; it looks at both barriers of a stage before it
-        // waits for either, so that two stages that are ready cost one look
-        if (elect_one()) {
+        // one thread issues, of a pair the even CTA's
+        if (rank == 0 && elect_one()) {
             uint32_t sa = 0, pa = 0, sx = 0, px = 0, d = 0;
             for (long long it = first; it < nitems && !failed; it += stride, ++d) {
                 const Tile t = tile_at(a, static_cast<int>(it / mgroups), ntiles);
-                const uint32_t idesc = idesc_f16((t.rows + 15) & ~15);
+                const uint32_t idesc = idesc_f16(MT * CL, mma_cols<CL>(t.rows));
                 const uint32_t acc = tmem + (d & 1) * NT;
-                if (d >= 2 && !mbar_wait_bounded(dempty + 8 * (d & 1), (d / 2 - 1) & 1, a.status, 4u)) failed = true;
-                for (int kt = 0; kt < nkt && !failed; ++kt) {
-                    const bool rx = mbar_test(xfull + 8 * sx, px), ra = mbar_test(afull + 8 * sa, pa);
-                    if (!(rx && ra) && !(mbar_wait_bounded(xfull + 8 * sx, px, a.status, 3u) &&
-                                         mbar_wait_bounded(afull + 8 * sa, pa, a.status, 3u))) {
+                if (d >= 2 && !wait_pair<CL>(dempty + 8 * (d & 1), (d / 2 - 1) & 1, a.status, 4u)) failed = true;
+                for (int c = 0; c < nch && !failed; ++c) {
+                    // two K tiles at a time, their three barriers looked at
+                    // together: this thread's own latency paces the loop
+                    // where the tile is narrow
+                    const bool rx = mbar_test<CL>(xfull + 8 * sx, px), r0 = mbar_test<CL>(afull + 8 * sa, pa),
+                               r1 = mbar_test<CL>(afull + 8 * sa + 8, pa);
+                    if (!(rx && r0 && r1) &&
+                        !(wait_pair<CL>(xfull + 8 * sx, px, a.status, 3u) && wait_pair<CL>(afull + 8 * sa, pa, a.status, 3u) &&
+                          wait_pair<CL>(afull + 8 * sa + 8, pa, a.status, 3u))) {
                         failed = true;
                         break;
                     }
                     tc_fence_after();
-                    const uint32_t at = tmem + ACOL0 + sa * 32;
-                    const uint64_t xd = desc_sw128(x0 + sx * XB);
 #pragma unroll
-                    for (int kk = 0; kk < KT / 16; ++kk)
-                        mma_f16_ta(acc, at + kk * 8, xd + kk * 2, idesc, kt + kk != 0);
-                    mma_commit(aempty + 8 * sa);
-                    if (CL > 1) mma_commit_mc(xempty + 8 * sx, (1u << CL) - 1);
-                    else mma_commit(xempty + 8 * sx);
-                    if (kt == nkt - 1) mma_commit(dfull + 8 * (d & 1));
-                    if (++sa == AS) {
+                    for (int h = 0; h < 2; ++h) {
+                        const uint32_t at = tmem + ACOL0 + (sa + h) * 32;
+                        const uint64_t xd = desc_sw128(x0 + (2 * sx + h) * XB);
+#pragma unroll
+                        for (int kk = 0; kk < KT / 16; ++kk) {
+                            if (CL > 1) mma_f16_ta_pair(acc, at + kk * 8, xd + kk * 2, idesc, c + h + kk != 0);
+                            else mma_f16_ta(acc, at + kk * 8, xd + kk * 2, idesc, c + h + kk != 0);
+                        }
+                        if (CL > 1) mma_commit_pair(aempty + 8 * (sa + h));
+                        else mma_commit(aempty + 8 * (sa + h));
+                    }
+                    sa += 2;
+                    if (sa == AS) {
                         sa = 0;
                         pa ^= 1u;
+                    }
+                    if (CL > 1) mma_commit_pair(xempty + 8 * sx);
+                    else mma_commit(xempty + 8 * sx);
+                    if (c == nch - 1) {
+                        if (CL > 1) mma_commit_pair(dfull + 8 * (d & 1));
+                        else mma_commit(dfull + 8 * (d & 1));
                     }
                     if (++sx == XS) {
                         sx = 0;
@@ -308,51 +400,79 @@ __global__ void __launch_bounds__(TC_THREADS, 1) q8_tc(const __grid_constant__ T
         }
         __syncwarp();
     } else if (warp >= CONV_WARP0 && warp < MMA_WARP) {
-        // thread = one weight row; group grp widens the K tiles 2 c + grp
+        // thread = one weight row; of the K tiles that this CTA streams, one
+        // after another over all its items, group grp widens every fourth
         const int ct = threadIdx.x - CONV_WARP0 * 32;
-        const uint32_t r = ct & (MT - 1), grp = ct >> 7;
-        uint32_t g = 0;
-        for (long long it = first; it < nitems && !failed; it += stride) {
-            for (int c = 0; c < nch; ++c, ++g) {
-                const uint32_t sw = g % WS, ga = 2 * g + grp, sa = ga % AS;
-                const bool ok = mbar_wait_bounded(wfull + 8 * sw, (g / WS) & 1, a.status, 5u) &&
-                                (ga < AS || mbar_wait_bounded(aempty + 8 * sa, (ga / AS - 1) & 1, a.status, 5u));
-                if (!__all_sync(FULL_MASK, ok)) {
-                    failed = true;
-                    break;
-                }
-                tc_fence_after();
-                const uint32_t row = w0 + sw * W_BYTES + r * 128u;
-                uint4 w[4];
+        const uint32_t r = ct & (MT - 1), grp = ct >> 7, half = grp & 1;
+        const uint32_t lead = CL > 1 ? mapa_shared(afull, 0) : afull;
+        const long long mine = first < nitems ? (nitems - first + stride - 1) / stride : 0;
+        const long long chunks = mine * nch;
+        uint32_t sw = (grp >> 1) % WS, pw = 0, sa = grp % AS, pa = 1;
+        bool round0 = true;
+        for (long long g = grp >> 1; g < chunks; g += CONV_GROUPS / 2) {
+            if (!__all_sync(FULL_MASK, mbar_wait_bounded(wfull + 8 * sw, pw, a.status, 5u))) {
+                failed = true;
+                break;
+            }
+            // widened in registers before the stage is waited for: only the
+            // store is between its release and its next use
+            const uint32_t row = w0 + sw * W_BYTES + r * 128u;
+            uint32_t v[2][16];
 #pragma unroll
-                for (int j = 0; j < 4; ++j) w[j] = lds128v(row + (((grp * 4 + j) ^ (r & 7)) << 4));
+            for (int j = 0; j < 4; ++j) {
+                const uint4 q = lds128v(row + (((half * 4 + j) ^ (r & 7)) << 4));
+                uint32_t *to = &v[j >> 1][8 * (j & 1)];
+                s8x4_to_f16(q.x, to[0], to[1]);
+                s8x4_to_f16(q.y, to[2], to[3]);
+                s8x4_to_f16(q.z, to[4], to[5]);
+                s8x4_to_f16(q.w, to[6], to[7]);
+            }
+            __syncwarp();
+            if (lane == 0) mbar_arrive(wempty + 8 * sw);
+            if (!__all_sync(FULL_MASK, round0 || mbar_wait_bounded(aempty + 8 * sa, pa, a.status, 5u))) {
+                failed = true;
+                break;
+            }
+            tc_fence_after();
 #pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    uint32_t v[16];
-#pragma unroll
-                    for (int j = 0; j < 2; ++j) {
-                        const uint4 q = w[2 * h + j];
-                        s8x4_to_f16(q.x, v[8 * j], v[8 * j + 1]);
-                        s8x4_to_f16(q.y, v[8 * j + 2], v[8 * j + 3]);
-                        s8x4_to_f16(q.z, v[8 * j + 4], v[8 * j + 5]);
-                        s8x4_to_f16(q.w, v[8 * j + 6], v[8 * j + 7]);
-                    }
-                    tmem_st16(tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16) + ACOL0 + sa * 32 + 16 * h, v);
-                }
-                tmem_wait_st();
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0) {
-                    mbar_arrive(wempty + 8 * sw);
-                    mbar_arrive(afull + 8 * sa);
-                }
+            for (int h = 0; h < 2; ++h)
+                tmem_st16(tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16) + ACOL0 + sa * 32 + 16 * h, v[h]);
+            tmem_wait_st();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) {
+                if (CL > 1) mbar_arrive_cluster(lead + 8 * sa);
+                else mbar_arrive(afull + 8 * sa);
+            }
+            sw += CONV_GROUPS / 2;
+            if (sw >= WS) {
+                sw -= WS;
+                pw ^= 1u;
+            }
+            sa += CONV_GROUPS;
+            if (sa >= AS) {
+                sa -= AS;
+                pa ^= 1u;
+                round0 = false;
             }
         }
+        // the last releases of this group's stages come from the even CTA
+        if (CL > 1 && !failed)
+            for (int j = 0; j < AS / CONV_GROUPS; ++j) {
+                if (!round0 && !mbar_wait_bounded(aempty + 8 * sa, pa, a.status, 5u)) failed = true;
+                sa += CONV_GROUPS;
+                if (sa >= AS) {
+                    sa -= AS;
+                    pa ^= 1u;
+                    round0 = false;
+                }
+            }
     } else if (warp < EPI_WARPS) {
         // warp w: TMEM lanes 32 (w % 4) .. + 31 = weight rows, the 16-column
         // blocks of parity w / 4
         const int q = warp & 3, h = warp >> 2;
         T *y = static_cast<T *>(a.y);
+        const uint32_t lead = CL > 1 ? mapa_shared(dempty, 0) : dempty;
         uint32_t d = 0;
         for (long long it = first; it < nitems; it += stride, ++d) {
             const Tile t = tile_at(a, static_cast<int>(it / mgroups), ntiles);
@@ -379,7 +499,10 @@ __global__ void __launch_bounds__(TC_THREADS, 1) q8_tc(const __grid_constant__ T
             }
             tc_fence_before();
             __syncwarp();
-            if (lane == 0) mbar_arrive(dempty + 8 * (d & 1));
+            if (lane == 0) {
+                if (CL > 1) mbar_arrive_cluster(lead + 8 * (d & 1));
+                else mbar_arrive(dempty + 8 * (d & 1));
+            }
         }
     }
     tc_fence_before();
@@ -393,7 +516,8 @@ __global__ void __launch_bounds__(TC_THREADS, 1) q8_tc(const __grid_constant__ T
     if (CL > 1) cluster_sync();  // no CTA leaves while the other's copies or releases may reach it
     if (warp == MMA_WARP) {
         tc_fence_after();
-        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem) : "memory");
+        if (CL > 1) asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, 512;" ::"r"(tmem) : "memory");
+        else asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem) : "memory");
     }
 }
 
@@ -406,17 +530,18 @@ struct PrepArgs {
     const float *xs;
     const int *order, *offsets;
     __half *x16;  // [R x K]
-    float *xss;   // [R]
+    float *xss;   // [R]: the sorted rows' scales
     void *y;
     int *ntiles;
     Tile *tiles;
     unsigned *status;
-    int nsrc, k, R, n, K, N, nt, max_tiles, zero_bytes;  // zero_bytes: bytes of one element of y
+    int nsrc, k, R, n, K, N, nt, unit, max_tiles, zero_bytes;  // unit: MMA columns; zero_bytes: an element of y
 };
 
 // Block 0 (with offsets): the tile list, every expert's rows cut into equal
-// tiles of at most nt.  The others: the rows in sorted order, widened to
-// f16, with their scales; rows past the last expert's get zeros in y.
+// tiles of at most nt.  The others: the activations widened to f16, the
+// sorted rows' sources and scales, and zeros in the rows of y past the last
+// expert's.
 __global__ void __launch_bounds__(PREP_THREADS) q8_prep(const PrepArgs a)
 {
     __shared__ int warp_sums[PREP_THREADS / 32];
@@ -439,7 +564,7 @@ __global__ void __launch_bounds__(PREP_THREADS) q8_prep(const PrepArgs a)
                 }
             }
             int cnt = (hi - lo + a.nt - 1) / a.nt;
-            const int step = cnt > 0 ? ((hi - lo + cnt - 1) / cnt + 15) & ~15 : 16;
+            const int step = cnt > 0 ? ((hi - lo + cnt - 1) / cnt + a.unit - 1) / a.unit * a.unit : a.unit;
             cnt = (hi - lo + step - 1) / step;
             int inc = cnt;
 #pragma unroll
@@ -461,30 +586,30 @@ __global__ void __launch_bounds__(PREP_THREADS) q8_prep(const PrepArgs a)
         if (tid == 0) *a.ntiles = min(run, a.max_tiles);
         return;
     }
-    const int b0 = a.offsets ? 1 : 0;
+    const int b0 = a.offsets ? 1 : 0, blocks = gridDim.x - b0;
     const int last = a.offsets ? max(0, min(a.offsets[a.n], a.R)) : a.R;
-    for (int r = blockIdx.x - b0; r < a.R; r += gridDim.x - b0) {
-        if (r >= last) {  // no expert: zeros
-            const size_t n = static_cast<size_t>(a.N);
-            for (size_t i = tid; i < n; i += PREP_THREADS) {
-                if (a.zero_bytes == 4) static_cast<float *>(a.y)[r * n + i] = 0.f;
-                else static_cast<uint16_t *>(a.y)[r * n + i] = 0;
-            }
-        }
+    for (int r = (blockIdx.x - b0) * PREP_THREADS + tid; r < a.R; r += blocks * PREP_THREADS) {
         const int src = r < last ? source_row(a.order, a.k, a.nsrc, r, a.status) : -1;
-        if (tid == 0) a.xss[r] = src >= 0 ? a.xs[src] : 0.f;
-        __half *out = a.x16 + static_cast<size_t>(r) * a.K;
-        for (int c = tid * 16; c < a.K; c += PREP_THREADS * 16) {
-            uint4 lo = make_uint4(0u, 0u, 0u, 0u), hi = lo;
-            if (src >= 0) {
-                const uint4 v = *reinterpret_cast<const uint4 *>(a.xq + static_cast<size_t>(src) * a.K + c);
-                s8x4_to_f16(v.x, lo.x, lo.y);
-                s8x4_to_f16(v.y, lo.z, lo.w);
-                s8x4_to_f16(v.z, hi.x, hi.y);
-                s8x4_to_f16(v.w, hi.z, hi.w);
-            }
-            reinterpret_cast<uint4 *>(out + c)[0] = lo;
-            reinterpret_cast<uint4 *>(out + c)[1] = hi;
+        a.xss[r] = src >= 0 ? a.xs[src] : 0.f;
+    }
+    const size_t zero0 = static_cast<size_t>(last) * a.N, zero1 = static_cast<size_t>(a.R) * a.N;
+    for (size_t i = zero0 + static_cast<size_t>(blockIdx.x - b0) * PREP_THREADS + tid; i < zero1;
+         i += static_cast<size_t>(blocks) * PREP_THREADS) {
+        if (a.zero_bytes == 4) static_cast<float *>(a.y)[i] = 0.f;
+        else static_cast<uint16_t *>(a.y)[i] = 0;
+    }
+    for (int r = blockIdx.x - b0; r < last; r += blocks) {
+        const int src = max(source_row(a.order, a.k, a.nsrc, r, a.status), 0);  // none: a row whose scale is 0
+        for (int c = tid; c < a.K / 16; c += PREP_THREADS) {
+            const uint4 v = reinterpret_cast<const uint4 *>(a.xq + static_cast<size_t>(src) * a.K)[c];
+            uint4 lo, hi;
+            s8x4_to_f16(v.x, lo.x, lo.y);
+            s8x4_to_f16(v.y, lo.z, lo.w);
+            s8x4_to_f16(v.z, hi.x, hi.y);
+            s8x4_to_f16(v.w, hi.z, hi.w);
+            uint4 *out = reinterpret_cast<uint4 *>(a.x16 + static_cast<size_t>(r) * a.K);
+            out[2 * c] = lo;
+            out[2 * c + 1] = hi;
         }
     }
 }
@@ -596,21 +721,25 @@ cudaError_t launch_q8_tc(const Q8Call &c, void *workspace, cudaStream_t stream)
     if (!dev || !status) return cudaErrorInvalidDevice;
     char *ws = static_cast<char *>(workspace);
     const Layout l = layout(c.R, c.n, c.K);
-    const int nt = pick_nt(c.R, c.n);
+    const int nt = pick_nt(c.R, c.n), cl = nt == 192 ? Form<192>::CL : Form<64>::CL, unit = 16 * cl;
     const int max_tiles = most_tiles(c.R, c.n, nt);
     int *ntiles = reinterpret_cast<int *>(ws);
     Tile *tiles = reinterpret_cast<Tile *>(ws + l.tiles);
     float *xss = reinterpret_cast<float *>(ws + l.xss);
     __half *x16 = reinterpret_cast<__half *>(ws + l.x16);
 
+    // one matrix: equal tiles of consecutive rows, a CTA's share one copy
+    const int nd = (c.R + nt - 1) / nt;
+    const int step = ((c.R + nd - 1) / nd + unit - 1) / unit * unit;
     TcArgs a = {};
+    a.box = c.offsets ? nt / cl / 2 : step / cl;
     if (!encode(&a.wmap, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, c.wq, c.K, static_cast<long long>(c.n) * c.N, 128, MT) ||
-        !encode(&a.xmap, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 2, x16, c.K, c.R, KT, nt == 192 ? Form<192>::BOX : Form<64>::BOX))
+        !encode(&a.xmap, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 2, x16, c.K, c.R, KT, a.box))
         return cudaErrorInvalidValue;
-    const PrepArgs p = {c.xq, c.xs, c.order, c.offsets, x16, xss, c.y, ntiles, tiles, status, c.nsrc, c.k, c.R, c.n, c.K,
-                        c.N, nt, max_tiles, c.dtype == SMOE_BF16 ? 2 : 4};
-    const int rows_blocks = c.R < dev->sm_count * 8 ? c.R : dev->sm_count * 8;
-    cudaError_t e = launch_pdl(q8_prep, dim3(static_cast<unsigned>(rows_blocks + (c.offsets ? 1 : 0))), dim3(PREP_THREADS), 0,
+    const PrepArgs p = {c.xq, c.xs, c.order, c.offsets, x16, xss, c.y, ntiles, tiles, status, c.nsrc, c.k, c.R, c.n,
+                        c.K, c.N, nt, unit, max_tiles, c.dtype == SMOE_BF16 ? 2 : 4};
+    const int blocks = c.R < dev->sm_count * 8 ? c.R : dev->sm_count * 8;
+    cudaError_t e = launch_pdl(q8_prep, dim3(static_cast<unsigned>(blocks + (c.offsets ? 1 : 0))), dim3(PREP_THREADS), 0,
                                stream, p);
     if (e != cudaSuccess) return e;
     a.ws = c.ws;
@@ -622,10 +751,8 @@ cudaError_t launch_q8_tc(const Q8Call &c, void *workspace, cudaStream_t stream)
     a.R = c.R;
     a.N = c.N;
     a.K = c.K;
-    const int nd = (c.R + nt - 1) / nt;
-    a.step = ((c.R + nd - 1) / nd + 15) & ~15;
+    a.step = step;
     a.mtiles = (c.N + MT - 1) / MT;
-    const int cl = nt == 192 ? 2 : 1;
     const long long most = static_cast<long long>(c.offsets ? max_tiles : nd) * ((a.mtiles + cl - 1) / cl);
     if (c.dtype == SMOE_BF16)
         return nt == 192 ? launch_tc<__nv_bfloat16, 192>(a, most, dev->sm_count, stream)
