@@ -30,6 +30,13 @@ __device__ __forceinline__ int source_row(const int *order, int k, int nsrc, int
 __device__ __forceinline__ void put(float *p, float v) { *p = v; }
 __device__ __forceinline__ void put(__nv_bfloat16 *p, float v) { *p = __float2bfloat16_rn(v); }
 
+// Two neighbouring elements, the first at an even index of an aligned row.
+__device__ __forceinline__ void put2(float *p, float a, float b) { *reinterpret_cast<float2 *>(p) = make_float2(a, b); }
+__device__ __forceinline__ void put2(__nv_bfloat16 *p, float a, float b)
+{
+    *reinterpret_cast<__nv_bfloat162 *>(p) = __floats2bfloat162_rn(a, b);
+}
+
 inline size_t up256(size_t v) { return (v + 255) & ~static_cast<size_t>(255); }
 
 // Most tiles of up to `step` rows that R rows of n experts (and the rows of

@@ -479,6 +479,13 @@ __global__ void __launch_bounds__(TC_THREADS, 1) q8_tc(const __grid_constant__ T
             const int n = (static_cast<int>(it % mgroups) * CL + rank) * MT + q * 32 + lane;
             const bool nok = n < a.N;
             const float ws = nok ? a.ws[static_cast<size_t>(t.expert) * a.N + n] : 0.f;
+            // the rows' scales, one lane a row of each 16-row block
+            float xv[NT / 32];
+#pragma unroll
+            for (int j = 0; j < NT / 32; ++j) {
+                const int c = h * 16 + j * 32 + (lane & 15);
+                xv[j] = c < t.rows ? a.xs[t.row0 + c] : 0.f;
+            }
             const bool ok = mbar_wait_bounded(dfull + 8 * (d & 1), (d / 2) & 1, a.status, 6u);
             if (!__all_sync(FULL_MASK, ok)) {
                 failed = true;
@@ -486,15 +493,30 @@ __global__ void __launch_bounds__(TC_THREADS, 1) q8_tc(const __grid_constant__ T
             }
             tc_fence_after();
             const uint32_t acc = tmem + (static_cast<uint32_t>(q * 32) << 16) + (d & 1) * NT;
-            for (int c = h * 16; c < t.rows; c += 32) {
+#pragma unroll
+            for (int j = 0; j < NT / 32; ++j) {
+                const int c = h * 16 + j * 32;
+                if (c >= t.rows) break;
                 float v[16];
                 tmem_ld<16>(acc + c, v);
-                const float xl = (lane & 15) < t.rows - c ? a.xs[t.row0 + c + (lane & 15)] : 0.f;
                 tmem_wait_ld();
 #pragma unroll
-                for (int i = 0; i < 16; ++i) {
-                    const float xi = __shfl_sync(FULL_MASK, xl, i);
-                    if (nok && c + i < t.rows) put(y + static_cast<size_t>(t.row0 + c + i) * a.N + n, v[i] * xi * ws);
+                for (int i = 0; i < 16; ++i) v[i] = v[i] * __shfl_sync(FULL_MASK, xv[j], i) * ws;
+                if ((a.N & 1) == 0) {
+                    // neighbouring lanes trade every other row, so that each
+                    // stores two columns of one row at once
+                    const bool odd = lane & 1;
+#pragma unroll
+                    for (int i = 0; i < 16; i += 2) {
+                        const float got = __shfl_xor_sync(FULL_MASK, odd ? v[i] : v[i + 1], 1);
+                        const int r = c + i + (odd ? 1 : 0);
+                        if (nok && r < t.rows)
+                            put2(y + static_cast<size_t>(t.row0 + r) * a.N + (n & ~1), odd ? got : v[i], odd ? v[i + 1] : got);
+                    }
+                } else {
+#pragma unroll
+                    for (int i = 0; i < 16; ++i)
+                        if (nok && c + i < t.rows) put(y + static_cast<size_t>(t.row0 + c + i) * a.N + n, v[i]);
                 }
             }
             tc_fence_before();
@@ -598,19 +620,31 @@ __global__ void __launch_bounds__(PREP_THREADS) q8_prep(const PrepArgs a)
         if (a.zero_bytes == 4) static_cast<float *>(a.y)[i] = 0.f;
         else static_cast<uint16_t *>(a.y)[i] = 0;
     }
-    for (int r = blockIdx.x - b0; r < last; r += blocks) {
-        const int src = max(source_row(a.order, a.k, a.nsrc, r, a.status), 0);  // none: a row whose scale is 0
-        for (int c = tid; c < a.K / 16; c += PREP_THREADS) {
-            const uint4 v = reinterpret_cast<const uint4 *>(a.xq + static_cast<size_t>(src) * a.K)[c];
-            uint4 lo, hi;
-            s8x4_to_f16(v.x, lo.x, lo.y);
-            s8x4_to_f16(v.y, lo.z, lo.w);
-            s8x4_to_f16(v.z, hi.x, hi.y);
-            s8x4_to_f16(v.w, hi.z, hi.w);
-            uint4 *out = reinterpret_cast<uint4 *>(a.x16 + static_cast<size_t>(r) * a.K);
-            out[2 * c] = lo;
-            out[2 * c + 1] = hi;
+    // eight columns a thread, so that a warp's stores are whole sectors in a
+    // row; the next row's source is on its way while this one is widened
+    int r = blockIdx.x - b0;
+    int src = r < last ? source_row(a.order, a.k, a.nsrc, r, a.status) : 0;
+    while (r < last) {
+        const int rn = r + blocks;
+        const int next = rn < last ? source_row(a.order, a.k, a.nsrc, rn, a.status) : 0;
+        const uint2 *in = reinterpret_cast<const uint2 *>(a.xq + static_cast<size_t>(max(src, 0)) * a.K);  // none: scale 0
+        uint4 *out = reinterpret_cast<uint4 *>(a.x16 + static_cast<size_t>(r) * a.K);
+        for (int c0 = tid; c0 < a.K / 8; c0 += 4 * PREP_THREADS) {
+            uint2 v[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                if (c0 + j * PREP_THREADS < a.K / 8) v[j] = in[c0 + j * PREP_THREADS];
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                if (c0 + j * PREP_THREADS < a.K / 8) {
+                    uint4 o;
+                    s8x4_to_f16(v[j].x, o.x, o.y);
+                    s8x4_to_f16(v[j].y, o.z, o.w);
+                    out[c0 + j * PREP_THREADS] = o;
+                }
         }
+        r = rn;
+        src = next;
     }
 }
 
