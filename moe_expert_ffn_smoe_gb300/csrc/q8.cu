@@ -323,13 +323,13 @@ cudaError_t launch_quantize_rows(const void *x, int dtype, bool act, int rows, i
              : quant_a<float, 1>(act, x, rows, cols, q, scales, stream);
 }
 
-#ifndef Q8_TC_MIN
-#define Q8_TC_MIN 16
-#endif
-static bool on_tensor_cores(int R, int n, int K)
-{
-    return K > 0 && R > static_cast<long long>(Q8_TC_MIN) * n;
-}
+// Where the tensor cores take the product: from three rows on, and from more
+// than three for every eight experts.  Below, the integer dots need no
+// preparation.  Measured (us; K = 4096), dots against tensor cores: one matrix
+// of 8192, 1 row 7.4 / 13.2, 2 rows 9.9 / 13.5, 4 rows 14.4 / 13.6; of 1536,
+// 1 row 6.0 / 8.6, 2 rows 9.1 / 8.6; 128 experts of 1536, 32 rows 38.9 /
+// 42.9, 64 rows 62.1 / 58.4.
+static bool on_tensor_cores(int R, int n, int K) { return K > 0 && R > 2 && R > 3LL * n / 8; }
 
 size_t q8_workspace(int nsrc, int R, int n, int N, int K)
 {
@@ -357,16 +357,14 @@ cudaError_t launch_q8(const int8_t *xq, const float *xs, int nsrc, const int *or
         if (e != cudaSuccess) return e;
     }
     const Q8Args a = {xq, xs, order, wq, ws, y, ntiles, tiles, status, k, nsrc, N, K, R};
-    // CTAs per tile: enough for about two waves of the device (two CTAs an
-    // SM) when every row has an expert of its own
+    // CTAs per tile: about eight waves of the device (two CTAs an SM) when
+    // every row has an expert of its own (two waves 130 us, four 103, eight
+    // 99, sixteen 100 for 128 rows over 128 experts of 1536 x 4096)
     const DeviceInfo *dev = device_info();
     if (!dev) return cudaErrorInvalidDevice;
     const int likely = offsets ? (R < n ? R : n) : max_tiles;
     const int blocks = (N + DOT_WARPS * DOT_OUTS - 1) / (DOT_WARPS * DOT_OUTS);
-#ifndef DOT_WAVES
-#define DOT_WAVES 16
-#endif
-    int per_tile = (DOT_WAVES * dev->sm_count + likely - 1) / likely;
+    int per_tile = (16 * dev->sm_count + likely - 1) / likely;
     if (per_tile > blocks) per_tile = blocks;
     const dim3 grid(static_cast<unsigned>(max_tiles), static_cast<unsigned>(per_tile));
     if (dtype == SMOE_BF16) return launch_pdl(q8_dot<__nv_bfloat16>, grid, dim3(DOT_WARPS * 32), 0, stream, a);

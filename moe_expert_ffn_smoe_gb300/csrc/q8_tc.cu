@@ -72,6 +72,7 @@ struct alignas(128) TcArgs {
     const Tile *tiles;     // null: one matrix, tiles of `step` rows
     unsigned *status;
     int R, N, K, step, mtiles, box;  // box: rows of one copy
+    int nsplit;            // CTAs that share an item's K range (single-CTA form)
 };
 
 // Four int8 in a word as two f16 pairs: byte b + 128 in the mantissa of
@@ -224,7 +225,9 @@ __global__ void __launch_bounds__(TC_THREADS, 1) q8_tc(const __grid_constant__ T
                    tslot = dempty + 16;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int rank = CL > 1 ? static_cast<int>(blockIdx.x % CL) : 0;
-    const int first = static_cast<int>(blockIdx.x / CL), stride = static_cast<int>(gridDim.x / CL);
+    const int nsplit = CL > 1 ? 1 : a.nsplit;
+    const int krank = nsplit > 1 ? static_cast<int>(blockIdx.x) % nsplit : 0;  // = the rank in the cluster
+    const int first = static_cast<int>(blockIdx.x) / (CL * nsplit), stride = static_cast<int>(gridDim.x) / (CL * nsplit);
 
     if (threadIdx.x == 0) {
         for (int i = 0; i < WS; ++i) {
@@ -263,6 +266,7 @@ __global__ void __launch_bounds__(TC_THREADS, 1) q8_tc(const __grid_constant__ T
     if (threadIdx.x == 0) pdl_launch_dependents();
 
     const int nch = (a.K + 127) / 128;  // weight chunks, two K tiles each (columns past K are zeros)
+    const int c0 = krank * nch / nsplit, c1 = (krank + 1) * nch / nsplit;  // this CTA's
     const int mgroups = (a.mtiles + CL - 1) / CL;
     // the tile list comes from the previous kernel; without one the weights,
     // which no kernel of this call writes, are asked for at once
@@ -278,7 +282,7 @@ __global__ void __launch_bounds__(TC_THREADS, 1) q8_tc(const __grid_constant__ T
             for (long long it = first; it < nitems && !failed; it += stride) {
                 const Tile t = tile_at(a, static_cast<int>(it / mgroups), ntiles);
                 const int row = t.expert * a.N + (static_cast<int>(it % mgroups) * CL + rank) * MT;
-                for (int c = 0; c < nch; ++c) {
+                for (int c = c0; c < c1; ++c) {
                     if (!round0 && !mbar_wait_bounded(wempty + 8 * s, p, a.status, 7u)) {
                         failed = true;
                         break;
@@ -309,7 +313,7 @@ __global__ void __launch_bounds__(TC_THREADS, 1) q8_tc(const __grid_constant__ T
                 const int share = mma_cols<CL>(t.rows) / CL;  // rows of this CTA's share, a multiple of 16
                 const int row0 = t.row0 + rank * share;
                 const int copies = (share + a.box - 1) / a.box;
-                for (int c = static_cast<int>(step ^ part); c < nch; c += 2) {
+                for (int c = c0 + static_cast<int>(step ^ part); c < c1; c += 2) {
                     if (!round0 && !mbar_wait_bounded(xempty + 8 * s, p, a.status, 8u)) {
                         failed = true;
                         break;
@@ -329,7 +333,7 @@ __global__ void __launch_bounds__(TC_THREADS, 1) q8_tc(const __grid_constant__ T
                         round0 = false;
                     }
                 }
-                step ^= static_cast<uint32_t>(nch & 1);
+                step ^= static_cast<uint32_t>((c1 - c0) & 1);
             }
             // the last releases of this warp's stages arrive here from the
             // other CTA's issue: they must have before this CTA may leave
@@ -355,7 +359,7 @@ __global__ void __launch_bounds__(TC_THREADS, 1) q8_tc(const __grid_constant__ T
                 const uint32_t idesc = idesc_f16(MT * CL, mma_cols<CL>(t.rows));
                 const uint32_t acc = tmem + (d & 1) * NT;
                 if (d >= 2 && !wait_pair<CL>(dempty + 8 * (d & 1), (d / 2 - 1) & 1, a.status, 4u)) failed = true;
-                for (int c = 0; c < nch && !failed; ++c) {
+                for (int c = c0; c < c1 && !failed; ++c) {
                     // two K tiles at a time, their three barriers looked at
                     // together: this thread's own latency paces the loop
                     // where the tile is narrow
@@ -374,8 +378,8 @@ __global__ void __launch_bounds__(TC_THREADS, 1) q8_tc(const __grid_constant__ T
                         const uint64_t xd = desc_sw128(x0 + (2 * sx + h) * XB);
 #pragma unroll
                         for (int kk = 0; kk < KT / 16; ++kk) {
-                            if (CL > 1) mma_f16_ta_pair(acc, at + kk * 8, xd + kk * 2, idesc, c + h + kk != 0);
-                            else mma_f16_ta(acc, at + kk * 8, xd + kk * 2, idesc, c + h + kk != 0);
+                            if (CL > 1) mma_f16_ta_pair(acc, at + kk * 8, xd + kk * 2, idesc, c - c0 + h + kk != 0);
+                            else mma_f16_ta(acc, at + kk * 8, xd + kk * 2, idesc, c - c0 + h + kk != 0);
                         }
                         if (CL > 1) mma_commit_pair(aempty + 8 * (sa + h));
                         else mma_commit(aempty + 8 * (sa + h));
@@ -387,7 +391,7 @@ __global__ void __launch_bounds__(TC_THREADS, 1) q8_tc(const __grid_constant__ T
                     }
                     if (CL > 1) mma_commit_pair(xempty + 8 * sx);
                     else mma_commit(xempty + 8 * sx);
-                    if (c == nch - 1) {
+                    if (c == c1 - 1) {
                         if (CL > 1) mma_commit_pair(dfull + 8 * (d & 1));
                         else mma_commit(dfull + 8 * (d & 1));
                     }
@@ -406,7 +410,7 @@ __global__ void __launch_bounds__(TC_THREADS, 1) q8_tc(const __grid_constant__ T
         const uint32_t r = ct & (MT - 1), grp = ct >> 7, half = grp & 1;
         const uint32_t lead = CL > 1 ? mapa_shared(afull, 0) : afull;
         const long long mine = first < nitems ? (nitems - first + stride - 1) / stride : 0;
-        const long long chunks = mine * nch;
+        const long long chunks = mine * (c1 - c0);
         uint32_t sw = (grp >> 1) % WS, pw = 0, sa = grp % AS, pa = 1;
         bool round0 = true;
         for (long long g = grp >> 1; g < chunks; g += CONV_GROUPS / 2) {
@@ -500,6 +504,13 @@ __global__ void __launch_bounds__(TC_THREADS, 1) q8_tc(const __grid_constant__ T
                 float v[16];
                 tmem_ld<16>(acc + c, v);
                 tmem_wait_ld();
+                if (nsplit > 1) {  // this K range's sums, for the reduction below
+                    const uint32_t to = x0 + static_cast<uint32_t>(c * MT + q * 32 + lane) * 4u;
+#pragma unroll
+                    for (int i = 0; i < 16; ++i)
+                        asm volatile("st.shared.f32 [%0], %1;" ::"r"(to + i * MT * 4u), "f"(v[i]) : "memory");
+                    continue;
+                }
 #pragma unroll
                 for (int i = 0; i < 16; ++i) v[i] = v[i] * __shfl_sync(FULL_MASK, xv[j], i) * ws;
                 if ((a.N & 1) == 0) {
@@ -535,7 +546,37 @@ __global__ void __launch_bounds__(TC_THREADS, 1) q8_tc(const __grid_constant__ T
         while (clock64() - t0 < 2000000LL) __nanosleep(1000);
         __syncthreads();
     }
-    if (CL > 1) cluster_sync();  // no CTA leaves while the other's copies or releases may reach it
+    if (nsplit > 1) {
+        // The cluster is an item's K ranges, each CTA's sums [row][128] in
+        // the shared memory of its row stages: every CTA adds every nsplit-th
+        // row of all of them, in rank order, and stores it.
+        static_assert(CL > 1 || NT * MT * 4u <= XS * 2 * XB, "the sums of a tile");
+        cluster_sync();
+        if (first < nitems) {
+            const Tile t = tile_at(a, first / mgroups, ntiles);
+            const int nb = (first % mgroups) * MT;
+            T *y = static_cast<T *>(a.y);
+            for (int i = threadIdx.x; i < (t.rows - krank + nsplit - 1) / nsplit * (MT / 4); i += TC_THREADS) {
+                const int r = krank + i / (MT / 4) * nsplit, n = nb + i % (MT / 4) * 4;
+                const uint32_t at = x0 + static_cast<uint32_t>(r * MT + n - nb) * 4u;
+                float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+                for (int k = 0; k < nsplit; ++k) {
+                    const float4 o = ld_dsmem_f32x4(mapa_shared(at, k));
+                    v.x += o.x;
+                    v.y += o.y;
+                    v.z += o.z;
+                    v.w += o.w;
+                }
+                const float xs = a.xs[t.row0 + r];
+                const float *ws = a.ws + static_cast<size_t>(t.expert) * a.N;
+                const float f[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                    if (n + j < a.N) put(y + static_cast<size_t>(t.row0 + r) * a.N + n + j, f[j] * xs * ws[n + j]);
+            }
+        }
+    }
+    if (CL > 1 || nsplit > 1) cluster_sync();  // no CTA leaves while another's copies, releases or reads may reach it
     if (warp == MMA_WARP) {
         tc_fence_after();
         if (CL > 1) asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, 512;" ::"r"(tmem) : "memory");
@@ -664,10 +705,16 @@ bool encode(CUtensorMap *map, CUtensorMapDataType type, int elem, const void *p,
            CUDA_SUCCESS;
 }
 
-// Row tile: 192 where the experts have more than a small tile of rows on
-// average, 64 (single CTAs, a deep ring of weights) where the product is
-// bound by reading the weights.
-int pick_nt(int R, int n) { return R > 64LL * n ? 192 : 64; }
+// Row tile: 64 (single CTAs, a deep ring of weights) where the product is
+// bound by reading the weights or its tiles fit the device at once, 192
+// (pairs) beyond.  Measured (us; K = 4096), 64 against 192: one matrix of
+// 8192, 128 rows 18.9 / 20.8, 192 rows 29.2 / 24.0; of 1536, 512 rows 18.8 /
+// 24.3; 128 experts of 1536, 32 rows each 157 / 170, 64 rows 199 / 186.
+int pick_nt(int R, int n, bool one, int mtiles, int sms)
+{
+    const long long tiles = one ? (R + 63) / 64 : most_tiles(R, n, 64);
+    return R <= 48LL * n || tiles * mtiles <= sms ? 64 : 192;
+}
 
 struct Layout {
     size_t tiles, xss, x16, total;
@@ -683,16 +730,17 @@ Layout layout(int R, int n, int K)
     return l;
 }
 
-// Clusters of a kernel that the current device holds at once (a cluster's
-// CTAs share a GPC, so this may be fewer than its SMs divided), looked up
-// once per kernel type and device; 0 if unknown.
+// Clusters of `csize` (2, 4 or 8) CTAs of a kernel that the current device
+// holds at once (a cluster's CTAs share a GPC, so this may be fewer than its
+// SMs divided), looked up once per kernel type and device; 0 if unknown.
 template <typename K>
 int resident_clusters(K kernel, int csize, size_t smem)
 {
-    static std::atomic<int> cache[64];
+    static std::atomic<int> cache[64][3];
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return 0;
-    int n = cache[dev].load(std::memory_order_relaxed);
+    std::atomic<int> &slot = cache[dev][csize == 2 ? 0 : (csize == 4 ? 1 : 2)];
+    int n = slot.load(std::memory_order_relaxed);
     if (n != 0) return n > 0 ? n : 0;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(static_cast<unsigned>(csize));
@@ -709,26 +757,37 @@ int resident_clusters(K kernel, int csize, size_t smem)
         (void)cudaGetLastError();
         n = -1;
     }
-    cache[dev].store(n, std::memory_order_relaxed);
+    slot.store(n, std::memory_order_relaxed);
     return n > 0 ? n : 0;
 }
 
 template <typename T, int NT>
-cudaError_t launch_tc(const TcArgs &a, long long most_items, int sms, cudaStream_t stream)
+cudaError_t launch_tc(const TcArgs &args, long long most_items, int sms, cudaStream_t stream)
 {
     using F = Form<NT>;
     constexpr size_t smem = tc_smem<NT>();
     auto k = q8_tc<T, NT>;
     cudaError_t e = ensure_dynamic_smem(k, smem);
     if (e != cudaSuccess) return e;
-    long long clusters = sms / F::CL;
+    // few items: their K ranges are split over clusters of 2, 4 or 8 CTAs,
+    // as many as the device holds at once, each at least two chunks
+    int size = F::CL;
+    if (F::CL == 1)
+        for (int s = 8; s > 1; s /= 2)
+            if (most_items * s <= sms && (args.K + 127) / 128 >= 2 * s && most_items <= resident_clusters(k, s, smem)) {
+                size = s;
+                break;
+            }
+    TcArgs a = args;
+    a.nsplit = F::CL > 1 ? 1 : size;
+    long long clusters = sms / size;
     if (F::CL > 1) {
         const int fit = resident_clusters(k, F::CL, smem);
         if (fit > 0 && fit < clusters) clusters = fit;
     }
     if (most_items < clusters) clusters = most_items;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(static_cast<unsigned>(clusters * F::CL));
+    cfg.gridDim = dim3(static_cast<unsigned>(clusters * size));
     cfg.blockDim = dim3(TC_THREADS);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = stream;
@@ -736,11 +795,11 @@ cudaError_t launch_tc(const TcArgs &a, long long most_items, int sms, cudaStream
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     attr[1].id = cudaLaunchAttributeClusterDimension;
-    attr[1].val.clusterDim.x = F::CL;
+    attr[1].val.clusterDim.x = static_cast<unsigned>(size);
     attr[1].val.clusterDim.y = 1;
     attr[1].val.clusterDim.z = 1;
     cfg.attrs = attr;
-    cfg.numAttrs = F::CL > 1 ? 2 : 1;
+    cfg.numAttrs = size > 1 ? 2 : 1;
     return cudaLaunchKernelEx(&cfg, k, a);
 }
 
@@ -755,7 +814,8 @@ cudaError_t launch_q8_tc(const Q8Call &c, void *workspace, cudaStream_t stream)
     if (!dev || !status) return cudaErrorInvalidDevice;
     char *ws = static_cast<char *>(workspace);
     const Layout l = layout(c.R, c.n, c.K);
-    const int nt = pick_nt(c.R, c.n), cl = nt == 192 ? Form<192>::CL : Form<64>::CL, unit = 16 * cl;
+    const int mtiles = (c.N + MT - 1) / MT;
+    const int nt = pick_nt(c.R, c.n, !c.offsets, mtiles, dev->sm_count), cl = nt == 192 ? Form<192>::CL : Form<64>::CL, unit = 16 * cl;
     const int max_tiles = most_tiles(c.R, c.n, nt);
     int *ntiles = reinterpret_cast<int *>(ws);
     Tile *tiles = reinterpret_cast<Tile *>(ws + l.tiles);
@@ -786,7 +846,7 @@ cudaError_t launch_q8_tc(const Q8Call &c, void *workspace, cudaStream_t stream)
     a.N = c.N;
     a.K = c.K;
     a.step = step;
-    a.mtiles = (c.N + MT - 1) / MT;
+    a.mtiles = mtiles;
     const long long most = static_cast<long long>(c.offsets ? max_tiles : nd) * ((a.mtiles + cl - 1) / cl);
     if (c.dtype == SMOE_BF16)
         return nt == 192 ? launch_tc<__nv_bfloat16, 192>(a, most, dev->sm_count, stream)
