@@ -632,7 +632,8 @@ int smoe_quantize_rows_q8(const void *x, int dtype, int act, int rows,
  * and y 16-byte aligned.  The integer products are exact; their sums are
  * taken in 32 bits (integer, or f32 on the tensor cores: exact up to 2^24).
  * workspace: smoe_matmul_q8_workspace_bytes(...) bytes, 16-byte aligned,
- * contents unspecified before and after.
+ * contents unspecified before and after; the size does not fall as n_rows
+ * grows, so that the largest batch's serves every smaller one.
  */
 size_t smoe_matmul_q8_workspace_bytes(int n_rows, int n_out, int n_in);
 int smoe_matmul_q8(const int8_t *xq, const float *x_scales, int n_rows,

@@ -331,12 +331,12 @@ cudaError_t launch_quantize_rows(const void *x, int dtype, bool act, int rows, i
 // 42.9, 64 rows 62.1 / 58.4.
 static bool on_tensor_cores(int R, int n, int K) { return K > 0 && R > 2 && R > 3LL * n / 8; }
 
-size_t q8_workspace(int nsrc, int R, int n, int N, int K)
+// Enough for either form, so that a larger batch never needs less.
+size_t q8_workspace(int R, int n, int K)
 {
-    (void)nsrc;
-    (void)N;
-    if (on_tensor_cores(R, n, K)) return q8_tc_workspace(R, n, K);
-    return up256(16 + static_cast<size_t>(most_tiles(R, n, DOT_ROWS)) * sizeof(Tile));
+    const size_t dots = up256(16 + static_cast<size_t>(most_tiles(R, n, DOT_ROWS)) * sizeof(Tile));
+    const size_t tensor = q8_tc_workspace(R, n, K);
+    return dots > tensor ? dots : tensor;
 }
 
 cudaError_t launch_q8(const int8_t *xq, const float *xs, int nsrc, const int *order, int k, const int *offsets, int R,
