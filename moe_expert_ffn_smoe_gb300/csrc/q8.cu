@@ -15,8 +15,6 @@ namespace {
 
 // ---------------------------------------------------------------- quantiser
 
-constexpr int QUANT_THREADS = 256;
-
 // The VE values at column c of row r: x itself, or silu(gate) * up of a row
 // [gate | up] of 2 cols.
 template <typename T, int VE, bool ACT>
@@ -34,6 +32,50 @@ __device__ __forceinline__ void quant_values(const T *row, int cols, int c, floa
         for (int i = 0; i < VE; ++i) v[i] = silu_f32(v[i]) * u[i];
     }
 }
+
+// Magnitudes as f32 bit patterns: their order is the integers', and a NaN or
+// an infinity is above every finite one.
+template <int VE>
+__device__ __forceinline__ uint32_t magnitude(const float (&v)[VE])
+{
+    uint32_t m = 0u;
+#pragma unroll
+    for (int i = 0; i < VE; ++i) m = max(m, __float_as_uint(v[i]) & 0x7fffffffu);
+    return m;
+}
+
+// What a thread keeps of a vector between the two passes over its row: the
+// loaded words, or the values of the activation.
+template <typename T, int VE, bool ACT>
+struct Held {
+    float v[VE];
+    __device__ __forceinline__ void load(const T *row, int cols, int c) { quant_values<T, VE, ACT>(row, cols, c, v); }
+    __device__ __forceinline__ void clear()
+    {
+#pragma unroll
+        for (int i = 0; i < VE; ++i) v[i] = 0.f;
+    }
+    __device__ __forceinline__ uint32_t most() const { return magnitude<VE>(v); }
+    __device__ __forceinline__ void get(float (&o)[VE]) const
+    {
+#pragma unroll
+        for (int i = 0; i < VE; ++i) o[i] = v[i];
+    }
+};
+template <>
+struct Held<__nv_bfloat16, 8, false> {
+    RowVec<__nv_bfloat16, 8> r;
+    __device__ __forceinline__ void load(const __nv_bfloat16 *row, int, int c) { r.load(row + c); }
+    __device__ __forceinline__ void clear() { r.zero(); }
+    // the same order holds for bf16's bits, two at a time
+    __device__ __forceinline__ uint32_t most() const
+    {
+        const uint32_t m = __vmaxu2(__vmaxu2(r.raw.x & 0x7fff7fffu, r.raw.y & 0x7fff7fffu),
+                                    __vmaxu2(r.raw.z & 0x7fff7fffu, r.raw.w & 0x7fff7fffu));
+        return max(m & 0xffff0000u, m << 16);
+    }
+    __device__ __forceinline__ void get(float (&o)[8]) const { r.get(o); }
+};
 
 // The code of a scaled value |p| <= 127.5 in the low byte: adding 1.5 2^23
 // rounds p to an integer, ties to even, in the lowest mantissa bits.
@@ -54,49 +96,43 @@ __device__ __forceinline__ void put_codes(int8_t *q, const uint32_t (&c)[8])
 __device__ __forceinline__ void put_codes(int8_t *q, const uint32_t (&c)[4]) { *reinterpret_cast<uint32_t *>(q) = pack4(c); }
 __device__ __forceinline__ void put_codes(int8_t *q, const uint32_t (&c)[1]) { *q = static_cast<int8_t>(c[0]); }
 
-// One CTA per row: the largest magnitude, then the rounding.  A thread keeps
-// its first NV vectors in registers, so that a row of up to NV x 256 vectors
-// is read (and its activation computed) once; what is beyond is read again.
-// Bound by reading x; measured against reading every row twice: 2047 rows of
-// 4096 bf16 (table in the design notes).
-template <typename T, int VE, bool ACT>
-__global__ void __launch_bounds__(QUANT_THREADS) quantize_rows(const T *__restrict__ x, int cols, int8_t *__restrict__ q,
-                                                               float *__restrict__ scales)
+// One CTA of THREADS per row: the largest magnitude, then the rounding.  A
+// thread keeps its first NV vectors, so that a row of up to NV x THREADS
+// vectors is read (and its activation computed) once; what is beyond is read
+// again.  Bound by instruction issue: with two warps a row instead of eight
+// the row's own work (reductions, two divisions) is done fewer times, which
+// pays once there are rows for the whole device (4096 rows of 4096 bf16 9
+// against 13.6 us); a single row is faster on eight (1.6 us).
+template <typename T, int VE, bool ACT, int THREADS>
+__global__ void __launch_bounds__(THREADS) quantize_rows(const T *__restrict__ x, int cols, int8_t *__restrict__ q,
+                                                         float *__restrict__ scales)
 {
-    constexpr int NV = 32 / VE < 8 ? 32 / VE : 8;
-    __shared__ uint32_t warp_max[QUANT_THREADS / 32];
+    constexpr int NV = VE == 1 ? 8 : (THREADS == 64 && !ACT ? 64 / VE : 32 / VE);
+    __shared__ uint32_t warp_most[THREADS / 32];
     pdl_launch_dependents();
     pdl_wait();
     const size_t r = blockIdx.x;
     const T *row = x + r * cols * (ACT ? 2 : 1);
     const int c0 = threadIdx.x * VE;
-    float held[NV][VE];
+    Held<T, VE, ACT> held[NV];
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-        if (c0 + i * QUANT_THREADS * VE < cols) quant_values<T, VE, ACT>(row, cols, c0 + i * QUANT_THREADS * VE, held[i]);
-        else {
-#pragma unroll
-            for (int j = 0; j < VE; ++j) held[i][j] = 0.f;
-        }
+        if (c0 + i * THREADS * VE < cols) held[i].load(row, cols, c0 + i * THREADS * VE);
+        else held[i].clear();
     }
-    // magnitudes as bit patterns: their order is the integers', and a NaN or
-    // an infinity is above every finite one
     uint32_t most = 0u;
 #pragma unroll
-    for (int i = 0; i < NV; ++i)
-#pragma unroll
-        for (int j = 0; j < VE; ++j) most = max(most, __float_as_uint(held[i][j]) & 0x7fffffffu);
-    for (int c = c0 + NV * QUANT_THREADS * VE; c < cols; c += QUANT_THREADS * VE) {
+    for (int i = 0; i < NV; ++i) most = max(most, held[i].most());
+    for (int c = c0 + NV * THREADS * VE; c < cols; c += THREADS * VE) {
         float v[VE];
         quant_values<T, VE, ACT>(row, cols, c, v);
-#pragma unroll
-        for (int j = 0; j < VE; ++j) most = max(most, __float_as_uint(v[j]) & 0x7fffffffu);
+        most = max(most, magnitude<VE>(v));
     }
     most = __reduce_max_sync(FULL_MASK, most);
-    if ((threadIdx.x & 31) == 0) warp_max[threadIdx.x >> 5] = most;
+    if ((threadIdx.x & 31) == 0) warp_most[threadIdx.x >> 5] = most;
     __syncthreads();
 #pragma unroll
-    for (int i = 0; i < QUANT_THREADS / 32; ++i) most = max(most, warp_max[i]);
+    for (int i = 0; i < THREADS / 32; ++i) most = max(most, warp_most[i]);
     // a row of zeros has scale 0; a row that is not finite scale NaN and
     // codes 0, so that every product of it is NaN
     const bool bad = most >= 0x7f800000u;
@@ -104,7 +140,8 @@ __global__ void __launch_bounds__(QUANT_THREADS) quantize_rows(const T *__restri
     const float up = bad || most == 0u ? 0.f : __fdiv_rn(127.f, top);
     if (threadIdx.x == 0) scales[r] = bad ? __int_as_float(0x7fffffff) : __fdiv_rn(top, 127.f);
     const bool plain = !bad && up < INFINITY;  // 127 / top overflows below 4e-37: those codes saturate
-    auto codes = [&](const float (&v)[VE], uint32_t (&k)[VE]) {
+    auto store = [&](const float (&v)[VE], int c) {
+        uint32_t k[VE];
         if (plain) {
 #pragma unroll
             for (int j = 0; j < VE; ++j) k[j] = code_bits(v[j], up);
@@ -113,21 +150,20 @@ __global__ void __launch_bounds__(QUANT_THREADS) quantize_rows(const T *__restri
             for (int j = 0; j < VE; ++j)
                 k[j] = bad || v[j] == 0.f ? 0u : static_cast<uint32_t>(v[j] > 0.f ? 127 : -127);
         }
+        put_codes(q + r * cols + c, k);
     };
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-        const int c = c0 + i * QUANT_THREADS * VE;
+        const int c = c0 + i * THREADS * VE;
         if (c >= cols) break;
-        uint32_t k[VE];
-        codes(held[i], k);
-        put_codes(q + r * cols + c, k);
-    }
-    for (int c = c0 + NV * QUANT_THREADS * VE; c < cols; c += QUANT_THREADS * VE) {
         float v[VE];
-        uint32_t k[VE];
+        held[i].get(v);
+        store(v, c);
+    }
+    for (int c = c0 + NV * THREADS * VE; c < cols; c += THREADS * VE) {
+        float v[VE];
         quant_values<T, VE, ACT>(row, cols, c, v);
-        codes(v, k);
-        put_codes(q + r * cols + c, k);
+        store(v, c);
     }
 }
 
@@ -297,8 +333,12 @@ __global__ void __launch_bounds__(DOT_WARPS * 32, 2) q8_dot(const Q8Args a)
 template <typename T, int VE, bool ACT>
 cudaError_t quant_t(const void *x, int rows, int cols, int8_t *q, float *scales, cudaStream_t stream)
 {
-    return launch_pdl(quantize_rows<T, VE, ACT>, dim3(static_cast<unsigned>(rows)), dim3(QUANT_THREADS), 0, stream,
-                      static_cast<const T *>(x), cols, q, scales);
+    const DeviceInfo *dev = device_info();
+    if (!dev) return cudaErrorInvalidDevice;
+    const dim3 grid(static_cast<unsigned>(rows));
+    if (rows >= 4 * dev->sm_count)
+        return launch_pdl(quantize_rows<T, VE, ACT, 64>, grid, dim3(64), 0, stream, static_cast<const T *>(x), cols, q, scales);
+    return launch_pdl(quantize_rows<T, VE, ACT, 256>, grid, dim3(256), 0, stream, static_cast<const T *>(x), cols, q, scales);
 }
 
 template <typename T, int VE>

@@ -103,7 +103,8 @@ template <int V>
 __global__ void __launch_bounds__(TOPK_WARPS * 32) topk_rows_warp(const float *__restrict__ logits, int T, int n, int ld,
                                                                   int k, int *__restrict__ idx, float *__restrict__ w)
 {
-    __shared__ uint2 left[TOPK_WARPS][32];  // key, expert
+    __shared__ __align__(16) uint32_t left_key[TOPK_WARPS][32];  // in expert order, then zeros
+    __shared__ uint16_t left_exp[TOPK_WARPS][32];
     const int wi = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int t = blockIdx.x * TOPK_WARPS + wi;
     pdl_launch_dependents();
@@ -119,14 +120,7 @@ __global__ void __launch_bounds__(TOPK_WARPS * 32) topk_rows_warp(const float *_
         uint32_t most = key[0];
 #pragma unroll
         for (int i = 1; i < V; ++i) most = max(most, key[i]);
-        uint32_t bound = 0u, first = 0u;
-        for (int r = 0; r < k; ++r) {
-            const uint32_t top = __reduce_max_sync(FULL_MASK, most);
-            if (top == 0u) break;  // every lane's maximum is among them
-            if (r == 0) first = top;
-            bound = top;
-            if (most == top) most = 0u;
-        }
+        const uint32_t first = __reduce_max_sync(FULL_MASK, most);
         if (first == kKeyNegInf) {  // nothing but masked experts
             if (lane < k) {
                 idx[lane] = -1;
@@ -134,31 +128,49 @@ __global__ void __launch_bounds__(TOPK_WARPS * 32) topk_rows_warp(const float *_
             }
             return;
         }
+        uint32_t bound = first;
+        if (most == first) most = 0u;
+#pragma unroll 4
+        for (int r = 1; r < k; ++r) {
+            const uint32_t top = __reduce_max_sync(FULL_MASK, most);
+            if (top != 0u) bound = top;  // 0: every lane's maximum is among them
+            if (most == top) most = 0u;
+        }
         int count = 0;
         const uint32_t before = (1u << lane) - 1u;
+        left_key[wi][lane] = 0u;
+        __syncwarp();
 #pragma unroll
         for (int i = 0; i < V; ++i) {
             const bool in = key[i] >= bound;
             const uint32_t m = __ballot_sync(FULL_MASK, in);
             const int at = count + __popc(m & before);
-            if (in && at < 32) left[wi][at] = make_uint2(key[i], static_cast<uint32_t>(i * 32 + lane));
+            if (in && at < 32) {
+                left_key[wi][at] = key[i];
+                left_exp[wi][at] = static_cast<uint16_t>(i * 32 + lane);
+            }
             count += __popc(m);
         }
         if (count <= 32) {
             __syncwarp();
-            const uint2 mine = lane < count ? left[wi][lane] : make_uint2(0u, 0u);
-            int rank = lane < count ? 0 : 32;
-            for (int c = 0; c < count; ++c) {
-                const uint32_t o = left[wi][c].x;
-                rank += c < lane ? o >= mine.x : o > mine.x;
+            // a candidate's rank: the larger ones, and of the equal ones those
+            // before it (in expert order)
+            const uint32_t mine = left_key[wi][lane];
+            int rank = 0;
+            for (int c = 0; c < count; c += 4) {
+                const uint4 o = *reinterpret_cast<const uint4 *>(&left_key[wi][c]);
+                rank += o.x >= mine + (c >= lane ? 1u : 0u);
+                rank += o.y >= mine + (c + 1 >= lane ? 1u : 0u);
+                rank += o.z >= mine + (c + 2 >= lane ? 1u : 0u);
+                rank += o.w >= mine + (c + 3 >= lane ? 1u : 0u);
             }
-            const bool sel = rank < k, there = sel && mine.x != kKeyNegInf;
-            const float x = there ? expf(value_of_key(mine.x) - value_of_key(first)) : 0.f;
+            const bool sel = lane < count && rank < k, there = sel && mine != kKeyNegInf;
+            const float x = there ? expf(value_of_key(mine) - value_of_key(first)) : 0.f;
             float sum = x;
 #pragma unroll
             for (int off = 16; off > 0; off >>= 1) sum += __shfl_xor_sync(FULL_MASK, sum, off);
             if (sel) {
-                idx[rank] = there ? static_cast<int>(mine.y) : -1;
+                idx[rank] = there ? static_cast<int>(left_exp[wi][lane]) : -1;
                 w[rank] = there ? x / sum : 0.f;
             }
             return;
@@ -366,7 +378,11 @@ __global__ void __launch_bounds__(SORT_THREADS) sort_place(const int *__restrict
         for (int i = tid; i <= n; i += SORT_THREADS) offsets[i] = first[i];
     if (a >= R) return;
     int rank = 0;
-    for (int i = 0; i < tid; ++i) rank += mine[i] == e;
+    for (int i = 0; i < (tid >> 2); ++i) {
+        const int4 o = reinterpret_cast<const int4 *>(mine)[i];
+        rank += (o.x == e) + (o.y == e) + (o.z == e) + (o.w == e);
+    }
+    for (int i = tid & ~3; i < tid; ++i) rank += mine[i] == e;
     const int row = first[e] + hist[static_cast<size_t>(blockIdx.x) * (n + 1) + e] + rank;
     order[row] = static_cast<int>(a);
     place[a] = e < n ? row : -1 - row;
