@@ -210,16 +210,6 @@ __device__ __forceinline__ uint2 lds64v(uint32_t addr)
     return v;
 }
 
-// L2 prefetch of one box of a 2-D tensor map at (x bytes, y rows); parts
-// outside the tensor are skipped.  x must be a multiple of 16.
-__device__ __forceinline__ void tma_prefetch_2d(const CUtensorMap *map, int x, int y)
-{
-    asm volatile("cp.async.bulk.prefetch.tensor.2d.L2.global.tile [%0, {%1, %2}];" ::"l"(
-                     reinterpret_cast<uint64_t>(map)),
-                 "r"(x), "r"(y)
-                 : "memory");
-}
-
 // L2 prefetch of `bytes` (a multiple of 16) from a 16-byte aligned global address.
 __device__ __forceinline__ void bulk_prefetch_l2(const void *src, uint32_t bytes)
 {

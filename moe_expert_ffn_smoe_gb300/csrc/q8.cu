@@ -239,7 +239,9 @@ struct Q8Args {
 // columns of each per lane and step.  A warp walks its groups of 4 rows as
 // one sequence of steps, the weights of the next DEPTH steps in flight
 // across the groups' ends.  Bound by streaming the weights; for one matrix
-// (tiles null) they are asked for before the previous kernel is waited for.
+// (tiles null) the first group's are brought into L2 while the previous
+// kernel ends (a prefetch only: that kernel may be the one that quantises
+// these weights).
 template <typename T>
 __global__ void __launch_bounds__(DOT_WARPS * 32, 2) q8_dot(const Q8Args a)
 {
@@ -248,10 +250,10 @@ __global__ void __launch_bounds__(DOT_WARPS * 32, 2) q8_dot(const Q8Args a)
     const int lane = threadIdx.x & 31;
     int n0 = (blockIdx.y * DOT_WARPS + (threadIdx.x >> 5)) * DOT_OUTS;  // the group being summed
     const int stride = gridDim.y * DOT_WARPS * DOT_OUTS;
-    if (a.tiles) {
-        pdl_wait();
-        if (static_cast<int>(blockIdx.x) >= *a.ntiles) return;
-    }
+    if (!a.tiles && lane < DOT_OUTS && n0 + lane < a.N && a.K > 0)
+        prefetch_l2(a.wq + static_cast<size_t>(n0 + lane) * a.K, static_cast<uint32_t>(a.K));
+    pdl_wait();
+    if (a.tiles && static_cast<int>(blockIdx.x) >= *a.ntiles) return;
     const int row0 = blockIdx.x * DOT_ROWS;
     const Tile tile = a.tiles ? a.tiles[blockIdx.x] : Tile{0, row0, min(DOT_ROWS, a.R - row0), 0};
     T *y = static_cast<T *>(a.y);
@@ -277,7 +279,6 @@ __global__ void __launch_bounds__(DOT_WARPS * 32, 2) q8_dot(const Q8Args a)
     };
 #pragma unroll
     for (int i = 0; i < DEPTH; ++i) fetch(wv[i]);
-    if (!a.tiles) pdl_wait();
     int src[DOT_ROWS];
 #pragma unroll
     for (int r = 0; r < DOT_ROWS; ++r)

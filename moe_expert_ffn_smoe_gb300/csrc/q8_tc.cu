@@ -268,9 +268,12 @@ __global__ void __launch_bounds__(TC_THREADS, 1) q8_tc(const __grid_constant__ T
     const int nch = (a.K + 127) / 128;  // weight chunks, two K tiles each (columns past K are zeros)
     const int c0 = krank * nch / nsplit, c1 = (krank + 1) * nch / nsplit;  // this CTA's
     const int mgroups = (a.mtiles + CL - 1) / CL;
-    // the tile list comes from the previous kernel; without one the weights,
-    // which no kernel of this call writes, are asked for at once
-    if (a.tiles || warp != W_WARP) pdl_wait();
+    // One matrix: this CTA's first weight chunks are known, and are brought
+    // into L2 while the previous kernel ends.  A prefetch only: that kernel
+    // may be the one that quantises these weights.
+    if (!a.tiles && warp == W_WARP && first < (a.R + a.step - 1) / a.step * mgroups && lane < WS && c0 + lane < c1)
+        tma_prefetch_2d(&a.wmap, (c0 + lane) * 128, (first % mgroups * CL + rank) * MT);
+    pdl_wait();
     const int ntiles = a.tiles ? *a.ntiles : (a.R + a.step - 1) / a.step;
     const long long nitems = static_cast<long long>(ntiles) * mgroups;
     bool failed = false;

@@ -102,6 +102,16 @@ __device__ __forceinline__ uint4 lds128v(uint32_t addr)
     return v;
 }
 
+// L2 prefetch of one box of a 2-D tensor map at (x bytes, y rows); parts
+// outside the tensor are skipped.  x must be a multiple of 16.
+__device__ __forceinline__ void tma_prefetch_2d(const CUtensorMap *map, int x, int y)
+{
+    asm volatile("cp.async.bulk.prefetch.tensor.2d.L2.global.tile [%0, {%1, %2}];" ::"l"(
+                     reinterpret_cast<uint64_t>(map)),
+                 "r"(x), "r"(y)
+                 : "memory");
+}
+
 // 2-D tensor copy global -> shared of one box at (x bytes, y rows),
 // completing on the mbarrier.  x must be a multiple of 16.
 __device__ __forceinline__ void tma_load_2d(uint32_t dst, const CUtensorMap *map, int x, int y, uint32_t bar)

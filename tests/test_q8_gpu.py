@@ -234,3 +234,82 @@ def test_experts_matmul_reports_bad_orders_and_offsets(smoe):
     smoe.smoe_experts_matmul_q8(x, one, R, order, 1, off, R, E, w, one, N, K, y, 0, wsp, need)
     assert smoe.smoe_last_device_status() == smoe.SMOE_ERR_ROUTE
     assert torch.equal(y[:10], torch.full((10, N), float(K), device="cuda"))
+
+
+@pytest.mark.parametrize("R", [1, 40, 400])
+def test_weights_quantised_just_before_their_product(smoe, R):
+    """The product's kernels start early; none may read weights that the
+    quantiser in front of it is still writing."""
+    N, K = 4096, 4096
+    g = torch.Generator(device="cuda").manual_seed(R)
+    x = torch.randn(R, K, generator=g, device="cuda")
+    xq, xs = torch.empty(R, K, dtype=torch.int8, device="cuda"), torch.empty(R, device="cuda")
+    wq, ws = torch.empty(N, K, dtype=torch.int8, device="cuda"), torch.empty(N, device="cuda")
+    need = smoe.smoe_matmul_q8_workspace_bytes(R, N, K)
+    wsp = torch.empty(need, dtype=torch.uint8, device="cuda")
+    w = [torch.randn(N, K, generator=g, device="cuda") for _ in range(4)]
+    y = [torch.empty(R, N, device="cuda") for _ in range(12)]
+    smoe.smoe_quantize_rows_q8(x, 0, 0, R, K, xq, xs)
+    torch.cuda.synchronize()
+    for i, out in enumerate(y):
+        smoe.smoe_quantize_rows_q8(w[i % 4], 0, 0, N, K, wq, ws)
+        if i % 2:
+            smoe.smoe_quantize_rows_q8(x, 0, 0, R, K, xq, xs)
+        smoe.smoe_matmul_q8(xq, xs, R, wq, ws, N, K, out, 0, wsp, need)
+    torch.cuda.synchronize()
+    for i in range(4):
+        smoe.smoe_quantize_rows_q8(w[i], 0, 0, N, K, wq, ws)
+        torch.cuda.synchronize()
+        smoe.smoe_matmul_q8(xq, xs, R, wq, ws, N, K, y[i], 0, wsp, need)
+        torch.cuda.synchronize()
+        for j in (4 + i, 8 + i):
+            assert torch.equal(y[j], y[i])
+
+
+@pytest.mark.parametrize("R", [40, 2000])
+def test_experts_weights_past_32_bits(smoe, R):
+    """4.4 GB of weights: the last expert's rows against float64."""
+    E, N, K = 130, 8200, 4096
+    wq = torch.zeros(E * N, K, dtype=torch.int8, device="cuda")
+    g = torch.Generator(device="cuda").manual_seed(R)
+    last = torch.randint(-127, 128, (N, K), generator=g, device="cuda").to(torch.int8)
+    wq[(E - 1) * N:] = last
+    ws = torch.ones(E * N, device="cuda")
+    xq = torch.randint(-127, 128, (R, K), generator=g, device="cuda").to(torch.int8)
+    xs = torch.ones(R, device="cuda")
+    off = torch.zeros(E + 1, dtype=torch.int32, device="cuda")
+    off[E] = R
+    y = torch.empty(R, N, device="cuda")
+    need = smoe.smoe_experts_matmul_q8_workspace_bytes(R, R, E, N, K)
+    wsp = torch.empty(need, dtype=torch.uint8, device="cuda")
+    smoe.smoe_experts_matmul_q8(xq, xs, R, None, 1, off, R, E, wq, ws, N, K, y, 0, wsp, need)
+    torch.cuda.synchronize()
+    ref = xq.double() @ last.double().t()
+    mag = xq.double().abs() @ last.double().abs().t()
+    assert ((y.double() - ref).abs() <= (K / 16 + 16) * U * mag).all()
+
+
+def test_matmul_rows_past_32_bits(smoe):
+    """Outputs past 4 GB."""
+    R, N, K = 33000, 33000, 64
+    g = torch.Generator(device="cuda").manual_seed(1)
+    xq = torch.randint(-127, 128, (R, K), generator=g, device="cuda").to(torch.int8)
+    wq = torch.randint(-127, 128, (N, K), generator=g, device="cuda").to(torch.int8)
+    one = torch.ones(R, device="cuda")
+    y = torch.empty(R, N, device="cuda")
+    need = smoe.smoe_matmul_q8_workspace_bytes(R, N, K)
+    wsp = torch.empty(need, dtype=torch.uint8, device="cuda")
+    smoe.smoe_matmul_q8(xq, one, R, wq, one, N, K, y, 0, wsp, need)
+    torch.cuda.synchronize()
+    for at in (0, R // 2, R - 100):
+        ref = xq[at:at + 100].double() @ wq.double().t()
+        assert torch.equal(y[at:at + 100].double(), ref)  # below 2^24: exact
+
+
+def test_workspace_does_not_fall_as_the_batch_grows(smoe):
+    for E in (1, 8, 128):
+        last = 0
+        for R in (1, 2, 3, 5, 40, 48, 49, 64, 65, 400, 5000, 6145, 20000):
+            need = smoe.smoe_experts_matmul_q8_workspace_bytes(R, R, E, 256, 256)
+            assert need >= last
+            last = need

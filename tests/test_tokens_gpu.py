@@ -362,3 +362,38 @@ def test_side_stream_and_graph(smoe):
         # weights that sum to one on copies of the row give the row back
         ref = x.double()
         assert ((out.double() - ref).abs() <= U * 32 * ref.abs()).all()
+
+
+@pytest.mark.parametrize("T,k,E", [(3000, 4, 8192), (1024, 4, 64), (1025, 4, 64), (70000, 2, 33)])
+def test_sort_of_many(smoe, T, k, E):
+    """Many buckets, the last size of the one-launch dispatch and the first
+    beyond it, many chunks."""
+    for kind in ("all", "dropped"):
+        idx = _indices(T, k, min(E, 64), 12, kind) if E <= 64 else _indices(T, k, E, 12, kind)
+        offsets, order, place, _ = _dispatch(smoe, idx, E)
+        ro, rr, rp = _sort_ref(idx, E)
+        np.testing.assert_array_equal(offsets.cpu().numpy(), ro)
+        np.testing.assert_array_equal(order.cpu().numpy(), rr)
+        np.testing.assert_array_equal(place.cpu().numpy().reshape(-1), rp)
+
+
+def test_rows_past_32_bits(smoe):
+    """5.3 GB of sorted rows: out and back."""
+    T, k, E, d = 8200, 8, 16, 40000
+    idx = _indices(T, k, E, 13, "all")
+    g = torch.Generator(device="cuda").manual_seed(13)
+    x = torch.randn(T, d, generator=g, device="cuda").to(torch.bfloat16)
+    offsets, order, place, xs = _dispatch(smoe, idx, E, x, "bf16")
+    for at in (0, T * k // 2, T * k - 64):
+        assert torch.equal(xs[at:at + 64], x[order[at:at + 64].long() // k])
+    w = torch.full((T, k), 1 / k, device="cuda")
+    out = torch.empty(T, d, dtype=torch.bfloat16, device="cuda")
+    smoe.smoe_combine_tokens(xs, 1, place, w, T, k, d, out)
+    assert torch.equal(out, x)  # eight eighths of a bf16 are exact
+    d_ys, d_w = torch.empty_like(xs), torch.empty(T, k, device="cuda")
+    smoe.smoe_combine_tokens_backward(x, xs, 1, place, w, T, k, d, d_ys, d_w)
+    torch.cuda.synchronize()
+    at = T * k - 64
+    assert torch.equal(d_ys[at:], (x[order[at:].long() // k].float() / k).to(torch.bfloat16))
+    ref = (x.double() ** 2).sum(1)
+    assert ((d_w.double() - ref[:, None]).abs() <= U * (d / 32 + 7) * ref[:, None]).all()
