@@ -42,6 +42,7 @@ if not os.path.exists(LIB_PATH):
         "(the library has no CPU fallback)")
 
 _lib = ctypes.CDLL(LIB_PATH)
+from . import _binding  # noqa: E402  (the same library, arguments marshalled in C)
 
 SMOE_OK = 0
 SMOE_ERR_NULL = 1
@@ -155,6 +156,9 @@ def _stream(s):
     if isinstance(s, int):
         return s
     return s.cuda_stream
+
+
+_binding.set_current_stream(_current_stream)
 
 
 def _check(status, where):
@@ -409,13 +413,13 @@ SMOE_Q8_SILU_MUL = 1
 def smoe_topk_rows(logits, n_tokens, n_experts, ld, k, top_idx, top_w, stream=None):
     """The k largest logits of each row (pitch ld floats) and their softmax
     weights; -inf is an expert that is off (index -1, weight 0)."""
-    _check(_lib.smoe_topk_rows(_ptr(logits), n_tokens, n_experts, ld, k, _ptr(top_idx), _ptr(top_w),
-                               _stream(stream)), "smoe_topk_rows")
+    _check(_binding.smoe_topk_rows(logits, n_tokens, n_experts, ld, k, top_idx, top_w,
+                                   stream), "smoe_topk_rows")
 
 
 def smoe_topk_rows_backward(top_idx, top_w, d_top_w, n_tokens, n_experts, k, d_logits, stream=None):
-    _check(_lib.smoe_topk_rows_backward(_ptr(top_idx), _ptr(top_w), _ptr(d_top_w), n_tokens, n_experts, k,
-                                        _ptr(d_logits), _stream(stream)), "smoe_topk_rows_backward")
+    _check(_binding.smoe_topk_rows_backward(top_idx, top_w, d_top_w, n_tokens, n_experts, k, d_logits,
+                                            stream), "smoe_topk_rows_backward")
 
 
 def smoe_dispatch_workspace_bytes(n_tokens, k, n_experts):
@@ -427,33 +431,32 @@ def smoe_dispatch_tokens(top_idx, n_tokens, k, n_experts, x, dtype, d_model, off
     """Sorts the slots by expert (offsets, order, place) and brings the rows
     of x into that order (x and xs None: the sort alone).  dtype: SMOE_F32 or
     SMOE_BF16, of x and xs."""
-    _check(_lib.smoe_dispatch_tokens(_ptr(top_idx), n_tokens, k, n_experts, _ptr(x), dtype, d_model,
-                                     _ptr(offsets), _ptr(order), _ptr(place), _ptr(xs), _ptr(workspace),
-                                     workspace_bytes, _stream(stream)), "smoe_dispatch_tokens")
+    _check(_binding.smoe_dispatch_tokens(top_idx, n_tokens, k, n_experts, x, dtype, d_model, offsets, order,
+                                         place, xs, workspace, workspace_bytes,
+                                         stream), "smoe_dispatch_tokens")
 
 
 def smoe_dispatch_tokens_backward(d_xs, dtype, place, n_tokens, k, d_model, d_x, stream=None):
-    _check(_lib.smoe_dispatch_tokens_backward(_ptr(d_xs), dtype, _ptr(place), n_tokens, k, d_model, _ptr(d_x),
-                                              _stream(stream)), "smoe_dispatch_tokens_backward")
+    _check(_binding.smoe_dispatch_tokens_backward(d_xs, dtype, place, n_tokens, k, d_model, d_x,
+                                                  stream), "smoe_dispatch_tokens_backward")
 
 
 def smoe_combine_tokens(ys, dtype, place, top_w, n_tokens, k, d_model, out, stream=None):
-    _check(_lib.smoe_combine_tokens(_ptr(ys), dtype, _ptr(place), _ptr(top_w), n_tokens, k, d_model, _ptr(out),
-                                    _stream(stream)), "smoe_combine_tokens")
+    _check(_binding.smoe_combine_tokens(ys, dtype, place, top_w, n_tokens, k, d_model, out,
+                                        stream), "smoe_combine_tokens")
 
 
 def smoe_combine_tokens_backward(d_out, ys, dtype, place, top_w, n_tokens, k, d_model, d_ys, d_top_w,
                                  stream=None):
-    _check(_lib.smoe_combine_tokens_backward(_ptr(d_out), _ptr(ys), dtype, _ptr(place), _ptr(top_w), n_tokens, k,
-                                             d_model, _ptr(d_ys), _ptr(d_top_w), _stream(stream)),
-           "smoe_combine_tokens_backward")
+    _check(_binding.smoe_combine_tokens_backward(d_out, ys, dtype, place, top_w, n_tokens, k, d_model, d_ys,
+                                                 d_top_w, stream), "smoe_combine_tokens_backward")
 
 
 def smoe_quantize_rows_q8(x, dtype, act, rows, cols, q, scales, stream=None):
     """int8 codes and one scale per row of x, or (SMOE_Q8_SILU_MUL) of
     SiLU(gate) * up of rows [gate | up] of 2 cols."""
-    _check(_lib.smoe_quantize_rows_q8(_ptr(x), dtype, act, rows, cols, _ptr(q), _ptr(scales), _stream(stream)),
-           "smoe_quantize_rows_q8")
+    _check(_binding.smoe_quantize_rows_q8(x, dtype, act, rows, cols, q, scales,
+                                          stream), "smoe_quantize_rows_q8")
 
 
 def smoe_matmul_q8_workspace_bytes(n_rows, n_out, n_in):
@@ -462,8 +465,8 @@ def smoe_matmul_q8_workspace_bytes(n_rows, n_out, n_in):
 
 def smoe_matmul_q8(xq, x_scales, n_rows, wq, w_scales, n_out, n_in, y, dtype, workspace, workspace_bytes,
                    stream=None):
-    _check(_lib.smoe_matmul_q8(_ptr(xq), _ptr(x_scales), n_rows, _ptr(wq), _ptr(w_scales), n_out, n_in, _ptr(y),
-                               dtype, _ptr(workspace), workspace_bytes, _stream(stream)), "smoe_matmul_q8")
+    _check(_binding.smoe_matmul_q8(xq, x_scales, n_rows, wq, w_scales, n_out, n_in, y, dtype, workspace,
+                                   workspace_bytes, stream), "smoe_matmul_q8")
 
 
 def smoe_experts_matmul_q8_workspace_bytes(n_src, n_rows, n_experts, n_out, n_in):
@@ -473,10 +476,9 @@ def smoe_experts_matmul_q8_workspace_bytes(n_src, n_rows, n_experts, n_out, n_in
 def smoe_experts_matmul_q8(xq, x_scales, n_src, order, k, offsets, n_rows, n_experts, wq, w_scales, n_out, n_in,
                            y, dtype, workspace, workspace_bytes, stream=None):
     """order None: xq is already in the sorted order."""
-    _check(_lib.smoe_experts_matmul_q8(_ptr(xq), _ptr(x_scales), n_src, _ptr(order), k, _ptr(offsets), n_rows,
-                                       n_experts, _ptr(wq), _ptr(w_scales), n_out, n_in, _ptr(y), dtype,
-                                       _ptr(workspace), workspace_bytes, _stream(stream)),
-           "smoe_experts_matmul_q8")
+    _check(_binding.smoe_experts_matmul_q8(xq, x_scales, n_src, order, k, offsets, n_rows, n_experts, wq,
+                                           w_scales, n_out, n_in, y, dtype, workspace, workspace_bytes,
+                                           stream), "smoe_experts_matmul_q8")
 
 
 def smoe_last_device_status(stream=None):

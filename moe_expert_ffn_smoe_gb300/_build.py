@@ -3,6 +3,8 @@
 Each translation unit is compiled in its own nvcc process (in parallel),
 then linked into one shared library with the CUDA runtime linked
 statically, so loading the library needs no GPU and no libcudart.
+A second module, _binding.so (csrc/binding.c, gcc, linked to libsmoe.so next
+to it), marshals the arguments of the calls that small batches make.
 Set SMOE_PTXAS_VERBOSE=1 to print register and shared-memory use, and
 SMOE_NVCC_EXTRA to pass extra nvcc flags (e.g. -D tuning macros).
 """
@@ -11,6 +13,7 @@ import glob
 import os
 import shutil
 import subprocess
+import sysconfig
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
@@ -18,6 +21,7 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libsmoe.so")
+BINDING = os.path.join(PKG, "_binding.so")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 
@@ -31,14 +35,14 @@ def _sources():
 
 
 def _deps():
-    return (_sources() + glob.glob(os.path.join(CSRC, "*.cuh")) + glob.glob(os.path.join(CSRC, "*.h"))
+    return (_sources() + glob.glob(os.path.join(CSRC, "*.cuh")) + glob.glob(os.path.join(CSRC, "*.c")) + glob.glob(os.path.join(CSRC, "*.h"))
             + glob.glob(os.path.join(INCLUDE, "*.h")) + [os.path.abspath(__file__)])
 
 
 def up_to_date() -> bool:
-    if not os.path.exists(LIB):
+    if not os.path.exists(LIB) or not os.path.exists(BINDING):
         return False
-    t = os.path.getmtime(LIB)
+    t = min(os.path.getmtime(LIB), os.path.getmtime(BINDING))
     return all(os.path.getmtime(d) <= t for d in _deps())
 
 
@@ -72,6 +76,13 @@ def build(force: bool = False, verbose: bool = False) -> str:
     if r.returncode != 0:
         raise RuntimeError(f"link failed:\n{r.stderr}")
     os.replace(tmp, LIB)
+    tmp = BINDING + ".tmp"
+    cmd = ["gcc", "-O2", "-shared", "-fPIC", "-I", INCLUDE, "-I", sysconfig.get_paths()["include"],
+           os.path.join(CSRC, "binding.c"), "-o", tmp, "-L", PKG, "-l:libsmoe.so", "-Wl,-rpath,$ORIGIN"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"gcc failed on binding.c:\n{r.stderr}")
+    os.replace(tmp, BINDING)
     return LIB
 
 

@@ -147,3 +147,29 @@ def test_q8_refusals(smoe):
     assert m(N=0, xq=None) == smoe.SMOE_OK
     assert L.smoe_matmul_q8(A, A + MB, 16, A + 2 * MB, A + 3 * MB, 96, 250, A + 4 * MB, 0, A + 5 * MB, MB, None) == \
         smoe.SMOE_ERR_SHAPE
+
+
+def test_binding_converts_and_refuses(smoe):
+    """Addresses, None and objects with data_ptr(); sizes beyond 32 bits and
+    other objects are refused before the library is called."""
+    class Buf:
+        def data_ptr(self):
+            return A
+
+    ok = (Buf(), 0, 128, 128, 8, None, A)
+    smoe.smoe_topk_rows(*ok, stream=0)  # no tokens: nothing is launched
+    with pytest.raises(smoe.SmoeError) as ei:
+        smoe.smoe_topk_rows(A, 16, 128, 64, 8, A + MB, A + 2 * MB, stream=0)
+    assert ei.value.status == smoe.SMOE_ERR_SHAPE
+    with pytest.raises(OverflowError):
+        smoe.smoe_topk_rows(A, 1 << 40, 128, 128, 8, A, A, stream=0)
+    with pytest.raises(AttributeError):
+        smoe.smoe_topk_rows("x", 0, 128, 128, 8, A, A, stream=0)
+    with pytest.raises(TypeError):
+        smoe.smoe_topk_rows(A, 1.5, 128, 128, 8, A, A, stream=0)
+    with pytest.raises(TypeError):
+        smoe._binding.smoe_topk_rows(A, 0)
+    # the two routes to the library agree on every refusal
+    for args in ((A, -1, 128, 128, 8, A, A, 0), (None, 16, 128, 128, 8, A, A, 0), (A + 2, 16, 128, 128, 8, A + MB, A + 2 * MB, 0),
+                 (A, 16, 128, 128, 8, A + MB, A + MB, 0)):
+        assert smoe._binding.smoe_topk_rows(*args) == smoe._lib.smoe_topk_rows(*args) != 0
