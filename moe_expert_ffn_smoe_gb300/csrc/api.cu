@@ -903,7 +903,7 @@ static int check_q8(int n_src, int n_rows, int n_experts, int n_out, int n_in)
 size_t smoe_experts_matmul_q8_workspace_bytes(int n_src, int n_rows, int n_experts, int n_out, int n_in)
 {
     if (check_q8(n_src, n_rows, n_experts, n_out, n_in) != SMOE_OK) return static_cast<size_t>(-1);
-    return n_rows == 0 || n_out == 0 ? 0 : smoe::q8_workspace(n_rows, n_experts, n_in);
+    return n_rows == 0 || n_out == 0 ? 0 : smoe::q8_workspace(n_src, n_rows, n_experts, n_in);
 }
 
 size_t smoe_matmul_q8_workspace_bytes(int n_rows, int n_out, int n_in)
@@ -925,7 +925,7 @@ static int q8_impl(const int8_t *xq, const float *x_scales, int n_src, const int
     if (!aligned_to(x_scales, 4) || !aligned16(w_scales) || !aligned16(y) || (order && !aligned_to(order, 4)) ||
         (sorted && !aligned_to(offsets, 4)) || (n_in > 0 && (!aligned16(xq) || !aligned16(wq))))
         return SMOE_ERR_ALIGN;
-    const size_t need = smoe::q8_workspace(n_rows, n_experts, n_in);
+    const size_t need = smoe::q8_workspace(n_src, n_rows, n_experts, n_in);
     if (!workspace || workspace_bytes < need) return SMOE_ERR_WORKSPACE;
     if (!aligned16(workspace)) return SMOE_ERR_ALIGN;
     const size_t wrows = static_cast<size_t>(n_experts) * n_out;

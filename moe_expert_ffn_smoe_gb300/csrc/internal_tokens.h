@@ -27,7 +27,7 @@ cudaError_t launch_zero_words(int *p, int n, cudaStream_t stream);
 // order null: row r of the batch is row r of xq.
 cudaError_t launch_quantize_rows(const void *x, int dtype, bool act, int rows, int cols, int8_t *q, float *scales,
                                  cudaStream_t stream);
-size_t q8_workspace(int R, int n, int K);
+size_t q8_workspace(int nsrc, int R, int n, int K);
 cudaError_t launch_q8(const int8_t *xq, const float *xs, int nsrc, const int *order, int k, const int *offsets, int R,
                       int n, const int8_t *wq, const float *ws, int N, int K, void *y, int dtype, void *workspace,
                       cudaStream_t stream);

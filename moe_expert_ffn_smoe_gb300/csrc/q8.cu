@@ -373,10 +373,10 @@ cudaError_t launch_quantize_rows(const void *x, int dtype, bool act, int rows, i
 static bool on_tensor_cores(int R, int n, int K) { return K > 0 && R > 2 && R > 3LL * n / 8; }
 
 // Enough for either form, so that a larger batch never needs less.
-size_t q8_workspace(int R, int n, int K)
+size_t q8_workspace(int nsrc, int R, int n, int K)
 {
     const size_t dots = up256(16 + static_cast<size_t>(most_tiles(R, n, DOT_ROWS)) * sizeof(Tile));
-    const size_t tensor = q8_tc_workspace(R, n, K);
+    const size_t tensor = q8_tc_workspace(nsrc, R, n, K);
     return dots > tensor ? dots : tensor;
 }
 

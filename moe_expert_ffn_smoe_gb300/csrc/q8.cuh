@@ -60,7 +60,7 @@ struct Q8Call {
 };
 
 // The product on the tensor cores (q8_tc.cu).
-size_t q8_tc_workspace(int R, int n, int K);
+size_t q8_tc_workspace(int nsrc, int R, int n, int K);
 cudaError_t launch_q8_tc(const Q8Call &c, void *workspace, cudaStream_t stream);
 
 }  // namespace smoe

@@ -20,10 +20,13 @@
 // weight rows at once, each CTA widening its own 128 and holding half of the
 // activation rows, so that a row tile crosses from L2 once for 256 weight
 // rows and its stages take half the shared memory: twice as many are in
-// flight.
+// flight.  Rows of a batch sorted by expert are gathered by the copies
+// themselves (gather4): the tokens' widened rows stay in L2, where sorted
+// copies of them (k times as many) went out to HBM and back (4096 tokens, k =
+// 8, 4096 columns: 50 us and a tenth of the product's time).
 // Roles (warps): 0-7 epilogue, 8-23 widen weights (four groups, every
 // fourth K tile each), 24 issues the MMAs (of the pair: the even CTA's), 25
-// streams the weights, 26-29 the rows.  Every wait is bounded.
+// streams the weights, 26-31 the rows.  Every wait is bounded.
 #include <cuda_fp16.h>
 
 #include <atomic>
@@ -40,7 +43,7 @@ constexpr int MT = 128;                 // weight rows per CTA tile
 constexpr uint32_t W_BYTES = MT * 128;  // one weight chunk: 128 rows x 128 columns (two K tiles)
 constexpr int EPI_WARPS = 8;
 constexpr int CONV_WARP0 = 8, CONV_GROUPS = 4;  // groups of four warps: a row each thread
-constexpr int MMA_WARP = CONV_WARP0 + 4 * CONV_GROUPS, W_WARP = MMA_WARP + 1, X_WARP = MMA_WARP + 2, X_WARPS = 4;
+constexpr int MMA_WARP = CONV_WARP0 + 4 * CONV_GROUPS, W_WARP = MMA_WARP + 1, X_WARP = MMA_WARP + 2, X_PARTS = 3, X_WARPS = 2 * X_PARTS;
 constexpr int TC_THREADS = (X_WARP + X_WARPS) * 32;
 
 // Shapes of the two forms: row tile NT, CTAs per tile CL, and the rings of A
@@ -61,7 +64,8 @@ template <int NT>
 constexpr size_t tc_smem()
 {
     using F = Form<NT>;
-    return 1024 + static_cast<size_t>(F::WS) * W_BYTES + static_cast<size_t>(F::XS) * (NT / F::CL) * 256 + 512;
+    return 1024 + static_cast<size_t>(F::WS) * W_BYTES + static_cast<size_t>(F::XS) * (NT / F::CL) * 256 + 512 +
+           static_cast<size_t>(X_WARPS) * (NT / F::CL) * 4;
 }
 
 struct alignas(128) TcArgs {
@@ -70,8 +74,9 @@ struct alignas(128) TcArgs {
     void *y;
     const int *ntiles;
     const Tile *tiles;     // null: one matrix, tiles of `step` rows
+    const int *srow;       // source row in xmap of every sorted row (gathered), or null
     unsigned *status;
-    int R, N, K, step, mtiles, box;  // box: rows of one copy
+    int R, N, K, step, mtiles, box;  // box: rows of one copy (not gathered)
     int nsplit;            // CTAs that share an item's K range (single-CTA form)
 };
 
@@ -129,6 +134,24 @@ __device__ __forceinline__ void tma_load_2d_pair(uint32_t dst, const CUtensorMap
         "cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes.cta_group::2 [%0], [%1, {%2, %3}], "
         "[%4];" ::"r"(dst),
         "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(bar)
+        : "memory");
+}
+
+// Four rows of a tensor map whose box is one row high, one below another.
+__device__ __forceinline__ void tma_gather4(uint32_t dst, const CUtensorMap *map, int x, const int4 &r, uint32_t bar)
+{
+    asm volatile(
+        "cp.async.bulk.tensor.2d.shared::cluster.global.tile::gather4.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, "
+        "%5, %6}], [%7];" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(r.x), "r"(r.y), "r"(r.z), "r"(r.w), "r"(bar)
+        : "memory");
+}
+__device__ __forceinline__ void tma_gather4_pair(uint32_t dst, const CUtensorMap *map, int x, const int4 &r, uint32_t bar)
+{
+    asm volatile(
+        "cp.async.bulk.tensor.2d.shared::cluster.global.tile::gather4.mbarrier::complete_tx::bytes.cta_group::2 [%0], [%1, "
+        "{%2, %3, %4, %5, %6}], [%7];" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(r.x), "r"(r.y), "r"(r.z), "r"(r.w), "r"(bar)
         : "memory");
 }
 
@@ -214,12 +237,13 @@ __global__ void __launch_bounds__(TC_THREADS, 1) q8_tc(const __grid_constant__ T
     constexpr int CL = F::CL, AS = F::AS, XS = F::XS, WS = F::WS;
     constexpr int XR = NT / CL;                            // rows of a CTA's share of a tile, at most
     constexpr uint32_t XB = XR * 128u, ACOL0 = 2u * NT;    // XB: one K tile of them; a row stage is two
+    static_assert(X_PARTS <= XS, "row stages");
     static_assert(2 * NT + AS * 32 <= 512 && AS % CONV_GROUPS == 0 && WS % (CONV_GROUPS / 2) == 0,
                   "tensor memory; stages of one group of widening warps");
     extern __shared__ uint8_t smem_raw[];
     const uint32_t raw = smem_addr(smem_raw);
     const uint32_t base = (raw + 1023u) & ~1023u;
-    const uint32_t w0 = base, x0 = w0 + WS * W_BYTES, bars = x0 + XS * 2 * XB;
+    const uint32_t w0 = base, x0 = w0 + WS * W_BYTES, list0 = x0 + XS * 2 * XB, bars = list0 + X_WARPS * XR * 4;
     const uint32_t wfull = bars, wempty = wfull + 8 * WS, xfull = wempty + 8 * WS, xempty = xfull + 8 * XS,
                    afull = xempty + 8 * XS, aempty = afull + 8 * AS, dfull = aempty + 8 * AS, dempty = dfull + 16,
                    tslot = dempty + 16;
@@ -302,57 +326,83 @@ __global__ void __launch_bounds__(TC_THREADS, 1) q8_tc(const __grid_constant__ T
         }
         __syncwarp();
     } else if (warp >= X_WARP) {
-        // A stage is two K tiles.  Each of the four warps loads one K tile of
-        // every other stage: a copy costs its issuer hundreds of clocks, and
-        // fewer issuers paced the K loop.  The bytes of both CTAs complete on
-        // the issuing CTA's barrier, which alone expects them.
+        // A stage is two K tiles.  Each of the six warps loads one K tile of
+        // every third stage: a copy costs its issuer 50 (a gather) to some
+        // hundred clocks beside the other roles, and fewer issuers paced the
+        // K loop.  The bytes of both CTAs complete on the issuing CTA's
+        // barrier, which alone expects them.
         const uint32_t half = (warp - X_WARP) & 1, part = (warp - X_WARP) >> 1;
         const uint32_t lead = CL > 1 ? mapa_shared(xfull, 0) : xfull;
-        if (elect_one()) {
-            uint32_t s = part, p = 1, step = 0;  // step: the ring's steps so far, mod 2
-            bool round0 = true;
-            for (long long it = first; it < nitems && !failed; it += stride) {
-                const Tile t = tile_at(a, static_cast<int>(it / mgroups), ntiles);
-                const int share = mma_cols<CL>(t.rows) / CL;  // rows of this CTA's share, a multiple of 16
-                const int row0 = t.row0 + rank * share;
+        int *list = reinterpret_cast<int *>(smem_raw + (list0 - raw)) + (warp - X_WARP) * XR;
+        uint32_t s = part, p = 1, due = part;  // due: chunks until this warp's next step
+        bool round0 = true;
+        for (long long it = first; it < nitems && !failed; it += stride) {
+            const Tile t = tile_at(a, static_cast<int>(it / mgroups), ntiles);
+            const int share = mma_cols<CL>(t.rows) / CL;  // rows of this CTA's share, a multiple of 16
+            const int row0 = t.row0 + rank * share;
+            if (a.srow) {  // rows past the tile's: any row, their columns are not stored
+                __syncwarp();
+                for (int i = lane; i < share; i += 32) list[i] = rank * share + i < t.rows ? a.srow[row0 + i] : 0;
+                __syncwarp();
+            }
+            if (elect_one()) {
                 const int copies = (share + a.box - 1) / a.box;
-                for (int c = c0 + static_cast<int>(step ^ part); c < c1; c += 2) {
+                const uint32_t bytes = static_cast<uint32_t>(a.srow ? share : copies * a.box) * (128u * CL);
+                int c = c0 + static_cast<int>(due);
+                for (; c < c1; c += X_PARTS) {
                     if (!round0 && !mbar_wait_bounded(xempty + 8 * s, p, a.status, 8u)) {
                         failed = true;
                         break;
                     }
-                    if (rank == 0) mbar_arrive_expect_tx(xfull + 8 * s, static_cast<uint32_t>(copies * a.box) * (128u * CL));
+                    if (rank == 0) mbar_arrive_expect_tx(xfull + 8 * s, bytes);
                     const int x = (2 * c + static_cast<int>(half)) * KT;
                     const uint32_t dst = x0 + (2 * s + half) * XB, bar = lead + 8 * s;
-                    for (int b = 0; b < copies; ++b) {
-                        const uint32_t to = dst + static_cast<uint32_t>(b * a.box) * 128u;
-                        if (CL > 1) tma_load_2d_pair(to, &a.xmap, x, row0 + b * a.box, bar);
-                        else tma_load_2d(to, &a.xmap, x, row0 + b * a.box, bar);
+                    if (a.srow) {
+                        for (int i = 0; i < share; i += 16) {
+                            int4 r[4];
+#pragma unroll
+                            for (int j = 0; j < 4; ++j) r[j] = *reinterpret_cast<const int4 *>(list + i + 4 * j);
+#pragma unroll
+                            for (int j = 0; j < 4; ++j) {
+                                const uint32_t to = dst + static_cast<uint32_t>(i + 4 * j) * 128u;
+                                if (CL > 1) tma_gather4_pair(to, &a.xmap, x, r[j], bar);
+                                else tma_gather4(to, &a.xmap, x, r[j], bar);
+                            }
+                        }
+                    } else {
+                        for (int b = 0; b < copies; ++b) {
+                            const uint32_t to = dst + static_cast<uint32_t>(b * a.box) * 128u;
+                            if (CL > 1) tma_load_2d_pair(to, &a.xmap, x, row0 + b * a.box, bar);
+                            else tma_load_2d(to, &a.xmap, x, row0 + b * a.box, bar);
+                        }
                     }
-                    s += 2;
+                    s += X_PARTS;
                     if (s >= XS) {
                         s -= XS;
                         p ^= 1u;
                         round0 = false;
                     }
                 }
-                step ^= static_cast<uint32_t>((c1 - c0) & 1);
+                due = static_cast<uint32_t>(c - c1);
             }
-            // the last releases of this warp's stages arrive here from the
-            // other CTA's issue: they must have before this CTA may leave
-            if (CL > 1 && !failed) {
-                for (int j = 0; j < XS / 2; ++j) {
-                    if (!round0 && !mbar_wait_bounded(xempty + 8 * s, p, a.status, 8u)) failed = true;
-                    s += 2;
-                    if (s >= XS) {
-                        s -= XS;
-                        p ^= 1u;
-                        round0 = false;
-                    }
-                }
-            }
+            // the elected lane's place in the ring, to all
+            const uint32_t from = __ffs(__ballot_sync(FULL_MASK, elect_one())) - 1;
+            s = __shfl_sync(FULL_MASK, s, from);
+            p = __shfl_sync(FULL_MASK, p, from);
+            due = __shfl_sync(FULL_MASK, due, from);
+            round0 = __shfl_sync(FULL_MASK, round0, from);
+            failed = __shfl_sync(FULL_MASK, failed, from);
         }
-        __syncwarp();
+        // The last releases of the stages arrive here from the other CTA's
+        // issue: they must have before this CTA may leave.  The first warp
+        // waits for all of them.
+        if (CL > 1 && !failed && warp == X_WARP) {
+            const long long steps = first < nitems ? (nitems - first + stride - 1) / stride * (c1 - c0) : 0;
+            for (long long g = steps > XS ? steps - XS : 0; g < steps; ++g)
+                if (!mbar_wait_bounded(xempty + 8 * static_cast<uint32_t>(g % XS), static_cast<uint32_t>(g / XS) & 1,
+                                       a.status, 8u))
+                    failed = true;
+        }
     } else if (warp == MMA_WARP) {
         // one thread issues, of a pair the even CTA's
         if (rank == 0 && elect_one()) {
@@ -595,12 +645,13 @@ struct PrepArgs {
     const int8_t *xq;
     const float *xs;
     const int *order, *offsets;
-    __half *x16;  // [R x K]
+    __half *x16;  // [(gathered: nsrc, else R) x K]
     float *xss;   // [R]: the sorted rows' scales
     void *y;
     int *ntiles;
     Tile *tiles;
     unsigned *status;
+    int *srow;    // [R]: the sorted rows' sources (gathered), or null
     int nsrc, k, R, n, K, N, nt, unit, max_tiles, zero_bytes;  // unit: MMA columns; zero_bytes: an element of y
 };
 
@@ -657,6 +708,7 @@ __global__ void __launch_bounds__(PREP_THREADS) q8_prep(const PrepArgs a)
     for (int r = (blockIdx.x - b0) * PREP_THREADS + tid; r < a.R; r += blocks * PREP_THREADS) {
         const int src = r < last ? source_row(a.order, a.k, a.nsrc, r, a.status) : -1;
         a.xss[r] = src >= 0 ? a.xs[src] : 0.f;
+        if (a.srow) a.srow[r] = max(src, 0);  // none: any row, its scale is 0
     }
     const size_t zero0 = static_cast<size_t>(last) * a.N, zero1 = static_cast<size_t>(a.R) * a.N;
     for (size_t i = zero0 + static_cast<size_t>(blockIdx.x - b0) * PREP_THREADS + tid; i < zero1;
@@ -664,31 +716,22 @@ __global__ void __launch_bounds__(PREP_THREADS) q8_prep(const PrepArgs a)
         if (a.zero_bytes == 4) static_cast<float *>(a.y)[i] = 0.f;
         else static_cast<uint16_t *>(a.y)[i] = 0;
     }
-    // eight columns a thread, so that a warp's stores are whole sectors in a
-    // row; the next row's source is on its way while this one is widened
-    int r = blockIdx.x - b0;
-    int src = r < last ? source_row(a.order, a.k, a.nsrc, r, a.status) : 0;
-    while (r < last) {
-        const int rn = r + blocks;
-        const int next = rn < last ? source_row(a.order, a.k, a.nsrc, rn, a.status) : 0;
-        const uint2 *in = reinterpret_cast<const uint2 *>(a.xq + static_cast<size_t>(max(src, 0)) * a.K);  // none: scale 0
-        uint4 *out = reinterpret_cast<uint4 *>(a.x16 + static_cast<size_t>(r) * a.K);
-        for (int c0 = tid; c0 < a.K / 8; c0 += 4 * PREP_THREADS) {
-            uint2 v[4];
+    // eight columns a thread, so that a warp's stores are whole sectors
+    const size_t vecs = static_cast<size_t>(a.srow ? a.nsrc : last) * (a.K / 8);
+    const size_t hop = static_cast<size_t>(blocks) * PREP_THREADS;
+    for (size_t i = static_cast<size_t>(blockIdx.x - b0) * PREP_THREADS + tid; i < vecs; i += 4 * hop) {
+        uint2 v[4];
 #pragma unroll
-            for (int j = 0; j < 4; ++j)
-                if (c0 + j * PREP_THREADS < a.K / 8) v[j] = in[c0 + j * PREP_THREADS];
+        for (int j = 0; j < 4; ++j)
+            if (i + j * hop < vecs) v[j] = reinterpret_cast<const uint2 *>(a.xq)[i + j * hop];
 #pragma unroll
-            for (int j = 0; j < 4; ++j)
-                if (c0 + j * PREP_THREADS < a.K / 8) {
-                    uint4 o;
-                    s8x4_to_f16(v[j].x, o.x, o.y);
-                    s8x4_to_f16(v[j].y, o.z, o.w);
-                    out[c0 + j * PREP_THREADS] = o;
-                }
-        }
-        r = rn;
-        src = next;
+        for (int j = 0; j < 4; ++j)
+            if (i + j * hop < vecs) {
+                uint4 o;
+                s8x4_to_f16(v[j].x, o.x, o.y);
+                s8x4_to_f16(v[j].y, o.z, o.w);
+                reinterpret_cast<uint4 *>(a.x16)[i + j * hop] = o;
+            }
     }
 }
 
@@ -720,16 +763,17 @@ int pick_nt(int R, int n, bool one, int mtiles, int sms)
 }
 
 struct Layout {
-    size_t tiles, xss, x16, total;
+    size_t tiles, xss, srow, x16, total;
 };
 
-Layout layout(int R, int n, int K)
+Layout layout(int nsrc, int R, int n, int K)
 {
     Layout l;
     l.tiles = 256;
     l.xss = l.tiles + up256(static_cast<size_t>(most_tiles(R, n, 64)) * sizeof(Tile));
-    l.x16 = l.xss + up256(static_cast<size_t>(R) * sizeof(float));
-    l.total = l.x16 + up256(static_cast<size_t>(R) * K * sizeof(__half));
+    l.srow = l.xss + up256(static_cast<size_t>(R) * sizeof(float));
+    l.x16 = l.srow + up256(static_cast<size_t>(R) * sizeof(int));
+    l.total = l.x16 + up256(static_cast<size_t>(nsrc) * K * sizeof(__half));
     return l;
 }
 
@@ -808,7 +852,7 @@ cudaError_t launch_tc(const TcArgs &args, long long most_items, int sms, cudaStr
 
 }  // namespace
 
-size_t q8_tc_workspace(int R, int n, int K) { return layout(R, n, K).total; }
+size_t q8_tc_workspace(int nsrc, int R, int n, int K) { return layout(nsrc, R, n, K).total; }
 
 cudaError_t launch_q8_tc(const Q8Call &c, void *workspace, cudaStream_t stream)
 {
@@ -816,13 +860,14 @@ cudaError_t launch_q8_tc(const Q8Call &c, void *workspace, cudaStream_t stream)
     unsigned *status = device_status_word();
     if (!dev || !status) return cudaErrorInvalidDevice;
     char *ws = static_cast<char *>(workspace);
-    const Layout l = layout(c.R, c.n, c.K);
+    const Layout l = layout(c.nsrc, c.R, c.n, c.K);
     const int mtiles = (c.N + MT - 1) / MT;
     const int nt = pick_nt(c.R, c.n, !c.offsets, mtiles, dev->sm_count), cl = nt == 192 ? Form<192>::CL : Form<64>::CL, unit = 16 * cl;
     const int max_tiles = most_tiles(c.R, c.n, nt);
     int *ntiles = reinterpret_cast<int *>(ws);
     Tile *tiles = reinterpret_cast<Tile *>(ws + l.tiles);
     float *xss = reinterpret_cast<float *>(ws + l.xss);
+    int *srow = c.order ? reinterpret_cast<int *>(ws + l.srow) : nullptr;
     __half *x16 = reinterpret_cast<__half *>(ws + l.x16);
 
     // one matrix: equal tiles of consecutive rows, a CTA's share one copy
@@ -831,16 +876,19 @@ cudaError_t launch_q8_tc(const Q8Call &c, void *workspace, cudaStream_t stream)
     TcArgs a = {};
     a.box = c.offsets ? nt / cl / 2 : step / cl;
     if (!encode(&a.wmap, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, c.wq, c.K, static_cast<long long>(c.n) * c.N, 128, MT) ||
-        !encode(&a.xmap, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 2, x16, c.K, c.R, KT, a.box))
+        !encode(&a.xmap, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 2, x16, c.K, srow ? c.nsrc : c.R, KT, srow ? 1 : a.box))
         return cudaErrorInvalidValue;
-    const PrepArgs p = {c.xq, c.xs, c.order, c.offsets, x16, xss, c.y, ntiles, tiles, status, c.nsrc, c.k, c.R, c.n,
+    const PrepArgs p = {c.xq, c.xs, c.order, c.offsets, x16, xss, c.y, ntiles, tiles, status, srow, c.nsrc, c.k, c.R, c.n,
                         c.K, c.N, nt, unit, max_tiles, c.dtype == SMOE_BF16 ? 2 : 4};
-    const int blocks = c.R < dev->sm_count * 8 ? c.R : dev->sm_count * 8;
+    const long long vecs = static_cast<long long>(srow ? c.nsrc : c.R) * (c.K / 8);
+    long long blocks = ((vecs > c.R ? vecs : c.R) + PREP_THREADS - 1) / PREP_THREADS;
+    if (blocks > dev->sm_count * 8) blocks = dev->sm_count * 8;
     cudaError_t e = launch_pdl(q8_prep, dim3(static_cast<unsigned>(blocks + (c.offsets ? 1 : 0))), dim3(PREP_THREADS), 0,
                                stream, p);
     if (e != cudaSuccess) return e;
     a.ws = c.ws;
     a.xs = xss;
+    a.srow = srow;
     a.y = c.y;
     a.ntiles = ntiles;
     a.tiles = c.offsets ? tiles : nullptr;
