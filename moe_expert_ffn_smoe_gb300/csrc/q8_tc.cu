@@ -762,6 +762,28 @@ int pick_nt(int R, int n, bool one, int mtiles, int sms)
     return R <= 48LL * n || tiles * mtiles <= sms ? 64 : 192;
 }
 
+// How many tiles one matrix's R rows are cut into for pairs: as many as keep
+// waves of `pairs` items on `slots` pairs of SMs shortest.  An item costs its
+// rows, but no less than 144 (below, widening the weights paces it), and some
+// 16 rows' time of its own.  Against the fewest tiles (us; K = 4096): N =
+// 8192, 192 rows 23.9 to 21.4, 512 rows 36.9 to 34.7, 1024 rows 56.0 to 52.2;
+// N = 1536, 1536 rows 30.9 to 26.8.
+int pair_tiles(int R, int pairs, int slots)
+{
+    int best = 0;
+    long long least = 0;
+    for (int nd = (R + 191) / 192; nd <= (R + 95) / 96; ++nd) {
+        const int step = ((R + nd - 1) / nd + 31) / 32 * 32;
+        const long long waves = (static_cast<long long>((R + step - 1) / step) * pairs + slots - 1) / slots;
+        const long long cost = waves * ((step > 144 ? step : 144) + 16);
+        if (best == 0 || cost < least) {
+            best = nd;
+            least = cost;
+        }
+    }
+    return best;
+}
+
 struct Layout {
     size_t tiles, xss, srow, x16, total;
 };
@@ -871,7 +893,7 @@ cudaError_t launch_q8_tc(const Q8Call &c, void *workspace, cudaStream_t stream)
     __half *x16 = reinterpret_cast<__half *>(ws + l.x16);
 
     // one matrix: equal tiles of consecutive rows, a CTA's share one copy
-    const int nd = (c.R + nt - 1) / nt;
+    const int nd = nt == 64 ? (c.R + 63) / 64 : pair_tiles(c.R, (mtiles + 1) / 2, dev->sm_count / 2);
     const int step = ((c.R + nd - 1) / nd + unit - 1) / unit * unit;
     TcArgs a = {};
     a.box = c.offsets ? nt / cl / 2 : step / cl;
