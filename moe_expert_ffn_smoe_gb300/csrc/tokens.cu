@@ -392,12 +392,30 @@ __global__ void __launch_bounds__(SORT_THREADS) sort_place(const int *__restrict
 
 constexpr int SMALL_THREADS = 256;
 
+// This CTA's columns (blockIdx.y of gridDim.y) of a token's row, copied to the
+// rows of its k slots; a slot without an expert gets zeros.
+template <typename T, int VE>
+__device__ __forceinline__ void copy_row(const T *__restrict__ x, const int *rows, int k, int d, T *__restrict__ xs)
+{
+    for (int c = (blockIdx.y * SMALL_THREADS + threadIdx.x) * VE; c < d; c += gridDim.y * SMALL_THREADS * VE) {
+        RowVec<T, VE> v, z;
+        v.load(x + c);
+        z.zero();
+        for (int s = 0; s < k; ++s) {
+            const int p = rows[s];
+            if (p >= 0) v.store(xs + static_cast<size_t>(p) * d + c);
+            else z.store(xs + static_cast<size_t>(-1 - p) * d + c);
+        }
+    }
+}
+
 // The whole dispatch of a small batch in one launch: every CTA finds the
 // rows of its own token's slots by counting, over all R slots, those that
 // sort before them, then copies its share of the token's row; one CTA more
-// counts the buckets and writes the offsets.  R^2 / 32 warp steps in all:
-// cheaper than three more launches up to SMALL_SLOTS.
-constexpr int SMALL_SLOTS = 4096;
+// counts the buckets and writes the offsets.  R^2 / 32 warp steps in all.
+// Against the two launches of the middle form (us, rows of 512 bytes, 128
+// experts): 256 slots 2.1 / 4.2, 1024 slots 3.3 / 4.3, 2048 slots 5.2 / 4.3.
+constexpr int SMALL_SLOTS = 1536;
 
 template <typename T, int VE>
 __global__ void __launch_bounds__(SMALL_THREADS) dispatch_small(const int *__restrict__ top_idx, int tokens, int k, int n,
@@ -450,16 +468,90 @@ __global__ void __launch_bounds__(SMALL_THREADS) dispatch_small(const int *__res
     }
     if (!xs) return;
     __syncthreads();
-    for (int c = (blockIdx.y * SMALL_THREADS + tid) * VE; c < d; c += gridDim.y * SMALL_THREADS * VE) {
-        RowVec<T, VE> v, z;
-        v.load(x + static_cast<size_t>(t) * d + c);
-        z.zero();
-        for (int s = 0; s < k; ++s) {
-            const int p = cnt[s];
-            if (p >= 0) v.store(xs + static_cast<size_t>(p) * d + c);
-            else z.store(xs + static_cast<size_t>(-1 - p) * d + c);
+    copy_row<T, VE>(x + static_cast<size_t>(t) * d, cnt, k, d, xs);
+}
+
+// ---------------------------------------------------------------- middle sorts
+
+// Between the one-launch dispatch and the four launches of a large one: with
+// few chunks a slot's row needs no scan of its own.  sort_below leaves, for
+// every chunk c and bucket e, how many of the chunk's slots are in buckets
+// below e (cum[e][c]); the row of a slot of bucket e in chunk c is then
+//   sum over all c' of cum[e][c'] + sum over c' < c of (cum[e + 1][c'] -
+//   cum[e][c']) + the equal slots before it in its chunk,
+// two short rows that the slot's warp reads in a step or four.  Against the
+// four launches (us, as above): 8000 slots 5.4 / 8.5, 24,000 slots 9.7 / 12.0,
+// 32,768 slots 12.1 / 12.2.
+constexpr int MIDDLE_CHUNKS = 128;
+
+__global__ void __launch_bounds__(SORT_THREADS) sort_below(const int *__restrict__ top_idx, int R, int n, int nchunks,
+                                                           int *__restrict__ cum)
+{
+    extern __shared__ int cnt[];  // [n + 1]
+    __shared__ int warp_sums[SORT_THREADS / 32];
+    pdl_launch_dependents();
+    const int tid = threadIdx.x;
+    for (int e = tid; e <= n; e += SORT_THREADS) cnt[e] = 0;
+    __syncthreads();
+    pdl_wait();
+    const int a = blockIdx.x * SORT_THREADS + tid;
+    if (a < R) atomicAdd(&cnt[bucket(top_idx[a], n)], 1);
+    __syncthreads();
+    int run = 0;
+    for (int b = 0; b <= n; b += SORT_THREADS) {
+        const int v = b + tid <= n ? cnt[b + tid] : 0;
+        const int ex = run + block_exclusive(v, warp_sums);
+        if (b + tid <= n) cum[static_cast<size_t>(b + tid) * nchunks + blockIdx.x] = ex;
+        if (tid == SORT_THREADS - 1) warp_sums[0] = ex + v;
+        __syncthreads();
+        run = warp_sums[0];
+        __syncthreads();
+    }
+    if (tid == 0) cum[static_cast<size_t>(n + 1) * nchunks + blockIdx.x] = run;
+}
+
+// CTAs [0, tokens): a token's rows found as above and its row copied to them;
+// the CTAs behind: the offsets, a warp each.
+template <typename T, int VE>
+__global__ void __launch_bounds__(SMALL_THREADS) dispatch_middle(const int *__restrict__ top_idx, int tokens, int k, int n,
+                                                                 int nchunks, const int *__restrict__ cum,
+                                                                 const T *__restrict__ x, int d, int *__restrict__ offsets,
+                                                                 int *__restrict__ order, int *__restrict__ place,
+                                                                 T *__restrict__ xs)
+{
+    __shared__ int rows[SMOE_MAX_TOP_K];
+    const int tid = threadIdx.x, lane = tid & 31;
+    pdl_launch_dependents();
+    pdl_wait();
+    const int t = blockIdx.x;
+    if (t >= tokens) {
+        const int e = (t - tokens) * (SMALL_THREADS / 32) + (tid >> 5);
+        if (e > n || blockIdx.y != 0) return;
+        int first = 0;
+        for (int c = lane; c < nchunks; c += 32) first += cum[static_cast<size_t>(e) * nchunks + c];
+        first = __reduce_add_sync(FULL_MASK, first);
+        if (lane == 0) offsets[e] = first;
+        return;
+    }
+    for (int s = tid >> 5; s < k; s += SMALL_THREADS / 32) {
+        const int a = t * k + s;
+        const int e = bucket(top_idx[a], n), mine = a / SORT_THREADS;
+        const int *lo = cum + static_cast<size_t>(e) * nchunks, *hi = lo + nchunks;
+        int before = 0;
+        for (int c = lane; c < nchunks; c += 32) before += c < mine ? hi[c] : lo[c];
+        for (int b = mine * SORT_THREADS + lane; b < a; b += 32) before += bucket(top_idx[b], n) == e;
+        const int row = __reduce_add_sync(FULL_MASK, before);
+        if (lane == 0) {
+            rows[s] = e < n ? row : -1 - row;
+            if (blockIdx.y == 0) {
+                order[row] = a;
+                place[a] = e < n ? row : -1 - row;
+            }
         }
     }
+    if (!xs) return;
+    __syncthreads();
+    copy_row<T, VE>(x + static_cast<size_t>(t) * d, rows, k, d, xs);
 }
 
 // ---------------------------------------------------------------- rows
@@ -622,7 +714,7 @@ size_t dispatch_workspace(int T, int k, int n)
 {
     const size_t R = static_cast<size_t>(T) * k;
     const size_t chunks = (R + SORT_THREADS - 1) / SORT_THREADS;
-    return ((chunks + 1) * (static_cast<size_t>(n) + 1) * sizeof(int) + 255) & ~static_cast<size_t>(255);
+    return ((chunks + 1) * (static_cast<size_t>(n) + 2) * sizeof(int) + 255) & ~static_cast<size_t>(255);
 }
 
 namespace {
@@ -687,6 +779,20 @@ cudaError_t small_t(const int *top_idx, int tokens, int k, int n, const void *x,
 
 }  // namespace
 
+namespace {
+
+template <typename T, int VE>
+cudaError_t middle_t(const int *top_idx, int tokens, int k, int n, int nchunks, const int *cum, const void *x, int d,
+                     int *offsets, int *order, int *place, void *xs, cudaStream_t stream)
+{
+    dim3 grid = row_grid<T, VE>(tokens, xs ? d : 1);
+    grid.x += static_cast<unsigned>((n + SMALL_THREADS / 32) / (SMALL_THREADS / 32));
+    return launch_pdl(dispatch_middle<T, VE>, grid, dim3(SMALL_THREADS), 0, stream, top_idx, tokens, k, n, nchunks, cum,
+                      static_cast<const T *>(x), d, offsets, order, place, static_cast<T *>(xs));
+}
+
+}  // namespace
+
 cudaError_t launch_dispatch(const int *top_idx, int tokens, int k, int n, const void *x, int dtype, int d, int *offsets,
                             int *order, int *place, void *xs, void *workspace, cudaStream_t stream)
 {
@@ -699,6 +805,19 @@ cudaError_t launch_dispatch(const int *top_idx, int tokens, int k, int n, const 
                      : small_t<__nv_bfloat16, 1>(top_idx, tokens, k, n, x, d, offsets, order, place, xs, stream);
         return v ? small_t<float, 4>(top_idx, tokens, k, n, x, d, offsets, order, place, xs, stream)
                  : small_t<float, 1>(top_idx, tokens, k, n, x, d, offsets, order, place, xs, stream);
+    }
+    const int chunks = (R + SORT_THREADS - 1) / SORT_THREADS;
+    if (chunks <= MIDDLE_CHUNKS) {
+        int *cum = static_cast<int *>(workspace);
+        const size_t smem = (static_cast<size_t>(n) + 1) * sizeof(int);
+        const cudaError_t e = launch_pdl(sort_below, dim3(static_cast<unsigned>(chunks)), dim3(SORT_THREADS), smem, stream,
+                                         top_idx, R, n, chunks, cum);
+        if (e != cudaSuccess) return e;
+        if (dtype == SMOE_BF16)
+            return v ? middle_t<__nv_bfloat16, 8>(top_idx, tokens, k, n, chunks, cum, x, d, offsets, order, place, xs, stream)
+                     : middle_t<__nv_bfloat16, 1>(top_idx, tokens, k, n, chunks, cum, x, d, offsets, order, place, xs, stream);
+        return v ? middle_t<float, 4>(top_idx, tokens, k, n, chunks, cum, x, d, offsets, order, place, xs, stream)
+                 : middle_t<float, 1>(top_idx, tokens, k, n, chunks, cum, x, d, offsets, order, place, xs, stream);
     }
     const cudaError_t e = launch_sort_tokens(top_idx, R, n, offsets, order, place, workspace, stream);
     if (e != cudaSuccess || !xs) return e;

@@ -366,8 +366,7 @@ def test_side_stream_and_graph(smoe):
 
 @pytest.mark.parametrize("T,k,E", [(3000, 4, 8192), (1024, 4, 64), (1025, 4, 64), (70000, 2, 33)])
 def test_sort_of_many(smoe, T, k, E):
-    """Many buckets, the last size of the one-launch dispatch and the first
-    beyond it, many chunks."""
+    """Many buckets, many chunks."""
     for kind in ("all", "dropped"):
         idx = _indices(T, k, min(E, 64), 12, kind) if E <= 64 else _indices(T, k, E, 12, kind)
         offsets, order, place, _ = _dispatch(smoe, idx, E)
@@ -375,6 +374,23 @@ def test_sort_of_many(smoe, T, k, E):
         np.testing.assert_array_equal(offsets.cpu().numpy(), ro)
         np.testing.assert_array_equal(order.cpu().numpy(), rr)
         np.testing.assert_array_equal(place.cpu().numpy().reshape(-1), rp)
+
+
+@pytest.mark.parametrize("T,k,E", [(192, 8, 64), (193, 8, 64), (4096, 8, 128), (4097, 8, 128), (10000, 4, 8192), (520, 63, 64),
+                                   (33000, 1, 5)])
+@pytest.mark.parametrize("kind", ["all", "dropped", "one", "none"])
+def test_sort_at_the_forms_borders(smoe, T, k, E, kind):
+    """The first and last sizes of the two-launch dispatch (1537 to 32,768
+    slots) and those around them, with rows of their own so that both the sort and the copy are seen."""
+    idx = _indices(T, k, E, 14, kind)
+    x = torch.arange(T, device="cuda", dtype=torch.float32)[:, None].expand(T, 4).contiguous()
+    offsets, order, place, xs = _dispatch(smoe, idx, E, x)
+    ro, rr, rp = _sort_ref(idx, E)
+    np.testing.assert_array_equal(offsets.cpu().numpy(), ro)
+    np.testing.assert_array_equal(order.cpu().numpy(), rr)
+    np.testing.assert_array_equal(place.cpu().numpy().reshape(-1), rp)
+    there = rp[rr] >= 0
+    np.testing.assert_array_equal(xs[:, 3].cpu().numpy(), np.where(there, rr // k, 0))
 
 
 def test_rows_past_32_bits(smoe):
