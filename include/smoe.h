@@ -505,9 +505,9 @@ int smoe_experts_ffn_routed_q2(int n_experts, int k,
  * address memory; a place, order or offset outside its range is reported by
  * smoe_last_device_status as SMOE_ERR_ROUTE and its slot counts as one
  * without an expert.  1 <= k <= SMOE_MAX_TOP_K, n_experts <=
- * SMOE_MAX_ROUTE_EXPERTS, n_tokens k <= SMOE_MAX_SLOTS, d_model >= 0 (any
- * number; rows whose pitch and base are multiples of 16 bytes move as
- * 16-byte vectors).  Index arrays are aligned to 4 bytes, rows to their
+ * SMOE_MAX_ROUTE_EXPERTS, n_tokens k <= SMOE_MAX_SLOTS, 0 <= d_model <=
+ * SMOE_MAX_SLOTS (any number; rows whose pitch and base are multiples of 16
+ * bytes move as 16-byte vectors).  Index arrays are aligned to 4 bytes, rows to their
  * element.  n_tokens == 0 is a no-op (offsets become zeros).
  */
 

@@ -740,7 +740,7 @@ static int check_slots(int n_tokens, int k)
 static int check_rows(int dtype, int d_model)
 {
     if (dtype != SMOE_F32 && dtype != SMOE_BF16) return SMOE_ERR_SHAPE;
-    return d_model < 0 ? SMOE_ERR_SHAPE : SMOE_OK;
+    return d_model < 0 || d_model > SMOE_MAX_SLOTS ? SMOE_ERR_SHAPE : SMOE_OK;
 }
 
 int smoe_topk_rows(const float *logits, int n_tokens, int n_experts, int ld, int k, int *top_idx, float *top_w,

@@ -392,17 +392,20 @@ __global__ void __launch_bounds__(SORT_THREADS) sort_place(const int *__restrict
 
 constexpr int SMALL_THREADS = 256;
 
-// This CTA's columns (blockIdx.y of gridDim.y) of a token's row, copied to the
-// rows of its k slots; a slot without an expert gets zeros.
+// This CTA's share (blockIdx.y of gridDim.y) of nt tokens' rows, each copied to
+// the rows of its k slots; a slot without an expert gets zeros.  The tokens'
+// vectors are one sequence over the threads, so that short rows fill them.
 template <typename T, int VE>
-__device__ __forceinline__ void copy_row(const T *__restrict__ x, const int *rows, int k, int d, T *__restrict__ xs)
+__device__ __forceinline__ void copy_rows(const T *__restrict__ x, const int *rows, int nt, int k, int d, T *__restrict__ xs)
 {
-    for (int c = (blockIdx.y * SMALL_THREADS + threadIdx.x) * VE; c < d; c += gridDim.y * SMALL_THREADS * VE) {
+    const int nvec = d / VE;
+    for (int i = blockIdx.y * SMALL_THREADS + threadIdx.x; i < nt * nvec; i += gridDim.y * SMALL_THREADS) {
+        const int j = nt > 1 ? i / nvec : 0, c = (i - j * nvec) * VE;
         RowVec<T, VE> v, z;
-        v.load(x + c);
+        v.load(x + static_cast<size_t>(j) * d + c);
         z.zero();
         for (int s = 0; s < k; ++s) {
-            const int p = rows[s];
+            const int p = rows[j * k + s];
             if (p >= 0) v.store(xs + static_cast<size_t>(p) * d + c);
             else z.store(xs + static_cast<size_t>(-1 - p) * d + c);
         }
@@ -418,17 +421,17 @@ __device__ __forceinline__ void copy_row(const T *__restrict__ x, const int *row
 constexpr int SMALL_SLOTS = 1536;
 
 template <typename T, int VE>
-__global__ void __launch_bounds__(SMALL_THREADS) dispatch_small(const int *__restrict__ top_idx, int tokens, int k, int n,
+__global__ void __launch_bounds__(SMALL_THREADS) dispatch_small(const int *__restrict__ top_idx, int tokens, int tpc, int k, int n,
                                                                 const T *__restrict__ x, int d, int *__restrict__ offsets,
                                                                 int *__restrict__ order, int *__restrict__ place,
                                                                 T *__restrict__ xs)
 {
-    extern __shared__ int cnt[];  // [n + 1]; the gathering CTAs use [0, k) for their rows
+    extern __shared__ int cnt[];  // [n + 1]; the gathering CTAs use [0, tpc k) for their rows
     __shared__ int warp_sums[SMALL_THREADS / 32];
     const int tid = threadIdx.x, lane = tid & 31;
     const int R = tokens * k;
     pdl_launch_dependents();
-    if (static_cast<int>(blockIdx.x) == tokens) {
+    if (blockIdx.x == gridDim.x - 1) {
         if (blockIdx.y != 0) return;
         for (int e = tid; e <= n; e += SMALL_THREADS) cnt[e] = 0;
         __syncthreads();
@@ -448,9 +451,9 @@ __global__ void __launch_bounds__(SMALL_THREADS) dispatch_small(const int *__res
         return;
     }
     pdl_wait();
-    const int t = blockIdx.x;
-    for (int s = tid >> 5; s < k; s += SMALL_THREADS / 32) {
-        const int a = t * k + s;
+    const int t0 = blockIdx.x * tpc, nt = min(tpc, tokens - t0);
+    for (int s = tid >> 5; s < nt * k; s += SMALL_THREADS / 32) {
+        const int a = t0 * k + s;
         const int e = bucket(top_idx[a], n);
         int before = 0;
         for (int b = lane; b < R; b += 32) {
@@ -468,7 +471,7 @@ __global__ void __launch_bounds__(SMALL_THREADS) dispatch_small(const int *__res
     }
     if (!xs) return;
     __syncthreads();
-    copy_row<T, VE>(x + static_cast<size_t>(t) * d, cnt, k, d, xs);
+    copy_rows<T, VE>(x + static_cast<size_t>(t0) * d, cnt, nt, k, d, xs);
 }
 
 // ---------------------------------------------------------------- middle sorts
@@ -484,25 +487,28 @@ __global__ void __launch_bounds__(SMALL_THREADS) dispatch_small(const int *__res
 // 32,768 slots 12.1 / 12.2.
 constexpr int MIDDLE_CHUNKS = 128;
 
-__global__ void __launch_bounds__(SORT_THREADS) sort_below(const int *__restrict__ top_idx, int R, int n, int nchunks,
-                                                           int *__restrict__ cum)
+constexpr int MIDDLE_SMALL_CHUNK = 256, MIDDLE_LARGE_CHUNK = 1024;
+
+// One CTA per chunk, one thread per slot.
+__global__ void __launch_bounds__(MIDDLE_LARGE_CHUNK) sort_below(const int *__restrict__ top_idx, int R, int n, int nchunks,
+                                                                 int *__restrict__ cum)
 {
     extern __shared__ int cnt[];  // [n + 1]
-    __shared__ int warp_sums[SORT_THREADS / 32];
+    __shared__ int warp_sums[MIDDLE_LARGE_CHUNK / 32];
     pdl_launch_dependents();
-    const int tid = threadIdx.x;
-    for (int e = tid; e <= n; e += SORT_THREADS) cnt[e] = 0;
+    const int tid = threadIdx.x, threads = blockDim.x;
+    for (int e = tid; e <= n; e += threads) cnt[e] = 0;
     __syncthreads();
     pdl_wait();
-    const int a = blockIdx.x * SORT_THREADS + tid;
+    const int a = blockIdx.x * threads + tid;
     if (a < R) atomicAdd(&cnt[bucket(top_idx[a], n)], 1);
     __syncthreads();
     int run = 0;
-    for (int b = 0; b <= n; b += SORT_THREADS) {
+    for (int b = 0; b <= n; b += threads) {
         const int v = b + tid <= n ? cnt[b + tid] : 0;
         const int ex = run + block_exclusive(v, warp_sums);
         if (b + tid <= n) cum[static_cast<size_t>(b + tid) * nchunks + blockIdx.x] = ex;
-        if (tid == SORT_THREADS - 1) warp_sums[0] = ex + v;
+        if (tid == threads - 1) warp_sums[0] = ex + v;
         __syncthreads();
         run = warp_sums[0];
         __syncthreads();
@@ -510,11 +516,11 @@ __global__ void __launch_bounds__(SORT_THREADS) sort_below(const int *__restrict
     if (tid == 0) cum[static_cast<size_t>(n + 1) * nchunks + blockIdx.x] = run;
 }
 
-// CTAs [0, tokens): a token's rows found as above and its row copied to them;
-// the CTAs behind: the offsets, a warp each.
+// The first CTAs: tpc tokens' rows found as above and the tokens' rows copied to
+// them; the CTAs behind: the offsets, a warp each.
 template <typename T, int VE>
-__global__ void __launch_bounds__(SMALL_THREADS) dispatch_middle(const int *__restrict__ top_idx, int tokens, int k, int n,
-                                                                 int nchunks, const int *__restrict__ cum,
+__global__ void __launch_bounds__(SMALL_THREADS) dispatch_middle(const int *__restrict__ top_idx, int tokens, int tpc, int k, int n,
+                                                                 int nchunks, int chunk, const int *__restrict__ cum,
                                                                  const T *__restrict__ x, int d, int *__restrict__ offsets,
                                                                  int *__restrict__ order, int *__restrict__ place,
                                                                  T *__restrict__ xs)
@@ -523,9 +529,9 @@ __global__ void __launch_bounds__(SMALL_THREADS) dispatch_middle(const int *__re
     const int tid = threadIdx.x, lane = tid & 31;
     pdl_launch_dependents();
     pdl_wait();
-    const int t = blockIdx.x;
-    if (t >= tokens) {
-        const int e = (t - tokens) * (SMALL_THREADS / 32) + (tid >> 5);
+    const int ctas = (tokens + tpc - 1) / tpc;
+    if (static_cast<int>(blockIdx.x) >= ctas) {
+        const int e = (blockIdx.x - ctas) * (SMALL_THREADS / 32) + (tid >> 5);
         if (e > n || blockIdx.y != 0) return;
         int first = 0;
         for (int c = lane; c < nchunks; c += 32) first += cum[static_cast<size_t>(e) * nchunks + c];
@@ -533,13 +539,14 @@ __global__ void __launch_bounds__(SMALL_THREADS) dispatch_middle(const int *__re
         if (lane == 0) offsets[e] = first;
         return;
     }
-    for (int s = tid >> 5; s < k; s += SMALL_THREADS / 32) {
-        const int a = t * k + s;
-        const int e = bucket(top_idx[a], n), mine = a / SORT_THREADS;
+    const int t0 = blockIdx.x * tpc, nt = min(tpc, tokens - t0);
+    for (int s = tid >> 5; s < nt * k; s += SMALL_THREADS / 32) {
+        const int a = t0 * k + s;
+        const int e = bucket(top_idx[a], n), mine = a / chunk;
         const int *lo = cum + static_cast<size_t>(e) * nchunks, *hi = lo + nchunks;
         int before = 0;
         for (int c = lane; c < nchunks; c += 32) before += c < mine ? hi[c] : lo[c];
-        for (int b = mine * SORT_THREADS + lane; b < a; b += 32) before += bucket(top_idx[b], n) == e;
+        for (int b = mine * chunk + lane; b < a; b += 32) before += bucket(top_idx[b], n) == e;
         const int row = __reduce_add_sync(FULL_MASK, before);
         if (lane == 0) {
             rows[s] = e < n ? row : -1 - row;
@@ -551,7 +558,7 @@ __global__ void __launch_bounds__(SMALL_THREADS) dispatch_middle(const int *__re
     }
     if (!xs) return;
     __syncthreads();
-    copy_row<T, VE>(x + static_cast<size_t>(t) * d, rows, k, d, xs);
+    copy_rows<T, VE>(x + static_cast<size_t>(t0) * d, rows, nt, k, d, xs);
 }
 
 // ---------------------------------------------------------------- rows
@@ -569,51 +576,59 @@ __device__ __forceinline__ int checked_place(int p, int R, unsigned *status)
     return p;
 }
 
-// xs[place[t, s]] = x[t]; the rows of slots without an expert are zeros.
-// One CTA per token and column block: x is read once and written k times.
+// xs[place[t, s]] = x[t]; the rows of slots without an expert are zeros.  A
+// CTA takes tpc tokens and a column block: x is read once and written k
+// times.  Bound by HBM writes (8191 tokens of 8 KB, k = 8: 91 us, 98% of the
+// copy rate).
 template <typename T, int VE>
-__global__ void __launch_bounds__(ROW_THREADS) gather_rows(const T *__restrict__ x, const int *__restrict__ place, int k,
-                                                           int d, T *__restrict__ xs)
+__global__ void __launch_bounds__(ROW_THREADS) gather_rows(const T *__restrict__ x, const int *__restrict__ place,
+                                                           int tokens, int tpc, int k, int d, T *__restrict__ xs)
 {
+    static_assert(ROW_THREADS == SMALL_THREADS, "copy_rows");
     pdl_launch_dependents();
     pdl_wait();
-    const size_t t = blockIdx.x;
-    for (int c = (blockIdx.y * ROW_THREADS + threadIdx.x) * VE; c < d; c += gridDim.y * ROW_THREADS * VE) {
-        RowVec<T, VE> v, z;
-        v.load(x + t * d + c);
-        z.zero();
-        for (int s = 0; s < k; ++s) {
-            const int p = place[t * k + s];
-            if (p >= 0) v.store(xs + static_cast<size_t>(p) * d + c);
-            else z.store(xs + static_cast<size_t>(-1 - p) * d + c);
-        }
-    }
+    const int t0 = blockIdx.x * tpc;
+    copy_rows<T, VE>(x + static_cast<size_t>(t0) * d, place + static_cast<size_t>(t0) * k, min(tpc, tokens - t0), k, d, xs);
 }
 
 // out[t] = sum over s, in order, of w[t, s] ys[place[t, s]] (w null: of the
-// rows themselves), f32 sums.
+// rows themselves), f32 sums.  A thread takes a vector of a token's row, four
+// slots' loads in flight; a CTA tpc tokens and a column block.  Bound by HBM
+// reads (4099 tokens of 16 KB, k = 8: 98 us, 92% of the copy rate).
 template <typename T, int VE>
 __global__ void __launch_bounds__(ROW_THREADS) sum_rows(const T *__restrict__ ys, const int *__restrict__ place,
-                                                        const float *__restrict__ w, int R, int k, int d,
+                                                        const float *__restrict__ w, int tokens, int tpc, int k, int d,
                                                         T *__restrict__ out, unsigned *status)
 {
     pdl_launch_dependents();
     pdl_wait();
-    const size_t t = blockIdx.x;
-    for (int c = (blockIdx.y * ROW_THREADS + threadIdx.x) * VE; c < d; c += gridDim.y * ROW_THREADS * VE) {
+    const int t0 = blockIdx.x * tpc, nt = min(tpc, tokens - t0), nvec = d / VE, R = tokens * k;
+    for (int i = blockIdx.y * ROW_THREADS + threadIdx.x; i < nt * nvec; i += gridDim.y * ROW_THREADS) {
+        const int j = nt > 1 ? i / nvec : 0, c = (i - j * nvec) * VE;
+        const size_t t = t0 + j;
         float acc[VE];
 #pragma unroll
-        for (int i = 0; i < VE; ++i) acc[i] = 0.f;
-        for (int s = 0; s < k; ++s) {
-            const int p = checked_place(place[t * k + s], R, status);
-            if (p < 0) continue;
-            const float ws = w ? w[t * k + s] : 1.f;
-            RowVec<T, VE> v;
-            v.load(ys + static_cast<size_t>(p) * d + c);
-            float f[VE];
-            v.get(f);
+        for (int v = 0; v < VE; ++v) acc[v] = 0.f;
+        for (int s0 = 0; s0 < k; s0 += 4) {
+            int p[4];
+            float ws[4];
+            RowVec<T, VE> y[4];
 #pragma unroll
-            for (int i = 0; i < VE; ++i) acc[i] = fmaf(ws, f[i], acc[i]);
+            for (int s = 0; s < 4; ++s) {
+                p[s] = s0 + s < k ? checked_place(place[t * k + s0 + s], R, status) : -1;
+                ws[s] = w && s0 + s < k ? w[t * k + s0 + s] : 1.f;
+            }
+#pragma unroll
+            for (int s = 0; s < 4; ++s)
+                if (p[s] >= 0) y[s].load(ys + static_cast<size_t>(p[s]) * d + c);
+#pragma unroll
+            for (int s = 0; s < 4; ++s)
+                if (p[s] >= 0) {
+                    float f[VE];
+                    y[s].get(f);
+#pragma unroll
+                    for (int v = 0; v < VE; ++v) acc[v] = fmaf(ws[s], f[v], acc[v]);
+                }
         }
         RowVec<T, VE> o;
         o.set(acc);
@@ -735,26 +750,50 @@ cudaError_t launch_sort_tokens(const int *top_idx, int R, int n, int *offsets, i
                       hist, total, offsets, order, place);
 }
 
-template <typename T, int VE>
-dim3 row_grid(int tokens, int d)
+// Tokens per CTA: as many as their rows' vectors take to fill its threads (or,
+// where a warp looks for each slot's row, as their slots take to fill its
+// warps), while that leaves four CTAs an SM.
+int tokens_per_cta(int tokens, int k, int nvec, bool search)
 {
-    const unsigned cols = static_cast<unsigned>((d + ROW_THREADS * VE - 1) / (ROW_THREADS * VE));
-    return dim3(static_cast<unsigned>(tokens), cols < 64u ? cols : 64u);
+    const DeviceInfo *dev = device_info();
+    const int sms = dev ? dev->sm_count : 152;
+    int tpc = nvec > 0 && nvec < ROW_THREADS ? ROW_THREADS / nvec : 1;
+    if (search && tpc < (SMALL_THREADS / 32) / k) tpc = (SMALL_THREADS / 32) / k;
+    if (tpc > SMOE_MAX_TOP_K / k) tpc = SMOE_MAX_TOP_K / k;
+    while (tpc > 1 && tokens / tpc < 4 * sms) tpc /= 2;
+    return tpc;
+}
+
+// (CTAs of tpc tokens, column blocks).  Every column block looks for its slots'
+// rows again, so there are only as many as make eight CTAs an SM.
+template <typename T, int VE>
+dim3 row_grid(int tokens, int tpc, int d, bool search)
+{
+    long long cols = (static_cast<long long>(tpc) * (d / VE) + ROW_THREADS - 1) / ROW_THREADS;
+    const int x = (tokens + tpc - 1) / tpc;
+    if (search) {
+        const DeviceInfo *dev = device_info();
+        const int want = (8 * (dev ? dev->sm_count : 152) + x - 1) / x;
+        if (cols > want) cols = want;
+    }
+    return dim3(static_cast<unsigned>(x), static_cast<unsigned>(cols < 1 ? 1 : (cols < 64 ? cols : 64)));
 }
 
 template <typename T, int VE>
 cudaError_t gather_t(const void *x, const int *place, int tokens, int k, int d, void *xs, cudaStream_t stream)
 {
-    return launch_pdl(gather_rows<T, VE>, row_grid<T, VE>(tokens, d), dim3(ROW_THREADS), 0, stream,
-                      static_cast<const T *>(x), place, k, d, static_cast<T *>(xs));
+    const int tpc = tokens_per_cta(tokens, k, d / VE, false);
+    return launch_pdl(gather_rows<T, VE>, row_grid<T, VE>(tokens, tpc, d, false), dim3(ROW_THREADS), 0, stream,
+                      static_cast<const T *>(x), place, tokens, tpc, k, d, static_cast<T *>(xs));
 }
 
 template <typename T, int VE>
 cudaError_t sum_t(const void *ys, const int *place, const float *w, int tokens, int k, int d, void *out, unsigned *status,
                   cudaStream_t stream)
 {
-    return launch_pdl(sum_rows<T, VE>, row_grid<T, VE>(tokens, d), dim3(ROW_THREADS), 0, stream,
-                      static_cast<const T *>(ys), place, w, tokens * k, k, d, static_cast<T *>(out), status);
+    const int tpc = tokens_per_cta(tokens, 1, d / VE, false);
+    return launch_pdl(sum_rows<T, VE>, row_grid<T, VE>(tokens, tpc, d, false), dim3(ROW_THREADS), 0, stream,
+                      static_cast<const T *>(ys), place, w, tokens, tpc, k, d, static_cast<T *>(out), status);
 }
 
 template <typename T, int VE>
@@ -770,10 +809,11 @@ template <typename T, int VE>
 cudaError_t small_t(const int *top_idx, int tokens, int k, int n, const void *x, int d, int *offsets, int *order,
                     int *place, void *xs, cudaStream_t stream)
 {
-    dim3 grid = row_grid<T, VE>(tokens, xs ? d : 1);
+    const int tpc = tokens_per_cta(tokens, k, xs ? d / VE : 0, true);
+    dim3 grid = row_grid<T, VE>(tokens, tpc, xs ? d : 0, true);
     grid.x += 1;
     const size_t words = static_cast<size_t>(n) + 1 > SMOE_MAX_TOP_K ? static_cast<size_t>(n) + 1 : SMOE_MAX_TOP_K;
-    return launch_pdl(dispatch_small<T, VE>, grid, dim3(SMALL_THREADS), words * sizeof(int), stream, top_idx, tokens, k, n,
+    return launch_pdl(dispatch_small<T, VE>, grid, dim3(SMALL_THREADS), words * sizeof(int), stream, top_idx, tokens, tpc, k, n,
                       static_cast<const T *>(x), d, offsets, order, place, static_cast<T *>(xs));
 }
 
@@ -782,13 +822,14 @@ cudaError_t small_t(const int *top_idx, int tokens, int k, int n, const void *x,
 namespace {
 
 template <typename T, int VE>
-cudaError_t middle_t(const int *top_idx, int tokens, int k, int n, int nchunks, const int *cum, const void *x, int d,
+cudaError_t middle_t(const int *top_idx, int tokens, int k, int n, int nchunks, int chunk, const int *cum, const void *x, int d,
                      int *offsets, int *order, int *place, void *xs, cudaStream_t stream)
 {
-    dim3 grid = row_grid<T, VE>(tokens, xs ? d : 1);
+    const int tpc = tokens_per_cta(tokens, k, xs ? d / VE : 0, true);
+    dim3 grid = row_grid<T, VE>(tokens, tpc, xs ? d : 0, true);
     grid.x += static_cast<unsigned>((n + SMALL_THREADS / 32) / (SMALL_THREADS / 32));
-    return launch_pdl(dispatch_middle<T, VE>, grid, dim3(SMALL_THREADS), 0, stream, top_idx, tokens, k, n, nchunks, cum,
-                      static_cast<const T *>(x), d, offsets, order, place, static_cast<T *>(xs));
+    return launch_pdl(dispatch_middle<T, VE>, grid, dim3(SMALL_THREADS), 0, stream, top_idx, tokens, tpc, k, n, nchunks, chunk,
+                      cum, static_cast<const T *>(x), d, offsets, order, place, static_cast<T *>(xs));
 }
 
 }  // namespace
@@ -806,18 +847,20 @@ cudaError_t launch_dispatch(const int *top_idx, int tokens, int k, int n, const 
         return v ? small_t<float, 4>(top_idx, tokens, k, n, x, d, offsets, order, place, xs, stream)
                  : small_t<float, 1>(top_idx, tokens, k, n, x, d, offsets, order, place, xs, stream);
     }
-    const int chunks = (R + SORT_THREADS - 1) / SORT_THREADS;
+    // larger chunks, whose search takes longer, where a token's k rows take
+    // longer still to copy
+    const bool wide = xs && static_cast<size_t>(k) * pitch >= 32768u;
+    const int chunk = R <= MIDDLE_CHUNKS * MIDDLE_SMALL_CHUNK || !wide ? MIDDLE_SMALL_CHUNK : MIDDLE_LARGE_CHUNK;
+    const int chunks = (R + chunk - 1) / chunk;
     if (chunks <= MIDDLE_CHUNKS) {
         int *cum = static_cast<int *>(workspace);
         const size_t smem = (static_cast<size_t>(n) + 1) * sizeof(int);
-        const cudaError_t e = launch_pdl(sort_below, dim3(static_cast<unsigned>(chunks)), dim3(SORT_THREADS), smem, stream,
-                                         top_idx, R, n, chunks, cum);
+        const cudaError_t e = launch_pdl(sort_below, dim3(static_cast<unsigned>(chunks)), dim3(static_cast<unsigned>(chunk)),
+                                         smem, stream, top_idx, R, n, chunks, cum);
         if (e != cudaSuccess) return e;
-        if (dtype == SMOE_BF16)
-            return v ? middle_t<__nv_bfloat16, 8>(top_idx, tokens, k, n, chunks, cum, x, d, offsets, order, place, xs, stream)
-                     : middle_t<__nv_bfloat16, 1>(top_idx, tokens, k, n, chunks, cum, x, d, offsets, order, place, xs, stream);
-        return v ? middle_t<float, 4>(top_idx, tokens, k, n, chunks, cum, x, d, offsets, order, place, xs, stream)
-                 : middle_t<float, 1>(top_idx, tokens, k, n, chunks, cum, x, d, offsets, order, place, xs, stream);
+        auto go = [&](auto run) { return run(top_idx, tokens, k, n, chunks, chunk, cum, x, d, offsets, order, place, xs, stream); };
+        if (dtype == SMOE_BF16) return v ? go(middle_t<__nv_bfloat16, 8>) : go(middle_t<__nv_bfloat16, 1>);
+        return v ? go(middle_t<float, 4>) : go(middle_t<float, 1>);
     }
     const cudaError_t e = launch_sort_tokens(top_idx, R, n, offsets, order, place, workspace, stream);
     if (e != cudaSuccess || !xs) return e;

@@ -376,7 +376,8 @@ def test_sort_of_many(smoe, T, k, E):
         np.testing.assert_array_equal(place.cpu().numpy().reshape(-1), rp)
 
 
-@pytest.mark.parametrize("T,k,E", [(192, 8, 64), (193, 8, 64), (4096, 8, 128), (4097, 8, 128), (10000, 4, 8192), (520, 63, 64),
+@pytest.mark.parametrize("T,k,E", [(192, 8, 64), (193, 8, 64), (4096, 8, 128), (4097, 8, 128), (16384, 8, 128), (16385, 8, 128), (10000, 4, 8192),
+                                   (33000, 4, 8192), (520, 63, 64),
                                    (33000, 1, 5)])
 @pytest.mark.parametrize("kind", ["all", "dropped", "one", "none"])
 def test_sort_at_the_forms_borders(smoe, T, k, E, kind):

@@ -82,7 +82,7 @@ def test_combine_and_gradients_refusals(smoe):
         return L.smoe_dispatch_tokens_backward(ys, dt, p, T, k, d, out, None)
 
     for f in (c, b):
-        for bad in (dict(T=-1), dict(k=0), dict(k=65), dict(dt=3), dict(d=-1)):
+        for bad in (dict(T=-1), dict(k=0), dict(k=65), dict(dt=3), dict(d=-1), dict(d=(1 << 30) + 1)):
             assert f(**bad) == smoe.SMOE_ERR_SHAPE, bad
         for bad in (dict(ys=None), dict(p=None), dict(out=None)):
             assert f(**bad) == smoe.SMOE_ERR_NULL, bad
