@@ -392,22 +392,45 @@ __global__ void __launch_bounds__(SORT_THREADS) sort_place(const int *__restrict
 
 constexpr int SMALL_THREADS = 256;
 
+constexpr int ODD_COLS = 256;  // columns that a warp takes at a time of rows that no 16-byte vector fits
+
 // This CTA's share (blockIdx.y of gridDim.y) of nt tokens' rows, each copied to
 // the rows of its k slots; a slot without an expert gets zeros.  The tokens'
 // vectors are one sequence over the threads, so that short rows fill them.
 template <typename T, int VE>
 __device__ __forceinline__ void copy_rows(const T *__restrict__ x, const int *rows, int nt, int k, int d, T *__restrict__ xs)
 {
-    const int nvec = d / VE;
-    for (int i = blockIdx.y * SMALL_THREADS + threadIdx.x; i < nt * nvec; i += gridDim.y * SMALL_THREADS) {
-        const int j = nt > 1 ? i / nvec : 0, c = (i - j * nvec) * VE;
-        RowVec<T, VE> v, z;
-        v.load(x + static_cast<size_t>(j) * d + c);
-        z.zero();
-        for (int s = 0; s < k; ++s) {
-            const int p = rows[j * k + s];
-            if (p >= 0) v.store(xs + static_cast<size_t>(p) * d + c);
-            else z.store(xs + static_cast<size_t>(-1 - p) * d + c);
+    if constexpr (VE == 1) {
+        // rows that no vector fits: a warp takes 256 columns, eight a lane
+        const int lane = threadIdx.x & 31, blocks = (d + ODD_COLS - 1) / ODD_COLS;
+        const int warps = SMALL_THREADS / 32;
+        for (int i = blockIdx.y * warps + (threadIdx.x >> 5); i < nt * blocks; i += gridDim.y * warps) {
+            const int j = i / blocks, c0 = (i - j * blocks) * ODD_COLS + lane;
+            RowVec<T, 1> v[ODD_COLS / 32], z;
+            z.zero();
+#pragma unroll
+            for (int u = 0; u < ODD_COLS / 32; ++u)
+                if (c0 + 32 * u < d) v[u].load(x + static_cast<size_t>(j) * d + c0 + 32 * u);
+            for (int s = 0; s < k; ++s) {
+                const int p = rows[j * k + s];
+                T *to = xs + static_cast<size_t>(p >= 0 ? p : -1 - p) * d + c0;
+#pragma unroll
+                for (int u = 0; u < ODD_COLS / 32; ++u)
+                    if (c0 + 32 * u < d) (p >= 0 ? v[u] : z).store(to + 32 * u);
+            }
+        }
+    } else {
+        const int nvec = d / VE;
+        for (int i = blockIdx.y * SMALL_THREADS + threadIdx.x; i < nt * nvec; i += gridDim.y * SMALL_THREADS) {
+            const int j = nt > 1 ? i / nvec : 0, c = (i - j * nvec) * VE;
+            RowVec<T, VE> v, z;
+            v.load(x + static_cast<size_t>(j) * d + c);
+            z.zero();
+            for (int s = 0; s < k; ++s) {
+                const int p = rows[j * k + s];
+                if (p >= 0) v.store(xs + static_cast<size_t>(p) * d + c);
+                else z.store(xs + static_cast<size_t>(-1 - p) * d + c);
+            }
         }
     }
 }
@@ -602,37 +625,79 @@ __global__ void __launch_bounds__(ROW_THREADS) sum_rows(const T *__restrict__ ys
 {
     pdl_launch_dependents();
     pdl_wait();
-    const int t0 = blockIdx.x * tpc, nt = min(tpc, tokens - t0), nvec = d / VE, R = tokens * k;
-    for (int i = blockIdx.y * ROW_THREADS + threadIdx.x; i < nt * nvec; i += gridDim.y * ROW_THREADS) {
-        const int j = nt > 1 ? i / nvec : 0, c = (i - j * nvec) * VE;
-        const size_t t = t0 + j;
-        float acc[VE];
+    const int t0 = blockIdx.x * tpc, nt = min(tpc, tokens - t0), R = tokens * k;
+    if constexpr (VE == 1) {
+        // rows that no vector fits: a warp takes 256 columns, eight a lane, so
+        // that a slot's place and weight are read once for eight (511 columns
+        // of bf16, 4001 tokens, k = 8: 20.1 us with one a lane, 15.5 so; 512
+        // columns in vectors 8.2)
+        const int lane = threadIdx.x & 31, blocks = (d + ODD_COLS - 1) / ODD_COLS, warps = ROW_THREADS / 32;
+        for (int i = blockIdx.y * warps + (threadIdx.x >> 5); i < nt * blocks; i += gridDim.y * warps) {
+            const int j = i / blocks, c0 = (i - j * blocks) * ODD_COLS + lane;
+            const size_t t = t0 + j;
+            float acc[ODD_COLS / 32];
 #pragma unroll
-        for (int v = 0; v < VE; ++v) acc[v] = 0.f;
-        for (int s0 = 0; s0 < k; s0 += 4) {
-            int p[4];
-            float ws[4];
-            RowVec<T, VE> y[4];
+            for (int u = 0; u < ODD_COLS / 32; ++u) acc[u] = 0.f;
+#pragma unroll 2
+            for (int s = 0; s < k; ++s) {
+                const int p = checked_place(place[t * k + s], R, status);
+                if (p < 0) continue;
+                const float ws = w ? w[t * k + s] : 1.f;
+                const T *y = ys + static_cast<size_t>(p) * d + c0;
+                RowVec<T, 1> v[ODD_COLS / 32];
 #pragma unroll
-            for (int s = 0; s < 4; ++s) {
-                p[s] = s0 + s < k ? checked_place(place[t * k + s0 + s], R, status) : -1;
-                ws[s] = w && s0 + s < k ? w[t * k + s0 + s] : 1.f;
+                for (int u = 0; u < ODD_COLS / 32; ++u)
+                    if (c0 + 32 * u < d) v[u].load(y + 32 * u);
+#pragma unroll
+                for (int u = 0; u < ODD_COLS / 32; ++u)
+                    if (c0 + 32 * u < d) {
+                        float f[1];
+                        v[u].get(f);
+                        acc[u] = fmaf(ws, f[0], acc[u]);
+                    }
             }
 #pragma unroll
-            for (int s = 0; s < 4; ++s)
-                if (p[s] >= 0) y[s].load(ys + static_cast<size_t>(p[s]) * d + c);
-#pragma unroll
-            for (int s = 0; s < 4; ++s)
-                if (p[s] >= 0) {
-                    float f[VE];
-                    y[s].get(f);
-#pragma unroll
-                    for (int v = 0; v < VE; ++v) acc[v] = fmaf(ws[s], f[v], acc[v]);
+            for (int u = 0; u < ODD_COLS / 32; ++u)
+                if (c0 + 32 * u < d) {
+                    const float f[1] = {acc[u]};
+                    RowVec<T, 1> o;
+                    o.set(f);
+                    o.store(out + t * d + c0 + 32 * u);
                 }
         }
-        RowVec<T, VE> o;
-        o.set(acc);
-        o.store(out + t * d + c);
+    } else {
+        const int nvec = d / VE;
+        for (int i = blockIdx.y * ROW_THREADS + threadIdx.x; i < nt * nvec; i += gridDim.y * ROW_THREADS) {
+            const int j = nt > 1 ? i / nvec : 0, c = (i - j * nvec) * VE;
+            const size_t t = t0 + j;
+            float acc[VE];
+#pragma unroll
+            for (int v = 0; v < VE; ++v) acc[v] = 0.f;
+            for (int s0 = 0; s0 < k; s0 += 4) {
+                int p[4];
+                float ws[4];
+                RowVec<T, VE> y[4];
+#pragma unroll
+                for (int s = 0; s < 4; ++s) {
+                    p[s] = s0 + s < k ? checked_place(place[t * k + s0 + s], R, status) : -1;
+                    ws[s] = w && s0 + s < k ? w[t * k + s0 + s] : 1.f;
+                }
+#pragma unroll
+                for (int s = 0; s < 4; ++s)
+                    if (p[s] >= 0) y[s].load(ys + static_cast<size_t>(p[s]) * d + c);
+#pragma unroll
+                for (int s = 0; s < 4; ++s)
+                    if (p[s] >= 0) {
+                        float f[VE];
+                        y[s].get(f);
+#pragma unroll
+                        for (int v = 0; v < VE; ++v) acc[v] = fmaf(ws[s], f[v], acc[v]);
+                    }
+            }
+            RowVec<T, VE> o;
+            o.set(acc);
+            o.store(out + t * d + c);
+        }
     }
 }
 
@@ -663,20 +728,29 @@ __global__ void __launch_bounds__(ROW_THREADS) combine_grad(const T *__restrict_
         }
         const float ws = w[t * k + s];
         float dot = 0.f;
-        for (int c = lane * VE; c < d; c += 32 * VE) {
-            RowVec<T, VE> gv, yv;
-            gv.load(g + c);
-            yv.load(ys + static_cast<size_t>(p) * d + c);
-            float gf[VE], yf[VE];
-            gv.get(gf);
-            yv.get(yf);
+        constexpr int U = VE > 1 ? 2 : (sizeof(T) == 4 ? 4 : 1);  // vectors of each row in flight (as measured)
+        for (int c0 = lane * VE; c0 < d; c0 += U * 32 * VE) {
+            RowVec<T, VE> gv[U], yv[U];
 #pragma unroll
-            for (int i = 0; i < VE; ++i) {
-                dot = fmaf(gf[i], yf[i], dot);
-                gf[i] *= ws;
-            }
-            gv.set(gf);
-            gv.store(d_ys + static_cast<size_t>(p) * d + c);
+            for (int u = 0; u < U; ++u)
+                if (c0 + u * 32 * VE < d) {
+                    gv[u].load(g + c0 + u * 32 * VE);
+                    yv[u].load(ys + static_cast<size_t>(p) * d + c0 + u * 32 * VE);
+                }
+#pragma unroll
+            for (int u = 0; u < U; ++u)
+                if (c0 + u * 32 * VE < d) {
+                    float gf[VE], yf[VE];
+                    gv[u].get(gf);
+                    yv[u].get(yf);
+#pragma unroll
+                    for (int i = 0; i < VE; ++i) {
+                        dot = fmaf(gf[i], yf[i], dot);
+                        gf[i] *= ws;
+                    }
+                    gv[u].set(gf);
+                    gv[u].store(d_ys + static_cast<size_t>(p) * d + c0 + u * 32 * VE);
+                }
         }
 #pragma unroll
         for (int off = 16; off > 0; off >>= 1) dot += __shfl_xor_sync(FULL_MASK, dot, off);
@@ -753,15 +827,22 @@ cudaError_t launch_sort_tokens(const int *top_idx, int R, int n, int *offsets, i
 // Tokens per CTA: as many as their rows' vectors take to fill its threads (or,
 // where a warp looks for each slot's row, as their slots take to fill its
 // warps), while that leaves four CTAs an SM.
-int tokens_per_cta(int tokens, int k, int nvec, bool search)
+int tokens_per_cta(int tokens, int k, int threads, bool search)
 {
     const DeviceInfo *dev = device_info();
     const int sms = dev ? dev->sm_count : 152;
-    int tpc = nvec > 0 && nvec < ROW_THREADS ? ROW_THREADS / nvec : 1;
+    int tpc = threads > 0 && threads < ROW_THREADS ? ROW_THREADS / threads : 1;
     if (search && tpc < (SMALL_THREADS / 32) / k) tpc = (SMALL_THREADS / 32) / k;
     if (tpc > SMOE_MAX_TOP_K / k) tpc = SMOE_MAX_TOP_K / k;
     while (tpc > 1 && tokens / tpc < 4 * sms) tpc /= 2;
     return tpc;
+}
+
+// Threads that a row takes: one a vector, or a warp for ODD_COLS columns.
+template <int VE>
+int row_threads(int d)
+{
+    return VE == 1 ? (d + ODD_COLS - 1) / ODD_COLS * 32 : d / VE;
 }
 
 // (CTAs of tpc tokens, column blocks).  Every column block looks for its slots'
@@ -769,7 +850,7 @@ int tokens_per_cta(int tokens, int k, int nvec, bool search)
 template <typename T, int VE>
 dim3 row_grid(int tokens, int tpc, int d, bool search)
 {
-    long long cols = (static_cast<long long>(tpc) * (d / VE) + ROW_THREADS - 1) / ROW_THREADS;
+    long long cols = (static_cast<long long>(tpc) * row_threads<VE>(d) + ROW_THREADS - 1) / ROW_THREADS;
     const int x = (tokens + tpc - 1) / tpc;
     if (search) {
         const DeviceInfo *dev = device_info();
@@ -782,7 +863,7 @@ dim3 row_grid(int tokens, int tpc, int d, bool search)
 template <typename T, int VE>
 cudaError_t gather_t(const void *x, const int *place, int tokens, int k, int d, void *xs, cudaStream_t stream)
 {
-    const int tpc = tokens_per_cta(tokens, k, d / VE, false);
+    const int tpc = tokens_per_cta(tokens, k, row_threads<VE>(d), false);
     return launch_pdl(gather_rows<T, VE>, row_grid<T, VE>(tokens, tpc, d, false), dim3(ROW_THREADS), 0, stream,
                       static_cast<const T *>(x), place, tokens, tpc, k, d, static_cast<T *>(xs));
 }
@@ -791,7 +872,7 @@ template <typename T, int VE>
 cudaError_t sum_t(const void *ys, const int *place, const float *w, int tokens, int k, int d, void *out, unsigned *status,
                   cudaStream_t stream)
 {
-    const int tpc = tokens_per_cta(tokens, 1, d / VE, false);
+    const int tpc = tokens_per_cta(tokens, 1, row_threads<VE>(d), false);
     return launch_pdl(sum_rows<T, VE>, row_grid<T, VE>(tokens, tpc, d, false), dim3(ROW_THREADS), 0, stream,
                       static_cast<const T *>(ys), place, w, tokens, tpc, k, d, static_cast<T *>(out), status);
 }
@@ -809,7 +890,7 @@ template <typename T, int VE>
 cudaError_t small_t(const int *top_idx, int tokens, int k, int n, const void *x, int d, int *offsets, int *order,
                     int *place, void *xs, cudaStream_t stream)
 {
-    const int tpc = tokens_per_cta(tokens, k, xs ? d / VE : 0, true);
+    const int tpc = tokens_per_cta(tokens, k, xs ? row_threads<VE>(d) : 0, true);
     dim3 grid = row_grid<T, VE>(tokens, tpc, xs ? d : 0, true);
     grid.x += 1;
     const size_t words = static_cast<size_t>(n) + 1 > SMOE_MAX_TOP_K ? static_cast<size_t>(n) + 1 : SMOE_MAX_TOP_K;
@@ -825,7 +906,7 @@ template <typename T, int VE>
 cudaError_t middle_t(const int *top_idx, int tokens, int k, int n, int nchunks, int chunk, const int *cum, const void *x, int d,
                      int *offsets, int *order, int *place, void *xs, cudaStream_t stream)
 {
-    const int tpc = tokens_per_cta(tokens, k, xs ? d / VE : 0, true);
+    const int tpc = tokens_per_cta(tokens, k, xs ? row_threads<VE>(d) : 0, true);
     dim3 grid = row_grid<T, VE>(tokens, tpc, xs ? d : 0, true);
     grid.x += static_cast<unsigned>((n + SMALL_THREADS / 32) / (SMALL_THREADS / 32));
     return launch_pdl(dispatch_middle<T, VE>, grid, dim3(SMALL_THREADS), 0, stream, top_idx, tokens, tpc, k, n, nchunks, chunk,
