@@ -304,7 +304,7 @@ __global__ void __launch_bounds__(TC_THREADS, 1) q8_tc(const __grid_constant__ T
 
     if (warp == W_WARP) {
         if (elect_one()) {
-            uint32_t s = 0, p = 1;  // parity of the release before this round; none waited for in the first
+            uint32_t s = 0, p = 1;  // parity of the slot's release one lap ago; none in the first
             bool round0 = true;
             for (long long it = first; it < nitems && !failed; it += stride) {
                 const Tile t = tile_at(a, static_cast<int>(it / mgroups), ntiles);
