@@ -98,6 +98,17 @@ def test_topk_rows(smoe, T, E, k, kind):
     np.testing.assert_allclose(w.cpu().numpy(), rw, rtol=U * (span + 16), atol=1e-37)
 
 
+@pytest.mark.parametrize("T,E,k", [(10001, 128, 8), (12003, 64, 3), (10002, 40, 16), (9999, 256, 9), (10003, 512, 1), (9730, 128, 8)])
+@pytest.mark.parametrize("kind", ["plain", "masked", "ties"])
+def test_topk_of_many_rows(smoe, T, E, k, kind):
+    """More rows than a wave of warps."""
+    l = _logits(T, E, 21, masked=kind == "masked", ties=kind == "ties")
+    idx, w = _topk(smoe, l, k)
+    ri, rw = _select_ref(l, k)
+    np.testing.assert_array_equal(idx.cpu().numpy(), ri)
+    np.testing.assert_allclose(w.cpu().numpy(), rw, rtol=U * (12 + 16), atol=1e-37)  # |l| < 6
+
+
 @pytest.mark.parametrize("E", [20, 600])
 def test_topk_rows_nan_and_infinities(smoe, E):
     l = np.full((4, E), -np.inf, np.float32)
