@@ -836,8 +836,15 @@ cudaError_t launch_tc(const TcArgs &args, long long most_items, int sms, cudaStr
     using F = Form<NT>;
     constexpr size_t smem = tc_smem<NT>();
     auto k = q8_tc<T, NT>;
-    cudaError_t e = ensure_dynamic_smem(k, smem);
-    if (e != cudaSuccess) return e;
+    // one size for every launch of this kernel: asked for once per device
+    static std::atomic<bool> opted[64];
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
+    if (!opted[dev].load(std::memory_order_relaxed)) {
+        const cudaError_t e = ensure_dynamic_smem(k, smem);
+        if (e != cudaSuccess) return e;
+        opted[dev].store(true, std::memory_order_relaxed);
+    }
     // few items: their K ranges are split over clusters of 2, 4 or 8 CTAs,
     // as many as the device holds at once, each at least two chunks
     int size = F::CL;
