@@ -15,6 +15,11 @@ namespace {
 
 // ---------------------------------------------------------------- quantiser
 
+// SiLU with the division by the reciprocal instruction (2 units in the last
+// place; 0 where the exponential is beyond 2^126): the quantiser is bound by
+// instructions, and its step is 2^16 times coarser.
+__device__ __forceinline__ float silu_row(float v) { return __fdividef(v, 1.0f + expf(-v)); }
+
 // The VE values at column c of row r: x itself, or silu(gate) * up of a row
 // [gate | up] of 2 cols.
 template <typename T, int VE, bool ACT>
@@ -29,7 +34,7 @@ __device__ __forceinline__ void quant_values(const T *row, int cols, int c, floa
         b.load(row + cols + c);
         b.get(u);
 #pragma unroll
-        for (int i = 0; i < VE; ++i) v[i] = silu_f32(v[i]) * u[i];
+        for (int i = 0; i < VE; ++i) v[i] = silu_row(v[i]) * u[i];
     }
 }
 
@@ -96,18 +101,24 @@ __device__ __forceinline__ void put_codes(int8_t *q, const uint32_t (&c)[8])
 __device__ __forceinline__ void put_codes(int8_t *q, const uint32_t (&c)[4]) { *reinterpret_cast<uint32_t *>(q) = pack4(c); }
 __device__ __forceinline__ void put_codes(int8_t *q, const uint32_t (&c)[1]) { *q = static_cast<int8_t>(c[0]); }
 
+// Vectors that a thread keeps between the two passes over its row.
+template <int VE, bool ACT, int THREADS>
+constexpr int held_vectors()
+{
+    return VE == 1 ? 8 : (THREADS <= 128 && !ACT ? 64 / VE : 32 / VE);
+}
+
 // One CTA of THREADS per row: the largest magnitude, then the rounding.  A
 // thread keeps its first NV vectors, so that a row of up to NV x THREADS
 // vectors is read (and its activation computed) once; what is beyond is read
-// again.  Bound by instruction issue: with two warps a row instead of eight
-// the row's own work (reductions, two divisions) is done fewer times, which
-// pays once there are rows for the whole device (4096 rows of 4096 bf16 9
-// against 13.6 us); a single row is faster on eight (1.6 us).
+// again.  Bound by instruction issue: with fewer warps a row, the row's own
+// work (reductions, two divisions) is done fewer times, which pays once there
+// are rows for the whole device (launch_quantize_rows).
 template <typename T, int VE, bool ACT, int THREADS>
 __global__ void __launch_bounds__(THREADS) quantize_rows(const T *__restrict__ x, int cols, int8_t *__restrict__ q,
                                                          float *__restrict__ scales)
 {
-    constexpr int NV = VE == 1 ? 8 : (THREADS == 64 && !ACT ? 64 / VE : 32 / VE);
+    constexpr int NV = held_vectors<VE, ACT, THREADS>();
     __shared__ uint32_t warp_most[THREADS / 32];
     pdl_launch_dependents();
     pdl_wait();
@@ -336,10 +347,20 @@ cudaError_t quant_t(const void *x, int rows, int cols, int8_t *q, float *scales,
 {
     const DeviceInfo *dev = device_info();
     if (!dev) return cudaErrorInvalidDevice;
-    const dim3 grid(static_cast<unsigned>(rows));
-    if (rows >= 4 * dev->sm_count)
-        return launch_pdl(quantize_rows<T, VE, ACT, 64>, grid, dim3(64), 0, stream, static_cast<const T *>(x), cols, q, scales);
-    return launch_pdl(quantize_rows<T, VE, ACT, 256>, grid, dim3(256), 0, stream, static_cast<const T *>(x), cols, q, scales);
+    auto go = [&](auto kernel, int threads) {
+        return launch_pdl(kernel, dim3(static_cast<unsigned>(rows)), dim3(static_cast<unsigned>(threads)), 0, stream,
+                          static_cast<const T *>(x), cols, q, scales);
+    };
+    // Few rows: eight warps each.  Rows for the whole device: the fewest warps
+    // that keep the row between its two passes.  Measured (us, bf16) on 64,
+    // 128 and 256 threads: 4096 rows of 4096 7.8 / 7.9 / 10.6, 2000 of 16384
+    // 25.0 / 20.0 / 17.3 (one warp is no faster than two: 8000 rows of 512 with
+    // the activation 8.7 / 8.6).
+    if (rows >= 4 * dev->sm_count) {
+        if (cols <= 64 * VE * held_vectors<VE, ACT, 64>()) return go(quantize_rows<T, VE, ACT, 64>, 64);
+        if (cols <= 128 * VE * held_vectors<VE, ACT, 128>()) return go(quantize_rows<T, VE, ACT, 128>, 128);
+    }
+    return go(quantize_rows<T, VE, ACT, 256>, 256);
 }
 
 template <typename T, int VE>
