@@ -10,6 +10,7 @@
 
 ``python examples/moe_layer.py`` runs both on a GPU with seeded weights.
 """
+import contextlib
 import os
 import sys
 
@@ -43,7 +44,7 @@ class Q8Layer:
 
     def __init__(self, gate, gate_up, down, k, max_tokens):
         dev = gate.device
-        self.gate, self.k = gate, k
+        self.gate, self.gate32, self.k = gate, gate.view(torch.bfloat16).float(), k
         self.n, self.d_ff, self.d = gate_up.shape[0], down.shape[2], down.shape[1]
         self.gu, self.gu_scales = quantize_weights(gate_up)
         self.dn, self.dn_scales = quantize_weights(down)
@@ -67,8 +68,12 @@ class Q8Layer:
         """out[t] (bf16) = the layer's output for x[t] (f32 [tokens, d_model])."""
         T, k, n, d, ff = x.shape[0], self.k, self.n, self.d, self.d_ff
         R = T * k
-        smoe.matvec_bf16_batch([self.gate] * T, [x.data_ptr() + 4 * d * t for t in range(T)],
-                               [self.logits.data_ptr() + 4 * n * t for t in range(T)], [n] * T, [d] * T, stream)
+        if T <= 64:
+            smoe.matvec_bf16_batch([self.gate] * T, [x.data_ptr() + 4 * d * t for t in range(T)],
+                                   [self.logits.data_ptr() + 4 * n * t for t in range(T)], [n] * T, [d] * T, stream)
+        else:  # a matvec a token would read the router's weights T times
+            with torch.cuda.stream(stream) if stream is not None else contextlib.nullcontext():
+                torch.mm(x, self.gate32.t(), out=self.logits[:T])
         smoe.smoe_topk_rows(self.logits, T, n, n, k, self.idx, self.w, stream)
         smoe.smoe_dispatch_tokens(self.idx, T, k, n, None, smoe.SMOE_F32, 0, self.offsets, self.order, self.place, None,
                                   self.ws, self.need, stream)
