@@ -91,20 +91,91 @@ __device__ __forceinline__ void select_by_rounds(uint32_t (&key)[V], int k, uint
     }
 }
 
-// n <= 32 V: one warp per row, V logits per lane.  Up to k = 16 the row is
-// first cut down: the k-th largest of the lanes' maxima is a lower bound of
-// the k-th largest logit, and the few logits not below it (k and one or two
-// more, as a rule) are gathered one to a lane in expert order, where counting
-// the larger ones before and after gives each its rank.  That takes half the
-// instructions of k rounds over the whole row, which is what bounds this
-// kernel (32,768 rows of 128, k = 8).  Where more than 32 logits are left
-// (ties) or k > 16 the rounds select.
+// The filter of a row for k <= FILTER_K: the k-th largest of the lanes' maxima
+// is a lower bound of the k-th largest logit; the few logits not below it (k
+// and one or two more, as a rule) are gathered one to a lane in expert order,
+// where counting the larger ones gives each its rank.  Against k rounds over
+// the whole row (us, 32,768 rows): 128 experts, k = 8 11.5 / 17.5, k = 16 15.9 /
+// 29.6; 512 experts, k = 8 24.3 / 49.5.
+constexpr int FILTER_K = 16;
+
+// The bound from every lane's maximum `most`; first: the row's largest key.
+__device__ __forceinline__ uint32_t filter_bound(uint32_t most, int k, uint32_t &first)
+{
+    first = __reduce_max_sync(FULL_MASK, most);
+    uint32_t bound = first;
+    if (most == first) most = 0u;
+#pragma unroll 4
+    for (int r = 1; r < k; ++r) {
+        const uint32_t top = __reduce_max_sync(FULL_MASK, most);
+        if (top != 0u) bound = top;  // 0: every lane's maximum is among them
+        if (most == top) most = 0u;
+    }
+    return bound;
+}
+
+// The filter's candidates of one row: keys in expert order, then zeros.
+struct Candidates {
+    uint32_t key[32];
+    uint16_t expert[32];
+};
+
+// One step of the gathering: this lane's key (expert e) joins if `in`.
+__device__ __forceinline__ void gather_candidate(Candidates &c, bool in, uint32_t key, int e, int &count)
+{
+    const uint32_t m = __ballot_sync(FULL_MASK, in);
+    const int at = count + __popc(m & ((1u << (threadIdx.x & 31)) - 1u));
+    if (in && at < 32) {
+        c.key[at] = key;
+        c.expert[at] = static_cast<uint16_t>(e);
+    }
+    count += __popc(m);
+}
+
+// Ranks and weighs `count` <= 32 candidates and writes the row's k selected.
+__device__ __forceinline__ void write_candidates(const Candidates &cand, int count, uint32_t first, int k,
+                                                 int *__restrict__ idx, float *__restrict__ w)
+{
+    const int lane = threadIdx.x & 31;
+    __syncwarp();
+    // the larger ones, and of the equal ones those before it (in expert order)
+    const uint32_t mine = cand.key[lane];
+    int rank = 0;
+    for (int c = 0; c < count; c += 4) {
+        const uint4 o = *reinterpret_cast<const uint4 *>(&cand.key[c]);
+        rank += o.x >= mine + (c >= lane ? 1u : 0u);
+        rank += o.y >= mine + (c + 1 >= lane ? 1u : 0u);
+        rank += o.z >= mine + (c + 2 >= lane ? 1u : 0u);
+        rank += o.w >= mine + (c + 3 >= lane ? 1u : 0u);
+    }
+    const bool sel = lane < count && rank < k, there = sel && mine != kKeyNegInf;
+    const float x = there ? expf(value_of_key(mine) - value_of_key(first)) : 0.f;
+    float sum = x;
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1) sum += __shfl_xor_sync(FULL_MASK, sum, off);
+    if (sel) {
+        idx[rank] = there ? static_cast<int>(cand.expert[lane]) : -1;
+        w[rank] = there ? x / sum : 0.f;
+    }
+}
+
+// A row of nothing but masked experts.
+__device__ __forceinline__ void write_masked(int k, int *__restrict__ idx, float *__restrict__ w)
+{
+    for (int r = threadIdx.x & 31; r < k; r += 32) {
+        idx[r] = -1;
+        w[r] = 0.f;
+    }
+}
+
+// n <= 32 V: one warp per row, V logits per lane; the filter up to k = FILTER_K,
+// rounds above it or where more than 32 candidates are left (ties).  Bound by
+// instruction issue (32,768 rows of 128, k = 8: 340 a row).
 template <int V>
 __global__ void __launch_bounds__(TOPK_WARPS * 32) topk_rows_warp(const float *__restrict__ logits, int T, int n, int ld,
                                                                   int k, int *__restrict__ idx, float *__restrict__ w)
 {
-    __shared__ __align__(16) uint32_t left_key[TOPK_WARPS][32];  // in expert order, then zeros
-    __shared__ uint16_t left_exp[TOPK_WARPS][32];
+    __shared__ __align__(16) Candidates cands[TOPK_WARPS];
     const int wi = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int t = blockIdx.x * TOPK_WARPS + wi;
     pdl_launch_dependents();
@@ -116,63 +187,23 @@ __global__ void __launch_bounds__(TOPK_WARPS * 32) topk_rows_warp(const float *_
     uint32_t key[V];
 #pragma unroll
     for (int i = 0; i < V; ++i) key[i] = i * 32 + lane < n ? value_key(row[i * 32 + lane]) : 0u;
-    if (k <= 16) {
-        uint32_t most = key[0];
+    if (k <= FILTER_K) {
+        uint32_t most = key[0], first;
 #pragma unroll
         for (int i = 1; i < V; ++i) most = max(most, key[i]);
-        const uint32_t first = __reduce_max_sync(FULL_MASK, most);
-        if (first == kKeyNegInf) {  // nothing but masked experts
-            if (lane < k) {
-                idx[lane] = -1;
-                w[lane] = 0.f;
-            }
+        const uint32_t bound = filter_bound(most, k, first);
+        if (first == kKeyNegInf) {
+            write_masked(k, idx, w);
             return;
         }
-        uint32_t bound = first;
-        if (most == first) most = 0u;
-#pragma unroll 4
-        for (int r = 1; r < k; ++r) {
-            const uint32_t top = __reduce_max_sync(FULL_MASK, most);
-            if (top != 0u) bound = top;  // 0: every lane's maximum is among them
-            if (most == top) most = 0u;
-        }
-        int count = 0;
-        const uint32_t before = (1u << lane) - 1u;
-        left_key[wi][lane] = 0u;
+        Candidates &c = cands[wi];
+        c.key[lane] = 0u;
         __syncwarp();
+        int count = 0;
 #pragma unroll
-        for (int i = 0; i < V; ++i) {
-            const bool in = key[i] >= bound;
-            const uint32_t m = __ballot_sync(FULL_MASK, in);
-            const int at = count + __popc(m & before);
-            if (in && at < 32) {
-                left_key[wi][at] = key[i];
-                left_exp[wi][at] = static_cast<uint16_t>(i * 32 + lane);
-            }
-            count += __popc(m);
-        }
+        for (int i = 0; i < V; ++i) gather_candidate(c, key[i] >= bound, key[i], i * 32 + lane, count);
         if (count <= 32) {
-            __syncwarp();
-            // a candidate's rank: the larger ones, and of the equal ones those
-            // before it (in expert order)
-            const uint32_t mine = left_key[wi][lane];
-            int rank = 0;
-            for (int c = 0; c < count; c += 4) {
-                const uint4 o = *reinterpret_cast<const uint4 *>(&left_key[wi][c]);
-                rank += o.x >= mine + (c >= lane ? 1u : 0u);
-                rank += o.y >= mine + (c + 1 >= lane ? 1u : 0u);
-                rank += o.z >= mine + (c + 2 >= lane ? 1u : 0u);
-                rank += o.w >= mine + (c + 3 >= lane ? 1u : 0u);
-            }
-            const bool sel = lane < count && rank < k, there = sel && mine != kKeyNegInf;
-            const float x = there ? expf(value_of_key(mine) - value_of_key(first)) : 0.f;
-            float sum = x;
-#pragma unroll
-            for (int off = 16; off > 0; off >>= 1) sum += __shfl_xor_sync(FULL_MASK, sum, off);
-            if (sel) {
-                idx[rank] = there ? static_cast<int>(left_exp[wi][lane]) : -1;
-                w[rank] = there ? x / sum : 0.f;
-            }
+            write_candidates(c, count, first, k, idx, w);
             return;
         }
     }
@@ -182,9 +213,88 @@ __global__ void __launch_bounds__(TOPK_WARPS * 32) topk_rows_warp(const float *_
     write_row(ka, kb, ea, eb, k, idx, w);
 }
 
+// n <= LONG_EXPERTS, k <= FILTER_K: the same filter over two passes of the row,
+// the second out of the cache; where more than 32 candidates are left (ties), k
+// passes that each find the next one in order.  Against one CTA per row
+// (topk_rows_block; us, k = 8): 1 row of 520 3.1 / 4.9, 1 of 1024 4.0 / 4.2,
+// 3000 of 1024 8.9 / 24.4, 32,768 of 520 37 / 218; but 1 of 8192 19.4 / 7.1.
+constexpr int LONG_EXPERTS = 2048;
+
+__global__ void __launch_bounds__(TOPK_WARPS * 32) topk_rows_long(const float *__restrict__ logits, int T, int n, int ld,
+                                                                  int k, int *__restrict__ idx, float *__restrict__ w)
+{
+    __shared__ __align__(16) Candidates cands[TOPK_WARPS];
+    const int wi = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int t = blockIdx.x * (blockDim.x >> 5) + wi;
+    pdl_launch_dependents();
+    pdl_wait();
+    if (t >= T) return;
+    const float *row = logits + static_cast<size_t>(t) * ld;
+    idx += static_cast<size_t>(t) * k;
+    w += static_cast<size_t>(t) * k;
+    // eight loads in flight at a time
+    uint32_t most = 0u, first;
+    float v[8];
+    auto fetch = [&](int e0) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[i] = e0 + i * 32 + lane < n ? row[e0 + i * 32 + lane] : 0.f;
+    };
+    for (int e0 = 0; e0 < n; e0 += 256) {
+        fetch(e0);
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            if (e0 + i * 32 + lane < n) most = max(most, value_key(v[i]));
+    }
+    const uint32_t bound = filter_bound(most, k, first);
+    if (first == kKeyNegInf) {
+        write_masked(k, idx, w);
+        return;
+    }
+    Candidates &c = cands[wi];
+    c.key[lane] = 0u;
+    __syncwarp();
+    int count = 0;
+    for (int e0 = 0; e0 < n; e0 += 256) {
+        fetch(e0);
+        uint32_t key[8], in = 0u;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            key[i] = e0 + i * 32 + lane < n ? value_key(v[i]) : 0u;
+            in |= static_cast<uint32_t>(key[i] >= bound) << i;
+        }
+        const uint32_t any = __reduce_or_sync(FULL_MASK, in);
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            if (any >> i & 1u) gather_candidate(c, in >> i & 1u, key[i], e0 + i * 32 + lane, count);
+    }
+    if (count <= 32) {
+        write_candidates(c, count, first, k, idx, w);
+        return;
+    }
+    uint32_t ka = 0u, last = 0xFFFFFFFFu;
+    int ea = -1, last_e = -1;
+    for (int r = 0; r < k; ++r) {
+        uint32_t best = 0u, be = 0xFFFFFFFFu;
+        for (int e = lane; e < n; e += 32) {
+            const uint32_t key = value_key(row[e]);
+            if ((key < last || (key == last && e > last_e)) && key > best) {
+                best = key;
+                be = static_cast<uint32_t>(e);
+            }
+        }
+        last = __reduce_max_sync(FULL_MASK, best);
+        last_e = static_cast<int>(__reduce_min_sync(FULL_MASK, best == last ? be : 0xFFFFFFFFu));
+        if (lane == r) {
+            ka = last;
+            ea = last_e;
+        }
+    }
+    write_row(ka, 0u, ea, -1, k, idx, w);
+}
+
 constexpr int TOPK_BLOCK = 256;
 
-// Any n: one CTA per row, the keys in shared memory.
+// Any n and k: one CTA per row, k rounds over the keys in shared memory.
 __global__ void __launch_bounds__(TOPK_BLOCK) topk_rows_block(const float *__restrict__ logits, int n, int ld, int k,
                                                               int *__restrict__ idx, float *__restrict__ w)
 {
@@ -780,6 +890,11 @@ cudaError_t launch_topk_rows(const float *logits, int T, int n, int ld, int k, i
     if (n <= 128) return launch_pdl(topk_rows_warp<4>, grid, block, 0, stream, logits, T, n, ld, k, idx, w);
     if (n <= 256) return launch_pdl(topk_rows_warp<8>, grid, block, 0, stream, logits, T, n, ld, k, idx, w);
     if (n <= 512) return launch_pdl(topk_rows_warp<16>, grid, block, 0, stream, logits, T, n, ld, k, idx, w);
+    if (k <= FILTER_K && n <= LONG_EXPERTS) {
+        const int warps = T <= 1024 ? 1 : TOPK_WARPS;  // few rows: an SM each
+        return launch_pdl(topk_rows_long, dim3(static_cast<unsigned>((T + warps - 1) / warps)),
+                          dim3(static_cast<unsigned>(warps * 32)), 0, stream, logits, T, n, ld, k, idx, w);
+    }
     const size_t smem = static_cast<size_t>(n) * sizeof(uint32_t);
     return launch_pdl(topk_rows_block, dim3(static_cast<unsigned>(T)), dim3(TOPK_BLOCK), smem, stream, logits, n, ld, k,
                       idx, w);

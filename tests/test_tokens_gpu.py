@@ -98,6 +98,17 @@ def test_topk_rows(smoe, T, E, k, kind):
     np.testing.assert_allclose(w.cpu().numpy(), rw, rtol=U * (span + 16), atol=1e-37)
 
 
+@pytest.mark.parametrize("T,E,k", [(9, 513, 16), (70, 8192, 8), (5, 2047, 16), (1030, 2048, 3), (5, 2049, 16), (33, 1000, 17),
+                                   (4, 5000, 40)])
+@pytest.mark.parametrize("kind", ["plain", "masked", "ties"])
+def test_topk_of_many_experts(smoe, T, E, k, kind):
+    l = _logits(T, E, 22, masked=kind == "masked", ties=kind == "ties")
+    idx, w = _topk(smoe, l, k, ld=E + 3)
+    ri, rw = _select_ref(l, k)
+    np.testing.assert_array_equal(idx.cpu().numpy(), ri)
+    np.testing.assert_allclose(w.cpu().numpy(), rw, rtol=U * (12 + 16), atol=1e-37)  # |l| < 6
+
+
 @pytest.mark.parametrize("T,E,k", [(10001, 128, 8), (12003, 64, 3), (10002, 40, 16), (9999, 256, 9), (10003, 512, 1), (9730, 128, 8)])
 @pytest.mark.parametrize("kind", ["plain", "masked", "ties"])
 def test_topk_of_many_rows(smoe, T, E, k, kind):
