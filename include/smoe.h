@@ -6,7 +6,8 @@
  * "Metal Compute Kernels"; each declaration names the section it follows.
  * Two support functions are not steps of that method: smoe_copy (a step's
  * host I/O) and smoe_selftest_bounded_wait (a diagnostic of the device-side
- * failure detection).
+ * failure detection); nor are the calls for many tokens and for 8-bit weights,
+ * which are defined where they are declared.
  *
  * Common conventions
  * ------------------
