@@ -159,7 +159,8 @@ __device__ __forceinline__ void write_candidates(const Candidates &cand, int cou
     }
 }
 
-// A row of nothing but masked experts.
+// A row whose k selected are all masked experts.  That no logit beats -inf does
+// not say so: a NaN ranks below it, and is selected where fewer than k are -inf.
 __device__ __forceinline__ void write_masked(int k, int *__restrict__ idx, float *__restrict__ w)
 {
     for (int r = threadIdx.x & 31; r < k; r += 32) {
@@ -193,8 +194,13 @@ __global__ void __launch_bounds__(TOPK_WARPS * 32) topk_rows_warp(const float *_
         for (int i = 1; i < V; ++i) most = max(most, key[i]);
         const uint32_t bound = filter_bound(most, k, first);
         if (first == kKeyNegInf) {
-            write_masked(k, idx, w);
-            return;
+            int masked = 0;
+#pragma unroll
+            for (int i = 0; i < V; ++i) masked += key[i] == kKeyNegInf;
+            if (__reduce_add_sync(FULL_MASK, masked) >= k) {
+                write_masked(k, idx, w);
+                return;
+            }
         }
         Candidates &c = cands[wi];
         c.key[lane] = 0u;
@@ -247,8 +253,13 @@ __global__ void __launch_bounds__(TOPK_WARPS * 32) topk_rows_long(const float *_
     }
     const uint32_t bound = filter_bound(most, k, first);
     if (first == kKeyNegInf) {
-        write_masked(k, idx, w);
-        return;
+        int masked = 0;
+        for (int e0 = 0; e0 < n && masked < k; e0 += 32)
+            masked += __popc(__ballot_sync(FULL_MASK, e0 + lane < n && value_key(row[e0 + lane]) == kKeyNegInf));
+        if (masked >= k) {
+            write_masked(k, idx, w);
+            return;
+        }
     }
     Candidates &c = cands[wi];
     c.key[lane] = 0u;
