@@ -611,7 +611,9 @@ int smoe_combine_tokens_backward(const void *d_out, const void *ys, int dtype,
 /*
  * Quantises rows of v = x (act SMOE_Q8_PLAIN; x: [rows x cols]) or of
  * v = SiLU(gate) * up (SMOE_Q8_SILU_MUL; x: [rows x 2 cols], gate the first
- * cols of a row and up the last), in f32:
+ * cols of a row and up the last), in f32 (SiLU within 2^-20
+ * of its value, or 2^-142; scale and codes from that v by f32 operations that
+ * are rounded once each):
  *
  *   top = max |v|,  scales[r] = top / 127,
  *   q[r][c] = v (127 / top) rounded to the nearest integer, ties to even.

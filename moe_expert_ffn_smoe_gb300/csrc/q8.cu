@@ -15,10 +15,19 @@ namespace {
 
 // ---------------------------------------------------------------- quantiser
 
-// SiLU with the division by the reciprocal instruction (2 units in the last
-// place; 0 where the exponential is beyond 2^126): the quantiser is bound by
-// instructions, and its step is 2^16 times coarser.
-__device__ __forceinline__ float silu_row(float v) { return __fdividef(v, 1.0f + expf(-v)); }
+// SiLU, v / (1 + e^-v), as max(v, 0) - |v| e / (1 + e) with e = e^-|v|: e itself
+// is never beyond what f32 holds, where SiLU(v) times a large factor may still
+// be its row's largest value, and the divisor stays within [1, 2], so that the
+// reciprocal instruction alone does (1 unit in the last place; the quantiser is
+// bound by instructions, and its step is 2^16 times coarser).  32,768 rows of
+// 1536 bf16 52.9 us, as a division of v or v e by 1 + e 60.8.
+__device__ __forceinline__ float silu_row(float v)
+{
+    const float e = expf(-fabsf(v));
+    float r;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.0f + e));
+    return fmaf(-fabsf(v), e * r, fmaxf(v, 0.f));
+}
 
 // The VE values at column c of row r: x itself, or silu(gate) * up of a row
 // [gate | up] of 2 cols.
