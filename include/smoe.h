@@ -533,8 +533,9 @@ int smoe_topk_rows(const float *logits, int n_tokens, int n_experts, int ld,
  *
  *   d_logits[t][top_idx[t][r]] = w_r (dw_r - sum over q of w_q dw_q),
  *
- * 0 for every other logit.  d_logits: f32 [n_tokens x n_experts], 16-byte
- * aligned, written whole.
+ * 0 for every other logit.  A slot whose index is outside [0, n_experts) has no
+ * expert and counts for nothing in the sum.  d_logits: f32 [n_tokens x
+ * n_experts], 16-byte aligned, written whole.
  */
 int smoe_topk_rows_backward(const int *top_idx, const float *top_w,
                             const float *d_top_w, int n_tokens, int n_experts,

@@ -390,7 +390,7 @@ __global__ void __launch_bounds__(TOPK_WARPS * 32) topk_rows_grad(const int *__r
         float c = 0.f;
 #pragma unroll
         for (int h = 0; h < 2; ++h)
-            if (e[i][h] >= 0) c = fmaf(wr[i][h], g[i][h], c);
+            if (e[i][h] >= 0 && e[i][h] < n) c = fmaf(wr[i][h], g[i][h], c);
 #pragma unroll
         for (int off = 16; off > 0; off >>= 1) c += __shfl_xor_sync(FULL_MASK, c, off);
 #pragma unroll
