@@ -197,12 +197,12 @@ __global__ void __launch_bounds__(PLAN_THREADS) plan_tiles(const int *__restrict
                                                            int max_tiles, int *__restrict__ ntiles,
                                                            Tile *__restrict__ tiles, unsigned *status)
 {
-    __shared__ int warp_sums[PLAN_THREADS / 32];
-    __shared__ int run_s;
+    __shared__ long long warp_sums[PLAN_THREADS / 32];
+    __shared__ long long run_s;
     pdl_launch_dependents();
     pdl_wait();
     const int tid = threadIdx.x, lane = tid & 31, wi = tid >> 5;
-    int run = 0;
+    long long run = 0;  // 64 bits: ranges that overlap (reported) can add up to more than 32
     for (int b = 0; b <= n; b += PLAN_THREADS) {
         const int e = b + tid;
         int lo = 0, hi = 0;
@@ -215,24 +215,24 @@ __global__ void __launch_bounds__(PLAN_THREADS) plan_tiles(const int *__restrict
             }
         }
         const int cnt = (hi - lo + step - 1) / step;
-        int inc = cnt;
+        long long inc = cnt;
 #pragma unroll
         for (int off = 1; off < 32; off <<= 1) {
-            const int o = __shfl_up_sync(FULL_MASK, inc, off);
+            const long long o = __shfl_up_sync(FULL_MASK, inc, off);
             if (lane >= off) inc += o;
         }
         if (lane == 31) warp_sums[wi] = inc;
         __syncthreads();
-        int before = run;
+        long long before = run;
         for (int i = 0; i < wi; ++i) before += warp_sums[i];
         if (tid == PLAN_THREADS - 1) run_s = before + inc;
-        const int t0 = before + inc - cnt;
+        const long long t0 = before + inc - cnt;
         for (int i = 0; i < cnt && t0 + i < max_tiles; ++i)
             tiles[t0 + i] = Tile{e < n ? e : -1, lo + i * step, min(step, hi - lo - i * step), 0};
         __syncthreads();
         run = run_s;
     }
-    if (tid == 0) *ntiles = min(run, max_tiles);
+    if (tid == 0) *ntiles = static_cast<int>(min(run, static_cast<long long>(max_tiles)));
 }
 
 // ---------------------------------------------------------------- products

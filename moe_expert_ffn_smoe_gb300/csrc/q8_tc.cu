@@ -661,14 +661,14 @@ struct PrepArgs {
 // expert's.
 __global__ void __launch_bounds__(PREP_THREADS) q8_prep(const PrepArgs a)
 {
-    __shared__ int warp_sums[PREP_THREADS / 32];
-    __shared__ int run_s;
+    __shared__ long long warp_sums[PREP_THREADS / 32];
+    __shared__ long long run_s;
     pdl_launch_dependents();
     pdl_wait();
     const int tid = threadIdx.x;
     if (a.offsets && blockIdx.x == 0) {
         const int lane = tid & 31, wi = tid >> 5;
-        int run = 0;
+        long long run = 0;  // 64 bits: ranges that overlap (reported) can add up to more than 32
         for (int b = 0; b < a.n; b += PREP_THREADS) {
             const int e = b + tid;
             int lo = 0, hi = 0;
@@ -683,24 +683,24 @@ __global__ void __launch_bounds__(PREP_THREADS) q8_prep(const PrepArgs a)
             int cnt = (hi - lo + a.nt - 1) / a.nt;
             const int step = cnt > 0 ? ((hi - lo + cnt - 1) / cnt + a.unit - 1) / a.unit * a.unit : a.unit;
             cnt = (hi - lo + step - 1) / step;
-            int inc = cnt;
+            long long inc = cnt;
 #pragma unroll
             for (int off = 1; off < 32; off <<= 1) {
-                const int o = __shfl_up_sync(FULL_MASK, inc, off);
+                const long long o = __shfl_up_sync(FULL_MASK, inc, off);
                 if (lane >= off) inc += o;
             }
             if (lane == 31) warp_sums[wi] = inc;
             __syncthreads();
-            int before = run;
+            long long before = run;
             for (int i = 0; i < wi; ++i) before += warp_sums[i];
             if (tid == PREP_THREADS - 1) run_s = before + inc;
-            const int t0 = before + inc - cnt;
+            const long long t0 = before + inc - cnt;
             for (int i = 0; i < cnt && t0 + i < a.max_tiles; ++i)
                 a.tiles[t0 + i] = Tile{e, lo + i * step, min(step, hi - lo - i * step), 0};
             __syncthreads();
             run = run_s;
         }
-        if (tid == 0) *a.ntiles = min(run, a.max_tiles);
+        if (tid == 0) *a.ntiles = static_cast<int>(min(run, static_cast<long long>(a.max_tiles)));
         return;
     }
     const int b0 = a.offsets ? 1 : 0, blocks = gridDim.x - b0;
