@@ -655,9 +655,9 @@ int smoe_matmul_q8(const int8_t *xq, const float *x_scales, int n_rows,
  * product, the tokens are quantised once), or i = r when order is NULL (xq
  * already sorted).  Rows from offsets[n_experts] on are zeros.
  * offsets and order: device arrays as smoe_dispatch_tokens writes them;
- * xq: int8 [n_src x n_in]; wq: int8 [n_experts x n_out x n_in] and w_scales:
- * f32 [n_experts x n_out], the experts one after another; y: [n_rows x
- * n_out].  workspace: smoe_experts_matmul_q8_workspace_bytes(...) bytes.
+ * xq: int8 [n_src x n_in], n_src >= 1 unless there are no rows; wq: int8
+ * [n_experts x n_out x n_in] and w_scales: f32 [n_experts x n_out], the experts
+ * one after another; y: [n_rows x n_out].  workspace: smoe_experts_matmul_q8_workspace_bytes(...) bytes.
  */
 size_t smoe_experts_matmul_q8_workspace_bytes(int n_src, int n_rows,
                                               int n_experts, int n_out,

@@ -889,11 +889,12 @@ int smoe_quantize_rows_q8(const void *x, int dtype, int act, int rows, int cols,
                                                 static_cast<cudaStream_t>(stream)));
 }
 
-// Sizes of an 8-bit product: rows of whole 16-byte vectors; the weights' rows
-// are counted in 32 bits.
+// Sizes of an 8-bit product: rows of whole 16-byte vectors, with source rows to
+// come from; the weights' rows are counted in 32 bits.
 static int check_q8(int n_src, int n_rows, int n_experts, int n_out, int n_in)
 {
-    if (n_src < 0 || n_rows < 0 || n_rows > SMOE_MAX_SLOTS || n_out < 0 || n_in < 0) return SMOE_ERR_SHAPE;
+    if (n_src < 0 || (n_src == 0 && n_rows > 0)) return SMOE_ERR_SHAPE;
+    if (n_rows < 0 || n_rows > SMOE_MAX_SLOTS || n_out < 0 || n_in < 0) return SMOE_ERR_SHAPE;
     if (n_experts < 1 || n_experts > SMOE_MAX_ROUTE_EXPERTS) return SMOE_ERR_SHAPE;
     if (n_in % 16 != 0 || n_in > SMOE_MAX_COLS) return SMOE_ERR_SHAPE;
     if (static_cast<long long>(n_experts) * n_out > SMOE_MAX_SLOTS) return SMOE_ERR_SHAPE;
