@@ -22,6 +22,21 @@ import moe_expert_ffn_smoe_gb300 as smoe  # noqa: E402
 _CODE = {torch.float32: smoe.SMOE_F32, torch.bfloat16: smoe.SMOE_BF16}
 
 
+def _check(name, t, shape, dtypes):
+    """t is a GPU tensor of `shape` (None: any length) and of one of `dtypes`:
+    the library takes addresses, and what it is handed wrongly it reads wrongly."""
+    if t.dtype not in dtypes:
+        raise TypeError(f"{name} is {t.dtype}, not " + " or ".join(map(str, dtypes)))
+    if not t.is_cuda:
+        raise ValueError(f"{name} is on {t.device}, not on a GPU")
+    if t.dim() != len(shape) or any(w is not None and w != n for n, w in zip(t.shape, shape)):
+        raise ValueError(f"{name} has the shape {tuple(t.shape)}, not {shape}")
+
+
+_FLOATS = (torch.float32, torch.bfloat16, torch.float16, torch.float64)
+_INTS = (torch.int32, torch.int64, torch.int16, torch.int8, torch.uint8)
+
+
 def _bytes(n, device):
     return torch.empty(max(n, 16), dtype=torch.uint8, device=device)
 
@@ -112,7 +127,7 @@ class _TopK(torch.autograd.Function):
 class _Dispatch(torch.autograd.Function):
     @staticmethod
     def forward(ctx, x, idx, n):
-        x = x.contiguous()
+        x, idx = x.contiguous(), idx.contiguous()
         T, k = idx.shape
         i32 = lambda m: torch.empty(m, dtype=torch.int32, device=x.device)  # noqa: E731
         offsets, order, place = i32(n + 1), i32(T * k), i32(T * k)
@@ -137,7 +152,7 @@ class _Dispatch(torch.autograd.Function):
 class _Combine(torch.autograd.Function):
     @staticmethod
     def forward(ctx, ys, place, w):
-        ys, w = ys.contiguous(), w.contiguous()
+        ys, place, w = ys.contiguous(), place.contiguous(), w.contiguous()
         T, k = w.shape
         out = torch.empty(T, ys.shape[1], dtype=ys.dtype, device=ys.device)
         smoe.smoe_combine_tokens(ys, _CODE[ys.dtype], place, w, T, k, ys.shape[1], out)
@@ -154,25 +169,38 @@ class _Combine(torch.autograd.Function):
 
 
 def top_k(logits, k):
-    """(indices, weights) of each row's k experts; differentiable in logits."""
-    return _TopK.apply(logits, k)
+    """(indices, weights) of each row's k experts, taken and summed in f32;
+    differentiable in logits (of any float type)."""
+    _check("logits", logits, (None, None), _FLOATS)
+    return _TopK.apply(logits.float(), k)
 
 
 def dispatch(x, idx, n_experts):
-    """(rows sorted by expert, offsets, place); differentiable in x."""
+    """(rows sorted by expert, offsets, place); differentiable in x (f32 or
+    bf16).  idx: integers [tokens, k], no expert where outside [0, n_experts)."""
+    _check("x", x, (None, None), tuple(_CODE))
+    _check("idx", idx, (x.shape[0], None), _INTS)
+    if idx.dtype != torch.int32:  # the library's type; clamped, so that none wraps into another expert
+        idx = idx.long().clamp(-1, n_experts).int()
     return _Dispatch.apply(x, idx, n_experts)
 
 
 def combine(ys, place, w):
-    """The experts' rows back in token order, weighted; differentiable in both."""
-    return _Combine.apply(ys, place, w)
+    """The experts' rows (f32 or bf16) back in token order, weighted (by any
+    float type, in f32); differentiable in both.  place: as dispatch gives it."""
+    _check("w", w, (None, None), _FLOATS)
+    _check("place", place, (w.numel(),), (torch.int32,))
+    _check("ys", ys, (w.numel(), None), tuple(_CODE))
+    return _Combine.apply(ys, place, w.float())
 
 
 def moe_train(x, router, gate_up, down, k):
     """The layer in torch with the routing above; every argument may need a
     gradient.  router [n, d], gate_up [n, 2 d_ff, d], down [n, d, d_ff]."""
     n, d_ff = router.shape[0], down.shape[2]
-    idx, w = top_k(x.float() @ router.float().t(), k)
+    with torch.autocast(x.device.type, enabled=False):  # the selection is made on f32 logits
+        logits = x.float() @ router.float().t()
+    idx, w = top_k(logits, k)
     xs, offsets, place = dispatch(x, idx, n)
     ys = []
     at = offsets.tolist()
