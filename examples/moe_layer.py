@@ -5,8 +5,8 @@
   calls, nothing read back to the host, so that the whole layer can be
   captured in one CUDA graph.
 * ``top_k``, ``dispatch``, ``combine``: the same routing under torch's
-  autograd (each backward is the library's own call), for training experts
-  written in torch.
+  autograd (each backward is the library's own call, and has none of its own:
+  a second gradient is refused), for training experts written in torch.
 
 ``python examples/moe_layer.py`` runs both on a GPU with seeded weights.
 """
@@ -15,6 +15,7 @@ import os
 import sys
 
 import torch
+from torch.autograd.function import once_differentiable
 
 sys.path.insert(0, os.path.dirname(os.path.dirname(os.path.abspath(__file__))))
 import moe_expert_ffn_smoe_gb300 as smoe  # noqa: E402
@@ -116,6 +117,7 @@ class _TopK(torch.autograd.Function):
         return idx, w
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, _, d_w):
         idx, w = ctx.saved_tensors
         T, k = idx.shape
@@ -141,6 +143,7 @@ class _Dispatch(torch.autograd.Function):
         return xs, offsets, place
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, d_xs, _, __):
         place, = ctx.saved_tensors
         T, k, d = ctx.shape
@@ -160,6 +163,7 @@ class _Combine(torch.autograd.Function):
         return out
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, d_out):
         ys, place, w = ctx.saved_tensors
         T, k = w.shape
