@@ -44,6 +44,7 @@ def _bytes(n, device):
 
 def quantize_weights(w):
     """int8 codes and one scale per output row of w [..., n_out, n_in]."""
+    _check("w", w, (None,) * w.dim(), tuple(_CODE))
     q = torch.empty(w.shape, dtype=torch.int8, device=w.device)
     scales = torch.empty(w.shape[:-1], device=w.device)
     rows = w.numel() // w.shape[-1]
@@ -52,14 +53,19 @@ def quantize_weights(w):
 
 
 class Q8Layer:
-    """n_experts experts of d_model -> d_ff -> d_model in 8 bits, top-k routed.
+    """n_experts experts of d_model -> d_ff -> d_model in 8 bits, top-k routed,
+    for up to max_tokens tokens a call.
 
     gate: router weights bf16 [n_experts, d_model] (bit patterns, int16);
     gate_up: [n_experts, 2 d_ff, d_model], the gate rows first, and
     down: [n_experts, d_model, d_ff], f32 or bf16, quantised here."""
 
     def __init__(self, gate, gate_up, down, k, max_tokens):
-        dev = gate.device
+        n, d, d_ff = *gate.shape, down.shape[-1]
+        _check("gate", gate, (n, d), (torch.int16, torch.bfloat16))
+        _check("gate_up", gate_up, (n, 2 * d_ff, d), tuple(_CODE))
+        _check("down", down, (n, d, d_ff), tuple(_CODE))
+        dev, gate, self.max_tokens = gate.device, gate.contiguous(), max_tokens
         self.gate, self.gate32, self.k = gate, gate.view(torch.bfloat16).float(), k
         self.n, self.d_ff, self.d = gate_up.shape[0], down.shape[2], down.shape[1]
         self.gu, self.gu_scales = quantize_weights(gate_up)
@@ -81,7 +87,14 @@ class Q8Layer:
         self.need = need
 
     def __call__(self, x, out, stream=None):
-        """out[t] (bf16) = the layer's output for x[t] (f32 [tokens, d_model])."""
+        """out[t] (bf16) = the layer's output for x[t] (f32 [tokens, d_model]),
+        both contiguous."""
+        _check("x", x, (None, self.d), (torch.float32,))
+        _check("out", out, (x.shape[0], self.d), (torch.bfloat16,))
+        if x.shape[0] > self.max_tokens:
+            raise ValueError(f"{x.shape[0]} tokens, where the layer was made for {self.max_tokens}")
+        if not (x.is_contiguous() and out.is_contiguous()):
+            raise ValueError("x and out are to be contiguous")
         T, k, n, d, ff = x.shape[0], self.k, self.n, self.d, self.d_ff
         R = T * k
         if T <= 64:
