@@ -31,6 +31,7 @@
 
 #include <atomic>
 
+#include "cluster_table.h"
 #include "q8.cuh"
 #include "smoe.h"
 #include "tcgen05.cuh"
@@ -801,33 +802,29 @@ Layout layout(int nsrc, int R, int n, int K)
 
 // Clusters of `csize` (2, 4 or 8) CTAs of a kernel that the current device
 // holds at once (a cluster's CTAs share a GPC, so this may be fewer than its
-// SMs divided), looked up once per kernel type and device; 0 if unknown.
-template <typename K>
-int resident_clusters(K kernel, int csize, size_t smem)
+// SMs divided); 0 if unknown.
+template <auto Kernel>
+int resident_clusters(int csize, size_t smem)
 {
-    static std::atomic<int> cache[64][3];
     int dev = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return 0;
-    std::atomic<int> &slot = cache[dev][csize == 2 ? 0 : (csize == 4 ? 1 : 2)];
-    int n = slot.load(std::memory_order_relaxed);
-    if (n != 0) return n > 0 ? n : 0;
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(static_cast<unsigned>(csize));
-    cfg.blockDim = dim3(TC_THREADS);
-    cfg.dynamicSmemBytes = smem;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim.x = static_cast<unsigned>(csize);
-    attr[0].val.clusterDim.y = 1;
-    attr[0].val.clusterDim.z = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    if (cudaOccupancyMaxActiveClusters(&n, kernel, &cfg) != cudaSuccess || n < 1) {
+    if (cudaGetDevice(&dev) != cudaSuccess) return 0;
+    return cluster_table<Kernel>().get(dev, csize, [&] {
+        cudaLaunchConfig_t cfg = {};
+        cfg.gridDim = dim3(static_cast<unsigned>(csize));
+        cfg.blockDim = dim3(TC_THREADS);
+        cfg.dynamicSmemBytes = smem;
+        cudaLaunchAttribute attr[1];
+        attr[0].id = cudaLaunchAttributeClusterDimension;
+        attr[0].val.clusterDim.x = static_cast<unsigned>(csize);
+        attr[0].val.clusterDim.y = 1;
+        attr[0].val.clusterDim.z = 1;
+        cfg.attrs = attr;
+        cfg.numAttrs = 1;
+        int n = 0;
+        if (cudaOccupancyMaxActiveClusters(&n, Kernel, &cfg) == cudaSuccess) return n;
         (void)cudaGetLastError();
-        n = -1;
-    }
-    slot.store(n, std::memory_order_relaxed);
-    return n > 0 ? n : 0;
+        return 0;
+    });
 }
 
 template <typename T, int NT>
@@ -850,7 +847,7 @@ cudaError_t launch_tc(const TcArgs &args, long long most_items, int sms, cudaStr
     int size = F::CL;
     if (F::CL == 1)
         for (int s = 8; s > 1; s /= 2)
-            if (most_items * s <= sms && (args.K + 127) / 128 >= 2 * s && most_items <= resident_clusters(k, s, smem)) {
+            if (most_items * s <= sms && (args.K + 127) / 128 >= 2 * s && most_items <= resident_clusters<q8_tc<T, NT>>(s, smem)) {
                 size = s;
                 break;
             }
@@ -858,7 +855,7 @@ cudaError_t launch_tc(const TcArgs &args, long long most_items, int sms, cudaStr
     a.nsplit = F::CL > 1 ? 1 : size;
     long long clusters = sms / size;
     if (F::CL > 1) {
-        const int fit = resident_clusters(k, F::CL, smem);
+        const int fit = resident_clusters<q8_tc<T, NT>>(F::CL, smem);
         if (fit > 0 && fit < clusters) clusters = fit;
     }
     if (most_items < clusters) clusters = most_items;
