@@ -31,7 +31,9 @@ smoe_experts_ffn_batch_q4/q2; a dense bf16 matvec is matvec_bf16, many of
 them in one submission matvec_bf16_batch.
 """
 import ctypes
+import operator
 import os
+import types
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "libsmoe.so")
@@ -42,7 +44,10 @@ if not os.path.exists(LIB_PATH):
         "(the library has no CPU fallback)")
 
 _lib = ctypes.CDLL(LIB_PATH)
-from . import _binding  # noqa: E402  (the same library, arguments marshalled in C)
+try:
+    from . import _binding  # noqa: E402  (the same library, arguments marshalled in C)
+except ImportError:  # built without Python's headers
+    _binding = None
 
 SMOE_OK = 0
 SMOE_ERR_NULL = 1
@@ -158,7 +163,33 @@ def _stream(s):
     return s.cuda_stream
 
 
-_binding.set_current_stream(_current_stream)
+def _by_ctypes(name):
+    """_binding's function of that name through ctypes: about 1 us more a call."""
+    params, f = _SIGS[name][0][:-1], getattr(_lib, name)
+
+    def integer(a):
+        a = operator.index(a)
+        if not -1 << 31 <= a < 1 << 31:  # ctypes would cut it
+            raise OverflowError("an argument does not fit 32 bits")
+        return a
+
+    convert = [{_P: _ptr, _I: integer, _SZ: operator.index}[t] for t in params]
+
+    def call(*args):
+        if len(args) != len(params) + 1:
+            raise TypeError(f"{name} takes {len(params) + 1} arguments ({len(args)} given)")
+        return f(*[c(a) for c, a in zip(convert, args)], _stream(args[-1]))
+
+    return call
+
+
+if _binding is not None:
+    _binding.set_current_stream(_current_stream)
+else:
+    _binding = types.SimpleNamespace(**{_name: _by_ctypes(_name) for _name in (
+        "smoe_topk_rows", "smoe_topk_rows_backward", "smoe_dispatch_tokens", "smoe_dispatch_tokens_backward",
+        "smoe_combine_tokens", "smoe_combine_tokens_backward", "smoe_quantize_rows_q8", "smoe_matmul_q8",
+        "smoe_experts_matmul_q8")})
 
 
 def _check(status, where):

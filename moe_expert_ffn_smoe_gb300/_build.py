@@ -4,7 +4,8 @@ Each translation unit is compiled in its own nvcc process (in parallel),
 then linked into one shared library with the CUDA runtime linked
 statically, so loading the library needs no GPU and no libcudart.
 A second module, _binding.so (csrc/binding.c, gcc, linked to libsmoe.so next
-to it), marshals the arguments of the calls that small batches make.
+to it), marshals the arguments of the calls that small batches make; without
+Python's headers it is left out, and the package makes those calls by ctypes.
 Set SMOE_PTXAS_VERBOSE=1 to print register and shared-memory use, and
 SMOE_NVCC_EXTRA to pass extra nvcc flags (e.g. -D tuning macros).
 """
@@ -39,10 +40,17 @@ def _deps():
             + glob.glob(os.path.join(INCLUDE, "*.h")) + [os.path.abspath(__file__)])
 
 
+def _python_headers():
+    """The folder of Python.h, or None."""
+    d = sysconfig.get_paths()["include"]
+    return d if os.path.exists(os.path.join(d, "Python.h")) else None
+
+
 def up_to_date() -> bool:
-    if not os.path.exists(LIB) or not os.path.exists(BINDING):
+    made = [LIB] + ([BINDING] if _python_headers() else [])
+    if not all(os.path.exists(m) for m in made):
         return False
-    t = min(os.path.getmtime(LIB), os.path.getmtime(BINDING))
+    t = min(os.path.getmtime(m) for m in made)
     return all(os.path.getmtime(d) <= t for d in _deps())
 
 
@@ -76,8 +84,11 @@ def build(force: bool = False, verbose: bool = False) -> str:
     if r.returncode != 0:
         raise RuntimeError(f"link failed:\n{r.stderr}")
     os.replace(tmp, LIB)
+    headers = _python_headers()
+    if headers is None:
+        return LIB
     tmp = BINDING + ".tmp"
-    cmd = ["gcc", "-O2", "-shared", "-fPIC", "-I", INCLUDE, "-I", sysconfig.get_paths()["include"],
+    cmd = ["gcc", "-O2", "-shared", "-fPIC", "-I", INCLUDE, "-I", headers,
            os.path.join(CSRC, "binding.c"), "-o", tmp, "-L", PKG, "-l:libsmoe.so", "-Wl,-rpath,$ORIGIN"]
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
