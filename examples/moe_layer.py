@@ -97,7 +97,7 @@ class Q8Layer:
             raise ValueError("x and out are to be contiguous")
         T, k, n, d, ff = x.shape[0], self.k, self.n, self.d, self.d_ff
         R = T * k
-        if T <= 64:
+        if T <= 64 and n % 4 == 0:  # a matvec writes to 16-byte boundaries
             smoe.matvec_bf16_batch([self.gate] * T, [x.data_ptr() + 4 * d * t for t in range(T)],
                                    [self.logits.data_ptr() + 4 * n * t for t in range(T)], [n] * T, [d] * T, stream)
         else:  # a matvec a token would read the router's weights T times
