@@ -498,18 +498,22 @@ int smoe_experts_ffn_routed_q2(int n_experts, int k,
  * Many tokens: from a batch's router logits to its experts and back.
  *
  * smoe_topk_rows -> smoe_dispatch_tokens -> the experts' products on the
- * sorted rows -> smoe_combine_tokens is a whole MoE layer for a batch, with
- * no host round trip; every step has a gradient.  Slot a = t k + s is token
- * t's s-th selection.  None of these calls uses atomics on sums: the same
+ * sorted rows -> smoe_combine_tokens is a whole MoE layer for a batch.  With
+ * experts in 8 bits (smoe_experts_matmul_q8) it needs no host round trip;
+ * smoe_experts_ffn_batch_q4/q2 take the experts' token counts on the host,
+ * which have to be read from the offsets.  The selection, the dispatch and the
+ * combine have gradients, the 8-bit products have none.  Slot a = t k + s is
+ * token t's s-th selection.  None of these calls uses atomics on sums: the same
  * inputs give the same bits.  Sizes that the host cannot check (indices,
  * places, offsets: device data) are checked on the device before they
- * address memory; a place, order or offset outside its range is reported by
+ * address memory; a place or order outside its range is reported by
  * smoe_last_device_status as SMOE_ERR_ROUTE and its slot counts as one
- * without an expert.  1 <= k <= SMOE_MAX_TOP_K, n_experts <=
+ * without an expert; offsets that leave the rows or do not ascend are reported
+ * likewise, and the rows that they concern are unspecified.  1 <= k <= SMOE_MAX_TOP_K, n_experts <=
  * SMOE_MAX_ROUTE_EXPERTS, n_tokens k <= SMOE_MAX_SLOTS, 0 <= d_model <=
  * SMOE_MAX_SLOTS (any number; rows whose pitch and base are multiples of 16
- * bytes move as 16-byte vectors).  Index arrays are aligned to 4 bytes, rows to their
- * element.  n_tokens == 0 is a no-op (offsets become zeros).
+ * bytes move as 16-byte vectors).  Index arrays are aligned to 4 bytes, rows
+ * to their element.  n_tokens == 0 is a no-op (offsets become zeros).
  */
 
 /*
@@ -520,7 +524,9 @@ int smoe_experts_ffn_routed_q2(int n_experts, int k,
  *   top_w[t][r] = exp(l_r - l_0) / sum over r' < k of exp(l_r' - l_0).
  *
  * A logit of -infinity is an expert that is off for the token: selected, it
- * gives index -1 and weight 0, and a row of nothing else is all -1 and 0.
+ * gives index -1 and weight 0, and a row of nothing else is all -1 and 0.  A
+ * NaN that is selected (all that rank above it are, too) has its index, and the
+ * weights of its row that are not 0 are NaN.
  * logits: f32 [n_tokens x n_experts] with row pitch ld >= n_experts (in
  * floats); top_idx: int32 [n_tokens x k], top_w: f32 [n_tokens x k], written.
  * One launch.

@@ -95,8 +95,8 @@ __device__ __forceinline__ void select_by_rounds(uint32_t (&key)[V], int k, uint
 // is a lower bound of the k-th largest logit; the few logits not below it (k
 // and one or two more, as a rule) are gathered one to a lane in expert order,
 // where counting the larger ones gives each its rank.  Against k rounds over
-// the whole row (us, 32,768 rows): 128 experts, k = 8 11.5 / 17.5, k = 16 15.9 /
-// 29.6; 512 experts, k = 8 24.3 / 49.5.
+// the whole row (us, 32,768 rows): 128 experts, k = 8 11.8 / 17.5, k = 16 16.2 /
+// 29.6; 512 experts, k = 8 21.3 / 46.6.
 constexpr int FILTER_K = 16;
 
 // The bound from every lane's maximum `most`; first: the row's largest key.
@@ -222,8 +222,8 @@ __global__ void __launch_bounds__(TOPK_WARPS * 32) topk_rows_warp(const float *_
 // n <= LONG_EXPERTS, k <= FILTER_K: the same filter over two passes of the row,
 // the second out of the cache; where more than 32 candidates are left (ties), k
 // passes that each find the next one in order.  Against one CTA per row
-// (topk_rows_block; us, k = 8): 1 row of 520 3.1 / 4.9, 1 of 1024 4.0 / 4.2,
-// 3000 of 1024 8.9 / 24.4, 32,768 of 520 37 / 218; but 1 of 8192 19.4 / 7.1.
+// (topk_rows_block; us, k = 8): 1 row of 520 3.3 / 4.8, 1 of 1024 4.3 / 4.3,
+// 3000 of 1024 6.7 / 24.5, 32,768 of 520 34.8 / 216; but 1 of 8192 19.4 / 7.2.
 constexpr int LONG_EXPERTS = 2048;
 
 __global__ void __launch_bounds__(TOPK_WARPS * 32) topk_rows_long(const float *__restrict__ logits, int T, int n, int ld,
@@ -722,7 +722,7 @@ __device__ __forceinline__ int checked_place(int p, int R, unsigned *status)
 
 // xs[place[t, s]] = x[t]; the rows of slots without an expert are zeros.  A
 // CTA takes tpc tokens and a column block: x is read once and written k
-// times.  Bound by HBM writes (8191 tokens of 8 KB, k = 8: 91 us, 98% of the
+// times.  Bound by HBM writes (16,400 tokens of 8 KB, k = 8: 190 us, 95% of the
 // copy rate).
 template <typename T, int VE>
 __global__ void __launch_bounds__(ROW_THREADS) gather_rows(const T *__restrict__ x, const int *__restrict__ place,
@@ -738,7 +738,8 @@ __global__ void __launch_bounds__(ROW_THREADS) gather_rows(const T *__restrict__
 // out[t] = sum over s, in order, of w[t, s] ys[place[t, s]] (w null: of the
 // rows themselves), f32 sums.  A thread takes a vector of a token's row, four
 // slots' loads in flight; a CTA tpc tokens and a column block.  Bound by HBM
-// reads (4099 tokens of 16 KB, k = 8: 98 us, 92% of the copy rate).
+// reads (4099 tokens of 16 KB, k = 8, one slot in twenty without an expert: 88.7
+// us, 98% of the copy rate).
 template <typename T, int VE>
 __global__ void __launch_bounds__(ROW_THREADS) sum_rows(const T *__restrict__ ys, const int *__restrict__ place,
                                                         const float *__restrict__ w, int tokens, int tpc, int k, int d,
