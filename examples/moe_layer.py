@@ -213,7 +213,8 @@ def combine(ys, place, w):
 
 def moe_train(x, router, gate_up, down, k):
     """The layer in torch with the routing above, expert by expert (which reads
-    the offsets back); every argument may need a gradient.  router [n, d], gate_up [n, 2 d_ff, d], down [n, d, d_ff]."""
+    the offsets back); every argument may need a gradient.  router [n, d],
+    gate_up [n, 2 d_ff, d], down [n, d, d_ff]."""
     n, d_ff = router.shape[0], down.shape[2]
     with torch.autocast(x.device.type, enabled=False):  # the selection is made on f32 logits
         logits = x.float() @ router.float().t()
