@@ -618,13 +618,14 @@ int smoe_combine_tokens_backward(const void *d_out, const void *ys, int dtype,
 /*
  * Quantises rows of v = x (act SMOE_Q8_PLAIN; x: [rows x cols]) or of
  * v = SiLU(gate) * up (SMOE_Q8_SILU_MUL; x: [rows x 2 cols], gate the first
- * cols of a row and up the last), in f32 (SiLU within 2^-20
- * of its value, or 2^-142; scale and codes from that v by f32 operations that
- * are rounded once each):
+ * cols of a row and up the last), in f32 (SiLU within 2^-20 of its value, or
+ * 2^-142; scale and codes from that v by f32 operations that are rounded once
+ * each):
  *
  *   top = max |v|,  scales[r] = top / 127,
- *   q[r][c] = v (127 / top) rounded to the nearest integer, ties to even.
+ *   q[r][c] = v (127 / top) rounded to the nearest integer, ties to even
  *
+ * (where 127 / top is beyond f32, v and top are taken 2^64 times).
  * A row of zeros has scale 0 and codes 0; a row that holds a NaN or an
  * infinity has scale NaN and codes 0, so that every product of it is NaN.
  * cols <= SMOE_MAX_COLS; q 16-byte aligned.

@@ -20,7 +20,7 @@ namespace {
 // be its row's largest value, and the divisor stays within [1, 2], so that the
 // reciprocal instruction alone does (1 unit in the last place; the quantiser is
 // bound by instructions, and its step is 2^16 times coarser).  32,768 rows of
-// 1536 bf16 52.9 us, as a division of v or v e by 1 + e 60.8.
+// 1536 bf16 52.5 us, as a division of v or v e by 1 + e 60.8.
 __device__ __forceinline__ float silu_row(float v)
 {
     const float e = expf(-fabsf(v));
@@ -159,18 +159,24 @@ __global__ void __launch_bounds__(THREADS) quantize_rows(const T *__restrict__ x
     const float top = __uint_as_float(most);
     const float up = bad || most == 0u ? 0.f : __fdiv_rn(127.f, top);
     if (threadIdx.x == 0) scales[r] = bad ? __int_as_float(0x7fffffff) : __fdiv_rn(top, 127.f);
-    const bool plain = !bad && up < INFINITY;  // 127 / top overflows below 4e-37: those codes saturate
+    int8_t *out = q + r * cols;
+    if (bad || up == INFINITY) {
+        // rare, and kept out of the way of the other rows: 127 / top is beyond
+        // f32 below 3.8e-37, where the row is taken 2^64 times
+        const float lifted = bad ? 0.f : __fdiv_rn(127.f, top * 0x1p64f);
+#pragma unroll 1
+        for (int c = threadIdx.x; c < cols; c += THREADS) {
+            float v[1];
+            quant_values<T, 1, ACT>(row, cols, c, v);
+            out[c] = bad ? 0 : static_cast<int8_t>(code_bits(v[0] * 0x1p64f, lifted));
+        }
+        return;
+    }
     auto store = [&](const float (&v)[VE], int c) {
         uint32_t k[VE];
-        if (plain) {
 #pragma unroll
-            for (int j = 0; j < VE; ++j) k[j] = code_bits(v[j], up);
-        } else {
-#pragma unroll
-            for (int j = 0; j < VE; ++j)
-                k[j] = bad || v[j] == 0.f ? 0u : static_cast<uint32_t>(v[j] > 0.f ? 127 : -127);
-        }
-        put_codes(q + r * cols + c, k);
+        for (int j = 0; j < VE; ++j) k[j] = code_bits(v[j], up);
+        put_codes(out + c, k);
     };
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
