@@ -676,6 +676,154 @@ int smoe_experts_matmul_q8(const int8_t *xq, const float *x_scales, int n_src,
                            void *y, int dtype, void *workspace,
                            size_t workspace_bytes, void *stream);
 
+/*
+ * Routing by scores, for a batch: with the scores
+ *
+ *   s_i = 1 / (1 + exp(-l_i))                                (SMOE_SCORE_SIGMOID)
+ *   s_i = exp(l_i - max) / sum over the row of exp(l_j - max)  (SMOE_SCORE_SOFTMAX)
+ *
+ * the choice goes by c_i = s_i + bias_i (bias: f32 [n_experts], or NULL for none;
+ * it moves the choice alone, as a term that balances the experts' load does).  The
+ * experts are n_groups groups of n_experts / n_groups neighbours; a group counts
+ * the sum of its group_best (1 or 2) largest c; the top_groups best groups stay
+ * (ties to the lower group), and of their experts the k with the largest c, in
+ * descending order, ties to the lower expert.  The weights are of the scores:
+ *
+ *   top_w[t][r] = scale s_r / sum over r' < k of s_r'   (norm != 0)
+ *   top_w[t][r] = scale s_r                             (norm == 0)
+ *
+ * The order is that of the real numbers c: where f32 cannot tell two of them apart,
+ * 64 bits decide (equal there: a tie).  An expert whose logit or bias is -infinity is
+ * off: it is not chosen, and counts for nothing in its group (its logit stays in the
+ * softmax's sum where only the bias is -infinity).  Slots for which no expert is left
+ * have index -1 and weight 0.  A row that holds a NaN logit, a logit of +infinity
+ * under softmax, or a NaN or +infinite bias at an expert whose logit is not -infinity
+ * has no order: it gets the experts 0 to k - 1 with weights NaN, so that its outputs
+ * are NaN.
+ * logits: f32 [n_tokens x n_experts] with row pitch ld >= n_experts (in floats);
+ * top_idx: int32 [n_tokens x k], top_w: f32 [n_tokens x k], written.  n_experts <=
+ * SMOE_MAX_SCORE_EXPERTS, n_groups <= SMOE_MAX_GROUPS and a divisor of n_experts, the
+ * kept groups hold k experts at least; scale is finite and not 0.  One launch; the
+ * results go on to smoe_dispatch_tokens and smoe_combine_tokens.
+ */
+#define SMOE_SCORE_SOFTMAX 0
+#define SMOE_SCORE_SIGMOID 1
+#define SMOE_MAX_SCORE_EXPERTS 1024
+#define SMOE_MAX_GROUPS 32
+int smoe_route_rows(const float *logits, int n_tokens, int n_experts, int ld,
+                    const float *bias, int score, int n_groups, int top_groups,
+                    int group_best, int k, int norm, float scale, int *top_idx,
+                    float *top_w, void *stream);
+
+/*
+ * Gradient of those weights to the logits, the choice being constant (the bias has
+ * none).  With g_r = top_w_r (dw_r - sum over q of top_w_q dw_q / scale) where norm
+ * != 0, and g_r = top_w_r dw_r where not:
+ *
+ *   sigmoid:                  d_logits[t][top_idx[t][r]] = g_r (1 - s_r)
+ *   softmax, norm != 0:       d_logits[t][top_idx[t][r]] = g_r
+ *   softmax, norm == 0:       d_logits[t][j] = g of j's slot - s_j sum over r of g_r
+ *
+ * 0 for what is not named.  A slot whose index is outside [0, n_experts) has no
+ * expert and counts for nothing; slots of one expert add up.  score, norm, scale:
+ * as in the call that made top_idx and top_w.  d_logits: f32 [n_tokens x n_experts],
+ * 16-byte aligned, written whole.
+ */
+int smoe_route_rows_backward(const float *logits, int n_tokens, int n_experts,
+                             int ld, int score, int k, int norm, float scale,
+                             const int *top_idx, const float *top_w,
+                             const float *d_top_w, float *d_logits,
+                             void *stream);
+
+/*
+ * 8-bit floating point ("F8"): e4m3 codes (sign, 4 bits of exponent, 3 of mantissa, no
+ * infinity, largest 448, 0x7f and 0xff NaN) with one f32 scale for each block of 128.
+ * Activations, and gradients of outputs, have blocks of 1 x 128: scales f32
+ * [rows x ceil(cols / 128)].  Weights have blocks of 128 x 128 of each matrix: scales
+ * f32 [n x ceil(rows / 128) x ceil(cols / 128)].  The last block of a row or column may
+ * be short.
+ *
+ * Quantises rows of v = x (SMOE_Q8_PLAIN) or of v = SiLU(gate) * up (SMOE_Q8_SILU_MUL;
+ * x: [rows x 2 cols]), as smoe_quantize_rows_q8 takes them:
+ *
+ *   top = max |v| of the block,  scale = top / 448,  q = e4m3(v (448 / top))
+ *
+ * (f32 operations rounded once each, the code to nearest, ties to even; where
+ * 448 / top is beyond f32, v and top are taken 2^64 times).  A block of zeros has
+ * scale 0 and codes 0; one that holds a NaN or an infinity has scale NaN and codes 0,
+ * so that every product of it is NaN.  cols <= SMOE_MAX_COLS; q: [rows x cols],
+ * 16-byte aligned.
+ */
+int smoe_quantize_rows_f8(const void *x, int dtype, int act, int rows, int cols,
+                          uint8_t *q, float *scales, void *stream);
+
+/*
+ * Quantises n_mats matrices w [n_mats x rows x cols] of dtype in blocks of 128 x 128,
+ * by the same steps, and, where qt and scales_t are not NULL (both or neither), writes
+ * them transposed too: qt [n_mats x cols x rows], scales_t [n_mats x ceil(cols / 128) x
+ * ceil(rows / 128)].  The gradient of a product to its rows is a product with the
+ * transposed weights: smoe_experts_matmul_f8 of the quantised output gradients with
+ * (qt, scales_t), where rows is a multiple of 16.  Codes 16-byte aligned; n_mats rows
+ * and n_mats cols <= SMOE_MAX_SLOTS.
+ */
+int smoe_quantize_blocks_f8(const void *w, int dtype, int n_mats, int rows,
+                            int cols, uint8_t *q, float *scales, uint8_t *qt,
+                            float *scales_t, void *stream);
+
+/*
+ * Product of F8 rows with one F8 matrix: with b the blocks of 128 columns,
+ *
+ *   y[r][n] = sum over b of x_scales[r][b] w_scales[n / 128][b]
+ *             sum over c in b of xq[r][c] wq[n][c]
+ *
+ * (products exact, sums f32; a block's scales are multiplied first).  xq: [n_rows x
+ * n_in], wq: [n_out x n_in], both 16-byte aligned, n_in a multiple of 16 (any n_out);
+ * y: [n_rows x n_out] of dtype, 16-byte aligned.  workspace:
+ * smoe_matmul_f8_workspace_bytes(...) bytes, 16-byte aligned, contents unspecified
+ * before and after; the size does not fall as n_rows grows.
+ */
+size_t smoe_matmul_f8_workspace_bytes(int n_rows, int n_out, int n_in);
+int smoe_matmul_f8(const uint8_t *xq, const float *x_scales, int n_rows,
+                   const uint8_t *wq, const float *w_scales, int n_out,
+                   int n_in, void *y, int dtype, void *workspace,
+                   size_t workspace_bytes, void *stream);
+
+/*
+ * The same product over the experts of a sorted batch, as smoe_experts_matmul_q8
+ * takes it: row r of [offsets[e], offsets[e + 1]) by expert e's matrix, its source row
+ * order[r] / k of xq [n_src x n_in] (r itself where order is NULL); rows from
+ * offsets[n_experts] on are zeros.  wq: [n_experts x n_out x n_in], w_scales:
+ * [n_experts x ceil(n_out / 128) x ceil(n_in / 128)].
+ */
+size_t smoe_experts_matmul_f8_workspace_bytes(int n_src, int n_rows,
+                                              int n_experts, int n_out,
+                                              int n_in);
+int smoe_experts_matmul_f8(const uint8_t *xq, const float *x_scales, int n_src,
+                           const int *order, int k, const int *offsets,
+                           int n_rows, int n_experts, const uint8_t *wq,
+                           const float *w_scales, int n_out, int n_in,
+                           void *y, int dtype, void *workspace,
+                           size_t workspace_bytes, void *stream);
+
+/*
+ * Gradient of the weights of the experts' products on a sorted batch:
+ *
+ *   d_w[e][n][c] = sum over rows r of [offsets[e], offsets[e + 1]) of
+ *                  d_ys[r][n] xs[r][c]       (added to d_w: accumulate != 0)
+ *
+ * d_ys: bf16 [n_rows x n_out], xs: bf16 [n_rows x n_in], both in sorted order and
+ * 16-byte aligned, n_out and n_in multiples of 8 up to SMOE_MAX_COLS; d_w: of dtype
+ * [n_experts x n_out x n_in], 16-byte aligned device memory, written whole (zeros for an
+ * expert without rows).  Products exact, sums f32, rounded once to dtype; accumulated,
+ * that rounded sum is added to what is there and the result rounded again, so that
+ * gradients of many batches belong in f32.  Rows outside the experts' are not read
+ * into any sum.
+ */
+int smoe_experts_weight_grad(const void *d_ys, const void *xs,
+                             const int *offsets, int n_rows, int n_experts,
+                             int n_out, int n_in, int accumulate, void *d_w,
+                             int dtype, void *stream);
+
 /* Size of the device array ffn_batch_q4_noalloc uses as its workspace. */
 #define SMOE_NOALLOC_SCRATCH_BYTES (32u << 20)
 

@@ -48,6 +48,10 @@ try:
     from . import _binding  # noqa: E402  (the same library, arguments marshalled in C)
 except ImportError:  # built without Python's headers
     _binding = None
+try:
+    from . import _binding_f8  # noqa: E402
+except ImportError:
+    _binding_f8 = None
 
 SMOE_OK = 0
 SMOE_ERR_NULL = 1
@@ -66,6 +70,7 @@ SMOE_FFN_SYNC_BYTES = 512
 
 _P = ctypes.c_void_p
 _I = ctypes.c_int
+_F = ctypes.c_float
 _SZ = ctypes.c_size_t
 
 _SIGS = {
@@ -108,6 +113,15 @@ _SIGS = {
     "smoe_matmul_q8": ([_P, _P, _I, _P, _P, _I, _I, _P, _I, _P, _SZ, _P], _I),
     "smoe_experts_matmul_q8_workspace_bytes": ([_I, _I, _I, _I, _I], _SZ),
     "smoe_experts_matmul_q8": ([_P, _P, _I, _P, _I, _P, _I, _I, _P, _P, _I, _I, _P, _I, _P, _SZ, _P], _I),
+    "smoe_route_rows": ([_P, _I, _I, _I, _P, _I, _I, _I, _I, _I, _I, _F, _P, _P, _P], _I),
+    "smoe_route_rows_backward": ([_P, _I, _I, _I, _I, _I, _I, _F, _P, _P, _P, _P, _P], _I),
+    "smoe_quantize_rows_f8": ([_P, _I, _I, _I, _I, _P, _P, _P], _I),
+    "smoe_quantize_blocks_f8": ([_P, _I, _I, _I, _I, _P, _P, _P, _P, _P], _I),
+    "smoe_matmul_f8_workspace_bytes": ([_I, _I, _I], _SZ),
+    "smoe_matmul_f8": ([_P, _P, _I, _P, _P, _I, _I, _P, _I, _P, _SZ, _P], _I),
+    "smoe_experts_matmul_f8_workspace_bytes": ([_I, _I, _I, _I, _I], _SZ),
+    "smoe_experts_matmul_f8": ([_P, _P, _I, _P, _I, _P, _I, _I, _P, _P, _I, _I, _P, _I, _P, _SZ, _P], _I),
+    "smoe_experts_weight_grad": ([_P, _P, _P, _I, _I, _I, _I, _I, _P, _I, _P], _I),
     "smoe_last_device_status": ([_P], _I),
     "smoe_selftest_bounded_wait": ([_I, _P], _I),
     "smoe_copy": ([_P, _P, ctypes.c_size_t, _P], _I),
@@ -173,7 +187,12 @@ def _by_ctypes(name):
             raise OverflowError("an argument does not fit 32 bits")
         return a
 
-    convert = [{_P: _ptr, _I: integer, _SZ: operator.index}[t] for t in params]
+    def real(a):
+        if isinstance(a, (str, bytes, bytearray)):  # float would read it
+            raise TypeError("an argument is no number")
+        return float(a)
+
+    convert = [{_P: _ptr, _I: integer, _F: real, _SZ: operator.index}[t] for t in params]
 
     def call(*args):
         if len(args) != len(params) + 1:
@@ -190,6 +209,12 @@ else:
         "smoe_topk_rows", "smoe_topk_rows_backward", "smoe_dispatch_tokens", "smoe_dispatch_tokens_backward",
         "smoe_combine_tokens", "smoe_combine_tokens_backward", "smoe_quantize_rows_q8", "smoe_matmul_q8",
         "smoe_experts_matmul_q8")})
+if _binding_f8 is not None:
+    _binding_f8.set_current_stream(_current_stream)
+else:
+    _binding_f8 = types.SimpleNamespace(**{_name: _by_ctypes(_name) for _name in (
+        "smoe_route_rows", "smoe_route_rows_backward", "smoe_quantize_rows_f8", "smoe_quantize_blocks_f8",
+        "smoe_matmul_f8", "smoe_experts_matmul_f8", "smoe_experts_weight_grad")})
 
 
 def _check(status, where):
@@ -510,6 +535,70 @@ def smoe_experts_matmul_q8(xq, x_scales, n_src, order, k, offsets, n_rows, n_exp
     _check(_binding.smoe_experts_matmul_q8(xq, x_scales, n_src, order, k, offsets, n_rows, n_experts, wq,
                                            w_scales, n_out, n_in, y, dtype, workspace, workspace_bytes,
                                            stream), "smoe_experts_matmul_q8")
+
+
+# ---- routing by scores, 8-bit floating point, the weights' gradient
+
+SMOE_SCORE_SOFTMAX = 0
+SMOE_SCORE_SIGMOID = 1
+SMOE_MAX_SCORE_EXPERTS = 1024
+SMOE_MAX_GROUPS = 32
+
+
+def smoe_route_rows(logits, n_tokens, n_experts, ld, bias, score, n_groups, top_groups, group_best, k, norm, scale,
+                    top_idx, top_w, stream=None):
+    """The k experts of each row by their scores (SMOE_SCORE_SOFTMAX or
+    SMOE_SCORE_SIGMOID) plus bias (or None), out of the top_groups best groups,
+    and their weights: scale times the scores, over their sum where norm."""
+    _check(_binding_f8.smoe_route_rows(logits, n_tokens, n_experts, ld, bias, score, n_groups, top_groups, group_best, k,
+                                       norm, scale, top_idx, top_w, stream), "smoe_route_rows")
+
+
+def smoe_route_rows_backward(logits, n_tokens, n_experts, ld, score, k, norm, scale, top_idx, top_w, d_top_w, d_logits,
+                             stream=None):
+    _check(_binding_f8.smoe_route_rows_backward(logits, n_tokens, n_experts, ld, score, k, norm, scale, top_idx, top_w,
+                                                d_top_w, d_logits, stream), "smoe_route_rows_backward")
+
+
+def smoe_quantize_rows_f8(x, dtype, act, rows, cols, q, scales, stream=None):
+    """e4m3 codes (a byte each) and one scale per row and 128 columns of x, or
+    (SMOE_Q8_SILU_MUL) of SiLU(gate) * up of rows [gate | up] of 2 cols."""
+    _check(_binding_f8.smoe_quantize_rows_f8(x, dtype, act, rows, cols, q, scales, stream), "smoe_quantize_rows_f8")
+
+
+def smoe_quantize_blocks_f8(w, dtype, n_mats, rows, cols, q, scales, qt=None, scales_t=None, stream=None):
+    """e4m3 codes and one scale per 128 x 128 block of each matrix, and
+    (qt, scales_t not None) the same transposed, for the gradient to the rows."""
+    _check(_binding_f8.smoe_quantize_blocks_f8(w, dtype, n_mats, rows, cols, q, scales, qt, scales_t, stream),
+           "smoe_quantize_blocks_f8")
+
+
+def smoe_matmul_f8_workspace_bytes(n_rows, n_out, n_in):
+    return _lib.smoe_matmul_f8_workspace_bytes(n_rows, n_out, n_in)
+
+
+def smoe_matmul_f8(xq, x_scales, n_rows, wq, w_scales, n_out, n_in, y, dtype, workspace, workspace_bytes, stream=None):
+    _check(_binding_f8.smoe_matmul_f8(xq, x_scales, n_rows, wq, w_scales, n_out, n_in, y, dtype, workspace,
+                                      workspace_bytes, stream), "smoe_matmul_f8")
+
+
+def smoe_experts_matmul_f8_workspace_bytes(n_src, n_rows, n_experts, n_out, n_in):
+    return _lib.smoe_experts_matmul_f8_workspace_bytes(n_src, n_rows, n_experts, n_out, n_in)
+
+
+def smoe_experts_matmul_f8(xq, x_scales, n_src, order, k, offsets, n_rows, n_experts, wq, w_scales, n_out, n_in, y, dtype,
+                           workspace, workspace_bytes, stream=None):
+    """order None: xq is already in the sorted order."""
+    _check(_binding_f8.smoe_experts_matmul_f8(xq, x_scales, n_src, order, k, offsets, n_rows, n_experts, wq, w_scales,
+                                              n_out, n_in, y, dtype, workspace, workspace_bytes, stream),
+           "smoe_experts_matmul_f8")
+
+
+def smoe_experts_weight_grad(d_ys, xs, offsets, n_rows, n_experts, n_out, n_in, accumulate, d_w, dtype, stream=None):
+    """d_w[e] (of dtype) = the sum over expert e's rows of d_ys[r]^T xs[r] (bf16,
+    sorted), or that added to it (accumulate)."""
+    _check(_binding_f8.smoe_experts_weight_grad(d_ys, xs, offsets, n_rows, n_experts, n_out, n_in, accumulate, d_w, dtype,
+                                                stream), "smoe_experts_weight_grad")
 
 
 def smoe_last_device_status(stream=None):

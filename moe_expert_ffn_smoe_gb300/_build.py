@@ -3,9 +3,10 @@
 Each translation unit is compiled in its own nvcc process (in parallel),
 then linked into one shared library with the CUDA runtime linked
 statically, so loading the library needs no GPU and no libcudart.
-A second module, _binding.so (csrc/binding.c, gcc, linked to libsmoe.so next
-to it), marshals the arguments of the calls that small batches make; without
-Python's headers it is left out, and the package makes those calls by ctypes.
+Two modules, _binding.so and _binding_f8.so (csrc/binding.c and binding_f8.c,
+gcc, linked to libsmoe.so next to them), marshal the arguments of the calls that
+small batches make; without Python's headers they are left out, and the package
+makes those calls by ctypes.
 Set SMOE_PTXAS_VERBOSE=1 to print register and shared-memory use, and
 SMOE_NVCC_EXTRA to pass extra nvcc flags (e.g. -D tuning macros).
 """
@@ -23,6 +24,7 @@ INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libsmoe.so")
 BINDING = os.path.join(PKG, "_binding.so")
+BINDING_F8 = os.path.join(PKG, "_binding_f8.so")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 
@@ -47,7 +49,7 @@ def _python_headers():
 
 
 def up_to_date() -> bool:
-    made = [LIB] + ([BINDING] if _python_headers() else [])
+    made = [LIB] + ([BINDING, BINDING_F8] if _python_headers() else [])
     if not all(os.path.exists(m) for m in made):
         return False
     t = min(os.path.getmtime(m) for m in made)
@@ -87,13 +89,14 @@ def build(force: bool = False, verbose: bool = False) -> str:
     headers = _python_headers()
     if headers is None:
         return LIB
-    tmp = BINDING + ".tmp"
-    cmd = ["gcc", "-O2", "-shared", "-fPIC", "-I", INCLUDE, "-I", headers,
-           os.path.join(CSRC, "binding.c"), "-o", tmp, "-L", PKG, "-l:libsmoe.so", "-Wl,-rpath,$ORIGIN"]
-    r = subprocess.run(cmd, capture_output=True, text=True)
-    if r.returncode != 0:
-        raise RuntimeError(f"gcc failed on binding.c:\n{r.stderr}")
-    os.replace(tmp, BINDING)
+    for made, source in ((BINDING, "binding.c"), (BINDING_F8, "binding_f8.c")):
+        tmp = made + ".tmp"
+        cmd = ["gcc", "-O2", "-shared", "-fPIC", "-I", INCLUDE, "-I", headers,
+               os.path.join(CSRC, source), "-o", tmp, "-L", PKG, "-l:libsmoe.so", "-Wl,-rpath,$ORIGIN"]
+        r = subprocess.run(cmd, capture_output=True, text=True)
+        if r.returncode != 0:
+            raise RuntimeError(f"gcc failed on {source}:\n{r.stderr}")
+        os.replace(tmp, made)
     return LIB
 
 

@@ -1,5 +1,6 @@
 // The extern "C" entry points declared in include/smoe.h: argument checks
 // on the host, then the kernel launches.  Nothing here allocates memory.
+#include <cmath>
 #include <mutex>
 
 #include "internal_tokens.h"
@@ -955,6 +956,186 @@ int smoe_experts_matmul_q8(const int8_t *xq, const float *x_scales, int n_src, c
 {
     return q8_impl(xq, x_scales, n_src, order, k, offsets, true, n_rows, n_experts, wq, w_scales, n_out, n_in, y, dtype,
                    workspace, workspace_bytes, stream);
+}
+
+// ---- routing by scores
+
+static int check_route(int n_tokens, int n_experts, int ld, int score, int k, float scale)
+{
+    const int st = check_slots(n_tokens, k);
+    if (st != SMOE_OK) return st;
+    if (n_experts < 1 || n_experts > SMOE_MAX_SCORE_EXPERTS || k > n_experts || ld < n_experts) return SMOE_ERR_SHAPE;
+    if (score != SMOE_SCORE_SOFTMAX && score != SMOE_SCORE_SIGMOID) return SMOE_ERR_SHAPE;
+    return std::isfinite(scale) && scale != 0.f ? SMOE_OK : SMOE_ERR_SHAPE;
+}
+
+static size_t pitched(int rows, int ld, int cols)
+{
+    return (static_cast<size_t>(rows - 1) * ld + static_cast<size_t>(cols)) * sizeof(float);
+}
+
+int smoe_route_rows(const float *logits, int n_tokens, int n_experts, int ld, const float *bias, int score, int n_groups,
+                    int top_groups, int group_best, int k, int norm, float scale, int *top_idx, float *top_w, void *stream)
+{
+    const int st = check_route(n_tokens, n_experts, ld, score, k, scale);
+    if (st != SMOE_OK) return st;
+    if (n_groups < 1 || n_groups > SMOE_MAX_GROUPS || n_experts % n_groups != 0) return SMOE_ERR_SHAPE;
+    if (top_groups < 1 || top_groups > n_groups || (group_best != 1 && group_best != 2)) return SMOE_ERR_SHAPE;
+    if (static_cast<long long>(n_experts / n_groups) * top_groups < k) return SMOE_ERR_SHAPE;
+    if (n_tokens == 0) return SMOE_OK;
+    if (!logits || !top_idx || !top_w) return SMOE_ERR_NULL;
+    if (!aligned_to(logits, 4) || !aligned_to(top_idx, 4) || !aligned_to(top_w, 4) || !aligned_to(bias, 4))
+        return SMOE_ERR_ALIGN;
+    const size_t slots = static_cast<size_t>(n_tokens) * k;
+    const Span outs[2] = {{top_idx, slots * sizeof(int)}, {top_w, slots * sizeof(float)}};
+    const Span ins[2] = {{logits, pitched(n_tokens, ld, n_experts)},
+                         {bias, bias ? static_cast<size_t>(n_experts) * sizeof(float) : 0}};
+    if (any_alias(outs, 2, ins, 2)) return SMOE_ERR_ALIAS;
+    return to_status(smoe::launch_route_rows(logits, n_tokens, n_experts, ld, bias, score == SMOE_SCORE_SOFTMAX, n_groups,
+                                             top_groups, group_best, k, norm != 0, scale, top_idx, top_w,
+                                             static_cast<cudaStream_t>(stream)));
+}
+
+int smoe_route_rows_backward(const float *logits, int n_tokens, int n_experts, int ld, int score, int k, int norm,
+                             float scale, const int *top_idx, const float *top_w, const float *d_top_w, float *d_logits,
+                             void *stream)
+{
+    const int st = check_route(n_tokens, n_experts, ld, score, k, scale);
+    if (st != SMOE_OK) return st;
+    if (n_tokens == 0) return SMOE_OK;
+    if (!logits || !top_idx || !top_w || !d_top_w || !d_logits) return SMOE_ERR_NULL;
+    if (!aligned_to(logits, 4) || !aligned_to(top_idx, 4) || !aligned_to(top_w, 4) || !aligned_to(d_top_w, 4) ||
+        !aligned16(d_logits))
+        return SMOE_ERR_ALIGN;
+    const size_t slots = static_cast<size_t>(n_tokens) * k;
+    const Span outs[1] = {{d_logits, static_cast<size_t>(n_tokens) * n_experts * sizeof(float)}};
+    const Span ins[4] = {{logits, pitched(n_tokens, ld, n_experts)},
+                         {top_idx, slots * sizeof(int)},
+                         {top_w, slots * sizeof(float)},
+                         {d_top_w, slots * sizeof(float)}};
+    if (any_alias(outs, 1, ins, 4)) return SMOE_ERR_ALIAS;
+    return to_status(smoe::launch_route_rows_grad(logits, n_tokens, n_experts, ld, score == SMOE_SCORE_SOFTMAX, k, norm != 0,
+                                                  scale, top_idx, top_w, d_top_w, d_logits,
+                                                  static_cast<cudaStream_t>(stream)));
+}
+
+// ---- 8-bit floating point with a scale for each block of 128
+
+static size_t blocks_of(int cols) { return (static_cast<size_t>(cols) + 127) / 128; }
+
+int smoe_quantize_rows_f8(const void *x, int dtype, int act, int rows, int cols, uint8_t *q, float *scales, void *stream)
+{
+    const int st = check_rows(dtype, cols);
+    if (st != SMOE_OK) return st;
+    if (rows < 0 || rows > SMOE_MAX_SLOTS || cols > SMOE_MAX_COLS || (act != SMOE_Q8_PLAIN && act != SMOE_Q8_SILU_MUL))
+        return SMOE_ERR_SHAPE;
+    if (rows == 0 || cols == 0) return SMOE_OK;
+    if (!scales || !x || !q) return SMOE_ERR_NULL;
+    const size_t e = elem_bytes(dtype), n = static_cast<size_t>(rows) * cols;
+    if (!aligned_to(scales, 4) || !aligned_to(x, e) || !aligned16(q)) return SMOE_ERR_ALIGN;
+    const Span outs[2] = {{q, n}, {scales, static_cast<size_t>(rows) * blocks_of(cols) * sizeof(float)}};
+    const Span ins[1] = {{x, n * e * (act == SMOE_Q8_SILU_MUL ? 2 : 1)}};
+    if (any_alias(outs, 2, ins, 1)) return SMOE_ERR_ALIAS;
+    return to_status(smoe::launch_quantize_rows_f8(x, dtype, act == SMOE_Q8_SILU_MUL, rows, cols, q, scales,
+                                                   static_cast<cudaStream_t>(stream)));
+}
+
+int smoe_quantize_blocks_f8(const void *w, int dtype, int n_mats, int rows, int cols, uint8_t *q, float *scales, uint8_t *qt,
+                            float *scales_t, void *stream)
+{
+    const int st = check_rows(dtype, cols);
+    if (st != SMOE_OK) return st;
+    if (n_mats < 0 || rows < 0 || static_cast<long long>(n_mats) * rows > SMOE_MAX_SLOTS) return SMOE_ERR_SHAPE;
+    if (static_cast<long long>(n_mats) * cols > SMOE_MAX_SLOTS) return SMOE_ERR_SHAPE;
+    // one CTA a block, counted in 31 bits
+    if (n_mats > 0 && blocks_of(rows) * blocks_of(cols) > 0x7fffffffull / n_mats) return SMOE_ERR_SHAPE;
+    if (n_mats == 0 || rows == 0 || cols == 0) return SMOE_OK;
+    if (!w || !q || !scales || !qt != !scales_t) return SMOE_ERR_NULL;
+    const size_t e = elem_bytes(dtype), n = static_cast<size_t>(n_mats) * rows * cols;
+    const size_t s = n_mats * blocks_of(rows) * blocks_of(cols) * sizeof(float);
+    if (!aligned_to(w, e) || !aligned16(q) || !aligned16(qt) || !aligned_to(scales, 4) || !aligned_to(scales_t, 4))
+        return SMOE_ERR_ALIGN;
+    const Span outs[4] = {{q, n}, {scales, s}, {qt, qt ? n : 0}, {scales_t, qt ? s : 0}};
+    const Span ins[1] = {{w, n * e}};
+    if (any_alias(outs, 4, ins, 1)) return SMOE_ERR_ALIAS;
+    return to_status(smoe::launch_quantize_blocks_f8(w, dtype, n_mats, rows, cols, q, scales, qt, scales_t,
+                                                     static_cast<cudaStream_t>(stream)));
+}
+
+size_t smoe_experts_matmul_f8_workspace_bytes(int n_src, int n_rows, int n_experts, int n_out, int n_in)
+{
+    if (check_q8(n_src, n_rows, n_experts, n_out, n_in) != SMOE_OK) return static_cast<size_t>(-1);
+    return n_rows == 0 || n_out == 0 ? 0 : smoe::f8_workspace(n_rows, n_experts);
+}
+
+size_t smoe_matmul_f8_workspace_bytes(int n_rows, int n_out, int n_in)
+{
+    return smoe_experts_matmul_f8_workspace_bytes(n_rows, n_rows, 1, n_out, n_in);
+}
+
+static int f8_impl(const uint8_t *xq, const float *x_scales, int n_src, const int *order, int k, const int *offsets,
+                   bool sorted, int n_rows, int n_experts, const uint8_t *wq, const float *w_scales, int n_out, int n_in,
+                   void *y, int dtype, void *workspace, size_t workspace_bytes, void *stream)
+{
+    int st = check_q8(n_src, n_rows, n_experts, n_out, n_in);
+    if (st == SMOE_OK) st = check_rows(dtype, 0);
+    if (st != SMOE_OK) return st;
+    if (order ? (k < 1 || k > SMOE_MAX_TOP_K) : n_src < n_rows) return SMOE_ERR_SHAPE;
+    if (n_rows == 0 || n_out == 0) return SMOE_OK;
+    if (!y || (sorted && !offsets) || (n_in > 0 && (!xq || !wq || !x_scales || !w_scales))) return SMOE_ERR_NULL;
+    const size_t e = elem_bytes(dtype);
+    if (!aligned_to(x_scales, 4) || !aligned_to(w_scales, 4) || !aligned16(y) || (order && !aligned_to(order, 4)) ||
+        (sorted && !aligned_to(offsets, 4)) || (n_in > 0 && (!aligned16(xq) || !aligned16(wq))))
+        return SMOE_ERR_ALIGN;
+    const size_t need = smoe::f8_workspace(n_rows, n_experts);
+    if (!workspace || workspace_bytes < need) return SMOE_ERR_WORKSPACE;
+    if (!aligned16(workspace)) return SMOE_ERR_ALIGN;
+    const size_t kb = blocks_of(n_in);
+    const Span outs[2] = {{y, static_cast<size_t>(n_rows) * n_out * e}, {workspace, need}};
+    const Span ins[6] = {{xq, static_cast<size_t>(n_src) * n_in},
+                         {x_scales, static_cast<size_t>(n_src) * kb * sizeof(float)},
+                         {wq, static_cast<size_t>(n_experts) * n_out * n_in},
+                         {w_scales, n_experts * blocks_of(n_out) * kb * sizeof(float)},
+                         {order, order ? static_cast<size_t>(n_rows) * sizeof(int) : 0},
+                         {offsets, sorted ? (static_cast<size_t>(n_experts) + 1) * sizeof(int) : 0}};
+    if (any_alias(outs, 2, ins, 6)) return SMOE_ERR_ALIAS;
+    return to_status(smoe::launch_f8(xq, x_scales, n_src, order, k, sorted ? offsets : nullptr, n_rows, n_experts, wq,
+                                     w_scales, n_out, n_in, y, dtype, workspace, static_cast<cudaStream_t>(stream)));
+}
+
+int smoe_matmul_f8(const uint8_t *xq, const float *x_scales, int n_rows, const uint8_t *wq, const float *w_scales, int n_out,
+                   int n_in, void *y, int dtype, void *workspace, size_t workspace_bytes, void *stream)
+{
+    return f8_impl(xq, x_scales, n_rows, nullptr, 1, nullptr, false, n_rows, 1, wq, w_scales, n_out, n_in, y, dtype,
+                   workspace, workspace_bytes, stream);
+}
+
+int smoe_experts_matmul_f8(const uint8_t *xq, const float *x_scales, int n_src, const int *order, int k, const int *offsets,
+                           int n_rows, int n_experts, const uint8_t *wq, const float *w_scales, int n_out, int n_in, void *y,
+                           int dtype, void *workspace, size_t workspace_bytes, void *stream)
+{
+    return f8_impl(xq, x_scales, n_src, order, k, offsets, true, n_rows, n_experts, wq, w_scales, n_out, n_in, y, dtype,
+                   workspace, workspace_bytes, stream);
+}
+
+int smoe_experts_weight_grad(const void *d_ys, const void *xs, const int *offsets, int n_rows, int n_experts, int n_out,
+                             int n_in, int accumulate, void *d_w, int dtype, void *stream)
+{
+    const int st = check_rows(dtype, n_in);
+    if (st != SMOE_OK) return st;
+    if (n_rows < 0 || n_rows > SMOE_MAX_SLOTS || n_out < 0 || n_experts < 1 || n_experts > SMOE_MAX_ROUTE_EXPERTS)
+        return SMOE_ERR_SHAPE;
+    if (n_out % 8 != 0 || n_in % 8 != 0 || n_out > SMOE_MAX_COLS || n_in > SMOE_MAX_COLS) return SMOE_ERR_SHAPE;
+    if (n_out == 0 || n_in == 0 || (n_rows == 0 && accumulate)) return SMOE_OK;
+    if (!offsets || !d_w || (n_rows > 0 && (!d_ys || !xs))) return SMOE_ERR_NULL;
+    if (!aligned_to(offsets, 4) || !aligned16(d_w) || (n_rows > 0 && (!aligned16(d_ys) || !aligned16(xs)))) return SMOE_ERR_ALIGN;
+    const Span outs[1] = {{d_w, static_cast<size_t>(n_experts) * n_out * n_in * elem_bytes(dtype)}};
+    const Span ins[3] = {{d_ys, static_cast<size_t>(n_rows) * n_out * 2},
+                         {xs, static_cast<size_t>(n_rows) * n_in * 2},
+                         {offsets, (static_cast<size_t>(n_experts) + 1) * sizeof(int)}};
+    if (any_alias(outs, 1, ins, 3)) return SMOE_ERR_ALIAS;
+    return to_status(smoe::launch_weight_grad(d_ys, xs, offsets, n_rows, n_experts, n_out, n_in, accumulate != 0, d_w, dtype,
+                                              static_cast<cudaStream_t>(stream)));
 }
 
 int smoe_copy(void *dst, const void *src, size_t bytes, void *stream)

@@ -34,7 +34,7 @@
 #include "cluster_table.h"
 #include "q8.cuh"
 #include "smoe.h"
-#include "tcgen05.cuh"
+#include "tc_pair.cuh"
 
 namespace smoe {
 namespace {
@@ -93,15 +93,6 @@ __device__ __forceinline__ void s8x4_to_f16(uint32_t w, uint32_t &lo, uint32_t &
     hi = *reinterpret_cast<uint32_t *>(&hb);
 }
 
-// Shared-memory matrix descriptor, 128-byte swizzle, K-major: 8-row groups
-// 1024 bytes apart, version 1, swizzle mode 2.
-__device__ __forceinline__ uint64_t desc_sw128(uint32_t addr)
-{
-    return static_cast<uint64_t>((addr >> 4) & 0x3FFFu) | (static_cast<uint64_t>(1) << 16) |
-           (static_cast<uint64_t>(1024u >> 4) << 32) | (static_cast<uint64_t>(1) << 46) |
-           (static_cast<uint64_t>(2) << 61);
-}
-
 // Instruction descriptor, kind::f16: f32 accumulate, A and B f16, K-major.
 __device__ __forceinline__ uint32_t idesc_f16(int m, int n)
 {
@@ -117,111 +108,6 @@ __device__ __forceinline__ void mma_f16_ta_pair(uint32_t tmem, uint32_t a_tmem, 
         "tcgen05.mma.cta_group::2.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(tmem),
         "r"(a_tmem), "l"(b), "r"(idesc), "r"(acc)
         : "memory");
-}
-
-// Arrives on the barrier at this place in both CTAs of the pair.
-__device__ __forceinline__ void mma_commit_pair(uint32_t bar)
-{
-    asm volatile(
-        "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(bar),
-        "h"(static_cast<uint16_t>(3))
-        : "memory");
-}
-
-// Copies into this CTA that complete on a barrier of either CTA of the pair.
-__device__ __forceinline__ void tma_load_2d_pair(uint32_t dst, const CUtensorMap *map, int x, int y, uint32_t bar)
-{
-    asm volatile(
-        "cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes.cta_group::2 [%0], [%1, {%2, %3}], "
-        "[%4];" ::"r"(dst),
-        "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(bar)
-        : "memory");
-}
-
-// Four rows of a tensor map whose box is one row high, one below another.
-__device__ __forceinline__ void tma_gather4(uint32_t dst, const CUtensorMap *map, int x, const int4 &r, uint32_t bar)
-{
-    asm volatile(
-        "cp.async.bulk.tensor.2d.shared::cluster.global.tile::gather4.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, "
-        "%5, %6}], [%7];" ::"r"(dst),
-        "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(r.x), "r"(r.y), "r"(r.z), "r"(r.w), "r"(bar)
-        : "memory");
-}
-__device__ __forceinline__ void tma_gather4_pair(uint32_t dst, const CUtensorMap *map, int x, const int4 &r, uint32_t bar)
-{
-    asm volatile(
-        "cp.async.bulk.tensor.2d.shared::cluster.global.tile::gather4.mbarrier::complete_tx::bytes.cta_group::2 [%0], [%1, "
-        "{%2, %3, %4, %5, %6}], [%7];" ::"r"(dst),
-        "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(r.x), "r"(r.y), "r"(r.z), "r"(r.w), "r"(bar)
-        : "memory");
-}
-
-// Arrives on a barrier of either CTA of the cluster (a shared::cluster
-// address).  What it hands over is tensor memory, ordered by the tcgen05
-// fences and waits around it; a release at cluster scope would also wait for
-// this thread's earlier reads and writes elsewhere (1,700 clocks a K tile
-// against 500).
-__device__ __forceinline__ void mbar_arrive_cluster(uint32_t bar)
-{
-    asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
-}
-
-// mbar_wait_bounded for barriers that the other CTA's threads arrive on:
-// acquires at cluster scope.
-__device__ __forceinline__ bool mbar_try_wait_cluster(uint32_t bar, uint32_t parity)
-{
-    uint32_t done;
-    asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2, 20000;\n\t"
-        "selp.u32 %0, 1, 0, p;\n\t}"
-        : "=r"(done)
-        : "r"(bar), "r"(parity)
-        : "memory");
-    return done != 0;
-}
-template <int CL>
-__device__ __forceinline__ bool wait_pair(uint32_t bar, uint32_t parity, unsigned *status, unsigned code)
-{
-    if (CL == 1) return mbar_wait_bounded(bar, parity, status, code);
-    if (mbar_try_wait_cluster(bar, parity)) return true;
-    const long long t0 = clock64();
-    for (uint32_t i = 0; i < (1u << 24); ++i) {
-        __nanosleep(64);
-        if (mbar_try_wait_cluster(bar, parity)) return true;
-        if (clock64() - t0 > 4000000000LL) break;
-    }
-    atomicExch(status, code);
-    return false;
-}
-
-// Whether phase `parity` has completed, without waiting.
-template <int CL>
-__device__ __forceinline__ bool mbar_test(uint32_t bar, uint32_t parity)
-{
-    uint32_t done;
-    if (CL > 1)
-        asm volatile(
-            "{\n\t.reg .pred p;\n\tmbarrier.test_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
-            "selp.u32 %0, 1, 0, p;\n\t}"
-            : "=r"(done)
-            : "r"(bar), "r"(parity)
-            : "memory");
-    else
-        asm volatile(
-            "{\n\t.reg .pred p;\n\tmbarrier.test_wait.parity.acquire.cta.shared::cta.b64 p, [%1], %2;\n\t"
-            "selp.u32 %0, 1, 0, p;\n\t}"
-            : "=r"(done)
-            : "r"(bar), "r"(parity)
-            : "memory");
-    return done != 0;
-}
-
-// Columns of the MMA for a tile of `rows`: a pair's come in 32s.
-template <int CL>
-__device__ __forceinline__ int mma_cols(int rows)
-{
-    return (rows + 16 * CL - 1) & ~(16 * CL - 1);
 }
 
 __device__ __forceinline__ Tile tile_at(const TcArgs &a, int i, int ntiles)
@@ -662,46 +548,11 @@ struct PrepArgs {
 // expert's.
 __global__ void __launch_bounds__(PREP_THREADS) q8_prep(const PrepArgs a)
 {
-    __shared__ long long warp_sums[PREP_THREADS / 32];
-    __shared__ long long run_s;
     pdl_launch_dependents();
     pdl_wait();
     const int tid = threadIdx.x;
     if (a.offsets && blockIdx.x == 0) {
-        const int lane = tid & 31, wi = tid >> 5;
-        long long run = 0;  // 64 bits: ranges that overlap (reported) can add up to more than 32
-        for (int b = 0; b < a.n; b += PREP_THREADS) {
-            const int e = b + tid;
-            int lo = 0, hi = 0;
-            if (e < a.n) {
-                lo = a.offsets[e];
-                hi = a.offsets[e + 1];
-                if (lo < 0 || hi < lo || hi > a.R) {
-                    atomicExch(a.status, kStatusRoute);
-                    lo = hi = 0;
-                }
-            }
-            int cnt = (hi - lo + a.nt - 1) / a.nt;
-            const int step = cnt > 0 ? ((hi - lo + cnt - 1) / cnt + a.unit - 1) / a.unit * a.unit : a.unit;
-            cnt = (hi - lo + step - 1) / step;
-            long long inc = cnt;
-#pragma unroll
-            for (int off = 1; off < 32; off <<= 1) {
-                const long long o = __shfl_up_sync(FULL_MASK, inc, off);
-                if (lane >= off) inc += o;
-            }
-            if (lane == 31) warp_sums[wi] = inc;
-            __syncthreads();
-            long long before = run;
-            for (int i = 0; i < wi; ++i) before += warp_sums[i];
-            if (tid == PREP_THREADS - 1) run_s = before + inc;
-            const long long t0 = before + inc - cnt;
-            for (int i = 0; i < cnt && t0 + i < a.max_tiles; ++i)
-                a.tiles[t0 + i] = Tile{e, lo + i * step, min(step, hi - lo - i * step), 0};
-            __syncthreads();
-            run = run_s;
-        }
-        if (tid == 0) *a.ntiles = static_cast<int>(min(run, static_cast<long long>(a.max_tiles)));
+        list_tiles<PREP_THREADS>(a.offsets, a.n, a.R, a.nt, a.unit, a.max_tiles, a.ntiles, a.tiles, a.status);
         return;
     }
     const int b0 = a.offsets ? 1 : 0, blocks = gridDim.x - b0;
@@ -737,20 +588,6 @@ __global__ void __launch_bounds__(PREP_THREADS) q8_prep(const PrepArgs a)
 }
 
 // ---------------------------------------------------------------- host
-
-bool encode(CUtensorMap *map, CUtensorMapDataType type, int elem, const void *p, long long cols, long long rows, int box_x,
-            int box_y)
-{
-    EncodeTiled fn = encoder();
-    if (!fn) return false;
-    const cuuint64_t dims[2] = {static_cast<cuuint64_t>(cols), static_cast<cuuint64_t>(rows)};
-    const cuuint64_t strides[1] = {static_cast<cuuint64_t>(cols) * elem};
-    const cuuint32_t box[2] = {static_cast<cuuint32_t>(box_x), static_cast<cuuint32_t>(box_y)};
-    const cuuint32_t estr[2] = {1u, 1u};
-    return fn(map, type, 2, const_cast<void *>(p), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
-              CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) ==
-           CUDA_SUCCESS;
-}
 
 // Row tile: 64 (single CTAs, a deep ring of weights) where the product is
 // bound by reading the weights or its tiles fit the device at once, 192

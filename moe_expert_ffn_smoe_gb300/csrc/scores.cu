@@ -1,0 +1,580 @@
+// Routing by scores: softmax or sigmoid scores of every row of logits, a bias
+// that moves the choice alone, groups of experts, the k best of the best groups,
+// and their weights; and the gradient of the weights to the logits.
+//
+//   s_i = 1 / (1 + e^-l_i)   or   e^(l_i - max) / sum over the row
+//   c_i = s_i + b_i                      (what the choice goes by)
+//   w_r = scale s_r / sum over the chosen   or   scale s_r
+//
+// The choice is the one that the real numbers c_i make.  Where no bias is added
+// and no two scores are summed, that is the order of the logits.  Elsewhere c_i
+// is taken in f32 with a bound of its error, and what lies closer than the bounds
+// (a row in some thousands) is decided by the same values in 64 bits: of the
+// candidates alone, one a lane, or, where the border between groups is in doubt,
+// of the whole row.  64-bit arithmetic runs at a 64th of the f32 rate here: all
+// scores in it took 30 times as long as the rest.
+#include "common.cuh"
+#include "internal_tokens.h"
+#include "smoe.h"
+#include "topk.cuh"
+
+namespace smoe {
+namespace {
+
+constexpr int ROUTE_WARPS = 8;
+
+// What the choice goes by.
+enum class By { Logit, Sigmoid, Softmax };
+
+struct RouteArgs {
+    const float *logits, *bias;  // bias null: none
+    int *idx;
+    float *w;
+    int T, n, ld, k, groups, top_groups, best;
+    int size;        // experts of a group
+    unsigned magic;  // ceil(2^20 / size): e magic >> 20 = e / size for e < 1024
+    float scale;
+    bool softmax, norm;
+};
+
+__device__ __forceinline__ float warp_max(float v)
+{
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1) v = fmaxf(v, __shfl_xor_sync(FULL_MASK, v, off));
+    return v;
+}
+__device__ __forceinline__ float warp_sum(float v)
+{
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1) v += __shfl_xor_sync(FULL_MASK, v, off);
+    return v;
+}
+
+__device__ __forceinline__ float rcp_approx(float v)
+{
+    float r;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v));
+    return r;
+}
+
+// A row's constants: its largest logit and what e^(l - m) is multiplied by
+// (softmax), and the row itself.
+struct Row {
+    const float *l, *b;
+    float m, inv;
+    int n, V;
+};
+
+// c of logit l and bias b, and a bound of its error.  Sigmoid: e^-l to 2 units
+// in the last place, the sum and the reciprocal instruction to one each: below
+// 2^-21 of s.  Softmax: l - m is rounded (2^-24 of its size, in the exponent),
+// the row's sum has V + 5 additions after terms as exact; the rounding of s + b
+// is 2^-24 of c.  Below the normal numbers the instructions flush.
+template <By BY>
+__device__ __forceinline__ float choice(const Row &r, float l, float b, float &err)
+{
+    float s, rel;
+    if (BY == By::Sigmoid) {
+        s = rcp_approx(1.0f + expf(-l));
+        rel = 0x1p-21f;
+    } else {
+        s = expf(l - r.m) * r.inv;
+        rel = (fabsf(l - r.m) + static_cast<float>(r.V + 32)) * 0x1p-24f;
+    }
+    const float c = s + b;
+    err = fmaf(s, rel, fmaf(fabsf(c), 0x1p-23f, 1e-37f));
+    return c;
+}
+
+// The same in 64 bits; inv64: 1 / the row's sum (softmax).
+template <By BY>
+__device__ __forceinline__ double choice64(const Row &r, int e, double inv64)
+{
+    const double l = r.l[e], b = r.b ? r.b[e] : 0.f;
+    return (BY == By::Sigmoid ? 1.0 / (1.0 + exp(-l)) : exp(l - r.m) * inv64) + b;
+}
+
+__device__ __forceinline__ bool is_off(const Row &r, int e)
+{
+    return r.l[e] == -INFINITY || (r.b && r.b[e] == -INFINITY);
+}
+
+template <By BY>
+__device__ __noinline__ double inverse_sum64(const Row r)
+{
+    if (BY != By::Softmax) return 0.0;
+    double sum = 0.0;
+    for (int e = threadIdx.x & 31; e < r.n; e += 32) sum += exp(static_cast<double>(r.l[e]) - r.m);
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1) sum += __shfl_xor_sync(FULL_MASK, sum, off);
+    return 1.0 / sum;
+}
+
+// Whether all experts of the row that are on have one logit and one bias: then
+// equal sums of scores are equal, and no 64-bit look is needed (a router whose
+// weights are still zero).
+__device__ __noinline__ bool all_alike(const Row r)
+{
+    float lo = INFINITY, hi = -INFINITY, blo = INFINITY, bhi = -INFINITY;
+    for (int e = threadIdx.x & 31; e < r.n; e += 32)
+        if (!is_off(r, e)) {
+            lo = fminf(lo, r.l[e]);
+            hi = fmaxf(hi, r.l[e]);
+            blo = fminf(blo, r.b ? r.b[e] : 0.f);
+            bhi = fmaxf(bhi, r.b ? r.b[e] : 0.f);
+        }
+    return -warp_max(-lo) == warp_max(hi) && -warp_max(-blo) == warp_max(bhi);
+}
+
+// Lanes P g .. P g + P - 1 look at group g: the largest power of two that
+// leaves every group its lanes.
+__device__ __forceinline__ int lanes_of_group(int groups)
+{
+    return 1 << (31 - __clz(32 / groups));
+}
+
+// The groups taken, as a mask of their first lanes, from every lane's value of
+// its group (equal in all lanes of a group; -inf: no expert on); err: bound of
+// its error; doubt: whether the border lies within the bounds.
+template <typename F>
+__device__ __forceinline__ uint32_t take_groups(F value, F err, int P, const RouteArgs &a, bool &doubt)
+{
+    const int lane = threadIdx.x & 31, g = lane / P;
+    int before = 0;
+    for (int h = 0; h < a.groups; ++h) {
+        const F o = __shfl_sync(FULL_MASK, value, h * P);
+        before += o > value || (o == value && h < g);
+    }
+    const bool on = g < a.groups && value > -INFINITY, taken = on && before < a.top_groups;
+    const float low = warp_max(taken ? static_cast<float>(err - value) : -INFINITY);          // = -(least sure value)
+    const float high = warp_max(on && !taken ? static_cast<float>(value + err) : -INFINITY);
+    doubt = high >= -low && low > -INFINITY && high > -INFINITY;
+    return __ballot_sync(FULL_MASK, taken && lane % P == 0);
+}
+
+// The same from scores in 64 bits.
+template <By BY>
+__device__ __noinline__ uint32_t take_groups64(const Row r, const RouteArgs &a, int P)
+{
+    const double inv64 = inverse_sum64<BY>(r);
+    const int lane = threadIdx.x & 31, g = lane / P;
+    double b1 = -INFINITY, b2 = -INFINITY;
+    if (g < a.groups)
+        for (int e = g * a.size + lane % P; e < (g + 1) * a.size; e += P) {
+            const double t = is_off(r, e) ? -INFINITY : choice64<BY>(r, e, inv64);
+            b2 = fmax(b2, fmin(b1, t));
+            b1 = fmax(b1, t);
+        }
+    for (int off = P >> 1; off > 0; off >>= 1) {
+        const double o1 = __shfl_xor_sync(FULL_MASK, b1, off), o2 = __shfl_xor_sync(FULL_MASK, b2, off);
+        b2 = fmax(fmin(b1, o1), fmax(b2, o2));
+        b1 = fmax(b1, o1);
+    }
+    const double value = b1 + (a.best == 2 && b2 > -INFINITY ? b2 : 0.0);
+    int before = 0;
+    for (int h = 0; h < a.groups; ++h) {
+        const double o = __shfl_sync(FULL_MASK, value, h * P);
+        before += o > value || (o == value && h < g);
+    }
+    return __ballot_sync(FULL_MASK, g < a.groups && value > -INFINITY && before < a.top_groups && lane % P == 0);
+}
+
+// The next of the row in the order of the real c, among those not yet taken
+// (key > kKeyNegInf): the largest in f32, unless others lie within the bound
+// `err` of it that are not its equals.
+template <By BY, int V>
+__device__ __noinline__ int next_in_doubt(const uint32_t (&key)[V], const Row r, float top, float err, double inv64)
+{
+    const int lane = threadIdx.x & 31;
+    double best = -INFINITY;
+    int be = 0x7fffffff;
+#pragma unroll 1
+    for (int e = lane; e < r.n; e += 32) {
+        uint32_t mine = 0u;
+#pragma unroll
+        for (int i = 0; i < V; ++i)
+            if (i == e / 32) mine = key[i];
+        if (mine <= kKeyNegInf || value_of_key(mine) < top - 2.f * err) continue;
+        const double c = choice64<BY>(r, e, inv64);
+        if (c > best) {
+            best = c;
+            be = e;
+        }
+    }
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1) {
+        const double o = __shfl_xor_sync(FULL_MASK, best, off);
+        const int oe = __shfl_xor_sync(FULL_MASK, be, off);
+        if (o > best || (o == best && oe < be)) {
+            best = o;
+            be = oe;
+        }
+    }
+    return be;
+}
+
+// k rounds over the row by c, for rows that the filter leaves with more than a
+// warp's candidates, and for k > FILTER_K.  Lane l ends with ranks l and l + 32
+// (-1: none left).
+template <By BY, int V>
+__device__ __forceinline__ void choose_by_rounds(uint32_t (&key)[V], const Row &r, int k, float err, int &ea, int &eb)
+{
+    const int lane = threadIdx.x & 31;
+    double inv64 = 0.0;
+    bool summed = false;
+    for (int q = 0; q < k; ++q) {
+        uint32_t best = 0u;
+        int bi = 0;
+#pragma unroll
+        for (int i = 0; i < V; ++i)
+            if (key[i] > best) {
+                best = key[i];
+                bi = i;
+            }
+        const uint32_t top = __reduce_max_sync(FULL_MASK, best);
+        if (top <= kKeyNegInf) return;
+        int e = static_cast<int>(
+            __reduce_min_sync(FULL_MASK, best == top ? static_cast<unsigned>(bi * 32 + lane) : 0xFFFFFFFFu));
+        const float ct = value_of_key(top), lt = r.l[e], bt = r.b ? r.b[e] : 0.f;
+        bool doubt = false;
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+            const int o = i * 32 + lane;
+            if (key[i] > kKeyNegInf && o != e && value_of_key(key[i]) >= ct - 2.f * err)
+                doubt |= r.l[o] != lt || (r.b && r.b[o] != bt);
+        }
+        if (__any_sync(FULL_MASK, doubt)) {
+            if (!summed) inv64 = inverse_sum64<BY>(r);
+            summed = true;
+            e = next_in_doubt<BY, V>(key, r, ct, err, inv64);
+        }
+#pragma unroll
+        for (int i = 0; i < V; ++i)
+            if (e == i * 32 + lane) key[i] = 0u;
+        if (q == lane) ea = e;
+        if (q == lane + 32) eb = e;
+    }
+}
+
+// Weights of the experts that this warp's lanes hold (ea and eb; -1: none), at
+// the ranks ra and rb.  Where every chosen score is small, renormalised weights come
+// from e^(l - largest l), which keeps the digits that small scores lose: a sigmoid
+// that far down is e^l to 2^-28.
+__device__ __forceinline__ void write_weights(const RouteArgs &a, const Row &r, int ea, int eb, int ra, int rb, int *idx, float *w)
+{
+    const float la = ea >= 0 ? r.l[ea] - (a.softmax ? r.m : 0.f) : -INFINITY;
+    const float lb = eb >= 0 ? r.l[eb] - (a.softmax ? r.m : 0.f) : -INFINITY;
+    float sa, sb = 0.f;
+    const float top = a.norm ? warp_max(fmaxf(la, lb)) : 0.f;
+    if (top < -20.f) {
+        sa = ea >= 0 ? expf(la - top) : 0.f;
+        sb = eb >= 0 ? expf(lb - top) : 0.f;
+    } else if (a.softmax) {
+        sa = ea >= 0 ? expf(la) * r.inv : 0.f;
+        sb = eb >= 0 ? expf(lb) * r.inv : 0.f;
+    } else {
+        sa = ea >= 0 ? 1.f / (1.f + expf(-la)) : 0.f;
+        if (eb >= 0) sb = 1.f / (1.f + expf(-lb));
+    }
+    const float sum = a.norm ? warp_sum(sa + sb) : 1.f;
+    if (ra >= 0 && ra < a.k) {
+        idx[ra] = ea;
+        w[ra] = ea >= 0 ? a.scale * (sa / sum) : 0.f;
+    }
+    if (rb >= 0 && rb < a.k) {
+        idx[rb] = eb;
+        w[rb] = eb >= 0 ? a.scale * (sb / sum) : 0.f;
+    }
+}
+
+// One warp per row, n <= 32 V: expert i 32 + lane.  Bound by instruction issue.
+template <By BY, int V>
+__global__ void __launch_bounds__(ROUTE_WARPS * 32) route_rows_warp(const RouteArgs a)
+{
+    __shared__ float rows[ROUTE_WARPS][32 * V];
+    __shared__ __align__(16) Candidates cands[ROUTE_WARPS];
+    const int wi = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int t = blockIdx.x * ROUTE_WARPS + wi;
+    pdl_launch_dependents();
+    pdl_wait();
+    if (t >= a.T) return;
+    Row r = {a.logits + static_cast<size_t>(t) * a.ld, a.bias, 0.f, 0.f, a.n, V};
+    int *idx = a.idx + static_cast<size_t>(t) * a.k;
+    float *w = a.w + static_cast<size_t>(t) * a.k;
+    float l[V], b[V];
+    bool bad = false;
+    float top = -INFINITY;
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+        const int e = i * 32 + lane;
+        l[i] = e < a.n ? r.l[e] : -INFINITY;
+        b[i] = a.bias && e < a.n ? a.bias[e] : 0.f;
+        bad |= l[i] != l[i] || (a.softmax && l[i] == INFINITY) ||
+               (l[i] != -INFINITY && (b[i] != b[i] || b[i] == INFINITY));
+        top = fmaxf(top, l[i]);
+    }
+    if (__any_sync(FULL_MASK, bad)) {
+        // no order and no weights: NaN for k experts, so that the token's output is NaN
+        for (int q = lane; q < a.k; q += 32) {
+            idx[q] = q;
+            w[q] = __int_as_float(0x7fffffff);
+        }
+        return;
+    }
+    if (a.softmax) {
+        r.m = warp_max(top);
+        if (r.m > -INFINITY && (BY == By::Softmax || !a.norm)) {
+            float sum = 0.f;
+#pragma unroll
+            for (int i = 0; i < V; ++i) sum += expf(l[i] - r.m);
+            r.inv = 1.f / warp_sum(sum);
+        } else {
+            r.inv = 1.f;  // weights that are renormalised need no sum
+        }
+    }
+    // the keys of what the choice goes by; off: kKeyNegInf
+    uint32_t key[V];
+    float err = 0.f;
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+        const int e = i * 32 + lane;
+        key[i] = e < a.n ? kKeyNegInf : 0u;
+        if (l[i] == -INFINITY || b[i] == -INFINITY) continue;
+        if (BY == By::Logit) {
+            key[i] = value_key(l[i]);
+        } else {
+            float d;
+            key[i] = value_key(choice<BY>(r, l[i], b[i], d));
+            err = fmaxf(err, d);
+        }
+    }
+    if (BY != By::Logit) err = warp_max(err);
+
+    if (a.groups > 1) {
+        float *c = rows[wi];
+        const int P = lanes_of_group(a.groups), g = lane / P;
+        float b1 = -INFINITY, b2 = -INFINITY;
+#pragma unroll
+        for (int i = 0; i < V; ++i)
+            if (i * 32 + lane < a.n) c[i * 32 + lane] = value_of_key(key[i]);
+        __syncwarp();
+        if (g < a.groups)
+            for (int e = g * a.size + lane % P; e < (g + 1) * a.size; e += P) {
+                const float v = c[e];
+                b2 = fmaxf(b2, fminf(b1, v));
+                b1 = fmaxf(b1, v);
+            }
+        for (int off = P >> 1; off > 0; off >>= 1) {
+            const float o1 = __shfl_xor_sync(FULL_MASK, b1, off), o2 = __shfl_xor_sync(FULL_MASK, b2, off);
+            b2 = fmaxf(fminf(b1, o1), fmaxf(b2, o2));
+            b1 = fmaxf(b1, o1);
+        }
+        const float value = b1 + (a.best == 2 && b2 > -INFINITY ? b2 : 0.f);
+        bool doubt;
+        uint32_t taken = take_groups(value, BY == By::Logit ? 0.f : fmaf(fabsf(value), 0x1p-23f, 2.f * err), P, a, doubt);
+        if (BY != By::Logit && doubt && !all_alike(r)) taken = take_groups64<BY>(r, a, P);
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+            const int e = i * 32 + lane;
+            const int of = static_cast<int>((static_cast<unsigned>(e) * a.magic) >> 20);
+            if (e < a.n && !(taken >> (of * P) & 1u)) key[i] = kKeyNegInf;
+        }
+    }
+
+    if (a.k <= FILTER_K) {
+        uint32_t most = key[0], first;
+#pragma unroll
+        for (int i = 1; i < V; ++i) most = max(most, key[i]);
+        uint32_t bound = filter_bound(most, a.k, first);
+        if (first <= kKeyNegInf) {
+            write_masked(a.k, idx, w);
+            return;
+        }
+        // what may be among the k best: within the bounds of the bound
+        if (BY != By::Logit && bound > kKeyNegInf) bound = value_key(value_of_key(bound) - 2.f * err);
+        bound = max(bound, kKeyNegInf + 1u);
+        Candidates &c = cands[wi];
+        c.key[lane] = 0u;
+        __syncwarp();
+        int count = 0;
+#pragma unroll
+        for (int i = 0; i < V; ++i) gather_candidate(c, key[i] >= bound, key[i], i * 32 + lane, count);
+        __syncwarp();
+        if (count <= 32) {
+            const int e = lane < count ? c.expert[lane] : -1;
+            const uint32_t mine = c.key[lane];
+            // the larger ones, and of the equal ones those before it (in expert order)
+            int rank = 0;
+            for (int o = 0; o < count; o += 4) {
+                const uint4 v = *reinterpret_cast<const uint4 *>(&c.key[o]);
+                rank += v.x >= mine + (o >= lane ? 1u : 0u);
+                rank += v.y >= mine + (o + 1 >= lane ? 1u : 0u);
+                rank += v.z >= mine + (o + 2 >= lane ? 1u : 0u);
+                rank += v.w >= mine + (o + 3 >= lane ? 1u : 0u);
+            }
+            if (BY != By::Logit) {
+                const float ce = value_of_key(mine);
+                bool doubt = false;
+                for (int o = 0; o < count; ++o)
+                    doubt |= o != lane && fabsf(value_of_key(c.key[o]) - ce) <= 2.f * err;
+                if (__any_sync(FULL_MASK, doubt && lane < count && rank <= a.k)) {
+                    const double inv64 = inverse_sum64<BY>(r);
+                    const double c64 = e >= 0 ? choice64<BY>(r, e, inv64) : -INFINITY;
+                    rank = 0;
+                    for (int o = 0; o < count; ++o) {
+                        const double v = __shfl_sync(FULL_MASK, c64, o);
+                        rank += v > c64 || (v == c64 && o < lane);
+                    }
+                }
+            }
+            // ranks past the candidates: none left
+            const bool sel = lane < count && rank < a.k;
+            write_weights(a, r, sel ? e : -1, -1, sel ? rank : (lane >= count ? lane : -1), -1, idx, w);
+            return;
+        }
+    }
+    int ea = -1, eb = -1;
+    choose_by_rounds<BY, V>(key, r, a.k, err, ea, eb);
+    write_weights(a, r, ea, eb, lane, lane + 32, idx, w);
+}
+
+// ---------------------------------------------------------------- gradient
+
+struct RouteGradArgs {
+    const float *logits;
+    const int *idx;
+    const float *w, *dw;
+    float *dl;
+    int T, n, ld, k;
+    float scale;
+    bool softmax, norm;
+};
+
+// With g_r = w_r (dw_r - sum_q w_q dw_q / scale) where the weights are
+// renormalised, w_r dw_r where not:
+//   sigmoid            dl_r = g_r (1 - s_r)
+//   softmax, norm      dl_r = g_r
+//   softmax            dl_j = (g_r of the slot of j) - s_j sum_r g_r, for every j
+// A warp per row, which makes the row in shared memory and writes it once.  Bound
+// by writing the gradients (and, for the last form, reading the logits).
+template <int V>
+__global__ void __launch_bounds__(ROUTE_WARPS * 32) route_rows_grad(const RouteGradArgs a)
+{
+    __shared__ float rows[ROUTE_WARPS][32 * V];
+    const int wi = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int t = blockIdx.x * ROUTE_WARPS + wi;
+    pdl_launch_dependents();
+    pdl_wait();
+    if (t >= a.T) return;
+    const float *l = a.logits + static_cast<size_t>(t) * a.ld;
+    const bool dense = a.softmax && !a.norm;
+    float p[V];
+    if (dense) {
+#pragma unroll
+        for (int i = 0; i < V; ++i) p[i] = i * 32 + lane < a.n ? l[i * 32 + lane] : -INFINITY;
+    }
+    int e[2];
+    float w[2], g[2];
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+        const bool in = lane + 32 * h < a.k;
+        const size_t at = static_cast<size_t>(t) * a.k + lane + 32 * h;
+        e[h] = in ? a.idx[at] : -1;
+        w[h] = in ? a.w[at] : 0.f;
+        g[h] = in ? a.dw[at] : 0.f;
+        if (e[h] < 0 || e[h] >= a.n) e[h] = -1;  // no expert: counts for nothing
+    }
+    float dot = 0.f;
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+        if (e[h] >= 0) dot = fmaf(w[h], g[h], dot);
+    dot = warp_sum(dot);
+    const float mean = a.norm ? dot / a.scale : 0.f;
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+        g[h] = w[h] * (g[h] - mean);
+        if (!a.softmax && e[h] >= 0) g[h] /= 1.f + expf(l[e[h]]);  // 1 - s = 1 / (1 + e^l)
+    }
+    float *row = rows[wi];
+    if (dense) {
+        float top = p[0];
+#pragma unroll
+        for (int i = 1; i < V; ++i) top = fmaxf(top, p[i]);
+        top = warp_max(top);
+        const float m = top > -INFINITY ? top : 0.f;  // a row of nothing else: scores of 0
+        float sum = 0.f;
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+            p[i] = expf(p[i] - m);
+            sum += p[i];
+        }
+        sum = warp_sum(sum);
+        const float inv = sum > 0.f || sum != sum ? dot / sum : 0.f;
+#pragma unroll
+        for (int i = 0; i < V; ++i)
+            if (i * 32 + lane < a.n) row[i * 32 + lane] = 0.f - p[i] * inv;
+    } else {
+#pragma unroll
+        for (int i = 0; i < V; ++i) row[i * 32 + lane] = 0.f;
+    }
+    __syncwarp();
+    // slots of one expert (a selection has none twice, a caller's list may) in slot order
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+        if (h == 1 && a.k <= 32) break;
+        const unsigned same = __match_any_sync(FULL_MASK, e[h] >= 0 ? e[h] : -1 - lane);
+        if (__all_sync(FULL_MASK, __popc(same) == 1)) {
+            if (e[h] >= 0) row[e[h]] += g[h];
+        } else {
+            for (int q = 0; q < 32; ++q) {
+                if (q == lane && e[h] >= 0) row[e[h]] += g[h];
+                __syncwarp();
+            }
+        }
+        __syncwarp();
+    }
+    float *dl = a.dl + static_cast<size_t>(t) * a.n;
+    if ((a.n & 3) == 0) {
+        for (int c = lane; c < (a.n >> 2); c += 32)
+            reinterpret_cast<float4 *>(dl)[c] = reinterpret_cast<const float4 *>(row)[c];
+    } else {
+        for (int c = lane; c < a.n; c += 32) dl[c] = row[c];
+    }
+}
+
+template <By BY>
+cudaError_t route_by(const RouteArgs &a, cudaStream_t stream)
+{
+    const dim3 grid(static_cast<unsigned>((a.T + ROUTE_WARPS - 1) / ROUTE_WARPS)), block(ROUTE_WARPS * 32);
+    if (a.n <= 128) return launch_pdl(route_rows_warp<BY, 4>, grid, block, 0, stream, a);
+    if (a.n <= 256) return launch_pdl(route_rows_warp<BY, 8>, grid, block, 0, stream, a);
+    if (a.n <= 512) return launch_pdl(route_rows_warp<BY, 16>, grid, block, 0, stream, a);
+    return launch_pdl(route_rows_warp<BY, 32>, grid, block, 0, stream, a);
+}
+
+}  // namespace
+
+cudaError_t launch_route_rows(const float *logits, int T, int n, int ld, const float *bias, bool softmax, int groups,
+                              int top_groups, int best, int k, bool norm, float scale, int *idx, float *w,
+                              cudaStream_t stream)
+{
+    const int size = n / groups;
+    if (groups > 1 && top_groups >= groups) groups = top_groups = 1;  // all of them
+    const RouteArgs a = {logits, bias, idx, w, T, n, ld, k, groups, top_groups, best, size,
+                         static_cast<unsigned>(((1 << 20) + size - 1) / size), scale, softmax, norm};
+    if (!bias && (groups == 1 || best == 1)) return route_by<By::Logit>(a, stream);
+    return softmax ? route_by<By::Softmax>(a, stream) : route_by<By::Sigmoid>(a, stream);
+}
+
+cudaError_t launch_route_rows_grad(const float *logits, int T, int n, int ld, bool softmax, int k, bool norm, float scale,
+                                   const int *idx, const float *w, const float *dw, float *dl, cudaStream_t stream)
+{
+    const RouteGradArgs a = {logits, idx, w, dw, dl, T, n, ld, k, scale, softmax, norm};
+    const dim3 grid(static_cast<unsigned>((T + ROUTE_WARPS - 1) / ROUTE_WARPS)), block(ROUTE_WARPS * 32);
+    if (n <= 128) return launch_pdl(route_rows_grad<4>, grid, block, 0, stream, a);
+    if (n <= 256) return launch_pdl(route_rows_grad<8>, grid, block, 0, stream, a);
+    if (n <= 512) return launch_pdl(route_rows_grad<16>, grid, block, 0, stream, a);
+    return launch_pdl(route_rows_grad<32>, grid, block, 0, stream, a);
+}
+
+}  // namespace smoe
