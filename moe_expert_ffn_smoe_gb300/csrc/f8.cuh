@@ -24,7 +24,7 @@ struct F8Call {
 };
 
 // The product on the tensor cores (f8_tc.cu).
-size_t f8_tc_workspace(int R, int n);
+size_t f8_tc_workspace(int R, int n, int K);
 cudaError_t launch_f8_tc(const F8Call &c, void *workspace, cudaStream_t stream);
 
 }  // namespace smoe

@@ -10,17 +10,21 @@
 //
 // The weights are the MMA's M side (128 rows of one expert: one scale a block), the
 // activation rows its N side, so that any number of rows of an expert costs its own
-// share of tensor-core time.  The accumulator is read in the shape 16x256b, where a
-// thread holds two neighbouring columns of four rows: the scales of its columns (the
-// activation rows') are then read from shared memory once for four products; with a
-// row a thread (32x32b) every product needs its own, eight times the reads.
+// share of tensor-core time.  The accumulator is read in the shape 16x128b, where a
+// thread holds every fourth column of four rows: the scales of its columns (the
+// activation rows') are then read from shared memory once for four products.  (A row a
+// thread, 32x32b, needs a scale for every product, 512 clocks of shared memory a block
+// of 256 rows, as long as its MMAs take; 16x256b reads tensor memory at half the rate.)
 //
 // Persistent: CTAs (row tiles of up to 64: a deep ring of weights, many small
 // accumulators) or pairs of them (cta_group::2, up to 256 rows by 256 weight rows)
 // walk the items (tile of rows, weight tiles).  Roles (warps): 0-7 epilogue, 8 issues
 // the MMAs (of the pair: the even CTA's), 9 streams the weights, 10 brings the row
-// scales, 12-15 the rows (gathered by the copies where the batch is sorted by an
-// order).  Every wait is bounded.
+// scales of the small tiles, 12-15 the rows (gathered by the copies where the batch is
+// sorted by an order).  The pairs' row scales are laid out beforehand, in the order in
+// which they are read, so that copies bring them: one warp that fetched and stored 256
+// of them paced the loop (1999 rows x 8192 x 4096 113 us, without its scales 86).
+// Every wait is bounded.
 #include <atomic>
 
 #include "f8.cuh"
@@ -35,9 +39,9 @@ constexpr uint32_t W_BYTES = MT * F8_BLOCK;  // a block of columns of them
 constexpr int EPI_WARPS = 8, MMA_WARP = 8, W_WARP = 9, S_WARP = 10, X_WARP = 12, X_WARPS = 4;
 constexpr int TC_THREADS = (X_WARP + X_WARPS) * 32;
 constexpr int SLOTS = 8;                     // blocks whose row scales are on hand
-// A warp's place for 16 rows of 32 outputs on their way out: rows of 32 elements
+// A warp's place for 8 rows of 32 outputs on their way out: rows of 32 elements
 // and 16 bytes (the 16-byte reads of eight lanes then meet no bank twice).
-constexpr uint32_t OUT_BYTES = 16 * (32 * 4 + 16);
+constexpr uint32_t OUT_BYTES = 8 * (32 * 4 + 16);
 
 // Shapes of the two forms: row tile NT, CTAs per tile CL, stages of the operands
 // (weights and a CTA's share of the rows), accumulators D, and the columns CB that
@@ -63,12 +67,13 @@ constexpr size_t tc_smem()
 
 struct alignas(128) TcArgs {
     CUtensorMap wmap, xmap;
-    const float *ws, *xs;  // scales [n x nb x kb], [nsrc x kb]
+    const float *ws, *xs;  // scales [n x nb x kb]; [nsrc x kb], of the pairs laid out [kb x pitch]
     void *y;
     const int *ntiles;
     const Tile *tiles;     // null: one matrix, tiles of `step` rows
     const int *order;      // source of every sorted row, times k (gathered), or null
     unsigned *status;
+    long long pitch;
     int R, N, K, kb, nb, k, nsrc, step, mtiles, box;  // box: rows of one copy (not gathered)
     int nsplit;            // CTAs that share an item's K range (single-CTA form)
 };
@@ -102,18 +107,18 @@ __device__ __forceinline__ void commit(uint32_t bar)
     else mma_commit(bar);
 }
 
-// 16 tensor-memory lanes (from that of the address on) by CB columns: of each eight
-// columns 8 g, v[4 g ..] = (row lane / 4, columns 2 (lane % 4) and + 1), (row + 8, the same).
-__device__ __forceinline__ void tmem_ld_16x256(uint32_t at, uint32_t (&v)[16])
+// 16 tensor-memory lanes (from that of the address on) by 32 or 16 columns: v[2 i] is
+// row lane / 4, column 4 i + lane % 4, v[2 i + 1] row lane / 4 + 8 of it.
+__device__ __forceinline__ void tmem_ld_16x128(uint32_t at, uint32_t (&v)[16])
 {
-    asm volatile("tcgen05.ld.sync.aligned.16x256b.x4.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+    asm volatile("tcgen05.ld.sync.aligned.16x128b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
                  : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7]),
                    "=r"(v[8]), "=r"(v[9]), "=r"(v[10]), "=r"(v[11]), "=r"(v[12]), "=r"(v[13]), "=r"(v[14]), "=r"(v[15])
                  : "r"(at));
 }
-__device__ __forceinline__ void tmem_ld_16x256(uint32_t at, uint32_t (&v)[8])
+__device__ __forceinline__ void tmem_ld_16x128(uint32_t at, uint32_t (&v)[8])
 {
-    asm volatile("tcgen05.ld.sync.aligned.16x256b.x2.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+    asm volatile("tcgen05.ld.sync.aligned.16x128b.x4.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
                  : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7])
                  : "r"(at));
 }
@@ -131,18 +136,18 @@ __device__ __forceinline__ void tmem_loaded(uint32_t (&v)[N], uint32_t (&w)[N])
 }
 
 // a += d f, two at a time.
-__device__ __forceinline__ void fma2(float2 &a, uint32_t d0, uint32_t d1, const float2 &f)
+__device__ __forceinline__ void fma2(float2 &a, uint32_t d0, uint32_t d1, float f)
 {
-    asm("{\n\t.reg .b64 d, f, a;\n\tmov.b64 d, {%2, %3};\n\tmov.b64 f, {%4, %5};\n\tmov.b64 a, {%0, %1};\n\t"
+    asm("{\n\t.reg .b64 d, f, a;\n\tmov.b64 d, {%2, %3};\n\tmov.b64 f, {%4, %4};\n\tmov.b64 a, {%0, %1};\n\t"
         "fma.rn.f32x2 a, d, f, a;\n\tmov.b64 {%0, %1}, a;\n\t}"
         : "+f"(a.x), "+f"(a.y)
-        : "r"(d0), "r"(d1), "f"(f.x), "f"(f.y));
+        : "r"(d0), "r"(d1), "f"(f));
 }
 
-__device__ __forceinline__ float2 lds64(uint32_t addr)
+__device__ __forceinline__ float4 lds128f(uint32_t addr)
 {
-    float2 v;
-    asm volatile("ld.shared.v2.f32 {%0, %1}, [%2];" : "=f"(v.x), "=f"(v.y) : "r"(addr) : "memory");
+    float4 v;
+    asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(addr) : "memory");
     return v;
 }
 __device__ __forceinline__ void sts32(uint32_t addr, float v) { asm volatile("st.shared.f32 [%0], %1;" ::"r"(addr), "f"(v) : "memory"); }
@@ -150,6 +155,14 @@ __device__ __forceinline__ void sts_out(uint32_t addr, float v, float *) { sts32
 __device__ __forceinline__ void sts_out(uint32_t addr, float v, __nv_bfloat16 *)
 {
     asm volatile("st.shared.b16 [%0], %1;" ::"r"(addr), "h"(__bfloat16_as_ushort(__float2bfloat16_rn(v))) : "memory");
+}
+
+// Where column c of a group of CB stands among the scales that are read: every
+// fourth one's after one another.
+template <int CB>
+__host__ __device__ __forceinline__ int scale_at(int c)
+{
+    return (c & 3) * (CB / 4) + c / 4;
 }
 
 __device__ __forceinline__ Tile tile_at(const TcArgs &a, int i, int ntiles)
@@ -166,7 +179,9 @@ __global__ void __launch_bounds__(TC_THREADS, 1) f8_tc(const __grid_constant__ T
     constexpr int CL = F::CL, ST = F::ST, D = F::D, CB = F::CB;
     constexpr int XR = NT / CL;                              // rows of a CTA's share of a tile, at most
     constexpr uint32_t STAGE = W_BYTES + XR * F8_BLOCK;
-    constexpr int JB = NT / (2 * CB), G = CB / 8;            // column blocks of an epilogue warp, of eight columns each
+    constexpr int JB = NT / (2 * CB), G = CB / 4;            // column blocks of an epilogue warp, of four columns each
+    constexpr bool LAID = NT == 256;                         // the row scales are laid out
+    static_assert(!LAID || (SLOTS >= ST + D && CB == GROUP), "slots that are free with their stage; the order of the scales");
     static_assert(D * NT <= 512, "tensor memory");
     extern __shared__ uint8_t smem_raw[];
     const uint32_t raw = smem_addr(smem_raw);
@@ -230,7 +245,7 @@ __global__ void __launch_bounds__(TC_THREADS, 1) f8_tc(const __grid_constant__ T
         if (warp == W_WARP) {
             if (elect_one()) {
                 const uint32_t lead = CL > 1 ? mapa_shared(full, 0) : full;
-                uint32_t s = 0, p = 1;  // parity of the stage's release one lap ago; none in the first
+                uint32_t s = 0, p = 1, sl = 0;  // p: parity of the stage's release one lap ago; none in the first
                 bool round0 = true;
                 for (long long it = first; it < nitems && !failed; it += stride) {
                     const Tile t = tile_at(a, static_cast<int>(it / mgroups), ntiles);
@@ -243,6 +258,14 @@ __global__ void __launch_bounds__(TC_THREADS, 1) f8_tc(const __grid_constant__ T
                         if (rank == 0) mbar_arrive_expect_tx(full + 8 * s, W_BYTES * CL);
                         if (CL > 1) tma_load_2d_pair(w0 + s * W_BYTES, &a.wmap, c * F8_BLOCK, row, lead + 8 * s);
                         else tma_load_2d(w0 + s * W_BYTES, &a.wmap, c * F8_BLOCK, row, full + 8 * s);
+                        if (LAID) {
+                            // The slot is free: its last scales were read before the accumulator of
+                            // that block was handed back, which the block D later waited for, and
+                            // that block's stage has been released.
+                            mbar_arrive_expect_tx(sfull + 8 * sl, NT * 4);
+                            bulk_g2s(f0 + sl * (NT * 4), a.xs + c * a.pitch + (a.tiles ? t.laid : t.row0), NT * 4, sfull + 8 * sl);
+                            if (++sl == SLOTS) sl = 0;
+                        }
                         if (++s == ST) {
                             s = 0;
                             p ^= 1u;
@@ -329,8 +352,10 @@ __global__ void __launch_bounds__(TC_THREADS, 1) f8_tc(const __grid_constant__ T
                     const Tile t = tile_at(a, static_cast<int>(it / mgroups), ntiles);
                     const uint32_t idesc = idesc_e4m3(MT * CL, mma_cols<CL>(t.rows));
                     for (int c = c0; c < c1; ++c) {
-                        if (!(mbar_test<CL>(full + 8 * s, p) || wait_pair<CL>(full + 8 * s, p, a.status, 3u)) ||
-                            !(round0 || mbar_test<CL>(dempty + 8 * d, pd) || wait_pair<CL>(dempty + 8 * d, pd, a.status, 4u))) {
+                        // both barriers looked at together: this thread's own latency counts
+                        const bool r0 = mbar_test<CL>(full + 8 * s, p), r1 = round0 || mbar_test<CL>(dempty + 8 * d, pd);
+                        if (!(r0 && r1) && !(wait_pair<CL>(full + 8 * s, p, a.status, 3u) &&
+                                             (round0 || wait_pair<CL>(dempty + 8 * d, pd, a.status, 4u)))) {
                             failed = true;
                             break;
                         }
@@ -339,8 +364,8 @@ __global__ void __launch_bounds__(TC_THREADS, 1) f8_tc(const __grid_constant__ T
 #pragma unroll
                         for (int kk = 0; kk < F8_BLOCK / 32; ++kk)
                             mma_f8<CL>(tmem + d * NT, wd + kk * 2, xd + kk * 2, idesc, kk != 0);
-                        commit<CL>(empty + 8 * s);
                         commit<CL>(dfull + 8 * d);
+                        commit<CL>(empty + 8 * s);
                         if (++s == ST) {
                             s = 0;
                             p ^= 1u;
@@ -354,7 +379,7 @@ __global__ void __launch_bounds__(TC_THREADS, 1) f8_tc(const __grid_constant__ T
                 }
             }
             failed = __any_sync(FULL_MASK, failed);
-        } else if (warp == S_WARP) {
+        } else if (!LAID && warp == S_WARP) {
             // a lane brings the scales of every 32nd row of the tile, times the weights'
             const bool v4 = (a.kb & 3) == 0 && (reinterpret_cast<uintptr_t>(a.xs) & 15u) == 0;
             uint32_t s = 0, p = 1;
@@ -401,7 +426,8 @@ __global__ void __launch_bounds__(TC_THREADS, 1) f8_tc(const __grid_constant__ T
                             for (int i = 0; i < 4; ++i) {
                                 if (i0 + i >= NT / 32) break;
                                 const float f = pick == 0 ? v[i].x : (pick == 1 ? v[i].y : (pick == 2 ? v[i].z : v[i].w));
-                                sts32(f0 + sj * (NT * 4) + static_cast<uint32_t>((i0 + i) * 32 + lane) * 4u, f * w);
+                                const int at = (i0 + i) * 32 + lane;
+                                sts32(f0 + sj * (NT * 4) + static_cast<uint32_t>(at / CB * CB + scale_at<CB>(at % CB)) * 4u, f * w);
                             }
                         }
                         if (failed) break;
@@ -431,38 +457,44 @@ __global__ void __launch_bounds__(TC_THREADS, 1) f8_tc(const __grid_constant__ T
         uint32_t d = 0, pd = 0, s = 0, p = 0;
         for (long long it = first; it < nitems && !failed; it += stride) {
             const Tile t = tile_at(a, static_cast<int>(it / mgroups), ntiles);
-            float2 acc[JB][G][4];  // columns 8 g + 2 (lane % 4), + 1 of rows lane / 4 + 8 i
+            float2 acc[JB][G][2];  // column 4 g + lane % 4 of rows lane / 4 + 16 i and + 8
 #pragma unroll
             for (int j = 0; j < JB; ++j)
 #pragma unroll
-                for (int g = 0; g < G; ++g)
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) acc[j][g][i] = make_float2(0.f, 0.f);
+                for (int g = 0; g < G; ++g) acc[j][g][0] = acc[j][g][1] = make_float2(0.f, 0.f);
+            const float *ws = a.ws + (static_cast<size_t>(t.expert) * a.nb + min(static_cast<int>(it % mgroups) * CL + rank, a.nb - 1)) * a.kb;
+            float wl = 0.f;  // the weights' scales, a block a lane
             for (int c = c0; c < c1; ++c) {
-                const bool ok = mbar_wait_bounded(sfull + 8 * s, p, a.status, 6u) && mbar_wait_bounded(dfull + 8 * d, pd, a.status, 6u);
-                if (!__all_sync(FULL_MASK, ok)) {
+                if (LAID && ((c - c0) & 31) == 0) wl = c + lane < c1 ? ws[c + lane] : 0.f;
+                const bool r0 = mbar_test<1>(sfull + 8 * s, p), r1 = mbar_test<1>(dfull + 8 * d, pd);
+                if (!__all_sync(FULL_MASK, r0 && r1) &&
+                    !__all_sync(FULL_MASK, mbar_wait_bounded(sfull + 8 * s, p, a.status, 6u) && mbar_wait_bounded(dfull + 8 * d, pd, a.status, 6u))) {
                     failed = true;
                     break;
                 }
                 tc_fence_after();
-                const uint32_t fs = f0 + s * (NT * 4) + static_cast<uint32_t>(lane & 3) * 8u;
+                const float w = LAID ? __shfl_sync(FULL_MASK, wl, (c - c0) & 31) : 1.f;
+                const uint32_t fs = f0 + s * (NT * 4) + static_cast<uint32_t>((lane & 3) * G) * 4u;
 #pragma unroll
                 for (int j = 0; j < JB; ++j) {
-                    const int col = (2 * j + h) * CB;
-                    if (col >= t.rows) break;
-                    uint32_t lo[CB / 2], hi[CB / 2];
-                    tmem_ld_16x256(mine + d * NT + col, lo);
-                    tmem_ld_16x256(mine + (16u << 16) + d * NT + col, hi);
-                    float2 f[G];
+                    const int at = (2 * j + h) * CB;
+                    if (at >= t.rows) break;
+                    uint32_t lo[2 * G], hi[2 * G];
+                    tmem_ld_16x128(mine + d * NT + at, lo);
+                    tmem_ld_16x128(mine + (16u << 16) + d * NT + at, hi);
+                    float4 f[G / 4];
 #pragma unroll
-                    for (int g = 0; g < G; ++g) f[g] = lds64(fs + static_cast<uint32_t>(col + 8 * g) * 4u);
+                    for (int g = 0; g < G / 4; ++g) {
+                        f[g] = lds128f(fs + static_cast<uint32_t>(at + 4 * g) * 4u);
+                        if (LAID) f[g] = make_float4(f[g].x * w, f[g].y * w, f[g].z * w, f[g].w * w);
+                    }
                     tmem_loaded(lo, hi);
 #pragma unroll
                     for (int g = 0; g < G; ++g) {
-                        fma2(acc[j][g][0], lo[4 * g], lo[4 * g + 1], f[g]);
-                        fma2(acc[j][g][1], lo[4 * g + 2], lo[4 * g + 3], f[g]);
-                        fma2(acc[j][g][2], hi[4 * g], hi[4 * g + 1], f[g]);
-                        fma2(acc[j][g][3], hi[4 * g + 2], hi[4 * g + 3], f[g]);
+                        const float4 v = f[g / 4];
+                        const float s1 = (g & 3) == 0 ? v.x : ((g & 3) == 1 ? v.y : ((g & 3) == 2 ? v.z : v.w));
+                        fma2(acc[j][g][0], lo[2 * g], lo[2 * g + 1], s1);
+                        fma2(acc[j][g][1], hi[2 * g], hi[2 * g + 1], s1);
                     }
                 }
                 tc_fence_before();
@@ -470,7 +502,7 @@ __global__ void __launch_bounds__(TC_THREADS, 1) f8_tc(const __grid_constant__ T
                 if (lane == 0) {
                     if (CL > 1) mbar_arrive_cluster(lead + 8 * d);
                     else mbar_arrive(dempty + 8 * d);
-                    mbar_arrive(sempty + 8 * s);
+                    if (!LAID) mbar_arrive(sempty + 8 * s);
                 }
                 if (++d == D) {
                     d = 0;
@@ -489,15 +521,17 @@ __global__ void __launch_bounds__(TC_THREADS, 1) f8_tc(const __grid_constant__ T
 #pragma unroll
                     for (int g = 0; g < G; ++g)
 #pragma unroll
-                        for (int i = 0; i < 4; ++i) {
-                            const int r = (2 * j + h) * CB + 8 * g + 2 * (lane & 3);
-                            const uint32_t to = x0 + static_cast<uint32_t>(r * MT + q * 32 + (lane >> 2) + 8 * i) * 4u;
-                            if (r < t.rows) sts32(to, acc[j][g][i].x);
-                            if (r + 1 < t.rows) sts32(to + MT * 4u, acc[j][g][i].y);
+                        for (int i = 0; i < 2; ++i) {
+                            const int r = (2 * j + h) * CB + 4 * g + (lane & 3);
+                            const uint32_t to = x0 + static_cast<uint32_t>(r * MT + q * 32 + (lane >> 2) + 16 * i) * 4u;
+                            if (r < t.rows) {
+                                sts32(to, acc[j][g][i].x);
+                                sts32(to + 32u, acc[j][g][i].y);
+                            }
                         }
                 continue;
             }
-            // 16 rows at a time through shared memory, out as 16-byte vectors of a row
+            // 8 rows at a time through shared memory, out as 16-byte vectors of a row
             constexpr uint32_t PITCH = 32 * sizeof(T) + 16;
             constexpr int VE = 16 / static_cast<int>(sizeof(T)), LR = 32 / VE;  // lanes of a row
             const uint32_t stage = out0 + warp * OUT_BYTES;
@@ -507,21 +541,21 @@ __global__ void __launch_bounds__(TC_THREADS, 1) f8_tc(const __grid_constant__ T
                 if ((2 * j + h) * CB >= t.rows) break;
 #pragma unroll
                 for (int g0 = 0; g0 < G; g0 += 2) {
-                    const int r0 = (2 * j + h) * CB + 8 * g0;
+                    const int r0 = (2 * j + h) * CB + 4 * g0;
                     if (r0 >= t.rows) break;
                     __syncwarp();
 #pragma unroll
                     for (int g = 0; g < 2; ++g)
 #pragma unroll
-                        for (int i = 0; i < 4; ++i) {
-                            const uint32_t to = stage + static_cast<uint32_t>(8 * g + 2 * (lane & 3)) * PITCH +
-                                                static_cast<uint32_t>((lane >> 2) + 8 * i) * static_cast<uint32_t>(sizeof(T));
+                        for (int i = 0; i < 2; ++i) {
+                            const uint32_t to = stage + static_cast<uint32_t>(4 * g + (lane & 3)) * PITCH +
+                                                static_cast<uint32_t>((lane >> 2) + 16 * i) * static_cast<uint32_t>(sizeof(T));
                             sts_out(to, acc[j][g0 + g][i].x, y);
-                            sts_out(to + PITCH, acc[j][g0 + g][i].y, y);
+                            sts_out(to + 8 * static_cast<uint32_t>(sizeof(T)), acc[j][g0 + g][i].y, y);
                         }
                     __syncwarp();
 #pragma unroll
-                    for (int i = 0; i < 16 * LR / 32; ++i) {
+                    for (int i = 0; i < 8 * LR / 32; ++i) {
                         const int r = (i * 32 + lane) / LR, n = (lane % LR) * VE;
                         const uint4 v = lds128v(stage + static_cast<uint32_t>(r) * PITCH + static_cast<uint32_t>(lane % LR) * 16u);
                         if (r0 + r >= t.rows || n0 + n >= a.N) continue;
@@ -591,28 +625,72 @@ __global__ void __launch_bounds__(TC_THREADS, 1) f8_tc(const __grid_constant__ T
 constexpr int PREP_THREADS = 256;
 
 struct PrepArgs {
-    const int *offsets;
+    const int *offsets;  // null: one matrix
+    const int *order;
+    const float *xs;
+    float *laid;         // null: no scales to lay out
     void *y;
     int *ntiles;
     Tile *tiles;
     unsigned *status;
-    int R, n, N, nt, unit, max_tiles, elem;  // elem: bytes of an element of y
+    long long pitch;
+    int R, n, N, nt, unit, max_tiles, elem, kb, k, nsrc;  // elem: bytes of an element of y
 };
 
-// Block 0: the tile list.  The others: zeros in the rows of y past the last
-// expert's.
+// Block 0 (with offsets): the tile list.  The others: zeros in the rows of y past the
+// last expert's, and the row scales of the pairs, [kb x pitch], every expert's rows from
+// laid_row on, those of each 32 in the order in which the epilogue reads them.
 __global__ void __launch_bounds__(PREP_THREADS) f8_prep(const PrepArgs a)
 {
     pdl_launch_dependents();
     pdl_wait();
-    if (blockIdx.x == 0) {
+    if (a.offsets && blockIdx.x == 0) {
         list_tiles<PREP_THREADS>(a.offsets, a.n, a.R, a.nt, a.unit, a.max_tiles, a.ntiles, a.tiles, a.status);
         return;
     }
-    const int last = max(0, min(a.offsets[a.n], a.R));
+    const int b0 = a.offsets ? 1 : 0, blocks = gridDim.x - b0;
+    const int last = a.offsets ? max(0, min(a.offsets[a.n], a.R)) : a.R;
+    if (a.laid) {
+        // a thread takes one row and four blocks of columns
+        const int quads = (a.kb + 3) / 4;
+        const bool v4 = (a.kb & 3) == 0 && (reinterpret_cast<uintptr_t>(a.xs) & 15u) == 0;
+        const int rows = (last + 31) & ~31;  // whole warps: neighbouring lanes, neighbouring rows
+        const long long total = static_cast<long long>(rows) * quads;
+        for (long long i = static_cast<long long>(blockIdx.x - b0) * PREP_THREADS + threadIdx.x; i < total;
+             i += static_cast<long long>(blocks) * PREP_THREADS) {
+            const int r = static_cast<int>(i % rows), c = static_cast<int>(i / rows) * 4;
+            if (r >= last) continue;
+            int at = r;
+            if (a.offsets) {  // the last expert whose rows begin at or before this one
+                int lo = 0, hi = a.n;
+                while (hi - lo > 1) {
+                    const int mid = (lo + hi) >> 1;
+                    if (a.offsets[mid] <= r) lo = mid;
+                    else hi = mid;
+                }
+                const int first = a.offsets[lo];
+                if (first < 0 || first > r) continue;  // no list (reported): its rows are unspecified
+                at = laid_row(first, lo) + r - first;
+            }
+            at = (at & ~(GROUP - 1)) + scale_at<GROUP>(at & (GROUP - 1));
+            const int src = source_row(a.order, a.k, a.nsrc, r, a.status);
+            const float *x = a.xs + static_cast<size_t>(max(src, 0)) * a.kb;
+            float v[4];
+            if (v4) {
+                const float4 q = *reinterpret_cast<const float4 *>(x + c);
+                v[0] = q.x; v[1] = q.y; v[2] = q.z; v[3] = q.w;
+            } else {
+#pragma unroll
+                for (int j = 0; j < 4; ++j) v[j] = c + j < a.kb ? x[c + j] : 0.f;
+            }
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                if (c + j < a.kb) a.laid[(c + j) * a.pitch + at] = src < 0 ? 0.f : v[j];
+        }
+    }
     const size_t end = static_cast<size_t>(a.R) * a.N;
-    for (size_t i = static_cast<size_t>(last) * a.N + (blockIdx.x - 1) * PREP_THREADS + threadIdx.x; i < end;
-         i += static_cast<size_t>(gridDim.x - 1) * PREP_THREADS) {
+    for (size_t i = static_cast<size_t>(last) * a.N + static_cast<size_t>(blockIdx.x - b0) * PREP_THREADS + threadIdx.x; i < end;
+         i += static_cast<size_t>(blocks) * PREP_THREADS) {
         if (a.elem == 4) static_cast<float *>(a.y)[i] = 0.f;
         else static_cast<uint16_t *>(a.y)[i] = 0;
     }
@@ -699,7 +777,19 @@ cudaError_t launch_tc(const TcArgs &args, long long most_items, int sms, cudaStr
 
 }  // namespace
 
-size_t f8_tc_workspace(int R, int n) { return 256 + up256(static_cast<size_t>(most_tiles(R, n, 64)) * sizeof(Tile)); }
+// Laid-out rows: each expert's begin at a multiple of GROUP, and a copy takes a
+// whole tile from any of them.
+static long long laid_pitch(int R, int n) { return (R + GROUP - 1) / GROUP * GROUP + static_cast<long long>(n) * GROUP + 256; }
+
+// 64 columns of rows' scales at least; all of them only where pairs may take the
+// product, which then has rows for the experts' padding.
+static size_t tiles_bytes(int R, int n) { return 256 + up256(static_cast<size_t>(most_tiles(R, n, 64)) * sizeof(Tile)); }
+
+size_t f8_tc_workspace(int R, int n, int K)
+{
+    const size_t laid = R > 48LL * n ? static_cast<size_t>(laid_pitch(R, n)) * ((K + F8_BLOCK - 1) / F8_BLOCK) * sizeof(float) : 0;
+    return tiles_bytes(R, n) + up256(laid);
+}
 
 cudaError_t launch_f8_tc(const F8Call &c, void *workspace, cudaStream_t stream)
 {
@@ -711,22 +801,29 @@ cudaError_t launch_f8_tc(const F8Call &c, void *workspace, cudaStream_t stream)
     const int max_tiles = most_tiles(c.R, c.n, nt);
     int *ntiles = static_cast<int *>(workspace);
     Tile *tiles = reinterpret_cast<Tile *>(static_cast<char *>(workspace) + 256);
+    float *laid = nt == 256 ? reinterpret_cast<float *>(static_cast<char *>(workspace) + tiles_bytes(c.R, c.n)) : nullptr;
 
     // one matrix: equal tiles of consecutive rows, a CTA's share one copy
     const int nd = nt == 64 ? (c.R + 63) / 64 : pair_tiles(c.R, (mtiles + 1) / 2, dev->sm_count / 2);
     const int step = ((c.R + nd - 1) / nd + unit - 1) / unit * unit;
     TcArgs a = {};
+    a.kb = (c.K + F8_BLOCK - 1) / F8_BLOCK;
+    a.pitch = laid_pitch(c.R, c.n);
     a.box = c.offsets ? nt / cl / 2 : step / cl;
     if (!encode(&a.wmap, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, c.wq, c.K, static_cast<long long>(c.n) * c.N, F8_BLOCK, MT) ||
         !encode(&a.xmap, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, c.xq, c.K, c.nsrc, F8_BLOCK, c.order ? 1 : a.box))
         return cudaErrorInvalidValue;
-    if (c.offsets) {
-        const PrepArgs p = {c.offsets, c.y, ntiles, tiles, status, c.R, c.n, c.N, nt, unit, max_tiles, elem};
-        const cudaError_t e = launch_pdl(f8_prep, dim3(33), dim3(PREP_THREADS), 0, stream, p);
+    if (c.offsets || laid) {
+        const PrepArgs p = {c.offsets, c.order, c.xs, laid, c.y, ntiles, tiles, status, a.pitch, c.R, c.n, c.N, nt, unit, max_tiles,
+                            elem, a.kb, c.k, c.nsrc};
+        long long blocks = laid ? (static_cast<long long>(c.R) * ((a.kb + 3) / 4) + PREP_THREADS - 1) / PREP_THREADS : 32;
+        if (blocks > 4LL * dev->sm_count) blocks = 4LL * dev->sm_count;
+        const cudaError_t e = launch_pdl(f8_prep, dim3(static_cast<unsigned>(blocks + (c.offsets ? 1 : 0))), dim3(PREP_THREADS), 0,
+                                         stream, p);
         if (e != cudaSuccess) return e;
     }
     a.ws = c.ws;
-    a.xs = c.xs;
+    a.xs = laid ? laid : c.xs;
     a.order = c.order;
     a.y = c.y;
     a.ntiles = ntiles;
@@ -735,7 +832,6 @@ cudaError_t launch_f8_tc(const F8Call &c, void *workspace, cudaStream_t stream)
     a.R = c.R;
     a.N = c.N;
     a.K = c.K;
-    a.kb = (c.K + F8_BLOCK - 1) / F8_BLOCK;
     a.nb = (c.N + F8_BLOCK - 1) / F8_BLOCK;
     a.k = c.k;
     a.nsrc = c.nsrc;
