@@ -1065,7 +1065,7 @@ int smoe_quantize_blocks_f8(const void *w, int dtype, int n_mats, int rows, int 
 size_t smoe_experts_matmul_f8_workspace_bytes(int n_src, int n_rows, int n_experts, int n_out, int n_in)
 {
     if (check_q8(n_src, n_rows, n_experts, n_out, n_in) != SMOE_OK) return static_cast<size_t>(-1);
-    return n_rows == 0 || n_out == 0 ? 0 : smoe::f8_workspace(n_rows, n_experts, n_in);
+    return n_rows == 0 || n_out == 0 ? 0 : smoe::f8_workspace(n_rows, n_experts);
 }
 
 size_t smoe_matmul_f8_workspace_bytes(int n_rows, int n_out, int n_in)
@@ -1087,7 +1087,7 @@ static int f8_impl(const uint8_t *xq, const float *x_scales, int n_src, const in
     if (!aligned_to(x_scales, 4) || !aligned_to(w_scales, 4) || !aligned16(y) || (order && !aligned_to(order, 4)) ||
         (sorted && !aligned_to(offsets, 4)) || (n_in > 0 && (!aligned16(xq) || !aligned16(wq))))
         return SMOE_ERR_ALIGN;
-    const size_t need = smoe::f8_workspace(n_rows, n_experts, n_in);
+    const size_t need = smoe::f8_workspace(n_rows, n_experts);
     if (!workspace || workspace_bytes < need) return SMOE_ERR_WORKSPACE;
     if (!aligned16(workspace)) return SMOE_ERR_ALIGN;
     const size_t kb = blocks_of(n_in);

@@ -174,7 +174,7 @@ __global__ void __launch_bounds__(DOT_WARPS * 32, 2) f8_dot(const DotArgs a)
 // three for every eight experts.
 static bool on_tensor_cores(int R, int n, int K) { return K > 0 && R > 2 && R > 3LL * n / 8; }
 
-size_t f8_workspace(int R, int n, int K) { return f8_tc_workspace(R, n, K); }
+size_t f8_workspace(int R, int n) { return f8_tc_workspace(R, n); }
 
 cudaError_t launch_f8(const uint8_t *xq, const float *xs, int nsrc, const int *order, int k, const int *offsets, int R, int n,
                       const uint8_t *wq, const float *ws, int N, int K, void *y, int dtype, void *workspace,

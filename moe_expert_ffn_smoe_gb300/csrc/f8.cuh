@@ -24,7 +24,10 @@ struct F8Call {
 };
 
 // The product on the tensor cores (f8_tc.cu).
-size_t f8_tc_workspace(int R, int n, int K);
+size_t f8_tc_workspace(int R, int n);
 cudaError_t launch_f8_tc(const F8Call &c, void *workspace, cudaStream_t stream);
+
+// The same by pairs of CTAs in row tiles of 256 (f8_pair.cu), from the tile list.
+cudaError_t launch_f8_pair(const F8Call &c, const int *ntiles, const Tile *tiles, int max_tiles, cudaStream_t stream);
 
 }  // namespace smoe

@@ -46,7 +46,7 @@ cudaError_t launch_quantize_rows_f8(const void *x, int dtype, bool act, int rows
                                     cudaStream_t stream);
 cudaError_t launch_quantize_blocks_f8(const void *w, int dtype, int n, int rows, int cols, uint8_t *q, float *scales,
                                       uint8_t *qt, float *scales_t, cudaStream_t stream);
-size_t f8_workspace(int R, int n, int K);
+size_t f8_workspace(int R, int n);
 cudaError_t launch_f8(const uint8_t *xq, const float *xs, int nsrc, const int *order, int k, const int *offsets, int R, int n,
                       const uint8_t *wq, const float *ws, int N, int K, void *y, int dtype, void *workspace,
                       cudaStream_t stream);

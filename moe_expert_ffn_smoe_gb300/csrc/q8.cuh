@@ -10,16 +10,10 @@
 
 namespace smoe {
 
-// At most `rows` consecutive sorted rows of one expert (-1: rows of none); laid: its
-// first row in a layout where every expert begins at a multiple of GROUP.
+// At most `rows` consecutive sorted rows of one expert (-1: rows of none).
 struct Tile {
-    int expert, row0, rows, laid;
+    int expert, row0, rows, pad;
 };
-
-constexpr int GROUP = 32;
-
-// That row of expert e's first, lo: past the rows of the experts before.
-__device__ __forceinline__ int laid_row(int lo, int e) { return (lo + GROUP - 1) / GROUP * GROUP + e * GROUP; }
 
 // Source row of sorted row r (order null: itself), or -1, reported, where
 // order points outside the nsrc rows.
@@ -72,7 +66,7 @@ __device__ __forceinline__ void list_tiles(const int *offsets, int n, int R, int
         if (tid == THREADS - 1) run_s = before + inc;
         const long long t0 = before + inc - cnt;
         for (int i = 0; i < cnt && t0 + i < max_tiles; ++i)
-            tiles[t0 + i] = Tile{e, lo + i * step, min(step, hi - lo - i * step), laid_row(lo, e) + i * step};
+            tiles[t0 + i] = Tile{e, lo + i * step, min(step, hi - lo - i * step), 0};
         __syncthreads();
         run = run_s;
     }
