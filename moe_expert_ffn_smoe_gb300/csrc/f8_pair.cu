@@ -266,10 +266,12 @@ __global__ void __launch_bounds__(PAIR_THREADS, 1) f8_pair(const __grid_constant
                 bool round0 = true;
                 for (long long it = first; it < nitems && !failed; it += stride) {
                     for (int c = 0; c < a.kb; ++c) {
-                        // both barriers looked at together: this thread's own latency counts
-                        const bool r0 = mbar_test<2>(full + 8 * s, p), r1 = round0 || mbar_test<2>(dempty + 8 * d, pd);
-                        if (!(r0 && r1) && !(wait_pair<2>(full + 8 * s, p, a.status, 3u) &&
-                                             (round0 || wait_pair<2>(dempty + 8 * d, pd, a.status, 4u)))) {
+                        // Both barriers looked at together: this thread's own latency counts.
+                        // What they hand over is read by the MMAs alone (operands that copies
+                        // brought) or is tensor memory, which the tcgen05 fences order.
+                        const bool r0 = mbar_test<1>(full + 8 * s, p), r1 = round0 || mbar_test<1>(dempty + 8 * d, pd);
+                        if (!(r0 && r1) && !(mbar_wait_bounded(full + 8 * s, p, a.status, 3u) &&
+                                             (round0 || mbar_wait_bounded(dempty + 8 * d, pd, a.status, 4u)))) {
                             failed = true;
                             break;
                         }
