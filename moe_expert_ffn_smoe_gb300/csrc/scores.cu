@@ -43,6 +43,11 @@ __device__ __forceinline__ float warp_max(float v)
     for (int off = 16; off > 0; off >>= 1) v = fmaxf(v, __shfl_xor_sync(FULL_MASK, v, off));
     return v;
 }
+// The largest of values that are not negative: their bits are ordered as they are.
+__device__ __forceinline__ float warp_max_positive(float v)
+{
+    return __uint_as_float(__reduce_max_sync(FULL_MASK, __float_as_uint(v)));
+}
 __device__ __forceinline__ float warp_sum(float v)
 {
 #pragma unroll
@@ -65,18 +70,18 @@ struct Row {
     int n, V;
 };
 
-// c of logit l and bias b, and a bound of its error.  Sigmoid: e^-l to 2 units
-// in the last place, the sum and the reciprocal instruction to one each: below
-// 2^-21 of s.  Softmax: l - m is rounded (2^-24 of its size, in the exponent),
-// the row's sum has V + 5 additions after terms as exact; the rounding of s + b
-// is 2^-24 of c.  Below the normal numbers the instructions flush.
+// c of logit l and bias b, and a bound of its error.  Sigmoid: __expf is off by 2 +
+// 1.173 |l| units of 2^-23 at most, the sum and the reciprocal instruction by one
+// each.  Softmax: l - m is rounded (2^-24 of its size, in the exponent), the row's
+// sum has V + 5 additions after terms as exact; the rounding of s + b is 2^-24 of c.
+// Below the normal numbers the instructions flush.
 template <By BY>
 __device__ __forceinline__ float choice(const Row &r, float l, float b, float &err)
 {
     float s, rel;
     if (BY == By::Sigmoid) {
-        s = rcp_approx(1.0f + expf(-l));
-        rel = 0x1p-21f;
+        s = rcp_approx(1.0f + __expf(-l));
+        rel = fmaf(fabsf(l), 1.25f * 0x1p-23f, 0x1p-21f);
     } else {
         s = expf(l - r.m) * r.inv;
         rel = (fabsf(l - r.m) + static_cast<float>(r.V + 32)) * 0x1p-24f;
@@ -136,20 +141,23 @@ __device__ __forceinline__ int lanes_of_group(int groups)
 // The groups taken, as a mask of their first lanes, from every lane's value of
 // its group (equal in all lanes of a group; -inf: no expert on); err: bound of
 // its error; doubt: whether the border lies within the bounds.
-template <typename F>
-__device__ __forceinline__ uint32_t take_groups(F value, F err, int P, const RouteArgs &a, bool &doubt)
+__device__ __forceinline__ uint32_t take_groups(float value, float err, int P, const RouteArgs &a, bool &doubt)
 {
     const int lane = threadIdx.x & 31, g = lane / P;
+    // each of a group's lanes looks at every P-th other group
     int before = 0;
-    for (int h = 0; h < a.groups; ++h) {
-        const F o = __shfl_sync(FULL_MASK, value, h * P);
-        before += o > value || (o == value && h < g);
+    for (int h0 = 0; h0 < a.groups; h0 += P) {
+        const int h = h0 + (lane & (P - 1));
+        const float o = __shfl_sync(FULL_MASK, value, h * P);  // (the lanes wrap round past the last group)
+        before += h < a.groups && (o > value || (o == value && h < g));
     }
+    for (int off = P >> 1; off > 0; off >>= 1) before += __shfl_xor_sync(FULL_MASK, before, off);
     const bool on = g < a.groups && value > -INFINITY, taken = on && before < a.top_groups;
-    const float low = warp_max(taken ? static_cast<float>(err - value) : -INFINITY);          // = -(least sure value)
-    const float high = warp_max(on && !taken ? static_cast<float>(value + err) : -INFINITY);
-    doubt = high >= -low && low > -INFINITY && high > -INFINITY;
-    return __ballot_sync(FULL_MASK, taken && lane % P == 0);
+    // the least sure value of those taken against the largest that those left out may have
+    const uint32_t low = __reduce_min_sync(FULL_MASK, taken ? value_key(value - err) : 0xFFFFFFFFu);
+    const uint32_t high = __reduce_max_sync(FULL_MASK, on && !taken ? value_key(value + err) : 0u);
+    doubt = high >= low;
+    return __ballot_sync(FULL_MASK, taken && (lane & (P - 1)) == 0);
 }
 
 // The same from scores in 64 bits.
@@ -256,34 +264,34 @@ __device__ __forceinline__ void choose_by_rounds(uint32_t (&key)[V], const Row &
     }
 }
 
+// Score of a chosen logit v (of softmax less the row's largest), times e^-m where
+// the weights are renormalised: with m the largest of the chosen, or 0 if that is
+// less, small scores keep the digits that they would lose on their own.
+__device__ __forceinline__ float chosen_score(const RouteArgs &a, const Row &r, float v, float m)
+{
+    if (a.softmax) return expf(v - m) * r.inv;
+    return v > 0.f || !a.norm ? rcp_approx(1.f + expf(-v)) : expf(v - m) * rcp_approx(1.f + expf(v));
+}
+
 // Weights of the experts that this warp's lanes hold (ea and eb; -1: none), at
-// the ranks ra and rb.  Where every chosen score is small, renormalised weights come
-// from e^(l - largest l), which keeps the digits that small scores lose: a sigmoid
-// that far down is e^l to 2^-28.
+// the ranks ra and rb.
 __device__ __forceinline__ void write_weights(const RouteArgs &a, const Row &r, int ea, int eb, int ra, int rb, int *idx, float *w)
 {
     const float la = ea >= 0 ? r.l[ea] - (a.softmax ? r.m : 0.f) : -INFINITY;
     const float lb = eb >= 0 ? r.l[eb] - (a.softmax ? r.m : 0.f) : -INFINITY;
-    float sa, sb = 0.f;
-    const float top = a.norm ? warp_max(fmaxf(la, lb)) : 0.f;
-    if (top < -20.f) {
-        sa = ea >= 0 ? expf(la - top) : 0.f;
-        sb = eb >= 0 ? expf(lb - top) : 0.f;
-    } else if (a.softmax) {
-        sa = ea >= 0 ? expf(la) * r.inv : 0.f;
-        sb = eb >= 0 ? expf(lb) * r.inv : 0.f;
-    } else {
-        sa = ea >= 0 ? 1.f / (1.f + expf(-la)) : 0.f;
-        if (eb >= 0) sb = 1.f / (1.f + expf(-lb));
-    }
-    const float sum = a.norm ? warp_sum(sa + sb) : 1.f;
+    const float m = a.norm ? fminf(value_of_key(__reduce_max_sync(FULL_MASK, value_key(fmaxf(la, lb)))), 0.f) : 0.f;
+    const float sa = ea >= 0 ? chosen_score(a, r, la, m) : 0.f;
+    float sb = 0.f;
+    if (a.k > 32 && eb >= 0) sb = chosen_score(a, r, lb, m);
+    // (the sum is never small: of a sigmoid at least a half, of a softmax 2^-11)
+    const float times = a.norm ? a.scale * rcp_approx(warp_sum(sa + sb)) : a.scale;
     if (ra >= 0 && ra < a.k) {
         idx[ra] = ea;
-        w[ra] = ea >= 0 ? a.scale * (sa / sum) : 0.f;
+        w[ra] = ea >= 0 ? sa * times : 0.f;
     }
     if (rb >= 0 && rb < a.k) {
         idx[rb] = eb;
-        w[rb] = eb >= 0 ? a.scale * (sb / sum) : 0.f;
+        w[rb] = eb >= 0 ? sb * times : 0.f;
     }
 }
 
@@ -293,6 +301,7 @@ __global__ void __launch_bounds__(ROUTE_WARPS * 32) route_rows_warp(const RouteA
 {
     __shared__ float rows[ROUTE_WARPS][32 * V];
     __shared__ __align__(16) Candidates cands[ROUTE_WARPS];
+    __shared__ float sorted[ROUTE_WARPS][32];
     const int wi = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int t = blockIdx.x * ROUTE_WARPS + wi;
     pdl_launch_dependents();
@@ -309,20 +318,12 @@ __global__ void __launch_bounds__(ROUTE_WARPS * 32) route_rows_warp(const RouteA
         const int e = i * 32 + lane;
         l[i] = e < a.n ? r.l[e] : -INFINITY;
         b[i] = a.bias && e < a.n ? a.bias[e] : 0.f;
-        bad |= l[i] != l[i] || (a.softmax && l[i] == INFINITY) ||
-               (l[i] != -INFINITY && (b[i] != b[i] || b[i] == INFINITY));
+        bad |= l[i] != l[i];
         top = fmaxf(top, l[i]);
     }
-    if (__any_sync(FULL_MASK, bad)) {
-        // no order and no weights: NaN for k experts, so that the token's output is NaN
-        for (int q = lane; q < a.k; q += 32) {
-            idx[q] = q;
-            w[q] = __int_as_float(0x7fffffff);
-        }
-        return;
-    }
+    if (a.softmax) bad |= top == INFINITY;
     if (a.softmax) {
-        r.m = warp_max(top);
+        r.m = value_of_key(__reduce_max_sync(FULL_MASK, value_key(top)));
         if (r.m > -INFINITY && (BY == By::Softmax || !a.norm)) {
             float sum = 0.f;
 #pragma unroll
@@ -339,16 +340,27 @@ __global__ void __launch_bounds__(ROUTE_WARPS * 32) route_rows_warp(const RouteA
     for (int i = 0; i < V; ++i) {
         const int e = i * 32 + lane;
         key[i] = e < a.n ? kKeyNegInf : 0u;
-        if (l[i] == -INFINITY || b[i] == -INFINITY) continue;
         if (BY == By::Logit) {
-            key[i] = value_key(l[i]);
+            if (l[i] != -INFINITY && b[i] != -INFINITY) key[i] = value_key(l[i]);
         } else {
             float d;
-            key[i] = value_key(choice<BY>(r, l[i], b[i], d));
-            err = fmaxf(err, d);
+            const float c = choice<BY>(r, l[i], b[i], d);
+            if (l[i] != -INFINITY && b[i] != -INFINITY) {
+                key[i] = value_key(c);
+                err = fmaxf(err, d);
+                bad |= !(c < INFINITY);  // a bias that is no number
+            }
         }
     }
-    if (BY != By::Logit) err = warp_max(err);
+    if (__any_sync(FULL_MASK, bad)) {
+        // no order and no weights: NaN for k experts, so that the token's output is NaN
+        for (int q = lane; q < a.k; q += 32) {
+            idx[q] = q;
+            w[q] = __int_as_float(0x7fffffff);
+        }
+        return;
+    }
+    if (BY != By::Logit) err = warp_max_positive(err);
 
     if (a.groups > 1) {
         float *c = rows[wi];
@@ -413,11 +425,14 @@ __global__ void __launch_bounds__(ROUTE_WARPS * 32) route_rows_warp(const RouteA
                 rank += v.w >= mine + (o + 3 >= lane ? 1u : 0u);
             }
             if (BY != By::Logit) {
-                const float ce = value_of_key(mine);
-                bool doubt = false;
-                for (int o = 0; o < count; ++o)
-                    doubt |= o != lane && fabsf(value_of_key(c.key[o]) - ce) <= 2.f * err;
-                if (__any_sync(FULL_MASK, doubt && lane < count && rank <= a.k)) {
+                // one bound for all: two that it does not separate make neighbours that it does not
+                float *by_rank = sorted[wi];
+                by_rank[lane] = -INFINITY;
+                __syncwarp();
+                if (lane < count) by_rank[rank] = value_of_key(mine);
+                __syncwarp();
+                const bool doubt = lane < a.k && lane + 1 < count && by_rank[lane] - by_rank[lane + 1] <= 2.f * err;
+                if (__any_sync(FULL_MASK, doubt)) {
                     const double inv64 = inverse_sum64<BY>(r);
                     const double c64 = e >= 0 ? choice64<BY>(r, e, inv64) : -INFINITY;
                     rank = 0;
@@ -457,9 +472,10 @@ struct RouteGradArgs {
 //   softmax            dl_j = (g_r of the slot of j) - s_j sum_r g_r, for every j
 // A warp per row, which makes the row in shared memory and writes it once.  Bound
 // by writing the gradients (and, for the last form, reading the logits).
-template <int V>
+template <int V, bool WIDE>  // WIDE: k > 32, lane l holds the slots l and l + 32
 __global__ void __launch_bounds__(ROUTE_WARPS * 32) route_rows_grad(const RouteGradArgs a)
 {
+    constexpr int H = WIDE ? 2 : 1;
     __shared__ float rows[ROUTE_WARPS][32 * V];
     const int wi = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int t = blockIdx.x * ROUTE_WARPS + wi;
@@ -473,66 +489,67 @@ __global__ void __launch_bounds__(ROUTE_WARPS * 32) route_rows_grad(const RouteG
 #pragma unroll
         for (int i = 0; i < V; ++i) p[i] = i * 32 + lane < a.n ? l[i * 32 + lane] : -INFINITY;
     }
-    int e[2];
-    float w[2], g[2];
+    int e[H];
+    float w[H], g[H], dot = 0.f, sum = 0.f;
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
+    for (int h = 0; h < H; ++h) {
         const bool in = lane + 32 * h < a.k;
         const size_t at = static_cast<size_t>(t) * a.k + lane + 32 * h;
         e[h] = in ? a.idx[at] : -1;
         w[h] = in ? a.w[at] : 0.f;
         g[h] = in ? a.dw[at] : 0.f;
         if (e[h] < 0 || e[h] >= a.n) e[h] = -1;  // no expert: counts for nothing
-    }
-    float dot = 0.f;
-#pragma unroll
-    for (int h = 0; h < 2; ++h)
         if (e[h] >= 0) dot = fmaf(w[h], g[h], dot);
-    dot = warp_sum(dot);
-    const float mean = a.norm ? dot / a.scale : 0.f;
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-        g[h] = w[h] * (g[h] - mean);
-        if (!a.softmax && e[h] >= 0) g[h] /= 1.f + expf(l[e[h]]);  // 1 - s = 1 / (1 + e^l)
     }
-    float *row = rows[wi];
     if (dense) {
         float top = p[0];
 #pragma unroll
         for (int i = 1; i < V; ++i) top = fmaxf(top, p[i]);
-        top = warp_max(top);
+        top = value_of_key(__reduce_max_sync(FULL_MASK, value_key(top)));
         const float m = top > -INFINITY ? top : 0.f;  // a row of nothing else: scores of 0
-        float sum = 0.f;
 #pragma unroll
         for (int i = 0; i < V; ++i) {
             p[i] = expf(p[i] - m);
             sum += p[i];
         }
         sum = warp_sum(sum);
-        const float inv = sum > 0.f || sum != sum ? dot / sum : 0.f;
+    }
+    dot = warp_sum(dot);
+    // slots of one expert (a selection has none twice, a caller's list may)?
+    float *row = rows[wi];
+    bool twice = false;
+    if (!WIDE) {
+        if (e[0] >= 0) reinterpret_cast<int *>(row)[e[0]] = lane;
+        __syncwarp();
+        twice = e[0] >= 0 && reinterpret_cast<const int *>(row)[e[0]] != lane;
+        twice = __any_sync(FULL_MASK, twice);
+    }
+    const float mean = a.norm ? dot / a.scale : 0.f;
 #pragma unroll
-        for (int i = 0; i < V; ++i)
-            if (i * 32 + lane < a.n) row[i * 32 + lane] = 0.f - p[i] * inv;
+    for (int h = 0; h < H; ++h) {
+        g[h] = w[h] * (g[h] - mean);
+        if (!a.softmax && e[h] >= 0) g[h] *= rcp_approx(1.f + expf(l[e[h]]));  // 1 - s = 1 / (1 + e^l)
+    }
+    if (dense) {
+        const float inv = sum > 0.f || sum != sum ? -dot / sum : 0.f;
+#pragma unroll
+        for (int i = 0; i < V; ++i) row[i * 32 + lane] = p[i] * inv;
     } else {
 #pragma unroll
         for (int i = 0; i < V; ++i) row[i * 32 + lane] = 0.f;
     }
     __syncwarp();
-    // slots of one expert (a selection has none twice, a caller's list may) in slot order
+    if (!WIDE && !twice) {
+        if (e[0] >= 0) row[e[0]] += g[0];
+    } else {  // in slot order
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-        if (h == 1 && a.k <= 32) break;
-        const unsigned same = __match_any_sync(FULL_MASK, e[h] >= 0 ? e[h] : -1 - lane);
-        if (__all_sync(FULL_MASK, __popc(same) == 1)) {
-            if (e[h] >= 0) row[e[h]] += g[h];
-        } else {
+        for (int h = 0; h < H; ++h)
             for (int q = 0; q < 32; ++q) {
                 if (q == lane && e[h] >= 0) row[e[h]] += g[h];
                 __syncwarp();
             }
-        }
-        __syncwarp();
     }
+    __syncwarp();
     float *dl = a.dl + static_cast<size_t>(t) * a.n;
     if ((a.n & 3) == 0) {
         for (int c = lane; c < (a.n >> 2); c += 32)
@@ -540,6 +557,16 @@ __global__ void __launch_bounds__(ROUTE_WARPS * 32) route_rows_grad(const RouteG
     } else {
         for (int c = lane; c < a.n; c += 32) dl[c] = row[c];
     }
+}
+
+template <bool WIDE>
+cudaError_t grad_wide(const RouteGradArgs &a, cudaStream_t stream)
+{
+    const dim3 grid(static_cast<unsigned>((a.T + ROUTE_WARPS - 1) / ROUTE_WARPS)), block(ROUTE_WARPS * 32);
+    if (a.n <= 128) return launch_pdl(route_rows_grad<4, WIDE>, grid, block, 0, stream, a);
+    if (a.n <= 256) return launch_pdl(route_rows_grad<8, WIDE>, grid, block, 0, stream, a);
+    if (a.n <= 512) return launch_pdl(route_rows_grad<16, WIDE>, grid, block, 0, stream, a);
+    return launch_pdl(route_rows_grad<32, WIDE>, grid, block, 0, stream, a);
 }
 
 template <By BY>
@@ -570,11 +597,7 @@ cudaError_t launch_route_rows_grad(const float *logits, int T, int n, int ld, bo
                                    const int *idx, const float *w, const float *dw, float *dl, cudaStream_t stream)
 {
     const RouteGradArgs a = {logits, idx, w, dw, dl, T, n, ld, k, scale, softmax, norm};
-    const dim3 grid(static_cast<unsigned>((T + ROUTE_WARPS - 1) / ROUTE_WARPS)), block(ROUTE_WARPS * 32);
-    if (n <= 128) return launch_pdl(route_rows_grad<4>, grid, block, 0, stream, a);
-    if (n <= 256) return launch_pdl(route_rows_grad<8>, grid, block, 0, stream, a);
-    if (n <= 512) return launch_pdl(route_rows_grad<16>, grid, block, 0, stream, a);
-    return launch_pdl(route_rows_grad<32>, grid, block, 0, stream, a);
+    return k > 32 ? grad_wide<true>(a, stream) : grad_wide<false>(a, stream);
 }
 
 }  // namespace smoe
