@@ -177,7 +177,7 @@ __global__ void __launch_bounds__(TC_THREADS, 1) f8_tc(const __grid_constant__ T
         tma_prefetch_2d(&a.wmap, (c0 + lane) * F8_BLOCK, first % a.mtiles * MT);
     pdl_wait();
     const int ntiles = a.tiles ? *a.ntiles : (a.R + a.step - 1) / a.step;
-    const long long nitems = static_cast<long long>(ntiles) * a.mtiles;
+    const int nitems = ntiles * a.mtiles;  // (below 2^26: y would not fit the device)
     bool failed = false;
 
     if (warp >= MMA_WARP) {
@@ -185,9 +185,9 @@ __global__ void __launch_bounds__(TC_THREADS, 1) f8_tc(const __grid_constant__ T
             if (elect_one()) {
                 uint32_t s = 0, p = 1;  // parity of the stage's release one lap ago; none in the first
                 bool round0 = true;
-                for (long long it = first; it < nitems && !failed; it += stride) {
-                    const Tile t = tile_at(a, static_cast<int>(it / a.mtiles), ntiles);
-                    const int row = t.expert * a.N + static_cast<int>(it % a.mtiles) * MT;
+                for (int it = first; it < nitems && !failed; it += stride) {
+                    const Tile t = tile_at(a, it / a.mtiles, ntiles);
+                    const int row = t.expert * a.N + it % a.mtiles * MT;
                     for (int c = c0; c < c1; ++c) {
                         if (!round0 && !mbar_wait_bounded(empty + 8 * s, p, a.status, 7u)) {
                             failed = true;
@@ -210,8 +210,8 @@ __global__ void __launch_bounds__(TC_THREADS, 1) f8_tc(const __grid_constant__ T
             int *list = reinterpret_cast<int *>(smem_raw + (list0 - raw)) + part * (NT / 4);
             uint32_t s = 0, p = 1;
             bool round0 = true;
-            for (long long it = first; it < nitems && !failed; it += stride) {
-                const Tile t = tile_at(a, static_cast<int>(it / a.mtiles), ntiles);
+            for (int it = first; it < nitems && !failed; it += stride) {
+                const Tile t = tile_at(a, it / a.mtiles, ntiles);
                 const int cols = mma_cols<1>(t.rows);  // a multiple of 16
                 if (a.order) {  // rows past the tile's: any row, their columns are not stored
                     const int at = 16 * (lane >> 2) + 4 * part + (lane & 3);
@@ -256,8 +256,8 @@ __global__ void __launch_bounds__(TC_THREADS, 1) f8_tc(const __grid_constant__ T
             if (elect_one()) {  // one thread issues
                 uint32_t s = 0, p = 0, d = 0, pd = 1;
                 bool round0 = true;
-                for (long long it = first; it < nitems && !failed; it += stride) {
-                    const Tile t = tile_at(a, static_cast<int>(it / a.mtiles), ntiles);
+                for (int it = first; it < nitems && !failed; it += stride) {
+                    const Tile t = tile_at(a, it / a.mtiles, ntiles);
                     const uint32_t idesc = idesc_e4m3(MT, mma_cols<1>(t.rows));
                     for (int c = c0; c < c1; ++c) {
                         // both barriers looked at together: this thread's own latency counts
@@ -302,9 +302,9 @@ __global__ void __launch_bounds__(TC_THREADS, 1) f8_tc(const __grid_constant__ T
             };
             uint32_t s = 0, p = 1;
             bool round0 = true;
-            for (long long it = first; it < nitems && !failed; it += stride) {
-                const Tile t = tile_at(a, static_cast<int>(it / a.mtiles), ntiles);
-                const float *ws = a.ws + (static_cast<size_t>(t.expert) * a.nb + static_cast<int>(it % a.mtiles)) * a.kb;
+            for (int it = first; it < nitems && !failed; it += stride) {
+                const Tile t = tile_at(a, it / a.mtiles, ntiles);
+                const float *ws = a.ws + (static_cast<size_t>(t.expert) * a.nb + it % a.mtiles) * a.kb;
                 const float *xs[2];  // null: no source, a scale of 0
 #pragma unroll
                 for (int i = 0; i < 2; ++i) {
@@ -346,8 +346,8 @@ __global__ void __launch_bounds__(TC_THREADS, 1) f8_tc(const __grid_constant__ T
         T *y = static_cast<T *>(a.y);
         const uint32_t mine = tmem + (static_cast<uint32_t>(q * 32) << 16) + static_cast<uint32_t>(col);
         uint32_t d = 0, pd = 0, s = 0, p = 0;
-        for (long long it = first; it < nitems && !failed; it += stride) {
-            const Tile t = tile_at(a, static_cast<int>(it / a.mtiles), ntiles);
+        for (int it = first; it < nitems && !failed; it += stride) {
+            const Tile t = tile_at(a, it / a.mtiles, ntiles);
             float2 acc[G][2];  // column 4 g + lane % 4 of rows lane / 4 + 16 i and + 8
 #pragma unroll
             for (int g = 0; g < G; ++g) acc[g][0] = acc[g][1] = make_float2(0.f, 0.f);
@@ -389,7 +389,7 @@ __global__ void __launch_bounds__(TC_THREADS, 1) f8_tc(const __grid_constant__ T
                 }
             }
             if (failed) break;
-            const int n0 = (static_cast<int>(it % a.mtiles)) * MT + q * 32;
+            const int n0 = it % a.mtiles * MT + q * 32;
             if (nsplit > 1) {  // this K range's sums [row][128], for the reduction below
 #pragma unroll
                 for (int g = 0; g < G; ++g)

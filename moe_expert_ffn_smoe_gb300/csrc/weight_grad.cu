@@ -11,10 +11,11 @@
 // memory by tensor copies, which cut off what lies outside the expert's matrix, or add
 // (accumulate).
 //
-// An expert's rows begin and end anywhere.  The rows of its last, shorter tile come
-// eight at a time, the last few one by one, and copies from past the batch's end,
-// which fill with zeros, complete the 16 rows of an MMA: rows of other experts, which
-// may hold a NaN, never meet this one's.
+// An expert's rows begin and end anywhere.  The rows of its last, shorter stage come in
+// boxes of 32, 16, .. and 1 rows, and copies from past the batch's end, which fill with
+// zeros, complete the 16 rows of an MMA: rows of other experts, which may hold a NaN,
+// never meet this one's.  (In boxes of 8 and 1, up to 15 copies where there are now 5,
+// issuing them bound the kernel: 128 experts, 32,768 rows, 1536 x 4096 in bf16 409 us.)
 //
 // Bound by writing d_w where an expert has few rows (128 experts of 1536 x 4096 in f32
 // are 3.2 GB), by the tensor cores where it has many.  Roles (warps): 0-7 store, 8
@@ -33,6 +34,7 @@ namespace {
 constexpr int MT = 128, NT = 256;  // a CTA's rows of a tile, the tile's columns
 constexpr int RT = 64;             // rows of the batch in a stage
 constexpr int ST = 5;
+constexpr int BOXES = 7;
 constexpr uint32_t CHUNK = RT * 128;  // 64 columns of a stage
 constexpr uint32_t STAGE = 4 * CHUNK; // two chunks of d_ys, two (the CTA's half) of xs
 constexpr int EPI_WARPS = 8, MMA_WARP = 8, LOAD_WARP = 9, LOADERS = 4;
@@ -41,7 +43,7 @@ constexpr uint32_t BOX = 32 * 128;    // 32 rows of 128 bytes on their way out, 
 constexpr size_t WG_SMEM = 1024 + ST * STAGE + EPI_WARPS * 2 * BOX + 256;
 
 struct alignas(128) GradArgs {
-    CUtensorMap dy[3], x[3];  // boxes of 64, 8 and 1 rows
+    CUtensorMap dy[BOXES], x[BOXES];  // boxes of 64, 32, .. and 1 rows
     CUtensorMap out;
     const int *offsets;
     unsigned *status;
@@ -80,9 +82,12 @@ __device__ __forceinline__ void store_box(const CUtensorMap *map, uint32_t src, 
                      : "memory");
 }
 
-// Expert e's rows; a range that is none counts as empty and is reported.
-__device__ __forceinline__ int2 rows_of(const GradArgs &a, int e)
+// Item it's rows (looked up an item ahead: two reads of memory); a range that is none
+// counts as empty and is reported.
+__device__ __forceinline__ int2 rows_at(const GradArgs &a, int it, int per, int nitems)
 {
+    if (it >= nitems) return make_int2(0, 0);
+    const int e = it / per;
     const int lo = a.offsets[e], hi = a.offsets[e + 1];
     if (lo < 0 || hi < lo || hi > a.R) {
         atomicExch(a.status, kStatusRoute);
@@ -132,7 +137,7 @@ __global__ void __launch_bounds__(WG_THREADS, 1) weight_grad(const __grid_consta
     pdl_wait();
 
     const int per = a.mtiles * a.ntiles;
-    const long long nitems = static_cast<long long>(a.n) * per;
+    const int nitems = a.n * per;  // at most 2^27
     bool failed = false;
 
     if (warp >= LOAD_WARP) {
@@ -143,9 +148,11 @@ __global__ void __launch_bounds__(WG_THREADS, 1) weight_grad(const __grid_consta
             uint32_t s = 0, p = 1;  // parity of the stage's release one lap ago; none in the first
             bool round0 = true;
             long long steps = 0;
-            for (long long it = first; it < nitems && !failed; it += stride) {
-                const int e = static_cast<int>(it / per), m = static_cast<int>(it % per) / a.ntiles, c = static_cast<int>(it % per) % a.ntiles;
-                const int2 r = rows_of(a, e);
+            int2 r, next = rows_at(a, first, per, nitems);
+            for (int it = first; it < nitems && !failed; it += stride) {
+                const int m = it % per / a.ntiles, c = it % per % a.ntiles;
+                r = next;
+                next = rows_at(a, it + stride, per, nitems);
                 const int col = part < 2 ? (m * 2 + rank) * MT + part * 64 : c * NT + rank * (NT / 2) + (part - 2) * 64;
                 for (int t = 0; t < r.y; t += RT) {
                     if (!round0 && !mbar_wait_bounded(empty + 8 * s, p, a.status, 7u)) {
@@ -159,12 +166,17 @@ __global__ void __launch_bounds__(WG_THREADS, 1) weight_grad(const __grid_consta
                     if (rows == RT) {
                         tma_load_2d_pair(dst, &map[0], col, y, bar);
                     } else {
-                        int i = 0;
-                        for (; i + 8 <= rows; i += 8) tma_load_2d_pair(dst + i * 128, &map[1], col, y + i, bar);
-                        if (i < rows)  // the last rows, and zeros from past the batch's end
-                            for (const int end = i + 8; i < end; ++i)
-                                tma_load_2d_pair(dst + i * 128, &map[2], col, i < rows ? y + i : a.R, bar);
-                        if (i < used) tma_load_2d_pair(dst + i * 128, &map[1], col, a.R, bar);
+                        // the rows by the bits of their number, zeros by those of what is missing
+#pragma unroll
+                        for (int b = 1; b < BOXES; ++b) {
+                            const int size = RT >> b, at = rows & ~(2 * size - 1);
+                            if (rows & size) tma_load_2d_pair(dst + at * 128, &map[b], col, y + at, bar);
+                        }
+#pragma unroll
+                        for (int b = BOXES - 4; b < BOXES; ++b) {
+                            const int size = RT >> b, missing = used - rows;
+                            if (missing & size) tma_load_2d_pair(dst + (used - (missing & ~(size - 1))) * 128, &map[b], col, a.R, bar);
+                        }
                     }
                     ++steps;
                     if (++s == ST) {
@@ -187,8 +199,10 @@ __global__ void __launch_bounds__(WG_THREADS, 1) weight_grad(const __grid_consta
             const uint32_t idesc = (1u << 4) | (1u << 7) | (1u << 10) | (1u << 15) | (1u << 16) | (static_cast<uint32_t>(NT >> 3) << 17) |
                                    (static_cast<uint32_t>(2 * MT >> 4) << 24);
             uint32_t s = 0, p = 0, d = 0;
-            for (long long it = first; it < nitems && !failed; it += stride) {
-                const int2 r = rows_of(a, static_cast<int>(it / per));
+            int2 r, next = rows_at(a, first, per, nitems);
+            for (int it = first; it < nitems && !failed; it += stride) {
+                r = next;
+                next = rows_at(a, it + stride, per, nitems);
                 if (r.y == 0) continue;
                 if (d >= 2 && !wait_pair<2>(dempty + 8 * (d & 1), (d / 2 - 1) & 1, a.status, 4u)) {
                     failed = true;
@@ -223,9 +237,11 @@ __global__ void __launch_bounds__(WG_THREADS, 1) weight_grad(const __grid_consta
         const uint32_t lead = mapa_shared(dempty, 0);
         const uint32_t mine = out0 + warp * 2 * BOX;
         uint32_t d = 0, b = 0;
-        for (long long it = first; it < nitems; it += stride) {
-            const int e = static_cast<int>(it / per), m = static_cast<int>(it % per) / a.ntiles, c = static_cast<int>(it % per) % a.ntiles;
-            const int2 r = rows_of(a, e);
+        int2 r, next = rows_at(a, first, per, nitems);
+        for (int it = first; it < nitems; it += stride) {
+            const int e = it / per, m = it % per / a.ntiles, c = it % per % a.ntiles;
+            r = next;
+            next = rows_at(a, it + stride, per, nitems);
             if (r.y == 0 && a.accumulate) continue;
             if (r.y != 0) {
                 if (!__all_sync(FULL_MASK, mbar_wait_bounded(dfull + 8 * (d & 1), (d / 2) & 1, a.status, 6u))) {
@@ -360,8 +376,8 @@ cudaError_t launch_weight_grad(const void *d_ys, const void *xs, const int *offs
     if (R == 0)  // no operand to describe
         return cudaMemsetAsync(d_w, 0, static_cast<size_t>(n) * N * K * (dtype == SMOE_BF16 ? 2 : 4), stream);
     GradArgs a = {};
-    for (int i = 0; i < 3; ++i) {
-        const int rows = i == 0 ? RT : (i == 1 ? 8 : 1);
+    for (int i = 0; i < BOXES; ++i) {
+        const int rows = RT >> i;
         if (!encode(&a.dy[i], CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, d_ys, N, R, 64, rows) ||
             !encode(&a.x[i], CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, xs, K, R, 64, rows))
             return cudaErrorInvalidValue;
