@@ -14,11 +14,15 @@
 // An expert's rows begin and end anywhere.  The rows of its last, shorter stage come in
 // boxes of 32, 16, .. and 1 rows, and copies from past the batch's end, which fill with
 // zeros, complete the 16 rows of an MMA: rows of other experts, which may hold a NaN,
-// never meet this one's.  (In boxes of 8 and 1, up to 15 copies where there are now 5,
-// issuing them bound the kernel: 128 experts, 32,768 rows, 1536 x 4096 in bf16 409 us.)
+// never meet this one's.
 //
-// Bound by writing d_w where an expert has few rows (128 experts of 1536 x 4096 in f32
-// are 3.2 GB), by the tensor cores where it has many.  Roles (warps): 0-7 store, 8
+// Bound by what crosses between L2 and the SMs, whose reads (3.3 GB of them) wait
+// behind the writes of d_w: 128 experts, 32,768 rows, 1536 x 4096 in bf16 396 us (1.6 GB
+// written; without the stores 297), with five stages 412, with three 499.  8 experts of
+// 4096 rows each in f32 277 us, 1490 TFLOP/s.  Measured and not kept: two tiles an item
+// that share their rows of d_ys (2.5 GB read; both halves of tensor memory are then in
+// use, and nothing is summed while the second is stored): 397 and 277; four tiles an
+// item with the rows of d_ys kept in shared memory: 458.  Roles (warps): 0-7 store, 8
 // issues the MMAs (the even CTA's), 9-12 copy 64 columns each.  Every wait is bounded.
 #include <atomic>
 
@@ -33,14 +37,14 @@ namespace {
 
 constexpr int MT = 128, NT = 256;  // a CTA's rows of a tile, the tile's columns
 constexpr int RT = 64;             // rows of the batch in a stage
-constexpr int ST = 5;
+constexpr int ST = 6;
 constexpr int BOXES = 7;
 constexpr uint32_t CHUNK = RT * 128;  // 64 columns of a stage
 constexpr uint32_t STAGE = 4 * CHUNK; // two chunks of d_ys, two (the CTA's half) of xs
 constexpr int EPI_WARPS = 8, MMA_WARP = 8, LOAD_WARP = 9, LOADERS = 4;
 constexpr int WG_THREADS = (LOAD_WARP + LOADERS) * 32;
-constexpr uint32_t BOX = 32 * 128;    // 32 rows of 128 bytes on their way out, two of them a warp
-constexpr size_t WG_SMEM = 1024 + ST * STAGE + EPI_WARPS * 2 * BOX + 256;
+constexpr uint32_t BOX = 32 * 128;    // 32 rows of 128 bytes on their way out, a warp's
+constexpr size_t WG_SMEM = 1024 + ST * STAGE + EPI_WARPS * BOX + 256;
 
 struct alignas(128) GradArgs {
     CUtensorMap dy[BOXES], x[BOXES];  // boxes of 64, 32, .. and 1 rows
@@ -106,7 +110,7 @@ __global__ void __launch_bounds__(WG_THREADS, 1) weight_grad(const __grid_consta
 {
     extern __shared__ uint8_t smem_raw[];
     const uint32_t base = (smem_addr(smem_raw) + 1023u) & ~1023u;
-    const uint32_t out0 = base + ST * STAGE, bars = out0 + EPI_WARPS * 2 * BOX;
+    const uint32_t out0 = base + ST * STAGE, bars = out0 + EPI_WARPS * BOX;
     const uint32_t full = bars, empty = full + 8 * ST, dfull = empty + 8 * ST, dempty = dfull + 16, tslot = dempty + 16;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int rank = static_cast<int>(blockIdx.x & 1u);
@@ -235,8 +239,8 @@ __global__ void __launch_bounds__(WG_THREADS, 1) weight_grad(const __grid_consta
         const int q = warp & 3, h = warp >> 2;
         constexpr int COLS = 128 / static_cast<int>(sizeof(T));  // of a box
         const uint32_t lead = mapa_shared(dempty, 0);
-        const uint32_t mine = out0 + warp * 2 * BOX;
-        uint32_t d = 0, b = 0;
+        const uint32_t box = out0 + warp * BOX, row = box + static_cast<uint32_t>(lane) * 128u;
+        uint32_t d = 0;
         int2 r, next = rows_at(a, first, per, nitems);
         for (int it = first; it < nitems; it += stride) {
             const int e = it / per, m = it % per / a.ntiles, c = it % per % a.ntiles;
@@ -267,10 +271,9 @@ __global__ void __launch_bounds__(WG_THREADS, 1) weight_grad(const __grid_consta
                     __syncwarp();
                     if (lane == 0) mbar_arrive_cluster(lead + 8 * (d & 1));
                 }
-                // the box stored two ago has been read
-                if (lane == 0) asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory");
+                // the last one stored has been read
+                if (lane == 0) asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
                 __syncwarp();
-                const uint32_t box = mine + (b & 1) * BOX, row = box + static_cast<uint32_t>(lane) * 128u;
 #pragma unroll
                 for (int i = 0; i < 8; ++i) {
                     const uint32_t at = row + static_cast<uint32_t>((i ^ (lane & 7)) << 4);
@@ -292,9 +295,8 @@ __global__ void __launch_bounds__(WG_THREADS, 1) weight_grad(const __grid_consta
                 __syncwarp();
                 if (lane == 0) {
                     if (y < a.N && x0 + j * COLS < a.K) store_box(&a.out, box, x0 + j * COLS, y, e, a.accumulate);
-                    asm volatile("cp.async.bulk.commit_group;" ::: "memory");  // empty where nothing is stored: a group a box
+                    asm volatile("cp.async.bulk.commit_group;" ::: "memory");
                 }
-                ++b;
             }
             if (r.y != 0) ++d;
         }
