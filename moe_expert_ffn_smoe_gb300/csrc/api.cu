@@ -1099,8 +1099,9 @@ static int f8_impl(const uint8_t *xq, const float *x_scales, int n_src, const in
                          {order, order ? static_cast<size_t>(n_rows) * sizeof(int) : 0},
                          {offsets, sorted ? (static_cast<size_t>(n_experts) + 1) * sizeof(int) : 0}};
     if (any_alias(outs, 2, ins, 6)) return SMOE_ERR_ALIAS;
-    return to_status(smoe::launch_f8(xq, x_scales, n_src, order, k, sorted ? offsets : nullptr, n_rows, n_experts, wq,
-                                     w_scales, n_out, n_in, y, dtype, workspace, static_cast<cudaStream_t>(stream)));
+    const smoe::F8Call call = {xq, x_scales, n_src, order, k, sorted ? offsets : nullptr, n_rows, n_experts, wq, w_scales, n_out,
+                               n_in, y, dtype};
+    return to_status(smoe::launch_f8(call, workspace, static_cast<cudaStream_t>(stream)));
 }
 
 int smoe_matmul_f8(const uint8_t *xq, const float *x_scales, int n_rows, const uint8_t *wq, const float *w_scales, int n_out,

@@ -169,7 +169,7 @@ __global__ void __launch_bounds__(PAIR_THREADS, 1) f8_pair(const __grid_constant
         tma_prefetch_2d(&a.wmap, lane * F8_BLOCK, (first % a.groups * 2 + rank) * 128);
     pdl_wait();
     const int ntiles = a.tiles ? *a.ntiles : (a.R + a.step - 1) / a.step;
-    const int nitems = ntiles * a.groups;  // (below 2^26: y would not fit the device)
+    const long long nitems = static_cast<long long>(ntiles) * a.groups;
     bool failed = false;
 
     if (warp >= MMA_WARP) {
@@ -179,9 +179,9 @@ __global__ void __launch_bounds__(PAIR_THREADS, 1) f8_pair(const __grid_constant
                 const uint32_t lead = mapa_shared(full, 0);
                 uint32_t s = 0, p = 1;  // parity of the stage's release one lap ago; none in the first
                 bool round0 = true;
-                for (int it = first; it < nitems && !failed; it += stride) {
-                    const Tile t = tile_at(a, it / a.groups, ntiles);
-                    const int row = t.expert * a.N + (it % a.groups * 2 + rank) * 128;
+                for (long long it = first; it < nitems && !failed; it += stride) {
+                    const Tile t = tile_at(a, static_cast<int>(it / a.groups), ntiles);
+                    const int row = t.expert * a.N + (static_cast<int>(it % a.groups) * 2 + rank) * 128;
                     for (int c = 0; c < a.kb; ++c) {
                         if (!round0 && !mbar_wait_bounded(empty + 8 * s, p, a.status, 7u)) {
                             failed = true;
@@ -199,7 +199,7 @@ __global__ void __launch_bounds__(PAIR_THREADS, 1) f8_pair(const __grid_constant
                 // The last releases of the stages arrive here from the other CTA's
                 // issue: they must have before this CTA may leave.
                 if (!failed) {
-                    const long long steps = first < nitems ? static_cast<long long>((nitems - first + stride - 1) / stride) * a.kb : 0;
+                    const long long steps = first < nitems ? (nitems - first + stride - 1) / stride * a.kb : 0;
                     for (long long g = steps > ST ? steps - ST : 0; g < steps; ++g)
                         if (!mbar_wait_bounded(empty + 8 * static_cast<uint32_t>(g % ST), static_cast<uint32_t>(g / ST) & 1,
                                                a.status, 8u))
@@ -217,8 +217,8 @@ __global__ void __launch_bounds__(PAIR_THREADS, 1) f8_pair(const __grid_constant
                 const uint32_t lead = mapa_shared(full, 0);
                 uint32_t s = 0, p = 1;
                 bool round0 = true;
-                for (int it = first; it < nitems && !failed; it += stride) {
-                    const Tile t = tile_at(a, it / a.groups, ntiles);
+                for (long long it = first; it < nitems && !failed; it += stride) {
+                    const Tile t = tile_at(a, static_cast<int>(it / a.groups), ntiles);
                     const int share = share_of(t), row0 = t.row0 + rank * share;
                     int4 r[GATHERS];
                     if (a.order) {  // rows past the tile's: any row, their outputs are not stored
@@ -264,7 +264,7 @@ __global__ void __launch_bounds__(PAIR_THREADS, 1) f8_pair(const __grid_constant
             if (rank == 0 && elect_one()) {
                 uint32_t s = 0, p = 0, d = 0, pd = 1;
                 bool round0 = true;
-                for (int it = first; it < nitems && !failed; it += stride) {
+                for (long long it = first; it < nitems && !failed; it += stride) {
                     for (int c = 0; c < a.kb; ++c) {
                         // Both barriers looked at together: this thread's own latency counts.
                         // What they hand over is read by the MMAs alone (operands that copies
@@ -305,9 +305,9 @@ __global__ void __launch_bounds__(PAIR_THREADS, 1) f8_pair(const __grid_constant
         const uint32_t lead = mapa_shared(dempty, 0);
         const uint32_t mine = tmem + (static_cast<uint32_t>(q * 32) << 16) + static_cast<uint32_t>(h * 128);
         uint32_t d = 0, pd = 0;
-        for (int it = first; it < nitems && !failed; it += stride) {
-            const Tile t = tile_at(a, it / a.groups, ntiles);
-            const int share = share_of(t), nblk = it % a.groups * 2 + h;
+        for (long long it = first; it < nitems && !failed; it += stride) {
+            const Tile t = tile_at(a, static_cast<int>(it / a.groups), ntiles);
+            const int share = share_of(t), nblk = static_cast<int>(it % a.groups) * 2 + h;
             const int r = rank * share + q * 32 + lane;  // of the tile
             const bool some = q * 32 < share;
             const int src = q * 32 + lane < share && r < t.rows ? source_row(a.order, a.k, a.nsrc, t.row0 + r, a.status) : -1;

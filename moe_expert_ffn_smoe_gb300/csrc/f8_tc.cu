@@ -21,6 +21,7 @@
 // sums through distributed shared memory.  Roles (warps): 0-7 epilogue, 8 issues the
 // MMAs, 9 streams the weights, 10 brings the row scales, 12-15 the rows (gathered by the
 // copies where the batch is sorted by an order).  Every wait is bounded.
+#include <algorithm>
 #include <atomic>
 
 #include "f8.cuh"
@@ -522,12 +523,20 @@ __global__ void __launch_bounds__(PREP_THREADS) f8_prep(const PrepArgs a)
 
 // ---------------------------------------------------------------- host
 
-// Whether pairs take the product, in row tiles of 256: where reading the weights does
-// not bound it and its tiles of 64 rows do not fit the device at once.
-bool by_pairs(int R, int n, bool one, int mtiles, int sms)
+// Whether pairs take the product, in row tiles of 256.  A pair's item takes about twice
+// as long as a CTA's of 64 rows and 128 weights (half-empty or not), so they do where
+// they need less than half the rounds over the device, with half a tile an expert left
+// over on average.  One matrix of 8192 x 4096, this form and pairs: 128 rows 11.5 and
+// 19.5 us, 256 rows 20.0 and 21.9, 384 rows 28.0 and 20.9, 1024 rows 61 and 40; of
+// 1536 x 4096, 1024 rows 19.1 and 22.0; 128 experts top-8: 800 tokens 151 and 195 us,
+// 1024 tokens 178 and 200, 2048 tokens 296 and 219.
+bool by_pairs(int R, int n, bool one, int N, int sms)
 {
-    const long long tiles = one ? (R + NT - 1) / NT : most_tiles(R, n, NT);
-    return R > 48LL * n && tiles * mtiles > sms;
+    const auto rounds = [&](int rows, int cols, int at_once) {
+        const long long tiles = one ? (R + rows - 1) / rows : std::max(std::min(R, n), R / rows + n / 2);
+        return (tiles * ((N + cols - 1) / cols) + at_once - 1) / at_once;
+    };
+    return rounds(NT, MT, sms) > 2 * rounds(256, 256, sms / 2);
 }
 
 template <typename T>
@@ -544,11 +553,13 @@ cudaError_t launch_t(const TcArgs &args, long long most_items, int sms, cudaStre
         if (e != cudaSuccess) return e;
         opted[dev].store(true, std::memory_order_relaxed);
     }
-    // few items: their K ranges are split over clusters of 2, 4 or 8 CTAs,
-    // as many as the device holds at once, each at least two blocks
+    // Few items: their K ranges are split over clusters of 2, 4 or 8 CTAs, as many as
+    // the device holds at once, from 16 blocks on.  1536 x 4096: one row 9.2 -> 5.8 us,
+    // 192 rows 10.8 -> 8.3 us; of 8 blocks (1024 x 1024, 128 rows) 5.1 -> 6.4 us: the
+    // sum over the cluster costs more than the blocks that it saves.
     int size = 1;
     for (int s = 8; s > 1; s /= 2)
-        if (most_items * s <= sms && args.kb >= 2 * s && most_items <= clusters_held<f8_tc<T>>(s, TC_THREADS, TC_SMEM)) {
+        if (most_items * s <= sms && args.kb >= 16 && most_items <= clusters_held<f8_tc<T>>(s, TC_THREADS, TC_SMEM)) {
             size = s;
             break;
         }
@@ -574,15 +585,17 @@ cudaError_t launch_t(const TcArgs &args, long long most_items, int sms, cudaStre
 
 }  // namespace
 
-size_t f8_tc_workspace(int R, int n) { return 256 + up256(static_cast<size_t>(most_tiles(R, n, NT)) * sizeof(Tile)); }
+size_t f8_workspace(int R, int n) { return 256 + up256(static_cast<size_t>(most_tiles(R, n, NT)) * sizeof(Tile)); }
 
-cudaError_t launch_f8_tc(const F8Call &c, void *workspace, cudaStream_t stream)
+cudaError_t launch_f8(const F8Call &c, void *workspace, cudaStream_t stream)
 {
     const DeviceInfo *dev = device_info();
     unsigned *status = device_status_word();
     if (!dev || !status) return cudaErrorInvalidDevice;
+    if (c.K == 0)  // empty sums
+        return cudaMemsetAsync(c.y, 0, static_cast<size_t>(c.R) * c.N * (c.dtype == SMOE_BF16 ? 2 : 4), stream);
     const int mtiles = (c.N + MT - 1) / MT;
-    const bool pairs = by_pairs(c.R, c.n, !c.offsets, mtiles, dev->sm_count);
+    const bool pairs = by_pairs(c.R, c.n, !c.offsets, c.N, dev->sm_count);
     const int nt = pairs ? 256 : NT, max_tiles = most_tiles(c.R, c.n, nt);
     int *ntiles = static_cast<int *>(workspace);
     Tile *tiles = reinterpret_cast<Tile *>(static_cast<char *>(workspace) + 256);

@@ -41,15 +41,28 @@ cudaError_t launch_q8(const int8_t *xq, const float *xs, int nsrc, const int *or
                       cudaStream_t stream);
 
 // 8-bit floating-point rows, weights and products with a scale for each block of
-// 128 (quant_f8.cu, f8.cu).  qt null: one direction.
+// 128 (quant_f8.cu, f8_tc.cu).  qt null: one direction.
 cudaError_t launch_quantize_rows_f8(const void *x, int dtype, bool act, int rows, int cols, uint8_t *q, float *scales,
                                     cudaStream_t stream);
 cudaError_t launch_quantize_blocks_f8(const void *w, int dtype, int n, int rows, int cols, uint8_t *q, float *scales,
                                       uint8_t *qt, float *scales_t, cudaStream_t stream);
+// offsets null: one matrix (n == 1); order null: row r of the batch is row r of xq.
+struct F8Call {
+    const uint8_t *xq;
+    const float *xs;
+    int nsrc;
+    const int *order;
+    int k;
+    const int *offsets;
+    int R, n;
+    const uint8_t *wq;
+    const float *ws;
+    int N, K;
+    void *y;
+    int dtype;
+};
 size_t f8_workspace(int R, int n);
-cudaError_t launch_f8(const uint8_t *xq, const float *xs, int nsrc, const int *order, int k, const int *offsets, int R, int n,
-                      const uint8_t *wq, const float *ws, int N, int K, void *y, int dtype, void *workspace,
-                      cudaStream_t stream);
+cudaError_t launch_f8(const F8Call &c, void *workspace, cudaStream_t stream);
 
 // The gradient of the experts' weights (weight_grad.cu).
 cudaError_t launch_weight_grad(const void *d_ys, const void *xs, const int *offsets, int R, int n, int N, int K,
