@@ -4,11 +4,16 @@
   products with 8-bit weights and activations, the weighted sum back: eight
   calls, nothing read back to the host, so that the whole layer can be
   captured in one CUDA graph.
-* ``top_k``, ``dispatch``, ``combine``: the same routing under torch's
+* ``F8Layer``: the same in 8-bit floating point with a scale for each block of
+  128, routed by scores (softmax or sigmoid, with or without a bias and groups).
+* ``top_k``, ``route``, ``dispatch``, ``combine``: the same routing under torch's
   autograd (each backward is the library's own call, and has none of its own:
   a second gradient is refused), for training experts written in torch.
+* ``experts_f8``: the experts' product in 8-bit floating point under autograd;
+  its backward pass is a product with the transposed codes and the weights'
+  gradient.  ``moe_train_f8`` trains a whole layer with it, reading nothing back.
 
-``python examples/moe_layer.py`` runs both on a GPU with seeded weights.
+``python examples/moe_layer.py`` runs them on a GPU with seeded weights.
 """
 import contextlib
 import os
@@ -40,6 +45,17 @@ _INTS = (torch.int32, torch.int64, torch.int16, torch.int8, torch.uint8)
 
 def _bytes(n, device):
     return torch.empty(max(n, 16), dtype=torch.uint8, device=device)
+
+
+def _logits(x, gate, gate32, logits, stream):
+    """logits[t] = gate x[t] in f32: gate bf16, gate32 the same in f32."""
+    T, (n, d) = x.shape[0], gate.shape
+    if T <= 64 and n % 4 == 0:  # a matvec writes to 16-byte boundaries
+        smoe.matvec_bf16_batch([gate] * T, [x.data_ptr() + 4 * d * t for t in range(T)],
+                               [logits.data_ptr() + 4 * n * t for t in range(T)], [n] * T, [d] * T, stream)
+    else:  # a matvec a token would read the router's weights T times
+        with torch.cuda.stream(stream) if stream is not None else contextlib.nullcontext():
+            torch.mm(x, gate32.t(), out=logits[:T])
 
 
 def quantize_weights(w):
@@ -97,12 +113,7 @@ class Q8Layer:
             raise ValueError("x and out are to be contiguous")
         T, k, n, d, ff = x.shape[0], self.k, self.n, self.d, self.d_ff
         R = T * k
-        if T <= 64 and n % 4 == 0:  # a matvec writes to 16-byte boundaries
-            smoe.matvec_bf16_batch([self.gate] * T, [x.data_ptr() + 4 * d * t for t in range(T)],
-                                   [self.logits.data_ptr() + 4 * n * t for t in range(T)], [n] * T, [d] * T, stream)
-        else:  # a matvec a token would read the router's weights T times
-            with torch.cuda.stream(stream) if stream is not None else contextlib.nullcontext():
-                torch.mm(x, self.gate32.t(), out=self.logits[:T])
+        _logits(x, self.gate, self.gate32, self.logits, stream)
         smoe.smoe_topk_rows(self.logits, T, n, n, k, self.idx, self.w, stream)
         smoe.smoe_dispatch_tokens(self.idx, T, k, n, None, smoe.SMOE_F32, 0, self.offsets, self.order, self.place, None,
                                   self.ws, self.need, stream)
@@ -113,6 +124,83 @@ class Q8Layer:
         smoe.smoe_experts_matmul_q8(self.hq, self.h_scales, R, None, 1, self.offsets, R, n, self.dn, self.dn_scales, d, ff,
                                     self.ys, smoe.SMOE_BF16, self.ws, self.need, stream)
         smoe.smoe_combine_tokens(self.ys, smoe.SMOE_BF16, self.place, self.w, T, k, d, out, stream)
+        return out
+
+
+def quantize_weights_f8(w, both=False):
+    """e4m3 codes (bytes) and one scale for each 128 x 128 block of w [n, n_out,
+    n_in]; both: (codes, scales, and the same of the transposed matrices)."""
+    _check("w", w, (None, None, None), tuple(_CODE))
+    n, rows, cols = w.shape
+    up = lambda m: (m + 127) // 128  # noqa: E731
+    u8 = lambda *s: torch.empty(*s, dtype=torch.uint8, device=w.device)  # noqa: E731
+    q, scales = u8(n, rows, cols), torch.empty(n, up(rows), up(cols), device=w.device)
+    qt, scales_t = (u8(n, cols, rows), torch.empty(n, up(cols), up(rows), device=w.device)) if both else (None, None)
+    smoe.smoe_quantize_blocks_f8(w.contiguous(), _CODE[w.dtype], n, rows, cols, q, scales, qt, scales_t)
+    return (q, scales, qt, scales_t) if both else (q, scales)
+
+
+class F8Layer:
+    """n_experts experts of d_model -> d_ff -> d_model in 8-bit floating point,
+    routed by scores, for up to max_tokens tokens a call.
+
+    gate: router weights bf16 [n_experts, d_model];
+    gate_up: [n_experts, 2 d_ff, d_model], the gate rows first, and
+    down: [n_experts, d_model, d_ff], f32 or bf16, quantised here;
+    bias: f32 [n_experts], added to the scores for the choice, or None;
+    score, n_groups, top_groups, group_best, norm, scale: as smoe_route_rows."""
+
+    def __init__(self, gate, gate_up, down, k, max_tokens, bias=None, score=smoe.SMOE_SCORE_SOFTMAX, n_groups=1, top_groups=1,
+                 group_best=1, norm=True, scale=1.0):
+        n, d, ff = *gate.shape, down.shape[-1]
+        _check("gate", gate, (n, d), (torch.bfloat16,))
+        _check("gate_up", gate_up, (n, 2 * ff, d), tuple(_CODE))
+        _check("down", down, (n, d, ff), tuple(_CODE))
+        if bias is not None:
+            _check("bias", bias, (n,), (torch.float32,))
+        dev, self.n, self.d, self.d_ff, self.k, self.max_tokens = gate.device, n, d, ff, k, max_tokens
+        self.gate, self.gate32 = gate.contiguous(), gate.float().contiguous()
+        self.bias = None if bias is None else bias.contiguous()
+        self.choice, self.weighing = (score, n_groups, top_groups, group_best), (int(norm), scale)
+        self.gu, self.gu_scales = quantize_weights_f8(gate_up)
+        self.dn, self.dn_scales = quantize_weights_f8(down)
+        rows = max_tokens * k
+        f32 = lambda *s: torch.empty(*s, device=dev)  # noqa: E731
+        i32 = lambda *s: torch.empty(*s, dtype=torch.int32, device=dev)  # noqa: E731
+        u8 = lambda *s: torch.empty(*s, dtype=torch.uint8, device=dev)  # noqa: E731
+        bf = lambda *s: torch.empty(*s, dtype=torch.bfloat16, device=dev)  # noqa: E731
+        self.logits, self.idx, self.w = f32(max_tokens, n), i32(max_tokens, k), f32(max_tokens, k)
+        self.offsets, self.order, self.place = i32(n + 1), i32(rows), i32(rows)
+        self.xq, self.x_scales = u8(max_tokens, d), f32(max_tokens, (d + 127) // 128)
+        self.h, self.hq, self.h_scales = bf(rows, 2 * ff), u8(rows, ff), f32(rows, (ff + 127) // 128)
+        self.ys = bf(rows, d)
+        self.need = max(smoe.smoe_dispatch_workspace_bytes(max_tokens, k, n),
+                        smoe.smoe_experts_matmul_f8_workspace_bytes(max_tokens, rows, n, 2 * ff, d),
+                        smoe.smoe_experts_matmul_f8_workspace_bytes(rows, rows, n, d, ff))
+        self.ws = _bytes(self.need, dev)
+
+    def __call__(self, x, out, stream=None):
+        """out[t] (bf16) = the layer's output for x[t] (f32 [tokens, d_model]),
+        both contiguous."""
+        _check("x", x, (None, self.d), (torch.float32,))
+        _check("out", out, (x.shape[0], self.d), (torch.bfloat16,))
+        if x.shape[0] > self.max_tokens:
+            raise ValueError(f"{x.shape[0]} tokens, where the layer was made for {self.max_tokens}")
+        if not (x.is_contiguous() and out.is_contiguous()):
+            raise ValueError("x and out are to be contiguous")
+        T, k, n, d, ff = x.shape[0], self.k, self.n, self.d, self.d_ff
+        R, bf = T * k, smoe.SMOE_BF16
+        _logits(x, self.gate, self.gate32, self.logits, stream)
+        smoe.smoe_route_rows(self.logits, T, n, n, self.bias, *self.choice, k, *self.weighing, self.idx, self.w, stream)
+        smoe.smoe_dispatch_tokens(self.idx, T, k, n, None, smoe.SMOE_F32, 0, self.offsets, self.order, self.place, None,
+                                  self.ws, self.need, stream)
+        smoe.smoe_quantize_rows_f8(x, smoe.SMOE_F32, smoe.SMOE_Q8_PLAIN, T, d, self.xq, self.x_scales, stream)
+        smoe.smoe_experts_matmul_f8(self.xq, self.x_scales, T, self.order, k, self.offsets, R, n, self.gu, self.gu_scales,
+                                    2 * ff, d, self.h, bf, self.ws, self.need, stream)
+        smoe.smoe_quantize_rows_f8(self.h, bf, smoe.SMOE_Q8_SILU_MUL, R, ff, self.hq, self.h_scales, stream)
+        smoe.smoe_experts_matmul_f8(self.hq, self.h_scales, R, None, 1, self.offsets, R, n, self.dn, self.dn_scales, d, ff,
+                                    self.ys, bf, self.ws, self.need, stream)
+        smoe.smoe_combine_tokens(self.ys, bf, self.place, self.w, T, k, d, out, stream)
         return out
 
 
@@ -137,6 +225,29 @@ class _TopK(torch.autograd.Function):
         d = torch.empty(T, ctx.n, device=w.device)
         smoe.smoe_topk_rows_backward(idx, w, d_w.contiguous(), T, ctx.n, k, d)
         return d, None
+
+
+class _Route(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, logits, bias, k, score, n_groups, top_groups, group_best, norm, scale):
+        logits = logits.contiguous()
+        T, n = logits.shape
+        idx = torch.empty(T, k, dtype=torch.int32, device=logits.device)
+        w = torch.empty(T, k, device=logits.device)
+        smoe.smoe_route_rows(logits, T, n, n, bias, score, n_groups, top_groups, group_best, k, norm, scale, idx, w)
+        ctx.save_for_backward(logits, idx, w)
+        ctx.weighing = score, k, norm, scale
+        ctx.mark_non_differentiable(idx)
+        return idx, w
+
+    @staticmethod
+    @once_differentiable
+    def backward(ctx, _, d_w):
+        logits, idx, w = ctx.saved_tensors
+        T, n = logits.shape
+        d = torch.empty(T, n, device=w.device)
+        smoe.smoe_route_rows_backward(logits, T, n, n, *ctx.weighing, idx, w, d_w.contiguous(), d)
+        return (d,) + (None,) * 8
 
 
 class _Dispatch(torch.autograd.Function):
@@ -165,6 +276,44 @@ class _Dispatch(torch.autograd.Function):
         return d_x, None, None
 
 
+def _product_f8(x, w, w_scales, offsets):
+    """Rows x [R, n_in] (sorted by expert), quantised, by codes w [n, n_out, n_in]."""
+    (R, n_in), (n, n_out, _) = x.shape, w.shape
+    xq = torch.empty(R, n_in, dtype=torch.uint8, device=x.device)
+    x_scales = torch.empty(R, (n_in + 127) // 128, device=x.device)
+    y = torch.empty(R, n_out, dtype=x.dtype, device=x.device)
+    need = smoe.smoe_experts_matmul_f8_workspace_bytes(R, R, n, n_out, n_in)
+    smoe.smoe_quantize_rows_f8(x, _CODE[x.dtype], smoe.SMOE_Q8_PLAIN, R, n_in, xq, x_scales)
+    smoe.smoe_experts_matmul_f8(xq, x_scales, R, None, 1, offsets, R, n, w, w_scales, n_out, n_in, y, _CODE[x.dtype],
+                                _bytes(need, x.device), need)
+    return y
+
+
+class _ExpertsF8(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, xs, w, offsets):
+        xs, offsets = xs.contiguous(), offsets.contiguous()
+        back, grad = ctx.needs_input_grad[:2]
+        codes = quantize_weights_f8(w, back)
+        ctx.save_for_backward(xs.to(torch.bfloat16) if grad else None, *(codes[2:] if back else (None, None)), offsets)
+        ctx.sizes = xs.shape[0], *w.shape, w.dtype
+        return _product_f8(xs, *codes[:2], offsets)
+
+    @staticmethod
+    @once_differentiable
+    def backward(ctx, d_ys):
+        xs, qt, scales_t, offsets = ctx.saved_tensors
+        R, n, n_out, n_in, w_type = ctx.sizes
+        d_xs = d_w = None
+        d_ys = d_ys.contiguous()
+        if ctx.needs_input_grad[0]:
+            d_xs = _product_f8(d_ys, qt, scales_t, offsets)
+        if ctx.needs_input_grad[1]:
+            d_w = torch.empty(n, n_out, n_in, dtype=w_type, device=d_ys.device)
+            smoe.smoe_experts_weight_grad(d_ys.to(torch.bfloat16), xs, offsets, R, n, n_out, n_in, 0, d_w, _CODE[w_type])
+        return d_xs, d_w, None
+
+
 class _Combine(torch.autograd.Function):
     @staticmethod
     def forward(ctx, ys, place, w):
@@ -190,6 +339,31 @@ def top_k(logits, k):
     differentiable in logits (of any float type)."""
     _check("logits", logits, (None, None), _FLOATS)
     return _TopK.apply(logits.float(), k)
+
+
+def route(logits, k, bias=None, score=smoe.SMOE_SCORE_SOFTMAX, n_groups=1, top_groups=1, group_best=1, norm=True, scale=1.0):
+    """(indices, weights) of each row's k experts by their scores, as
+    smoe_route_rows takes them; differentiable in logits (of any float type)."""
+    _check("logits", logits, (None, None), _FLOATS)
+    if bias is not None:
+        _check("bias", bias, (logits.shape[1],), (torch.float32,))
+        bias = bias.detach().contiguous()
+    return _Route.apply(logits.float(), bias, k, score, n_groups, top_groups, group_best, int(norm), scale)
+
+
+def experts_f8(xs, w, offsets):
+    """ys[r] = w[e] xs[r] for the rows r of expert e, [offsets[e], offsets[e + 1]),
+    both quantised to 8-bit floating point; differentiable in xs [R, n_in] and w
+    [n, n_out, n_in] (each f32 or bf16, n_in and n_out multiples of 16), the
+    quantisers being passed through as if they were none.  The rows' gradient is
+    the product of the quantised output gradients and the transposed codes, the
+    weights' that of both operands in bf16."""
+    _check("xs", xs, (None, None), tuple(_CODE))
+    _check("w", w, (None, None, xs.shape[1]), tuple(_CODE))
+    _check("offsets", offsets, (w.shape[0] + 1,), (torch.int32,))
+    if w.shape[1] % 16 or w.shape[2] % 16:
+        raise ValueError(f"matrices of {tuple(w.shape[1:])}: both sizes are to be multiples of 16")
+    return _ExpertsF8.apply(xs, w, offsets)
 
 
 def dispatch(x, idx, n_experts):
@@ -229,6 +403,20 @@ def moe_train(x, router, gate_up, down, k):
     return combine(torch.cat(ys), place, w)
 
 
+def moe_train_f8(x, router, gate_up, down, k, bias=None, **how):
+    """The layer in 8-bit floating point, routed by scores (how: as route takes
+    it); nothing is read back, so that a step can be captured in a CUDA graph.
+    x bf16 or f32; every argument but bias may need a gradient."""
+    n, d_ff = router.shape[0], down.shape[2]
+    with torch.autocast(x.device.type, enabled=False):  # the selection is made on f32 logits
+        logits = x.float() @ router.float().t()
+        idx, w = route(logits, k, bias, **how)
+        xs, offsets, place = dispatch(x, idx, n)
+        h = experts_f8(xs, gate_up, offsets)
+        ys = experts_f8(torch.nn.functional.silu(h[:, :d_ff]) * h[:, d_ff:], down, offsets)
+        return combine(ys, place, w)
+
+
 def main():
     dev = torch.device("cuda:0")
     g = torch.Generator(device=dev).manual_seed(0)
@@ -241,10 +429,14 @@ def main():
     out = layer(x, torch.empty(T, d, dtype=torch.bfloat16, device=dev))
     ref = moe_train(x, router.to(torch.bfloat16).float(), gate_up, down, k)
     print("8-bit layer against the f32 experts: relative difference %.3f" % ((out.float() - ref).norm() / ref.norm()).item())
-    params = [p.requires_grad_() for p in (router, gate_up, down)]
-    loss = moe_train(x, *params, k).square().mean()
-    loss.backward()
-    print("loss %.5f, gradient norms %s" % (loss.item(), ["%.4g" % p.grad.norm().item() for p in params]))
+    layer = F8Layer(router.to(torch.bfloat16), gate_up, down, k, T)
+    out = layer(x, torch.empty(T, d, dtype=torch.bfloat16, device=dev))
+    print("8-bit floating-point layer:              relative difference %.3f" % ((out.float() - ref).norm() / ref.norm()).item())
+    for train in (moe_train, moe_train_f8):
+        params = [p.detach().clone().requires_grad_() for p in (router, gate_up, down)]
+        loss = train(x, *params, k).square().mean()
+        loss.backward()
+        print("%s: loss %.5f, gradient norms %s" % (train.__name__, loss.item(), ["%.4g" % p.grad.norm().item() for p in params]))
     if smoe.smoe_last_device_status() != smoe.SMOE_OK:
         raise RuntimeError("a kernel reported an error")
 
