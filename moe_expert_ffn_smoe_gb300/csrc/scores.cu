@@ -21,7 +21,7 @@
 namespace smoe {
 namespace {
 
-constexpr int ROUTE_WARPS = 8;
+constexpr int ROW_WARPS = 4, GRAD_WARPS = 8;  // rows of a CTA
 
 // What the choice goes by.
 enum class By { Logit, Sigmoid, Softmax };
@@ -32,10 +32,22 @@ struct RouteArgs {
     float *w;
     int T, n, ld, k, groups, top_groups, best;
     int size;        // experts of a group
+    int shift;       // 2^shift lanes look at a group: lanes g 2^shift .. at group g
     unsigned magic;  // ceil(2^20 / size): e magic >> 20 = e / size for e < 1024
     float scale;
     bool softmax, norm;
+    bool wide;       // logits and bias begin at 16-byte boundaries, in every row
 };
+
+// Which expert a lane's i-th value is.  NEAR: a lane holds V neighbours, so that a
+// group is some lanes' own; otherwise every 32nd, so that few experts are spread
+// over all lanes.
+template <int V, bool NEAR>
+__device__ __forceinline__ int expert_at(int i)
+{
+    const int lane = threadIdx.x & 31;
+    return NEAR ? lane * V + i : i * 32 + lane;
+}
 
 __device__ __forceinline__ float warp_max(float v)
 {
@@ -53,6 +65,13 @@ __device__ __forceinline__ float warp_sum(float v)
 #pragma unroll
     for (int off = 16; off > 0; off >>= 1) v += __shfl_xor_sync(FULL_MASK, v, off);
     return v;
+}
+
+// value_key of what is no NaN.
+__device__ __forceinline__ uint32_t number_key(float v)
+{
+    const uint32_t u = __float_as_uint(v + 0.f);
+    return u ^ (static_cast<uint32_t>(static_cast<int>(u) >> 31) | 0x80000000u);
 }
 
 __device__ __forceinline__ float rcp_approx(float v)
@@ -131,77 +150,102 @@ __device__ __noinline__ bool all_alike(const Row r)
     return -warp_max(-lo) == warp_max(hi) && -warp_max(-blo) == warp_max(bhi);
 }
 
-// Lanes P g .. P g + P - 1 look at group g: the largest power of two that
-// leaves every group its lanes.
-__device__ __forceinline__ int lanes_of_group(int groups)
-{
-    return 1 << (31 - __clz(32 / groups));
-}
+// The groups that lanes hold: every lane of a group the same.
+struct Groups {
+    float value, err;  // what the group counts (-inf: no expert on), a bound of its error
+    bool taken;
+    uint32_t low, high;  // keys of the least that one taken may count, of the most that one left out may
+};
 
-// The groups taken, as a mask of their first lanes, from every lane's value of
-// its group (equal in all lanes of a group; -inf: no expert on); err: bound of
-// its error; doubt: whether the border lies within the bounds.
-__device__ __forceinline__ uint32_t take_groups(float value, float err, int P, const RouteArgs &a, bool &doubt)
+__device__ __forceinline__ void take_groups(Groups &q, const RouteArgs &a)
 {
-    const int lane = threadIdx.x & 31, g = lane / P;
+    const int lane = threadIdx.x & 31, P = 1 << a.shift, g = lane >> a.shift, in = lane & (P - 1);
     // each of a group's lanes looks at every P-th other group
     int before = 0;
-    for (int h0 = 0; h0 < a.groups; h0 += P) {
-        const int h = h0 + (lane & (P - 1));
-        const float o = __shfl_sync(FULL_MASK, value, h * P);  // (the lanes wrap round past the last group)
-        before += h < a.groups && (o > value || (o == value && h < g));
+    for (int h = in; h - in < a.groups; h += P) {
+        const float o = __shfl_sync(FULL_MASK, q.value, h << a.shift);  // (the lanes wrap round past the last group)
+        before += h < a.groups && (o > q.value || (o == q.value && h < g));
     }
     for (int off = P >> 1; off > 0; off >>= 1) before += __shfl_xor_sync(FULL_MASK, before, off);
-    const bool on = g < a.groups && value > -INFINITY, taken = on && before < a.top_groups;
-    // the least sure value of those taken against the largest that those left out may have
-    const uint32_t low = __reduce_min_sync(FULL_MASK, taken ? value_key(value - err) : 0xFFFFFFFFu);
-    const uint32_t high = __reduce_max_sync(FULL_MASK, on && !taken ? value_key(value + err) : 0u);
-    doubt = high >= low;
-    return __ballot_sync(FULL_MASK, taken && (lane & (P - 1)) == 0);
+    const bool on = g < a.groups && q.value > -INFINITY;
+    q.taken = on && before < a.top_groups;
+    q.low = __reduce_min_sync(FULL_MASK, q.taken ? number_key(q.value - q.err) : 0xFFFFFFFFu);
+    q.high = __reduce_max_sync(FULL_MASK, on && !q.taken ? number_key(q.value + q.err) : 0u);
 }
 
-// The same from scores in 64 bits.
-template <By BY>
-__device__ __noinline__ uint32_t take_groups64(const Row r, const RouteArgs &a, int P)
+// Whether this lane's group is taken, where the border between the groups lies within
+// the bounds (high >= low): those that the bounds leave on one side of it stay there
+// (one taken that counts more than any left out may has less than top_groups before
+// it; one left out that counts less than any taken has as many), the others are
+// ordered by 64 bits.  least: what one of the best of this lane's group counts at
+// least.  v: the row's c (expert_at), err: their bound.  32,768 rows by groups in us,
+// against scores of the whole row in 64 bits: 512 experts 59 / 69, 128 experts 27 / 30.
+template <By BY, int V, bool NEAR>
+__device__ __noinline__ bool take_groups64(const Row r, const RouteArgs &a, const Groups q, const float (&v)[V], float least,
+                                           float err, Candidates &c)
 {
+    const int lane = threadIdx.x & 31, g = lane >> a.shift;
+    const bool first = (lane & ((1 << a.shift) - 1)) == 0;
+    const bool open = g < a.groups && q.value > -INFINITY &&
+                      (q.taken ? number_key(q.value - q.err) <= q.high : number_key(q.value + q.err) >= q.low);
+    const uint32_t opens = __ballot_sync(FULL_MASK, open);
+    const int places = a.top_groups - __popc(__ballot_sync(FULL_MASK, q.taken && !open && first));
     const double inv64 = inverse_sum64<BY>(r);
-    const int lane = threadIdx.x & 31, g = lane / P;
     double b1 = -INFINITY, b2 = -INFINITY;
-    if (g < a.groups)
-        for (int e = g * a.size + lane % P; e < (g + 1) * a.size; e += P) {
-            const double t = is_off(r, e) ? -INFINITY : choice64<BY>(r, e, inv64);
-            b2 = fmax(b2, fmin(b1, t));
-            b1 = fmax(b1, t);
+    int count = 0;
+    const auto weigh = [&] {  // the gathered experts' c, one a lane, into their groups' two best
+        __syncwarp();
+        const int e = lane < count ? c.expert[lane] : -1;
+        const double c64 = e >= 0 ? choice64<BY>(r, e, inv64) : 0.0;
+        for (int o = 0; o < count; ++o) {
+            const double t = __shfl_sync(FULL_MASK, c64, o);
+            const int of = static_cast<int>((static_cast<unsigned>(c.expert[o]) * a.magic) >> 20);
+            if (of == g) {
+                b2 = fmax(b2, fmin(b1, t));
+                b1 = fmax(b1, t);
+            }
         }
-    for (int off = P >> 1; off > 0; off >>= 1) {
-        const double o1 = __shfl_xor_sync(FULL_MASK, b1, off), o2 = __shfl_xor_sync(FULL_MASK, b2, off);
-        b2 = fmax(fmin(b1, o1), fmax(b2, o2));
-        b1 = fmax(b1, o1);
+        __syncwarp();
+        count = 0;
+    };
+#pragma unroll 1
+    for (int i = 0; i < V; ++i) {
+        float mine = -INFINITY;
+#pragma unroll
+        for (int j = 0; j < V; ++j)
+            if (j == i) mine = v[j];
+        const int e = expert_at<V, NEAR>(i);
+        const int at = (static_cast<int>((static_cast<unsigned>(e) * a.magic) >> 20) << a.shift) & 31;  // a lane of its group
+        const float floor = __shfl_sync(FULL_MASK, least, at) - 2.f * err;
+        const bool in = e < a.n && (opens >> at & 1u) && mine > -INFINITY && mine >= floor;
+        if (count + __popc(__ballot_sync(FULL_MASK, in)) > 32) weigh();
+        gather_candidate(c, in, 0u, e, count);
     }
+    weigh();
     const double value = b1 + (a.best == 2 && b2 > -INFINITY ? b2 : 0.0);
     int before = 0;
     for (int h = 0; h < a.groups; ++h) {
-        const double o = __shfl_sync(FULL_MASK, value, h * P);
-        before += o > value || (o == value && h < g);
+        const double o = __shfl_sync(FULL_MASK, value, h << a.shift);
+        before += (opens >> (h << a.shift) & 1u) && (o > value || (o == value && h < g));
     }
-    return __ballot_sync(FULL_MASK, g < a.groups && value > -INFINITY && before < a.top_groups && lane % P == 0);
+    return open ? before < places : q.taken;
 }
 
 // The next of the row in the order of the real c, among those not yet taken
 // (key > kKeyNegInf): the largest in f32, unless others lie within the bound
 // `err` of it that are not its equals.
-template <By BY, int V>
+template <By BY, int V, bool NEAR>
 __device__ __noinline__ int next_in_doubt(const uint32_t (&key)[V], const Row r, float top, float err, double inv64)
 {
-    const int lane = threadIdx.x & 31;
     double best = -INFINITY;
     int be = 0x7fffffff;
 #pragma unroll 1
-    for (int e = lane; e < r.n; e += 32) {
+    for (int j = 0; j < V; ++j) {
+        const int e = expert_at<V, NEAR>(j);
         uint32_t mine = 0u;
 #pragma unroll
         for (int i = 0; i < V; ++i)
-            if (i == e / 32) mine = key[i];
+            if (i == j) mine = key[i];
         if (mine <= kKeyNegInf || value_of_key(mine) < top - 2.f * err) continue;
         const double c = choice64<BY>(r, e, inv64);
         if (c > best) {
@@ -224,7 +268,7 @@ __device__ __noinline__ int next_in_doubt(const uint32_t (&key)[V], const Row r,
 // k rounds over the row by c, for rows that the filter leaves with more than a
 // warp's candidates, and for k > FILTER_K.  Lane l ends with ranks l and l + 32
 // (-1: none left).
-template <By BY, int V>
+template <By BY, int V, bool NEAR>
 __device__ __forceinline__ void choose_by_rounds(uint32_t (&key)[V], const Row &r, int k, float err, int &ea, int &eb)
 {
     const int lane = threadIdx.x & 31;
@@ -242,23 +286,23 @@ __device__ __forceinline__ void choose_by_rounds(uint32_t (&key)[V], const Row &
         const uint32_t top = __reduce_max_sync(FULL_MASK, best);
         if (top <= kKeyNegInf) return;
         int e = static_cast<int>(
-            __reduce_min_sync(FULL_MASK, best == top ? static_cast<unsigned>(bi * 32 + lane) : 0xFFFFFFFFu));
+            __reduce_min_sync(FULL_MASK, best == top ? static_cast<unsigned>(expert_at<V, NEAR>(bi)) : 0xFFFFFFFFu));
         const float ct = value_of_key(top), lt = r.l[e], bt = r.b ? r.b[e] : 0.f;
         bool doubt = false;
 #pragma unroll
         for (int i = 0; i < V; ++i) {
-            const int o = i * 32 + lane;
+            const int o = expert_at<V, NEAR>(i);
             if (key[i] > kKeyNegInf && o != e && value_of_key(key[i]) >= ct - 2.f * err)
                 doubt |= r.l[o] != lt || (r.b && r.b[o] != bt);
         }
         if (__any_sync(FULL_MASK, doubt)) {
             if (!summed) inv64 = inverse_sum64<BY>(r);
             summed = true;
-            e = next_in_doubt<BY, V>(key, r, ct, err, inv64);
+            e = next_in_doubt<BY, V, NEAR>(key, r, ct, err, inv64);
         }
 #pragma unroll
         for (int i = 0; i < V; ++i)
-            if (e == i * 32 + lane) key[i] = 0u;
+            if (e == expert_at<V, NEAR>(i)) key[i] = 0u;
         if (q == lane) ea = e;
         if (q == lane + 32) eb = e;
     }
@@ -295,29 +339,46 @@ __device__ __forceinline__ void write_weights(const RouteArgs &a, const Row &r, 
     }
 }
 
-// One warp per row, n <= 32 V: expert i 32 + lane.  Bound by instruction issue.
-template <By BY, int V>
-__global__ void __launch_bounds__(ROUTE_WARPS * 32) route_rows_warp(const RouteArgs a)
+// A row's values (which: expert_at); fill: past the last.
+template <int V, bool NEAR>
+__device__ __forceinline__ void load_row(const float *p, int n, bool wide, float fill, float (&v)[V])
 {
-    __shared__ float rows[ROUTE_WARPS][32 * V];
-    __shared__ __align__(16) Candidates cands[ROUTE_WARPS];
-    __shared__ float sorted[ROUTE_WARPS][32];
-    const int wi = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int t = blockIdx.x * ROUTE_WARPS + wi;
-    pdl_launch_dependents();
-    pdl_wait();
-    if (t >= a.T) return;
+    if (NEAR && wide) {
+#pragma unroll
+        for (int i = 0; i < V; i += 4) {
+            const float4 u = *reinterpret_cast<const float4 *>(p + expert_at<V, NEAR>(i));
+            v[i] = u.x, v[i + 1] = u.y, v[i + 2] = u.z, v[i + 3] = u.w;
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+            const int e = expert_at<V, NEAR>(i);
+            v[i] = NEAR || e < n ? p[e] : fill;
+        }
+    }
+}
+
+// What a warp has in shared memory.
+template <int V, bool NEAR>
+struct WarpRoom {
+    alignas(16) Candidates cands;
+    float sorted[32];
+    float row[NEAR ? 1 : 32 * V];
+};
+
+// One row: its logits and the biases of this lane's experts.
+template <By BY, int V, bool NEAR>
+__device__ __forceinline__ void route_row(const RouteArgs &a, int t, const float (&l)[V], const float (&b)[V],
+                                          WarpRoom<V, NEAR> &room)
+{
+    const int lane = threadIdx.x & 31;
     Row r = {a.logits + static_cast<size_t>(t) * a.ld, a.bias, 0.f, 0.f, a.n, V};
     int *idx = a.idx + static_cast<size_t>(t) * a.k;
     float *w = a.w + static_cast<size_t>(t) * a.k;
-    float l[V], b[V];
     bool bad = false;
     float top = -INFINITY;
 #pragma unroll
     for (int i = 0; i < V; ++i) {
-        const int e = i * 32 + lane;
-        l[i] = e < a.n ? r.l[e] : -INFINITY;
-        b[i] = a.bias && e < a.n ? a.bias[e] : 0.f;
         bad |= l[i] != l[i];
         top = fmaxf(top, l[i]);
     }
@@ -333,23 +394,19 @@ __global__ void __launch_bounds__(ROUTE_WARPS * 32) route_rows_warp(const RouteA
             r.inv = 1.f;  // weights that are renormalised need no sum
         }
     }
-    // the keys of what the choice goes by; off: kKeyNegInf
-    uint32_t key[V];
+    // what the choice goes by; off: -inf
+    float v[V];
     float err = 0.f;
 #pragma unroll
     for (int i = 0; i < V; ++i) {
-        const int e = i * 32 + lane;
-        key[i] = e < a.n ? kKeyNegInf : 0u;
-        if (BY == By::Logit) {
-            if (l[i] != -INFINITY && b[i] != -INFINITY) key[i] = value_key(l[i]);
-        } else {
+        v[i] = l[i];
+        if (BY != By::Logit) {
             float d;
             const float c = choice<BY>(r, l[i], b[i], d);
-            if (l[i] != -INFINITY && b[i] != -INFINITY) {
-                key[i] = value_key(c);
-                err = fmaxf(err, d);
-                bad |= !(c < INFINITY);  // a bias that is no number
-            }
+            const bool on = l[i] != -INFINITY && b[i] != -INFINITY;
+            v[i] = on ? c : -INFINITY;
+            err = fmaxf(err, on ? d : 0.f);
+            bad |= on && !(c < INFINITY);  // a bias that is no number
         }
     }
     if (__any_sync(FULL_MASK, bad)) {
@@ -362,36 +419,48 @@ __global__ void __launch_bounds__(ROUTE_WARPS * 32) route_rows_warp(const RouteA
     }
     if (BY != By::Logit) err = warp_max_positive(err);
 
-    if (a.groups > 1) {
-        float *c = rows[wi];
-        const int P = lanes_of_group(a.groups), g = lane / P;
+    if (NEAR || a.groups > 1) {
+        const int P = 1 << a.shift, g = lane >> a.shift;
         float b1 = -INFINITY, b2 = -INFINITY;
+        if (NEAR) {
 #pragma unroll
-        for (int i = 0; i < V; ++i)
-            if (i * 32 + lane < a.n) c[i * 32 + lane] = value_of_key(key[i]);
-        __syncwarp();
-        if (g < a.groups)
-            for (int e = g * a.size + lane % P; e < (g + 1) * a.size; e += P) {
-                const float v = c[e];
-                b2 = fmaxf(b2, fminf(b1, v));
-                b1 = fmaxf(b1, v);
+            for (int i = 0; i < V; ++i) {
+                b2 = fmaxf(b2, fminf(b1, v[i]));
+                b1 = fmaxf(b1, v[i]);
             }
+        } else {
+            float *c = room.row;
+#pragma unroll
+            for (int i = 0; i < V; ++i)
+                if (i * 32 + lane < a.n) c[i * 32 + lane] = v[i];
+            __syncwarp();
+            if (g < a.groups)
+                for (int e = g * a.size + (lane & (P - 1)); e < (g + 1) * a.size; e += P) {
+                    b2 = fmaxf(b2, fminf(b1, c[e]));
+                    b1 = fmaxf(b1, c[e]);
+                }
+        }
         for (int off = P >> 1; off > 0; off >>= 1) {
             const float o1 = __shfl_xor_sync(FULL_MASK, b1, off), o2 = __shfl_xor_sync(FULL_MASK, b2, off);
             b2 = fmaxf(fminf(b1, o1), fmaxf(b2, o2));
             b1 = fmaxf(b1, o1);
         }
-        const float value = b1 + (a.best == 2 && b2 > -INFINITY ? b2 : 0.f);
-        bool doubt;
-        uint32_t taken = take_groups(value, BY == By::Logit ? 0.f : fmaf(fabsf(value), 0x1p-23f, 2.f * err), P, a, doubt);
-        if (BY != By::Logit && doubt && !all_alike(r)) taken = take_groups64<BY>(r, a, P);
+        const bool two = a.best == 2 && b2 > -INFINITY;
+        const float value = b1 + (two ? b2 : 0.f);
+        Groups q = {value, BY == By::Logit ? 0.f : fmaf(fabsf(value), 0x1p-23f, 2.f * err)};
+        take_groups(q, a);
+        if (BY != By::Logit && q.high >= q.low && !all_alike(r))
+            q.taken = take_groups64<BY, V, NEAR>(r, a, q, v, two ? b2 : b1, err, room.cands);
+        const uint32_t taken = NEAR ? 0u : __ballot_sync(FULL_MASK, q.taken);
 #pragma unroll
         for (int i = 0; i < V; ++i) {
-            const int e = i * 32 + lane;
-            const int of = static_cast<int>((static_cast<unsigned>(e) * a.magic) >> 20);
-            if (e < a.n && !(taken >> (of * P) & 1u)) key[i] = kKeyNegInf;
+            const int of = static_cast<int>((static_cast<unsigned>(i * 32 + lane) * a.magic) >> 20) << a.shift;
+            if (NEAR ? !q.taken : i * 32 + lane < a.n && !(taken >> of & 1u)) v[i] = -INFINITY;
         }
     }
+    uint32_t key[V];
+#pragma unroll
+    for (int i = 0; i < V; ++i) key[i] = NEAR || i * 32 + lane < a.n ? number_key(v[i]) : 0u;
 
     if (a.k <= FILTER_K) {
         uint32_t most = key[0], first;
@@ -405,12 +474,35 @@ __global__ void __launch_bounds__(ROUTE_WARPS * 32) route_rows_warp(const RouteA
         // what may be among the k best: within the bounds of the bound
         if (BY != By::Logit && bound > kKeyNegInf) bound = value_key(value_of_key(bound) - 2.f * err);
         bound = max(bound, kKeyNegInf + 1u);
-        Candidates &c = cands[wi];
+        Candidates &c = room.cands;
         c.key[lane] = 0u;
         __syncwarp();
         int count = 0;
+        if (NEAR) {  // in expert order: after those of the lanes before
 #pragma unroll
-        for (int i = 0; i < V; ++i) gather_candidate(c, key[i] >= bound, key[i], i * 32 + lane, count);
+            for (int i = 0; i < V; ++i) count += key[i] >= bound;
+            int at = count;
+#pragma unroll
+            for (int off = 1; off < 32; off <<= 1) {
+                const int o = __shfl_up_sync(FULL_MASK, at, off);
+                if (lane >= off) at += o;
+            }
+            const int all = __shfl_sync(FULL_MASK, at, 31);
+            at -= count;
+#pragma unroll
+            for (int i = 0; i < V; ++i)
+                if (key[i] >= bound) {
+                    if (at < 32) {
+                        c.key[at] = key[i];
+                        c.expert[at] = static_cast<uint16_t>(lane * V + i);
+                    }
+                    ++at;
+                }
+            count = all;
+        } else {
+#pragma unroll
+            for (int i = 0; i < V; ++i) gather_candidate(c, key[i] >= bound, key[i], i * 32 + lane, count);
+        }
         __syncwarp();
         if (count <= 32) {
             const int e = lane < count ? c.expert[lane] : -1;
@@ -418,16 +510,21 @@ __global__ void __launch_bounds__(ROUTE_WARPS * 32) route_rows_warp(const RouteA
             // the larger ones, and of the equal ones those before it (in expert order)
             int rank = 0;
             for (int o = 0; o < count; o += 4) {
-                const uint4 v = *reinterpret_cast<const uint4 *>(&c.key[o]);
-                rank += v.x >= mine + (o >= lane ? 1u : 0u);
-                rank += v.y >= mine + (o + 1 >= lane ? 1u : 0u);
-                rank += v.z >= mine + (o + 2 >= lane ? 1u : 0u);
-                rank += v.w >= mine + (o + 3 >= lane ? 1u : 0u);
+                const uint4 u = *reinterpret_cast<const uint4 *>(&c.key[o]);
+                if (BY == By::Logit) {
+                    rank += u.x >= mine + (o >= lane ? 1u : 0u);
+                    rank += u.y >= mine + (o + 1 >= lane ? 1u : 0u);
+                    rank += u.z >= mine + (o + 2 >= lane ? 1u : 0u);
+                    rank += u.w >= mine + (o + 3 >= lane ? 1u : 0u);
+                } else {  // (equal ones are in doubt, below)
+                    rank += (u.x > mine) + (u.y > mine) + (u.z > mine) + (u.w > mine);
+                }
             }
             if (BY != By::Logit) {
-                // one bound for all: two that it does not separate make neighbours that it does not
-                float *by_rank = sorted[wi];
-                by_rank[lane] = -INFINITY;
+                // One bound for all: two that it does not separate make neighbours that it does
+                // not.  Equal ones leave the ranks after the first empty (infinite).
+                float *by_rank = room.sorted;
+                by_rank[lane] = INFINITY;
                 __syncwarp();
                 if (lane < count) by_rank[rank] = value_of_key(mine);
                 __syncwarp();
@@ -449,8 +546,29 @@ __global__ void __launch_bounds__(ROUTE_WARPS * 32) route_rows_warp(const RouteA
         }
     }
     int ea = -1, eb = -1;
-    choose_by_rounds<BY, V>(key, r, a.k, err, ea, eb);
+    choose_by_rounds<BY, V, NEAR>(key, r, a.k, err, ea, eb);
     write_weights(a, r, ea, eb, lane, lane + 32, idx, w);
+}
+
+// A warp per row, n <= 32 V; NEAR: n == 32 V, in groups of whole lanes.  Bound by
+// instruction issue and the gaps that 30 warps an SM leave: 32,768 rows of 128 experts in
+// 8 groups of which 4 stay, k = 8 24.6 us (8 warps a CTA 27; 690 instructions a row),
+// where reading and writing takes 2.8; CTAs that walk the rows, the next one's logits
+// loaded ahead, 29 us: the registers cost the warps that would have filled the gaps.
+template <By BY, int V, bool NEAR>
+__global__ void __launch_bounds__(ROW_WARPS * 32) route_rows_warp(const RouteArgs a)
+{
+    __shared__ WarpRoom<V, NEAR> rooms[ROW_WARPS];
+    const int wi = threadIdx.x >> 5, t = blockIdx.x * ROW_WARPS + wi;
+    pdl_launch_dependents();
+    pdl_wait();
+    if (t >= a.T) return;
+    float l[V], b[V];
+#pragma unroll
+    for (int i = 0; i < V; ++i) b[i] = 0.f;
+    load_row<V, NEAR>(a.logits + static_cast<size_t>(t) * a.ld, a.n, a.wide, -INFINITY, l);
+    if (a.bias) load_row<V, NEAR>(a.bias, a.n, a.wide, 0.f, b);
+    route_row<BY, V, NEAR>(a, t, l, b, rooms[wi]);
 }
 
 // ---------------------------------------------------------------- gradient
@@ -473,12 +591,12 @@ struct RouteGradArgs {
 // A warp per row, which makes the row in shared memory and writes it once.  Bound
 // by writing the gradients (and, for the last form, reading the logits).
 template <int V, bool WIDE>  // WIDE: k > 32, lane l holds the slots l and l + 32
-__global__ void __launch_bounds__(ROUTE_WARPS * 32) route_rows_grad(const RouteGradArgs a)
+__global__ void __launch_bounds__(GRAD_WARPS * 32) route_rows_grad(const RouteGradArgs a)
 {
     constexpr int H = WIDE ? 2 : 1;
-    __shared__ float rows[ROUTE_WARPS][32 * V];
+    __shared__ float rows[GRAD_WARPS][32 * V];
     const int wi = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int t = blockIdx.x * ROUTE_WARPS + wi;
+    const int t = blockIdx.x * GRAD_WARPS + wi;
     pdl_launch_dependents();
     pdl_wait();
     if (t >= a.T) return;
@@ -562,21 +680,39 @@ __global__ void __launch_bounds__(ROUTE_WARPS * 32) route_rows_grad(const RouteG
 template <bool WIDE>
 cudaError_t grad_wide(const RouteGradArgs &a, cudaStream_t stream)
 {
-    const dim3 grid(static_cast<unsigned>((a.T + ROUTE_WARPS - 1) / ROUTE_WARPS)), block(ROUTE_WARPS * 32);
+    const dim3 grid(static_cast<unsigned>((a.T + GRAD_WARPS - 1) / GRAD_WARPS)), block(GRAD_WARPS * 32);
     if (a.n <= 128) return launch_pdl(route_rows_grad<4, WIDE>, grid, block, 0, stream, a);
     if (a.n <= 256) return launch_pdl(route_rows_grad<8, WIDE>, grid, block, 0, stream, a);
     if (a.n <= 512) return launch_pdl(route_rows_grad<16, WIDE>, grid, block, 0, stream, a);
     return launch_pdl(route_rows_grad<32, WIDE>, grid, block, 0, stream, a);
 }
 
-template <By BY>
-cudaError_t route_by(const RouteArgs &a, cudaStream_t stream)
+template <By BY, int V>
+cudaError_t route_wide(const RouteArgs &a, bool near, cudaStream_t stream)
 {
-    const dim3 grid(static_cast<unsigned>((a.T + ROUTE_WARPS - 1) / ROUTE_WARPS)), block(ROUTE_WARPS * 32);
-    if (a.n <= 128) return launch_pdl(route_rows_warp<BY, 4>, grid, block, 0, stream, a);
-    if (a.n <= 256) return launch_pdl(route_rows_warp<BY, 8>, grid, block, 0, stream, a);
-    if (a.n <= 512) return launch_pdl(route_rows_warp<BY, 16>, grid, block, 0, stream, a);
-    return launch_pdl(route_rows_warp<BY, 32>, grid, block, 0, stream, a);
+    const dim3 grid(static_cast<unsigned>((a.T + ROW_WARPS - 1) / ROW_WARPS)), block(ROW_WARPS * 32);
+    return near ? launch_pdl(route_rows_warp<BY, V, true>, grid, block, 0, stream, a)
+                : launch_pdl(route_rows_warp<BY, V, false>, grid, block, 0, stream, a);
+}
+
+template <By BY>
+cudaError_t route_by(RouteArgs a, cudaStream_t stream)
+{
+    const int V = a.n <= 128 ? 4 : a.n <= 256 ? 8 : a.n <= 512 ? 16 : 32;
+    // Neighbours to a lane where groups are whole lanes and those that stay fill twice k
+    // lanes (with fewer, too many of their experts would be candidates), or leave a warp
+    // no more than its 32.  Against every 32nd, in us: 32,768 rows of 128 experts, 4 of 8
+    // groups stay, k = 8 27.4 / 31.7; k = 16 (which this leaves out) 69 / 38; 3 stay, k = 16
+    // 81 / 39; 512 experts, k = 8 66 / 80.
+    const int stay = a.top_groups * a.size;
+    const bool near = a.groups > 1 && a.n == 32 * V && a.size % V == 0 && (a.size / V & (a.size / V - 1)) == 0 &&
+                      (stay >= 2 * a.k * V || stay <= 32);
+    int lanes = near ? a.size / V : 32 / a.groups;  // the largest power of two that leaves every group its lanes
+    for (a.shift = 0; lanes > 1; lanes /= 2) ++a.shift;
+    if (V == 4) return route_wide<BY, 4>(a, near, stream);
+    if (V == 8) return route_wide<BY, 8>(a, near, stream);
+    if (V == 16) return route_wide<BY, 16>(a, near, stream);
+    return route_wide<BY, 32>(a, near, stream);
 }
 
 }  // namespace
@@ -587,8 +723,9 @@ cudaError_t launch_route_rows(const float *logits, int T, int n, int ld, const f
 {
     const int size = n / groups;
     if (groups > 1 && top_groups >= groups) groups = top_groups = 1;  // all of them
-    const RouteArgs a = {logits, bias, idx, w, T, n, ld, k, groups, top_groups, best, size,
-                         static_cast<unsigned>(((1 << 20) + size - 1) / size), scale, softmax, norm};
+    const RouteArgs a = {logits, bias, idx, w, T, n, ld, k, groups, top_groups, best, size, 0,
+                         static_cast<unsigned>(((1 << 20) + size - 1) / size), scale, softmax, norm,
+                         ld % 4 == 0 && reinterpret_cast<uintptr_t>(logits) % 16 == 0 && reinterpret_cast<uintptr_t>(bias) % 16 == 0};
     if (!bias && (groups == 1 || best == 1)) return route_by<By::Logit>(a, stream);
     return softmax ? route_by<By::Softmax>(a, stream) : route_by<By::Sigmoid>(a, stream);
 }

@@ -94,6 +94,30 @@ def test_choices_that_f32_cannot_tell_apart(env, softmax):
 
 
 @pytest.mark.parametrize("softmax", [True, False])
+@pytest.mark.parametrize("n,G,tg,k", [(128, 8, 4, 8), (128, 8, 4, 16), (128, 32, 9, 8), (96, 8, 3, 5), (120, 5, 2, 8), (256, 16, 5, 8),
+                                      (512, 8, 3, 7), (512, 8, 2, 16), (1024, 4, 2, 8), (1024, 32, 7, 20)])
+def test_borders_between_groups_that_f32_cannot_tell(env, softmax, n, G, tg, k):
+    """Groups that lead, groups that trail, and three at the border whose sums of two
+    are some 2^-24 apart; and every group of a row at the border."""
+    rng = np.random.default_rng([n, G, k])
+    T, size = 200, n // G
+    lead = np.argsort(rng.random((T, G)), axis=1)
+    level = np.where(lead < tg - 2, 2.0, np.where(lead < tg + 1, 1.0, -1.0))  # three for two places
+    l = np.repeat(level, size, axis=1) - 3 * rng.random((T, n))
+    border = np.repeat((lead >= tg - 2) & (lead < tg + 1), size, axis=1)
+    best = rng.random((T, G, size)).argsort(2).argsort(2).reshape(T, n) < min(3, size)  # three of each group near its top
+    l = np.where(best & border, 1 + rng.integers(-3, 4, size=(T, n)) * 2.0 ** -23, l).astype(np.float32)
+    b = (rng.integers(-2, 3, size=n) * 2.0 ** -26).astype(np.float32)
+    for ld in (None, n + 1):
+        check(env, l, b, softmax, G, tg, 2, k, True, ld=ld)
+        check(env, l, b, softmax, G, tg, 1, k, True, ld=ld)
+    l[l < 0.9] = -np.inf  # a group of less than two, and of none
+    check(env, l, b, softmax, G, tg, 2, k, True)
+    l = (1 + rng.integers(-3, 4, size=(T, n)) * 2.0 ** -23).astype(np.float32)
+    check(env, l, b, softmax, G, tg, 2, k, True)
+
+
+@pytest.mark.parametrize("softmax", [True, False])
 @pytest.mark.parametrize("G,tg,best", [(1, 1, 1), (8, 4, 2)])
 def test_equal_scores_go_to_the_lowest_expert(env, softmax, G, tg, best):
     n = 96 if G == 1 else 128
