@@ -7,7 +7,7 @@ namespace smoe {
 
 constexpr int F8_BLOCK = 128;  // columns (and weight rows) of one scale
 
-// The product by pairs of CTAs in row tiles of 256 (f8_pair.cu), from the tile list.
-cudaError_t launch_f8_pair(const F8Call &c, const int *ntiles, const Tile *tiles, int max_tiles, cudaStream_t stream);
+// The product in row tiles of 128 (f8_rows.cu), from the tile list.
+cudaError_t launch_f8_rows(const F8Call &c, const int *ntiles, const Tile *tiles, int max_tiles, cudaStream_t stream);
 
 }  // namespace smoe

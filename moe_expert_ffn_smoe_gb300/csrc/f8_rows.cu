@@ -1,6 +1,6 @@
-// The 8-bit floating-point product with a scale for each block of 128 on pairs of
-// CTAs, for batches that are bound by the tensor cores (tcgen05, kind::f8f6f4, e4m3
-// operands from shared memory):
+// The 8-bit floating-point product with a scale for each block of 128, with the rows on
+// the MMA's M side, for batches that are bound by the tensor cores (tcgen05,
+// kind::f8f6f4, e4m3 operands from shared memory):
 //   y[r][n] = sum_b xs[r][b] ws[e][n / 128][b] sum_{c in b} xq[r][c] wq[e][n][c].
 //
 // The scales change every 128 columns, inside the sum, so each block's products are a
@@ -9,17 +9,25 @@
 // scales, while the next block's MMAs run.  The sums of blocks are f32 in registers; a
 // block's own is the tensor core's f32.
 //
-// The rows are the MMA's M side, 128 of them a CTA, the weights its N side, 256 a
-// pair: a thread of the epilogue then holds 128 outputs of one row and of one block of
-// weights, whose scale is one number.  With the weights on the M side (as f8_tc.cu has
-// them, whose tiles are small) a tile costs its rows only, but every product needs the
-// scale of its own column: brought from shared memory beside the MMAs, a block took
-// 1150 clocks against the 512 of its MMAs (1999 rows x 8192 x 4096 88 us).  Here a
-// tile of fewer than 256 rows costs as much as a full one.
+// The rows are the MMA's M side, 128 of them, the weights its N side, 256: a thread of
+// the epilogue then holds 128 outputs of one row and of one block of weights, whose
+// scale is one number.  With the weights on the M side (as f8_tc.cu has them, whose
+// tiles are small) a tile costs its rows only, but every product needs the scale of its
+// own column: brought from shared memory beside the MMAs, a block took 1150 clocks
+// against the 512 of its MMAs (1999 rows x 8192 x 4096 88 us).  Here a tile of fewer
+// than 128 rows costs as much as a full one.
 //
-// Persistent: pairs walk the items (tile of rows, 256 weights).  Roles (warps): 0-7
-// epilogue, 8 issues the MMAs (the even CTA's), 9 streams the weights, 12-19 the rows,
-// gathered by the copies where the batch is sorted by an order.  Every wait is bounded.
+// Bound by handing the accumulators over: a block takes 1150 clocks, of which its MMAs
+// are 512, the way to the epilogue and back some 750, reading and adding 450 (1999 rows
+// x 8192 x 4096 74 us, 1.8 PFLOP/s; with an epilogue that reads nothing 66).  Pairs of
+// CTAs on 256 rows need two thirds of the copies and took 73 us there, but cost 256 rows
+// a tile: through 128 experts, 2047 tokens of 8 221 us against 192, 4096 tokens 307
+// against 291.  Accumulators in halves, barriers tested ahead, 16 epilogue warps and
+// spinning waits were no faster.
+//
+// Persistent: CTAs walk the items (tile of rows, 256 weights).  Roles (warps): 0-7
+// epilogue, 8 issues the MMAs, 9 streams the weights, 12-19 the rows, gathered by the
+// copies where the batch is sorted by an order.  Every wait is bounded.
 #include <atomic>
 
 #include "f8.cuh"
@@ -29,16 +37,15 @@
 namespace smoe {
 namespace {
 
-constexpr int MT = 128, NT = 256;            // a CTA's rows of a tile, the pair's weights
-constexpr uint32_t OP_BYTES = 128 * F8_BLOCK;  // a CTA's 128 rows, or 128 weights, of a block of columns
-constexpr int ST = 6, D = 2;                 // stages of the operands, accumulators
+constexpr int MT = 128, NT = 256;            // rows, weights of a tile
+constexpr uint32_t X_BYTES = MT * F8_BLOCK, W_BYTES = NT * F8_BLOCK;  // a block of columns of them
+constexpr int ST = 4, D = 2;                 // stages of the operands, accumulators
 constexpr int EPI_WARPS = 8, MMA_WARP = 8, W_WARP = 9, X_WARP = 12, X_WARPS = 8;
-constexpr int PAIR_THREADS = (X_WARP + X_WARPS) * 32;
+constexpr int ROWS_THREADS = (X_WARP + X_WARPS) * 32;
 constexpr int BOX = 64;                      // rows of one copy (not gathered)
-constexpr int GATHERS = MT / 4 / X_WARPS;    // of a loading warp and stage, at most
-constexpr size_t PAIR_SMEM = 1024 + ST * 2 * OP_BYTES + 256;
+constexpr size_t ROWS_SMEM = 1024 + ST * (X_BYTES + W_BYTES) + MT * 4 + 256;
 
-struct alignas(128) PairArgs {
+struct alignas(128) RowsArgs {
     CUtensorMap wmap, xmap;
     const float *ws, *xs;  // scales [n x nb x kb], [nsrc x kb]
     void *y;
@@ -50,13 +57,13 @@ struct alignas(128) PairArgs {
 };
 
 // Instruction descriptor, kind::f8f6f4: f32 accumulate, A and B e4m3, K-major.
-constexpr uint32_t kIdesc = (1u << 4) | (static_cast<uint32_t>(NT >> 3) << 17) | (static_cast<uint32_t>(2 * MT >> 4) << 24);
+constexpr uint32_t kIdesc = (1u << 4) | (static_cast<uint32_t>(NT >> 3) << 17) | (static_cast<uint32_t>(MT >> 4) << 24);
 
-__device__ __forceinline__ void mma_f8_pair(uint32_t tmem, uint64_t a, uint64_t b, uint32_t acc)
+__device__ __forceinline__ void mma_f8(uint32_t tmem, uint64_t a, uint64_t b, uint32_t acc)
 {
     asm volatile(
         "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::2.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(tmem),
+        "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(tmem),
         "l"(a), "l"(b), "r"(kIdesc), "r"(acc)
         : "memory");
 }
@@ -118,45 +125,40 @@ __device__ __forceinline__ void store32(__nv_bfloat16 *y, const float2 (&v)[16],
     }
 }
 
-__device__ __forceinline__ Tile tile_at(const PairArgs &a, int i, int ntiles)
+__device__ __forceinline__ Tile tile_at(const RowsArgs &a, int i, int ntiles)
 {
     if (i >= ntiles) return Tile{0, 0, 0, 0};
     if (a.tiles) return a.tiles[i];
     return Tile{0, i * a.step, min(a.step, a.R - i * a.step), 0};
 }
 
-// A tile's rows are halved between the CTAs.
-__device__ __forceinline__ int share_of(const Tile &t) { return (t.rows + 1) / 2; }
-
 template <typename T>
-__global__ void __launch_bounds__(PAIR_THREADS, 1) f8_pair(const __grid_constant__ PairArgs a)
+__global__ void __launch_bounds__(ROWS_THREADS, 1) f8_rows(const __grid_constant__ RowsArgs a)
 {
     extern __shared__ uint8_t smem_raw[];
-    const uint32_t base = (smem_addr(smem_raw) + 1023u) & ~1023u;
-    const uint32_t w0 = base, x0 = w0 + ST * OP_BYTES, bars = x0 + ST * OP_BYTES;
+    const uint32_t raw = smem_addr(smem_raw), base = (raw + 1023u) & ~1023u;
+    const uint32_t w0 = base, x0 = w0 + ST * W_BYTES, list0 = x0 + ST * X_BYTES, bars = list0 + MT * 4;
     const uint32_t full = bars, empty = full + 8 * ST, dfull = empty + 8 * ST, dempty = dfull + 8 * D, tslot = dempty + 8 * D;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int rank = static_cast<int>(blockIdx.x & 1u);
-    const int first = static_cast<int>(blockIdx.x >> 1), stride = static_cast<int>(gridDim.x >> 1);
+    const int first = static_cast<int>(blockIdx.x), stride = static_cast<int>(gridDim.x);
 
     if (threadIdx.x == 0) {
         for (int i = 0; i < ST; ++i) {
-            mbar_init(full + 8 * i, 1 + (a.order ? X_WARPS : 1));  // the loading warps; used in the issuing CTA
+            mbar_init(full + 8 * i, 1 + (a.order ? X_WARPS : 1));  // the loading warps
             mbar_init(empty + 8 * i, 1);
         }
         for (int i = 0; i < D; ++i) {
             mbar_init(dfull + 8 * i, 1);
-            mbar_init(dempty + 8 * i, EPI_WARPS * 2);  // used in the issuing CTA
+            mbar_init(dempty + 8 * i, EPI_WARPS);
         }
         fence_mbar_init();
     }
     if (warp == MMA_WARP) {
-        asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(tslot) : "memory");
-        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(tslot) : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
     }
     tc_fence_before();
     __syncthreads();
-    cluster_sync();  // nothing may reach a CTA whose barriers are not there yet
     tc_fence_after();
     uint32_t tmem;
     asm volatile("ld.shared.u32 %0, [%1];" : "=r"(tmem) : "r"(tslot));
@@ -166,89 +168,72 @@ __global__ void __launch_bounds__(PAIR_THREADS, 1) f8_pair(const __grid_constant
     // the previous kernel ends.  A prefetch only: that kernel may be the one that
     // quantises these weights.
     if (!a.tiles && warp == W_WARP && first < (a.R + a.step - 1) / a.step * a.groups && lane < ST && lane < a.kb)
-        tma_prefetch_2d(&a.wmap, lane * F8_BLOCK, (first % a.groups * 2 + rank) * 128);
+        tma_prefetch_2d(&a.wmap, lane * F8_BLOCK, first % a.groups * NT);
     pdl_wait();
     const int ntiles = a.tiles ? *a.ntiles : (a.R + a.step - 1) / a.step;
     const long long nitems = static_cast<long long>(ntiles) * a.groups;
     bool failed = false;
 
     if (warp >= MMA_WARP) {
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 40;");
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 32;");
         if (warp == W_WARP) {
             if (elect_one()) {
-                const uint32_t lead = mapa_shared(full, 0);
                 uint32_t s = 0, p = 1;  // parity of the stage's release one lap ago; none in the first
                 bool round0 = true;
                 for (long long it = first; it < nitems && !failed; it += stride) {
                     const Tile t = tile_at(a, static_cast<int>(it / a.groups), ntiles);
-                    const int row = t.expert * a.N + (static_cast<int>(it % a.groups) * 2 + rank) * 128;
+                    const int row = t.expert * a.N + static_cast<int>(it % a.groups) * NT;
                     for (int c = 0; c < a.kb; ++c) {
                         if (!round0 && !mbar_wait_bounded(empty + 8 * s, p, a.status, 7u)) {
                             failed = true;
                             break;
                         }
-                        if (rank == 0) mbar_arrive_expect_tx(full + 8 * s, OP_BYTES * 2);
-                        tma_load_2d_pair(w0 + s * OP_BYTES, &a.wmap, c * F8_BLOCK, row, lead + 8 * s);
+                        mbar_arrive_expect_tx(full + 8 * s, W_BYTES);
+                        tma_load_2d(w0 + s * W_BYTES, &a.wmap, c * F8_BLOCK, row, full + 8 * s);
                         if (++s == ST) {
                             s = 0;
                             p ^= 1u;
                             round0 = false;
                         }
                     }
-                }
-                // The last releases of the stages arrive here from the other CTA's
-                // issue: they must have before this CTA may leave.
-                if (!failed) {
-                    const long long steps = first < nitems ? (nitems - first + stride - 1) / stride * a.kb : 0;
-                    for (long long g = steps > ST ? steps - ST : 0; g < steps; ++g)
-                        if (!mbar_wait_bounded(empty + 8 * static_cast<uint32_t>(g % ST), static_cast<uint32_t>(g / ST) & 1,
-                                               a.status, 8u))
-                            failed = true;
                 }
             }
             failed = __any_sync(FULL_MASK, failed);
         } else if (warp >= X_WARP && (a.order || warp == X_WARP)) {
             // Gathered: each of the eight warps loads every eighth four rows of every
-            // stage, its indices in registers (a gather costs its issuer some 100
-            // clocks).  The bytes of both CTAs complete on the issuing CTA's barrier, which
-            // alone expects them.
-            if (elect_one()) {
-                const int part = warp - X_WARP;
-                const uint32_t lead = mapa_shared(full, 0);
-                uint32_t s = 0, p = 1;
-                bool round0 = true;
-                for (long long it = first; it < nitems && !failed; it += stride) {
-                    const Tile t = tile_at(a, static_cast<int>(it / a.groups), ntiles);
-                    const int share = share_of(t), row0 = t.row0 + rank * share;
-                    int4 r[GATHERS];
-                    if (a.order) {  // rows past the tile's: any row, their outputs are not stored
-                        auto source = [&](int i) {
-                            return rank * share + i < t.rows ? max(source_row(a.order, a.k, a.nsrc, row0 + i, a.status), 0) : 0;
-                        };
-#pragma unroll
-                        for (int i = 0; i < GATHERS; ++i) {
-                            const int at = 4 * (X_WARPS * i + part);
-                            r[i] = at < share ? make_int4(source(at), source(at + 1), source(at + 2), source(at + 3)) : make_int4(0, 0, 0, 0);
-                        }
-                    }
-                    const int copies = a.order ? max(0, ((share + 3) / 4 - part + X_WARPS - 1) / X_WARPS) : (share + BOX - 1) / BOX;
-                    // (both CTAs' shares are one number of rows)
-                    const uint32_t bytes = static_cast<uint32_t>(copies * (a.order ? 4 : BOX)) * (F8_BLOCK * 2);
+            // stage (a gather costs its issuer some 100 clocks; four warps: 304 us against
+            // 291 for 4096 tokens through 128 experts).
+            const int part = warp - X_WARP;
+            constexpr int PER = MT / X_WARPS;  // rows of a loading warp, at most
+            int *list = reinterpret_cast<int *>(smem_raw + (list0 - raw)) + part * PER;
+            uint32_t s = 0, p = 1;
+            bool round0 = true;
+            for (long long it = first; it < nitems && !failed; it += stride) {
+                const Tile t = tile_at(a, static_cast<int>(it / a.groups), ntiles);
+                if (a.order) {  // rows past the tile's: any row, their outputs are not stored
+                    const int at = 4 * X_WARPS * (lane >> 2) + 4 * part + (lane & 3);
+                    __syncwarp();
+                    if (lane < PER) list[lane] = at < t.rows ? max(source_row(a.order, a.k, a.nsrc, t.row0 + at, a.status), 0) : 0;
+                    __syncwarp();
+                }
+                if (elect_one()) {
+                    const int copies = a.order ? max(0, ((t.rows + 3) / 4 - part + X_WARPS - 1) / X_WARPS) : (t.rows + BOX - 1) / BOX;
+                    const uint32_t bytes = static_cast<uint32_t>(copies * (a.order ? 4 : BOX)) * F8_BLOCK;
                     for (int c = 0; c < a.kb; ++c) {
                         if (!round0 && !mbar_wait_bounded(empty + 8 * s, p, a.status, 8u)) {
                             failed = true;
                             break;
                         }
-                        const uint32_t dst = x0 + s * OP_BYTES, bar = lead + 8 * s;
-                        if (rank == 0) mbar_arrive_expect_tx(full + 8 * s, bytes);
+                        const uint32_t dst = x0 + s * X_BYTES, bar = full + 8 * s;
+                        mbar_arrive_expect_tx(bar, bytes);
                         if (a.order) {
-#pragma unroll
-                            for (int i = 0; i < GATHERS; ++i)
-                                if (i < copies)
-                                    tma_gather4_pair(dst + static_cast<uint32_t>(4 * (X_WARPS * i + part)) * F8_BLOCK, &a.xmap, c * F8_BLOCK, r[i], bar);
+                            for (int i = 0; i < copies; ++i) {
+                                const int4 r = *reinterpret_cast<const int4 *>(list + 4 * i);
+                                tma_gather4(dst + static_cast<uint32_t>(4 * (X_WARPS * i + part)) * F8_BLOCK, &a.xmap, c * F8_BLOCK, r, bar);
+                            }
                         } else {
                             for (int b = 0; b < copies; ++b)
-                                tma_load_2d_pair(dst + static_cast<uint32_t>(b * BOX) * F8_BLOCK, &a.xmap, c * F8_BLOCK, row0 + b * BOX, bar);
+                                tma_load_2d(dst + static_cast<uint32_t>(b * BOX) * F8_BLOCK, &a.xmap, c * F8_BLOCK, t.row0 + b * BOX, bar);
                         }
                         if (++s == ST) {
                             s = 0;
@@ -257,11 +242,16 @@ __global__ void __launch_bounds__(PAIR_THREADS, 1) f8_pair(const __grid_constant
                         }
                     }
                 }
+                // the elected lane's place in the ring, to all
+                const uint32_t from = __ffs(__ballot_sync(FULL_MASK, elect_one())) - 1;
+                s = __shfl_sync(FULL_MASK, s, from);
+                p = __shfl_sync(FULL_MASK, p, from);
+                round0 = __shfl_sync(FULL_MASK, round0, from);
+                failed = __shfl_sync(FULL_MASK, failed, from);
             }
-            failed = __any_sync(FULL_MASK, failed);
         } else if (warp == MMA_WARP) {
             // one thread issues, the even CTA's
-            if (rank == 0 && elect_one()) {
+            if (elect_one()) {
                 uint32_t s = 0, p = 0, d = 0, pd = 1;
                 bool round0 = true;
                 for (long long it = first; it < nitems && !failed; it += stride) {
@@ -276,11 +266,11 @@ __global__ void __launch_bounds__(PAIR_THREADS, 1) f8_pair(const __grid_constant
                             break;
                         }
                         tc_fence_after();
-                        const uint64_t xd = desc_sw128(x0 + s * OP_BYTES), wd = desc_sw128(w0 + s * OP_BYTES);
+                        const uint64_t xd = desc_sw128(x0 + s * X_BYTES), wd = desc_sw128(w0 + s * W_BYTES);
 #pragma unroll
-                        for (int kk = 0; kk < F8_BLOCK / 32; ++kk) mma_f8_pair(tmem + d * NT, xd + kk * 2, wd + kk * 2, kk != 0);
-                        mma_commit_pair(dfull + 8 * d);
-                        mma_commit_pair(empty + 8 * s);
+                        for (int kk = 0; kk < F8_BLOCK / 32; ++kk) mma_f8(tmem + d * NT, xd + kk * 2, wd + kk * 2, kk != 0);
+                        mma_commit(dfull + 8 * d);
+                        mma_commit(empty + 8 * s);
                         if (++s == ST) {
                             s = 0;
                             p ^= 1u;
@@ -296,21 +286,20 @@ __global__ void __launch_bounds__(PAIR_THREADS, 1) f8_pair(const __grid_constant
             failed = __any_sync(FULL_MASK, failed);
         }
     } else {
-        asm volatile("setmaxnreg.inc.sync.aligned.u32 176;");
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 192;");
         // warp w: tensor-memory lanes 32 (w % 4) .. + 31 = rows of this CTA's share, the
-        // columns of weights 128 (w / 4) .. + 127 of the pair's
+        // columns of weights 128 (w / 4) .. + 127 of the tile's
         const int q = warp & 3, h = warp >> 2;
         const bool v4 = (a.kb & 3) == 0 && (reinterpret_cast<uintptr_t>(a.xs) & 15u) == 0;
         T *y = static_cast<T *>(a.y);
-        const uint32_t lead = mapa_shared(dempty, 0);
         const uint32_t mine = tmem + (static_cast<uint32_t>(q * 32) << 16) + static_cast<uint32_t>(h * 128);
         uint32_t d = 0, pd = 0;
         for (long long it = first; it < nitems && !failed; it += stride) {
             const Tile t = tile_at(a, static_cast<int>(it / a.groups), ntiles);
-            const int share = share_of(t), nblk = static_cast<int>(it % a.groups) * 2 + h;
-            const int r = rank * share + q * 32 + lane;  // of the tile
-            const bool some = q * 32 < share;
-            const int src = q * 32 + lane < share && r < t.rows ? source_row(a.order, a.k, a.nsrc, t.row0 + r, a.status) : -1;
+            const int nblk = static_cast<int>(it % a.groups) * 2 + h;
+            const int r = q * 32 + lane;  // of the tile
+            const bool some = q * 32 < t.rows;
+            const int src = r < t.rows ? source_row(a.order, a.k, a.nsrc, t.row0 + r, a.status) : -1;
             const float *xs = src >= 0 ? a.xs + static_cast<size_t>(src) * a.kb : nullptr;  // no source: a scale of 0
             const float *ws = a.ws + (static_cast<size_t>(t.expert) * a.nb + min(nblk, a.nb - 1)) * a.kb;
             auto scales4 = [&](int c) {  // the row's, of blocks c .. c + 3, c a multiple of 4
@@ -355,14 +344,14 @@ __global__ void __launch_bounds__(PAIR_THREADS, 1) f8_pair(const __grid_constant
                 }
                 tc_fence_before();
                 __syncwarp();
-                if (lane == 0) mbar_arrive_cluster(lead + 8 * d);
+                if (lane == 0) mbar_arrive(dempty + 8 * d);
                 if (++d == D) {
                     d = 0;
                     pd ^= 1u;
                 }
             }
             if (failed) break;
-            if (q * 32 + lane < share && r < t.rows) {
+            if (r < t.rows) {
                 const int n0 = nblk * 128;
                 T *row = y + static_cast<size_t>(t.row0 + r) * a.N + n0;
                 const bool whole = a.N % (16 / static_cast<int>(sizeof(T))) == 0;
@@ -379,57 +368,49 @@ __global__ void __launch_bounds__(PAIR_THREADS, 1) f8_pair(const __grid_constant
         while (clock64() - t0 < 2000000LL) __nanosleep(1000);
         __syncthreads();
     }
-    cluster_sync();  // no CTA leaves while the other's copies or releases may reach it
     if (warp == MMA_WARP) {
         tc_fence_after();
-        asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, 512;" ::"r"(tmem) : "memory");
+        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem) : "memory");
     }
 }
 
 template <typename T>
-cudaError_t launch_t(const PairArgs &a, long long most_items, int sms, cudaStream_t stream)
+cudaError_t launch_t(const RowsArgs &a, long long most_items, int sms, cudaStream_t stream)
 {
-    static_assert(PAIR_SMEM <= 227 * 1024, "shared memory of a CTA");
-    auto k = f8_pair<T>;
+    static_assert(ROWS_SMEM <= 227 * 1024, "shared memory of a CTA");
+    auto k = f8_rows<T>;
     // one size for every launch of this kernel: asked for once per device
     static std::atomic<bool> opted[64];
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
     if (!opted[dev].load(std::memory_order_relaxed)) {
-        const cudaError_t e = ensure_dynamic_smem(k, PAIR_SMEM);
+        const cudaError_t e = ensure_dynamic_smem(k, ROWS_SMEM);
         if (e != cudaSuccess) return e;
         opted[dev].store(true, std::memory_order_relaxed);
     }
-    long long pairs = sms / 2;
-    const int fit = clusters_held<f8_pair<T>>(2, PAIR_THREADS, PAIR_SMEM);
-    if (fit > 0 && fit < pairs) pairs = fit;
-    if (most_items < pairs) pairs = most_items;
+    const long long ctas = most_items < sms ? most_items : sms;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(static_cast<unsigned>(2 * pairs));
-    cfg.blockDim = dim3(PAIR_THREADS);
-    cfg.dynamicSmemBytes = PAIR_SMEM;
+    cfg.gridDim = dim3(static_cast<unsigned>(ctas));
+    cfg.blockDim = dim3(ROWS_THREADS);
+    cfg.dynamicSmemBytes = ROWS_SMEM;
     cfg.stream = stream;
-    cudaLaunchAttribute attr[2];
+    cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
-    attr[1].id = cudaLaunchAttributeClusterDimension;
-    attr[1].val.clusterDim.x = 2;
-    attr[1].val.clusterDim.y = 1;
-    attr[1].val.clusterDim.z = 1;
     cfg.attrs = attr;
-    cfg.numAttrs = 2;
+    cfg.numAttrs = 1;
     return cudaLaunchKernelEx(&cfg, k, a);
 }
 
 }  // namespace
 
-cudaError_t launch_f8_pair(const F8Call &c, const int *ntiles, const Tile *tiles, int max_tiles, cudaStream_t stream)
+cudaError_t launch_f8_rows(const F8Call &c, const int *ntiles, const Tile *tiles, int max_tiles, cudaStream_t stream)
 {
     const DeviceInfo *dev = device_info();
     unsigned *status = device_status_word();
     if (!dev || !status) return cudaErrorInvalidDevice;
-    PairArgs a = {};
-    if (!encode(&a.wmap, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, c.wq, c.K, static_cast<long long>(c.n) * c.N, F8_BLOCK, 128) ||
+    RowsArgs a = {};
+    if (!encode(&a.wmap, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, c.wq, c.K, static_cast<long long>(c.n) * c.N, F8_BLOCK, NT) ||
         !encode(&a.xmap, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, c.xq, c.K, c.nsrc, F8_BLOCK, c.order ? 1 : BOX))
         return cudaErrorInvalidValue;
     a.ws = c.ws;
@@ -446,8 +427,8 @@ cudaError_t launch_f8_pair(const F8Call &c, const int *ntiles, const Tile *tiles
     a.k = c.k;
     a.nsrc = c.nsrc;
     a.groups = (c.N + NT - 1) / NT;
-    const int nd = (c.R + 2 * MT - 1) / (2 * MT);  // equal tiles: an item costs a full one whatever its rows
-    a.step = ((c.R + nd - 1) / nd + 1) & ~1;
+    const int nd = (c.R + MT - 1) / MT;  // equal tiles: an item costs a full one whatever its rows
+    a.step = (c.R + nd - 1) / nd;
     const long long most = static_cast<long long>(c.offsets ? max_tiles : nd) * a.groups;
     return c.dtype == SMOE_BF16 ? launch_t<__nv_bfloat16>(a, most, dev->sm_count, stream) : launch_t<float>(a, most, dev->sm_count, stream);
 }

@@ -2,7 +2,7 @@
 // for batches that are bound by reading the weights (tcgen05, kind::f8f6f4, e4m3
 // operands from shared memory):
 //   y[r][n] = sum_b xs[r][b] ws[e][n / 128][b] sum_{c in b} xq[r][c] wq[e][n][c].
-// Larger batches go on to f8_pair.cu, after the tile list that is made here.
+// Larger batches go on to f8_rows.cu, after the tile list that is made here.
 //
 // The scales change every 128 columns, inside the sum, so each block's products are a
 // sum of their own in tensor memory: the MMAs of a block write one accumulator (of
@@ -523,20 +523,20 @@ __global__ void __launch_bounds__(PREP_THREADS) f8_prep(const PrepArgs a)
 
 // ---------------------------------------------------------------- host
 
-// Whether pairs take the product, in row tiles of 256.  A pair's item takes about twice
-// as long as a CTA's of 64 rows and 128 weights (half-empty or not), so they do where
-// they need less than half the rounds over the device, with half a tile an expert left
-// over on average.  One matrix of 8192 x 4096, this form and pairs: 128 rows 11.5 and
-// 19.5 us, 256 rows 20.0 and 21.9, 384 rows 28.0 and 20.9, 1024 rows 61 and 40; of
-// 1536 x 4096, 1024 rows 19.1 and 22.0; 128 experts top-8: 800 tokens 151 and 195 us,
-// 1024 tokens 178 and 200, 2048 tokens 296 and 219.
-bool by_pairs(int R, int n, bool one, int N, int sms)
+// Whether f8_rows.cu takes the product, in row tiles of 128 and 256 weights.  An item
+// of its takes about twice as long as one of 64 rows and 128 weights (full or not), so
+// it does where it needs less than half the rounds over the device, with half a tile an
+// expert left over on average.  In us, this form and that, one matrix of 8192 x 4096:
+// 128 rows 12.2 and 21.1, 256 rows 20.5 and 21.2, 384 rows 28.7 and 21.6, 1024 rows 61
+// and 40; of 1536 x 4096: 1024 rows 19.4 and 21.4, 1999 rows 27.9 and 22.5; 128 experts
+// of it, k = 8: 512 tokens 131 and 146, 800 tokens 152 and 150, 2048 tokens 297 and 188.
+bool by_rows(int R, int n, bool one, int N, int sms)
 {
-    const auto rounds = [&](int rows, int cols, int at_once) {
+    const auto rounds = [&](int rows, int cols) {
         const long long tiles = one ? (R + rows - 1) / rows : std::max(std::min(R, n), R / rows + n / 2);
-        return (tiles * ((N + cols - 1) / cols) + at_once - 1) / at_once;
+        return (tiles * ((N + cols - 1) / cols) + sms - 1) / sms;
     };
-    return rounds(NT, MT, sms) > 2 * rounds(256, 256, sms / 2);
+    return rounds(NT, MT) > 2 * rounds(128, 256);
 }
 
 template <typename T>
@@ -595,8 +595,8 @@ cudaError_t launch_f8(const F8Call &c, void *workspace, cudaStream_t stream)
     if (c.K == 0)  // empty sums
         return cudaMemsetAsync(c.y, 0, static_cast<size_t>(c.R) * c.N * (c.dtype == SMOE_BF16 ? 2 : 4), stream);
     const int mtiles = (c.N + MT - 1) / MT;
-    const bool pairs = by_pairs(c.R, c.n, !c.offsets, c.N, dev->sm_count);
-    const int nt = pairs ? 256 : NT, max_tiles = most_tiles(c.R, c.n, nt);
+    const bool rows = by_rows(c.R, c.n, !c.offsets, c.N, dev->sm_count);
+    const int nt = rows ? 128 : NT, max_tiles = most_tiles(c.R, c.n, nt);
     int *ntiles = static_cast<int *>(workspace);
     Tile *tiles = reinterpret_cast<Tile *>(static_cast<char *>(workspace) + 256);
     if (c.offsets) {
@@ -604,7 +604,7 @@ cudaError_t launch_f8(const F8Call &c, void *workspace, cudaStream_t stream)
         const cudaError_t e = launch_pdl(f8_prep, dim3(33), dim3(PREP_THREADS), 0, stream, p);
         if (e != cudaSuccess) return e;
     }
-    if (pairs) return launch_f8_pair(c, ntiles, tiles, max_tiles, stream);
+    if (rows) return launch_f8_rows(c, ntiles, tiles, max_tiles, stream);
 
     // one matrix: equal tiles of consecutive rows
     const int nd = (c.R + NT - 1) / NT, step = ((c.R + nd - 1) / nd + 15) / 16 * 16;
