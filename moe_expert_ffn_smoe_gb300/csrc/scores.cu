@@ -589,7 +589,9 @@ struct RouteGradArgs {
 //   softmax, norm      dl_r = g_r
 //   softmax            dl_j = (g_r of the slot of j) - s_j sum_r g_r, for every j
 // A warp per row, which makes the row in shared memory and writes it once.  Bound
-// by writing the gradients (and, for the last form, reading the logits).
+// by writing the gradients (and, for the last form, reading the logits) and by
+// instruction issue: 16,383 rows of 128 experts, softmax of all, with the selection
+// before it 13.7 us (2.7 of them for the bytes).
 template <int V, bool WIDE>  // WIDE: k > 32, lane l holds the slots l and l + 32
 __global__ void __launch_bounds__(GRAD_WARPS * 32) route_rows_grad(const RouteGradArgs a)
 {

@@ -335,3 +335,131 @@ def test_the_same_inputs_give_the_same_bits(env):
     for R, N, K in ((1, 1000, 2048), (20, 512, 4096), (900, 1000, 1024)):
         a, b = product(env, 7, R, N, K, "f32")[0], product(env, 7, R, N, K, "f32")[0]
         assert (a == b).all()
+
+
+# ---------------------------------------------------------------- large batches: the rows on the other side of the product
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("R,N,K", [(1500, 2049, 1040), (1999, 4096, 512), (640, 8200, 16), (1100, 4000, 4240)])
+def test_one_matrix_and_many_rows(env, dtype, R, N, K):
+    hold(env[0], product(env, 8, R, N, K, dtype), K, dtype)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("gather", [True, False])
+@pytest.mark.parametrize("n,counts,tail,N,K", [
+    (6, [300, 17, 0, 256, 511, 33], 9, 4104, 272), (3, [1000, 0, 701], 3, 4097, 144), (40, [0, 90] * 20, 5, 2500, 1040),
+    (9, [128, 129, 127, 1, 0, 255, 257, 383, 4], 700, 4000, 640), (2, [0, 0], 1500, 4100, 128)])
+def test_experts_and_many_rows(env, dtype, gather, n, counts, tail, N, K):
+    rng = np.random.default_rng([n, N, K])
+    offsets, order, R, nsrc = batch(rng, n, counts, tail, 3 if gather else 1)
+    got = product(env, 9, R, N, K, dtype, n, offsets.tolist(), order if gather else None, 3 if gather else 1, nsrc)
+    hold(env[0], got, K, dtype)
+    assert (got[0][int(offsets[-1]):] == 0).all()  # rows of no expert
+
+
+@pytest.mark.parametrize("gather", [True, False])
+def test_nan_reaches_its_outputs_alone_among_many_rows(env, gather):
+    """NaN codes and scales of rows and weights, in the middle of a tile and at its
+    edges, and in rows that no expert has."""
+    torch = env[0]
+    N, K, n, R = 4100, 272, 2, 1207
+    offsets = [0, 500, 1200]
+    order = np.random.default_rng(2).permutation(R) if gather else np.arange(R)
+
+    def change(xq, xs, wq, ws):
+        xq[order[127], 7] = 0x7f
+        xs[order[500], 1] = np.nan
+        xq[order[1199], 271] = 0xff
+        xq[order[1204]] = 0x7f  # behind the last expert
+        wq[1, 131, 200] = 0xff
+        ws[1, 32, 2] = np.nan  # outputs 4096 to 4099
+
+    y, ref, mag = product(env, 10, R, N, K, "f32", n, offsets, order if gather else None, 1, change=change)
+    ref[1200:] = 0
+    assert (torch.isnan(y) == torch.isnan(ref)).all()
+    fine = ~torch.isnan(ref)
+    assert ((y - ref).abs()[fine] <= bound(K, "f32", mag)[fine]).all()
+
+
+def test_lists_that_are_none_are_reported_for_many_rows(env):
+    torch, smoe, dev = env
+    n, N, K, R = 4, 4104, 256, 1500
+    rng = np.random.default_rng(0)
+    xq, wq = torch.from_numpy(codes(rng, R, K)).to(dev), torch.from_numpy(codes(rng, n, N, K)).to(dev)
+    xs, ws = torch.ones(R, 2, device=dev), torch.ones(n, 33, 2, device=dev)
+    need = smoe.smoe_experts_matmul_f8_workspace_bytes(R, R, n, N, K)
+    work = torch.empty(need, dtype=torch.uint8, device=dev)
+    order = torch.arange(R, dtype=torch.int32, device=dev)
+    for off, bad in (([0, 900, 700, 1400, R], None), ([-5, 0, 700, 1400, R], None), ([0, 500, 700, R + 9, R], None),
+                     ([0, 500, 500, 600, R], 1 << 30), ([0, 500, 500, 600, R], -1), ([0, 500, 500, 600, R], R)):
+        o = order.clone()
+        if bad is not None:
+            o[R - 1] = bad
+        y = torch.full((R * N + 64,), 5.0, device=dev)
+        smoe.smoe_experts_matmul_f8(xq, xs, R, o, 1, torch.tensor(off, dtype=torch.int32, device=dev), R, n, wq, ws, N, K, y,
+                                    smoe.SMOE_F32, work, need)
+        assert smoe.smoe_last_device_status() == smoe.SMOE_ERR_ROUTE
+        assert (y[R * N:] == 5).all()
+        if bad is not None:
+            assert (y.view(-1)[(R - 1) * N:R * N] == 0).all()  # no source: zeros
+
+
+def test_scales_at_odd_addresses_among_many_rows(env):
+    """The row scales' vectors of four where they begin at no 16-byte boundary."""
+    torch, smoe, dev = env
+    R, N, K = 1300, 2100, 512
+    g = torch.Generator(device=dev).manual_seed(0)
+    x, w = torch.randn(R, K, generator=g, device=dev), torch.randn(1, N, K, generator=g, device=dev)
+    u8 = lambda *s: torch.empty(*s, dtype=torch.uint8, device=dev)  # noqa: E731
+    xq, xs, wq, ws = u8(R, K), torch.empty(R, 4, device=dev), u8(1, N, K), torch.empty(1, 17, 4, device=dev)
+    smoe.smoe_quantize_rows_f8(x, smoe.SMOE_F32, smoe.SMOE_Q8_PLAIN, R, K, xq, xs)
+    smoe.smoe_quantize_blocks_f8(w, smoe.SMOE_F32, 1, N, K, wq, ws)
+    odd_x, odd_w = torch.empty(R * 4 + 1, device=dev), torch.empty(17 * 4 + 1, device=dev)
+    odd_x[1:], odd_w[1:] = xs.view(-1), ws.view(-1)
+    ys = []
+    need = smoe.smoe_matmul_f8_workspace_bytes(R, N, K)
+    for a, b in ((xs, ws), (odd_x[1:], odd_w[1:])):
+        ys.append(torch.full((R, N), float("nan"), device=dev))
+        smoe.smoe_matmul_f8(xq, a, R, wq, b, N, K, ys[-1], smoe.SMOE_F32, u8(need), need)
+    assert torch.equal(*ys) and smoe.smoe_last_device_status() == smoe.SMOE_OK
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_sums_of_nothing(env, dtype):
+    torch, smoe, dev = env
+    dt, code = dtypes(torch, dtype)
+    R, N = 37, 101
+    one = torch.zeros(16, dtype=torch.uint8, device=dev)
+    f = torch.zeros(16, device=dev)
+    y = torch.full((R * N + 8,), 3.0, dtype=dt, device=dev)
+    need = smoe.smoe_matmul_f8_workspace_bytes(R, N, 0)
+    smoe.smoe_matmul_f8(one, f, R, one, f, N, 0, y, code, torch.empty(max(need, 16), dtype=torch.uint8, device=dev), need)
+    assert (y[:R * N] == 0).all() and (y[R * N:] == 3).all()
+
+
+def test_many_rows_at_once_on_two_streams(env):
+    """Two products with workspaces of their own, started together again and again."""
+    torch, smoe, dev = env
+    n, N, K, R = 8, 4000, 512, 1800
+    g = torch.Generator(device=dev).manual_seed(1)
+    u8 = lambda *s: torch.empty(*s, dtype=torch.uint8, device=dev)  # noqa: E731
+    need = smoe.smoe_experts_matmul_f8_workspace_bytes(R, R, n, N, K)
+    calls, streams = [], [torch.cuda.Stream() for _ in range(2)]
+    for off in ([0, 200, 200, 500, 900, 901, 1300, 1700, 1790], [0, 1000, 1100, 1200, 1300, 1400, 1500, 1600, 1800]):
+        x, w = torch.randn(R, K, generator=g, device=dev), torch.randn(n, N, K, generator=g, device=dev)
+        xq, xs, wq, ws = u8(R, K), torch.empty(R, 4, device=dev), u8(n, N, K), torch.empty(n, 32, 4, device=dev)
+        smoe.smoe_quantize_rows_f8(x, smoe.SMOE_F32, smoe.SMOE_Q8_PLAIN, R, K, xq, xs)
+        smoe.smoe_quantize_blocks_f8(w, smoe.SMOE_F32, n, N, K, wq, ws)
+        calls.append((xq, xs, R, None, 1, torch.tensor(off, dtype=torch.int32, device=dev), R, n, wq, ws, N, K))
+    run = lambda c, y, ws, s: smoe.smoe_experts_matmul_f8(*c, y, smoe.SMOE_F32, ws, need, s)  # noqa: E731
+    alone, outs = ([torch.empty(R, N, device=dev) for _ in range(2)] for _ in range(2))
+    work = [u8(need) for _ in range(2)]
+    for c, y in zip(calls, alone):
+        run(c, y, work[0], None)
+    torch.cuda.synchronize()
+    for _ in range(10):
+        for c, y, ws, s in zip(calls, outs, work, streams):
+            run(c, y, ws, s)
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(alone, outs)) and smoe.smoe_last_device_status() == smoe.SMOE_OK
