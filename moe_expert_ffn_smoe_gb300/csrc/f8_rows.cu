@@ -43,7 +43,11 @@ constexpr int ST = 4, D = 2;                 // stages of the operands, accumula
 constexpr int EPI_WARPS = 8, MMA_WARP = 8, W_WARP = 9, X_WARP = 12, X_WARPS = 8;
 constexpr int ROWS_THREADS = (X_WARP + X_WARPS) * 32;
 constexpr int BOX = 64;                      // rows of one copy (not gathered)
-constexpr size_t ROWS_SMEM = 1024 + ST * (X_BYTES + W_BYTES) + MT * 4 + 256;
+constexpr uint32_t OUT_PITCH = 64 + 16;      // 64 bytes of a row on their way out (rows that begin anywhere)
+constexpr size_t rows_smem(bool whole)
+{
+    return 1024 + ST * (X_BYTES + W_BYTES) + MT * 4 + 256 + (whole ? 0 : EPI_WARPS * 32 * OUT_PITCH);
+}
 
 struct alignas(128) RowsArgs {
     CUtensorMap wmap, xmap;
@@ -92,37 +96,54 @@ __device__ __forceinline__ uint32_t bf16x2(float a, float b)
     return *reinterpret_cast<const uint32_t *>(&p);
 }
 
-// 32 neighbouring outputs of a row, of which the first n are there; whole: the row
-// begins at a 16-byte boundary, and so do they.
-__device__ __forceinline__ void store32(float *y, const float2 (&v)[16], int n, bool whole)
+// 32 neighbouring outputs of a row that begins at a 16-byte boundary, of which the
+// first n are there.
+__device__ __forceinline__ void store32(float *y, const float2 (&v)[16], int n)
 {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        if (whole && 4 * i + 4 <= n) {
-            *reinterpret_cast<float4 *>(y + 4 * i) = make_float4(v[2 * i].x, v[2 * i].y, v[2 * i + 1].x, v[2 * i + 1].y);
-        } else {
-            const float e[4] = {v[2 * i].x, v[2 * i].y, v[2 * i + 1].x, v[2 * i + 1].y};
-#pragma unroll
-            for (int b = 0; b < 4; ++b)
-                if (4 * i + b < n) y[4 * i + b] = e[b];
-        }
-    }
+    for (int i = 0; i < 8; ++i)
+        if (4 * i < n) *reinterpret_cast<float4 *>(y + 4 * i) = make_float4(v[2 * i].x, v[2 * i].y, v[2 * i + 1].x, v[2 * i + 1].y);
 }
-__device__ __forceinline__ void store32(__nv_bfloat16 *y, const float2 (&v)[16], int n, bool whole)
+__device__ __forceinline__ void store32(__nv_bfloat16 *y, const float2 (&v)[16], int n)
 {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        if (whole && 8 * i + 8 <= n) {
+    for (int i = 0; i < 4; ++i)
+        if (8 * i < n)
             *reinterpret_cast<uint4 *>(y + 8 * i) = make_uint4(bf16x2(v[4 * i].x, v[4 * i].y), bf16x2(v[4 * i + 1].x, v[4 * i + 1].y),
                                                                bf16x2(v[4 * i + 2].x, v[4 * i + 2].y), bf16x2(v[4 * i + 3].x, v[4 * i + 3].y));
-        } else {
+}
+
+// The same of 32 rows, one a lane, that begin anywhere: 64 bytes of each at a time
+// through shared memory.  y: the first row's (of `rows`).
+__device__ __forceinline__ void sts128(uint32_t addr, uint32_t a, uint32_t b, uint32_t c, uint32_t d)
+{
+    asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(a), "r"(b), "r"(c), "r"(d) : "memory");
+}
+__device__ __forceinline__ void store32_anywhere(float *y, const float2 (&v)[16], int n, int N, int rows, uint32_t stage)
+{
+    const uint32_t mine = stage + (threadIdx.x & 31) * OUT_PITCH;
 #pragma unroll
-            for (int b = 0; b < 4; ++b) {
-                if (8 * i + 2 * b < n) put(y + 8 * i + 2 * b, v[4 * i + b].x);
-                if (8 * i + 2 * b + 1 < n) put(y + 8 * i + 2 * b + 1, v[4 * i + b].y);
-            }
+    for (int h = 0; h < 2; ++h) {
+        __syncwarp();
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const float2 a = v[8 * h + 2 * i], b = v[8 * h + 2 * i + 1];
+            sts128(mine + 16 * i, __float_as_uint(a.x), __float_as_uint(a.y), __float_as_uint(b.x), __float_as_uint(b.y));
         }
+        __syncwarp();
+        store_staged<32, 16>(stage, OUT_PITCH, y + 16 * h, N, rows, n - 16 * h);
     }
+}
+__device__ __forceinline__ void store32_anywhere(__nv_bfloat16 *y, const float2 (&v)[16], int n, int N, int rows, uint32_t stage)
+{
+    const uint32_t mine = stage + (threadIdx.x & 31) * OUT_PITCH;
+    __syncwarp();
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+        sts128(mine + 16 * i, bf16x2(v[4 * i].x, v[4 * i].y), bf16x2(v[4 * i + 1].x, v[4 * i + 1].y),
+               bf16x2(v[4 * i + 2].x, v[4 * i + 2].y), bf16x2(v[4 * i + 3].x, v[4 * i + 3].y));
+    __syncwarp();
+    store_staged<32, 32>(stage, OUT_PITCH, y, N, rows, n);
 }
 
 __device__ __forceinline__ Tile tile_at(const RowsArgs &a, int i, int ntiles)
@@ -132,12 +153,14 @@ __device__ __forceinline__ Tile tile_at(const RowsArgs &a, int i, int ntiles)
     return Tile{0, i * a.step, min(a.step, a.R - i * a.step), 0};
 }
 
-template <typename T>
+// WHOLE: every row of y begins at a 16-byte boundary.  (One kernel for both took 81 us
+// for 1999 rows x 8192 x 4096 against 74.)
+template <typename T, bool WHOLE>
 __global__ void __launch_bounds__(ROWS_THREADS, 1) f8_rows(const __grid_constant__ RowsArgs a)
 {
     extern __shared__ uint8_t smem_raw[];
     const uint32_t raw = smem_addr(smem_raw), base = (raw + 1023u) & ~1023u;
-    const uint32_t w0 = base, x0 = w0 + ST * W_BYTES, list0 = x0 + ST * X_BYTES, bars = list0 + MT * 4;
+    const uint32_t w0 = base, x0 = w0 + ST * W_BYTES, list0 = x0 + ST * X_BYTES, bars = list0 + MT * 4, out0 = bars + 256;
     const uint32_t full = bars, empty = full + 8 * ST, dfull = empty + 8 * ST, dempty = dfull + 8 * D, tslot = dempty + 8 * D;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int first = static_cast<int>(blockIdx.x), stride = static_cast<int>(gridDim.x);
@@ -351,12 +374,18 @@ __global__ void __launch_bounds__(ROWS_THREADS, 1) f8_rows(const __grid_constant
                 }
             }
             if (failed) break;
-            if (r < t.rows) {
-                const int n0 = nblk * 128;
+            const int n0 = nblk * 128;
+            if (WHOLE) {
                 T *row = y + static_cast<size_t>(t.row0 + r) * a.N + n0;
-                const bool whole = a.N % (16 / static_cast<int>(sizeof(T))) == 0;
+                if (r < t.rows) {
 #pragma unroll
-                for (int j = 0; j < 4; ++j) store32(row + 32 * j, acc[j], a.N - n0 - 32 * j, whole);
+                    for (int j = 0; j < 4; ++j) store32(row + 32 * j, acc[j], a.N - n0 - 32 * j);
+                }
+            } else if (some) {
+                T *rows = y + static_cast<size_t>(t.row0 + q * 32) * a.N + n0;
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                    store32_anywhere(rows + 32 * j, acc[j], a.N - n0 - 32 * j, a.N, t.rows - q * 32, out0 + warp * 32 * OUT_PITCH);
             }
         }
     }
@@ -374,17 +403,18 @@ __global__ void __launch_bounds__(ROWS_THREADS, 1) f8_rows(const __grid_constant
     }
 }
 
-template <typename T>
+template <typename T, bool WHOLE>
 cudaError_t launch_t(const RowsArgs &a, long long most_items, int sms, cudaStream_t stream)
 {
-    static_assert(ROWS_SMEM <= 227 * 1024, "shared memory of a CTA");
-    auto k = f8_rows<T>;
+    constexpr size_t smem = rows_smem(WHOLE);
+    static_assert(smem <= 227 * 1024, "shared memory of a CTA");
+    auto k = f8_rows<T, WHOLE>;
     // one size for every launch of this kernel: asked for once per device
     static std::atomic<bool> opted[64];
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
     if (!opted[dev].load(std::memory_order_relaxed)) {
-        const cudaError_t e = ensure_dynamic_smem(k, ROWS_SMEM);
+        const cudaError_t e = ensure_dynamic_smem(k, smem);
         if (e != cudaSuccess) return e;
         opted[dev].store(true, std::memory_order_relaxed);
     }
@@ -392,7 +422,7 @@ cudaError_t launch_t(const RowsArgs &a, long long most_items, int sms, cudaStrea
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(static_cast<unsigned>(ctas));
     cfg.blockDim = dim3(ROWS_THREADS);
-    cfg.dynamicSmemBytes = ROWS_SMEM;
+    cfg.dynamicSmemBytes = smem;
     cfg.stream = stream;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -430,7 +460,10 @@ cudaError_t launch_f8_rows(const F8Call &c, const int *ntiles, const Tile *tiles
     const int nd = (c.R + MT - 1) / MT;  // equal tiles: an item costs a full one whatever its rows
     a.step = (c.R + nd - 1) / nd;
     const long long most = static_cast<long long>(c.offsets ? max_tiles : nd) * a.groups;
-    return c.dtype == SMOE_BF16 ? launch_t<__nv_bfloat16>(a, most, dev->sm_count, stream) : launch_t<float>(a, most, dev->sm_count, stream);
+    const int sms = dev->sm_count;
+    if (c.dtype == SMOE_BF16)
+        return c.N % 8 == 0 ? launch_t<__nv_bfloat16, true>(a, most, sms, stream) : launch_t<__nv_bfloat16, false>(a, most, sms, stream);
+    return c.N % 4 == 0 ? launch_t<float, true>(a, most, sms, stream) : launch_t<float, false>(a, most, sms, stream);
 }
 
 }  // namespace smoe

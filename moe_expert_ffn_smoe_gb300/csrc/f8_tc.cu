@@ -131,7 +131,8 @@ __device__ __forceinline__ Tile tile_at(const TcArgs &a, int i, int ntiles)
     return Tile{0, i * a.step, min(a.step, a.R - i * a.step), 0};
 }
 
-template <typename T>
+// WHOLE: every row of y begins at a 16-byte boundary.
+template <typename T, bool WHOLE>
 __global__ void __launch_bounds__(TC_THREADS, 1) f8_tc(const __grid_constant__ TcArgs a)
 {
     extern __shared__ uint8_t smem_raw[];
@@ -408,11 +409,9 @@ __global__ void __launch_bounds__(TC_THREADS, 1) f8_tc(const __grid_constant__ T
                     }
                 continue;
             }
-            // 8 rows at a time through shared memory, out as 16-byte vectors of a row
+            // 8 rows at a time through shared memory
             constexpr uint32_t PITCH = 32 * sizeof(T) + 16;
-            constexpr int VE = 16 / static_cast<int>(sizeof(T)), LR = 32 / VE;  // lanes of a row
             const uint32_t stage = out0 + warp * OUT_BYTES;
-            const bool whole = a.N % VE == 0;
 #pragma unroll
             for (int g0 = 0; g0 < G; g0 += 2) {
                 const int r0 = col + 4 * g0;
@@ -428,24 +427,9 @@ __global__ void __launch_bounds__(TC_THREADS, 1) f8_tc(const __grid_constant__ T
                         sts_out(to + 8 * static_cast<uint32_t>(sizeof(T)), acc[g0 + g][i].y, y);
                     }
                 __syncwarp();
-#pragma unroll
-                for (int i = 0; i < 8 * LR / 32; ++i) {
-                    const int r = (i * 32 + lane) / LR, n = (lane % LR) * VE;
-                    const uint4 v = lds128v(stage + static_cast<uint32_t>(r) * PITCH + static_cast<uint32_t>(lane % LR) * 16u);
-                    if (r0 + r >= t.rows || n0 + n >= a.N) continue;
-                    T *to = y + static_cast<size_t>(t.row0 + r0 + r) * a.N + n0 + n;
-                    if (whole) {
-                        *reinterpret_cast<uint4 *>(to) = v;
-                    } else {
-                        const uint32_t e[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-                        for (int b = 0; b < VE; ++b)
-                            if (n0 + n + b < a.N) {
-                                if (sizeof(T) == 4) reinterpret_cast<uint32_t *>(to)[b] = e[b];
-                                else reinterpret_cast<uint16_t *>(to)[b] = static_cast<uint16_t>(e[b / 2] >> (16 * (b & 1)));
-                            }
-                    }
-                }
+                T *to = y + static_cast<size_t>(t.row0 + r0) * a.N + n0;
+                if (WHOLE) store_units<uint4, 8, 32>(stage, PITCH, to, a.N, t.rows - r0, a.N - n0);
+                else store_staged<8, 32>(stage, PITCH, to, a.N, t.rows - r0, a.N - n0);
             }
         }
     }
@@ -548,11 +532,11 @@ bool by_rows(int R, int n, bool one, int N, int sms)
     return rounds(NT, MT) > 2 * rounds(128, 256);
 }
 
-template <typename T>
+template <typename T, bool WHOLE>
 cudaError_t launch_t(const TcArgs &args, long long most_items, int sms, cudaStream_t stream)
 {
     static_assert(TC_SMEM <= 227 * 1024, "shared memory of a CTA");
-    auto k = f8_tc<T>;
+    auto k = f8_tc<T, WHOLE>;
     // one size for every launch of this kernel: asked for once per device
     static std::atomic<bool> opted[64];
     int dev = 0;
@@ -568,7 +552,7 @@ cudaError_t launch_t(const TcArgs &args, long long most_items, int sms, cudaStre
     // sum over the cluster costs more than the blocks that it saves.
     int size = 1;
     for (int s = 8; s > 1; s /= 2)
-        if (most_items * s <= sms && args.kb >= 16 && most_items <= clusters_held<f8_tc<T>>(s, TC_THREADS, TC_SMEM)) {
+        if (most_items * s <= sms && args.kb >= 16 && most_items <= clusters_held<f8_tc<T, WHOLE>>(s, TC_THREADS, TC_SMEM)) {
             size = s;
             break;
         }
@@ -637,7 +621,10 @@ cudaError_t launch_f8(const F8Call &c, void *workspace, cudaStream_t stream)
     a.step = step;
     a.mtiles = mtiles;
     const long long most = static_cast<long long>(c.offsets ? max_tiles : nd) * mtiles;
-    return c.dtype == SMOE_BF16 ? launch_t<__nv_bfloat16>(a, most, dev->sm_count, stream) : launch_t<float>(a, most, dev->sm_count, stream);
+    const int sms = dev->sm_count;
+    if (c.dtype == SMOE_BF16)
+        return c.N % 8 == 0 ? launch_t<__nv_bfloat16, true>(a, most, sms, stream) : launch_t<__nv_bfloat16, false>(a, most, sms, stream);
+    return c.N % 4 == 0 ? launch_t<float, true>(a, most, sms, stream) : launch_t<float, false>(a, most, sms, stream);
 }
 
 }  // namespace smoe
