@@ -26,6 +26,7 @@
 // (6.4 TB/s); one row of 8192 x 4096 9 us, of which a launch that does nothing is 3.
 #include <algorithm>
 #include <atomic>
+#include <type_traits>
 
 #include "f8.cuh"
 #include "smoe.h"
@@ -47,14 +48,20 @@ constexpr int NT = 64, ST = 8, D = 8;        // rows of a tile, stages of the op
 constexpr int CB = 32, G = CB / 4;           // columns of an epilogue warp, every fourth a thread
 constexpr uint32_t X_BYTES = NT * F8_BLOCK;
 constexpr int BOX = 16;                      // rows of one copy (not gathered)
-constexpr size_t TC_SMEM = 1024 + ST * (W_BYTES + X_BYTES) + SLOTS * NT * 4 + EPI_WARPS * OUT_BYTES + NT * 4 + 512;
+constexpr int OWN_TILES = 288;               // of a list that every CTA makes for itself
+constexpr size_t tc_smem(bool own)
+{
+    return 1024 + ST * (W_BYTES + X_BYTES) + SLOTS * NT * 4 + EPI_WARPS * OUT_BYTES + NT * 4 + 512 + (own ? OWN_TILES * sizeof(Tile) : 0);
+}
 
 struct alignas(128) TcArgs {
     CUtensorMap wmap, xmap;
     const float *ws, *xs;  // scales [n x nb x kb], [nsrc x kb]
     void *y;
     const int *ntiles;
-    const Tile *tiles;     // null: one matrix, tiles of `step` rows
+    const Tile *tiles;     // the list that f8_prep made; or null
+    const int *offsets;    // to make it of here (OWN: at most OWN_TILES); both null: one matrix, tiles of `step` rows
+    int n, max_tiles;
     const int *order;      // source of every sorted row, times k (gathered), or null
     unsigned *status;
     int R, N, kb, nb, k, nsrc, step, mtiles;
@@ -124,22 +131,37 @@ __device__ __forceinline__ void sts_out(uint32_t addr, float v, __nv_bfloat16 *)
 // one's after one another.
 __device__ __forceinline__ int scale_at(int c) { return (c & ~31) + (c & 3) * 8 + (c & 31) / 4; }
 
-__device__ __forceinline__ Tile tile_at(const TcArgs &a, int i, int ntiles)
+__device__ __forceinline__ Tile tile_at(const TcArgs &a, const Tile *tiles, int i, int ntiles)
 {
     if (i >= ntiles) return Tile{0, 0, 0, 0};
-    if (a.tiles) return a.tiles[i];
+    if (tiles) return tiles[i];
     return Tile{0, i * a.step, min(a.step, a.R - i * a.step), 0};
 }
 
-// WHOLE: every row of y begins at a 16-byte boundary.
-template <typename T, bool WHOLE>
+// Zeros in the rows of y past the last expert's, by thread `at` of `step`: whole 16
+// bytes (y begins at such a boundary), and what is before and after them.
+__device__ __forceinline__ void zero_tail(void *out, int last, int R, size_t pitch, size_t at, size_t step)
+{
+    const size_t from = max(0, min(last, R)) * pitch, end = R * pitch;
+    const size_t lo = min(end, (from + 15) & ~static_cast<size_t>(15)), hi = max(lo, end & ~static_cast<size_t>(15));
+    uint8_t *y = static_cast<uint8_t *>(out);
+    for (size_t i = lo + at * 16; i < hi; i += step * 16) *reinterpret_cast<uint4 *>(y + i) = make_uint4(0u, 0u, 0u, 0u);
+    if (at < 16) {
+        if (from + at < lo) y[from + at] = 0;
+        if (hi + at < end) y[hi + at] = 0;
+    }
+}
+
+// WHOLE: every row of y begins at a 16-byte boundary.  OWN: the tile list is made here
+// (its code in every kernel cost a matrix and one row 0.3 us of 9).
+template <typename T, bool WHOLE, bool OWN>
 __global__ void __launch_bounds__(TC_THREADS, 1) f8_tc(const __grid_constant__ TcArgs a)
 {
     extern __shared__ uint8_t smem_raw[];
     const uint32_t raw = smem_addr(smem_raw);
     const uint32_t base = (raw + 1023u) & ~1023u;
     const uint32_t w0 = base, x0 = w0 + ST * W_BYTES, f0 = x0 + ST * X_BYTES, out0 = f0 + SLOTS * NT * 4,
-                   list0 = out0 + EPI_WARPS * OUT_BYTES, bars = list0 + NT * 4;
+                   list0 = out0 + EPI_WARPS * OUT_BYTES, bars = list0 + NT * 4, own0 = bars + 512;
     const uint32_t full = bars, empty = full + 8 * ST, sfull = empty + 8 * ST, sempty = sfull + 8 * SLOTS,
                    dfull = sempty + 8 * SLOTS, dempty = dfull + 8 * D, tslot = dempty + 8 * D;
     static_assert(16 * (ST + SLOTS + D) + 4 <= 512 && D * NT <= 512, "barriers; tensor memory");
@@ -178,10 +200,23 @@ __global__ void __launch_bounds__(TC_THREADS, 1) f8_tc(const __grid_constant__ T
     // One matrix: this CTA's first weights are known, and are brought into L2 while
     // the previous kernel ends.  A prefetch only: that kernel may be the one that
     // quantises these weights.
-    if (!a.tiles && warp == W_WARP && first < (a.R + a.step - 1) / a.step * a.mtiles && lane < ST && c0 + lane < c1)
+    if (!OWN && !a.tiles && warp == W_WARP && first < (a.R + a.step - 1) / a.step * a.mtiles && lane < ST && c0 + lane < c1)
         tma_prefetch_2d(&a.wmap, (c0 + lane) * F8_BLOCK, first % a.mtiles * MT);
     pdl_wait();
-    const int ntiles = a.tiles ? *a.ntiles : (a.R + a.step - 1) / a.step;
+    const Tile *tiles = a.tiles;
+    int ntiles = 0;
+    if (OWN) {
+        __shared__ int count;
+        Tile *own = reinterpret_cast<Tile *>(smem_raw + (own0 - raw));
+        list_tiles<TC_THREADS>(a.offsets, a.n, a.R, NT, 16, a.max_tiles, &count, own, a.status);
+        zero_tail(a.y, a.offsets[a.n], a.R, static_cast<size_t>(a.N) * sizeof(T),
+                  static_cast<size_t>(blockIdx.x) * TC_THREADS + threadIdx.x, static_cast<size_t>(gridDim.x) * TC_THREADS);
+        __syncthreads();
+        tiles = own;
+        ntiles = count;
+    } else {
+        ntiles = tiles ? *a.ntiles : (a.R + a.step - 1) / a.step;
+    }
     const int nitems = ntiles * a.mtiles;  // (below 2^28: y or the weights would not fit the device)
     bool failed = false;
 
@@ -191,7 +226,7 @@ __global__ void __launch_bounds__(TC_THREADS, 1) f8_tc(const __grid_constant__ T
                 uint32_t s = 0, p = 1;  // parity of the stage's release one lap ago; none in the first
                 bool round0 = true;
                 for (int it = first; it < nitems && !failed; it += stride) {
-                    const Tile t = tile_at(a, it / a.mtiles, ntiles);
+                    const Tile t = tile_at(a, tiles, it / a.mtiles, ntiles);
                     const int row = t.expert * a.N + it % a.mtiles * MT;
                     for (int c = c0; c < c1; ++c) {
                         if (!round0 && !mbar_wait_bounded(empty + 8 * s, p, a.status, 7u)) {
@@ -216,7 +251,7 @@ __global__ void __launch_bounds__(TC_THREADS, 1) f8_tc(const __grid_constant__ T
             uint32_t s = 0, p = 1;
             bool round0 = true;
             for (int it = first; it < nitems && !failed; it += stride) {
-                const Tile t = tile_at(a, it / a.mtiles, ntiles);
+                const Tile t = tile_at(a, tiles, it / a.mtiles, ntiles);
                 const int cols = mma_cols<1>(t.rows);  // a multiple of 16
                 if (a.order) {  // rows past the tile's: any row, their columns are not stored
                     const int at = 16 * (lane >> 2) + 4 * part + (lane & 3);
@@ -262,7 +297,7 @@ __global__ void __launch_bounds__(TC_THREADS, 1) f8_tc(const __grid_constant__ T
                 uint32_t s = 0, p = 0, d = 0, pd = 1;
                 bool round0 = true;
                 for (int it = first; it < nitems && !failed; it += stride) {
-                    const Tile t = tile_at(a, it / a.mtiles, ntiles);
+                    const Tile t = tile_at(a, tiles, it / a.mtiles, ntiles);
                     const uint32_t idesc = idesc_e4m3(MT, mma_cols<1>(t.rows));
                     for (int c = c0; c < c1; ++c) {
                         // both barriers looked at together: this thread's own latency counts
@@ -308,7 +343,7 @@ __global__ void __launch_bounds__(TC_THREADS, 1) f8_tc(const __grid_constant__ T
             uint32_t s = 0, p = 1;
             bool round0 = true;
             for (int it = first; it < nitems && !failed; it += stride) {
-                const Tile t = tile_at(a, it / a.mtiles, ntiles);
+                const Tile t = tile_at(a, tiles, it / a.mtiles, ntiles);
                 const float *ws = a.ws + (static_cast<size_t>(t.expert) * a.nb + it % a.mtiles) * a.kb;
                 const float *xs[2];  // null: no source, a scale of 0
 #pragma unroll
@@ -352,7 +387,7 @@ __global__ void __launch_bounds__(TC_THREADS, 1) f8_tc(const __grid_constant__ T
         const uint32_t mine = tmem + (static_cast<uint32_t>(q * 32) << 16) + static_cast<uint32_t>(col);
         uint32_t d = 0, pd = 0, s = 0, p = 0;
         for (int it = first; it < nitems && !failed; it += stride) {
-            const Tile t = tile_at(a, it / a.mtiles, ntiles);
+            const Tile t = tile_at(a, tiles, it / a.mtiles, ntiles);
             float2 acc[G][2];  // column 4 g + lane % 4 of rows lane / 4 + 16 i and + 8
 #pragma unroll
             for (int g = 0; g < G; ++g) acc[g][0] = acc[g][1] = make_float2(0.f, 0.f);
@@ -448,7 +483,7 @@ __global__ void __launch_bounds__(TC_THREADS, 1) f8_tc(const __grid_constant__ T
         static_assert(NT * MT * 4 <= ST * X_BYTES, "the sums of a tile");
         cluster_sync();
         if (first < nitems) {
-            const Tile t = tile_at(a, first / a.mtiles, ntiles);
+            const Tile t = tile_at(a, tiles, first / a.mtiles, ntiles);
             const int nb = (first % a.mtiles) * MT;
             T *y = static_cast<T *>(a.y);
             for (int i = threadIdx.x; i < (t.rows - krank + nsplit - 1) / nsplit * (MT / 4); i += TC_THREADS) {
@@ -499,19 +534,8 @@ __global__ void __launch_bounds__(PREP_THREADS) f8_prep(const PrepArgs a)
         list_tiles<PREP_THREADS>(a.offsets, a.n, a.R, a.nt, a.unit, a.max_tiles, a.ntiles, a.tiles, a.status);
         return;
     }
-    // in bytes of y, whose base is at a 16-byte boundary: whole 16 bytes, and what is
-    // before and after them
-    const size_t pitch = static_cast<size_t>(a.N) * a.elem, end = a.R * pitch;
-    const size_t from = max(0, min(a.offsets[a.n], a.R)) * pitch;
-    const size_t lo = min(end, (from + 15) & ~static_cast<size_t>(15)), hi = max(lo, end & ~static_cast<size_t>(15));
-    const size_t at = static_cast<size_t>(blockIdx.x - 1) * PREP_THREADS + threadIdx.x;
-    const size_t step = static_cast<size_t>(gridDim.x - 1) * PREP_THREADS;
-    uint8_t *y = static_cast<uint8_t *>(a.y);
-    for (size_t i = lo + at * 16; i < hi; i += step * 16) *reinterpret_cast<uint4 *>(y + i) = make_uint4(0u, 0u, 0u, 0u);
-    if (at < 16) {
-        if (from + at < lo) y[from + at] = 0;
-        if (hi + at < end) y[hi + at] = 0;
-    }
+    zero_tail(a.y, a.offsets[a.n], a.R, static_cast<size_t>(a.N) * a.elem,
+              static_cast<size_t>(blockIdx.x - 1) * PREP_THREADS + threadIdx.x, static_cast<size_t>(gridDim.x - 1) * PREP_THREADS);
 }
 
 // ---------------------------------------------------------------- host
@@ -532,17 +556,18 @@ bool by_rows(int R, int n, bool one, int N, int sms)
     return rounds(NT, MT) > 2 * rounds(128, 256);
 }
 
-template <typename T, bool WHOLE>
+template <typename T, bool WHOLE, bool OWN>
 cudaError_t launch_t(const TcArgs &args, long long most_items, int sms, cudaStream_t stream)
 {
-    static_assert(TC_SMEM <= 227 * 1024, "shared memory of a CTA");
-    auto k = f8_tc<T, WHOLE>;
+    constexpr size_t smem = tc_smem(OWN);
+    static_assert(smem <= 226 * 1024, "shared memory of a CTA, with the list's sums");
+    auto k = f8_tc<T, WHOLE, OWN>;
     // one size for every launch of this kernel: asked for once per device
     static std::atomic<bool> opted[64];
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
     if (!opted[dev].load(std::memory_order_relaxed)) {
-        const cudaError_t e = ensure_dynamic_smem(k, TC_SMEM);
+        const cudaError_t e = ensure_dynamic_smem(k, smem);
         if (e != cudaSuccess) return e;
         opted[dev].store(true, std::memory_order_relaxed);
     }
@@ -552,7 +577,7 @@ cudaError_t launch_t(const TcArgs &args, long long most_items, int sms, cudaStre
     // sum over the cluster costs more than the blocks that it saves.
     int size = 1;
     for (int s = 8; s > 1; s /= 2)
-        if (most_items * s <= sms && args.kb >= 16 && most_items <= clusters_held<f8_tc<T, WHOLE>>(s, TC_THREADS, TC_SMEM)) {
+        if (most_items * s <= sms && args.kb >= 16 && most_items <= clusters_held<f8_tc<T, WHOLE, OWN>>(s, TC_THREADS, smem)) {
             size = s;
             break;
         }
@@ -562,7 +587,7 @@ cudaError_t launch_t(const TcArgs &args, long long most_items, int sms, cudaStre
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(static_cast<unsigned>(clusters * size));
     cfg.blockDim = dim3(TC_THREADS);
-    cfg.dynamicSmemBytes = TC_SMEM;
+    cfg.dynamicSmemBytes = smem;
     cfg.stream = stream;
     cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -592,7 +617,10 @@ cudaError_t launch_f8(const F8Call &c, void *workspace, cudaStream_t stream)
     const int nt = rows ? 128 : NT, max_tiles = most_tiles(c.R, c.n, nt);
     int *ntiles = static_cast<int *>(workspace);
     Tile *tiles = reinterpret_cast<Tile *>(static_cast<char *>(workspace) + 256);
-    if (c.offsets) {
+    // A short list is made by every CTA itself, a launch less: 3 tokens through 107 experts
+    // of 940 x 1168 7.8 -> 7.0 us, 93 through 106 of 884 x 624 20.7 -> 19.8 us.
+    const bool own = c.offsets && !rows && max_tiles <= OWN_TILES;
+    if (c.offsets && !own) {
         const PrepArgs p = {c.offsets, c.y, ntiles, tiles, status, c.R, c.n, c.N, nt, 16, max_tiles, c.dtype == SMOE_BF16 ? 2 : 4};
         const cudaError_t e = launch_pdl(f8_prep, dim3(33), dim3(PREP_THREADS), 0, stream, p);
         if (e != cudaSuccess) return e;
@@ -610,7 +638,10 @@ cudaError_t launch_f8(const F8Call &c, void *workspace, cudaStream_t stream)
     a.order = c.order;
     a.y = c.y;
     a.ntiles = ntiles;
-    a.tiles = c.offsets ? tiles : nullptr;
+    a.tiles = c.offsets && !own ? tiles : nullptr;
+    a.offsets = own ? c.offsets : nullptr;
+    a.n = c.n;
+    a.max_tiles = max_tiles;
     a.status = status;
     a.R = c.R;
     a.N = c.N;
@@ -622,9 +653,14 @@ cudaError_t launch_f8(const F8Call &c, void *workspace, cudaStream_t stream)
     a.mtiles = mtiles;
     const long long most = static_cast<long long>(c.offsets ? max_tiles : nd) * mtiles;
     const int sms = dev->sm_count;
-    if (c.dtype == SMOE_BF16)
-        return c.N % 8 == 0 ? launch_t<__nv_bfloat16, true>(a, most, sms, stream) : launch_t<__nv_bfloat16, false>(a, most, sms, stream);
-    return c.N % 4 == 0 ? launch_t<float, true>(a, most, sms, stream) : launch_t<float, false>(a, most, sms, stream);
+    const auto go = [&](auto zero, auto whole) {
+        using T = decltype(zero);
+        return own ? launch_t<T, whole.value, true>(a, most, sms, stream) : launch_t<T, whole.value, false>(a, most, sms, stream);
+    };
+    const auto typed = [&](auto zero) {
+        return c.N % (16 / static_cast<int>(sizeof(zero))) == 0 ? go(zero, std::true_type{}) : go(zero, std::false_type{});
+    };
+    return c.dtype == SMOE_BF16 ? typed(__nv_bfloat16{}) : typed(float{});
 }
 
 }  // namespace smoe
