@@ -273,7 +273,7 @@ __global__ void __launch_bounds__(ROWS_THREADS, 1) f8_rows(const __grid_constant
                 failed = __shfl_sync(FULL_MASK, failed, from);
             }
         } else if (warp == MMA_WARP) {
-            // one thread issues, the even CTA's
+            // one thread issues
             if (elect_one()) {
                 uint32_t s = 0, p = 0, d = 0, pd = 1;
                 bool round0 = true;
