@@ -17,9 +17,9 @@
 // against the 512 of its MMAs (1999 rows x 8192 x 4096 88 us).  Here a tile of fewer
 // than 128 rows costs as much as a full one.
 //
-// Bound by handing the accumulators over: a block takes 1150 clocks, of which its MMAs
-// are 512, the way to the epilogue and back some 750, reading and adding 450 (1999 rows
-// x 8192 x 4096 74 us, 1.8 PFLOP/s; with an epilogue that reads nothing 66).  Pairs of
+// Bound by handing the accumulators over: a block takes 1190 clocks, of which its MMAs
+// are 440 to 512, the way to the epilogue and back some 750, reading and adding 450 (1999
+// rows x 8192 x 4096 74.5 us, 1.8 PFLOP/s).  Pairs of
 // CTAs on 256 rows need two thirds of the copies and took 73 us there, but cost 256 rows
 // a tile: through 128 experts, 2047 tokens of 8 221 us against 192, 4096 tokens 307
 // against 291.  Accumulators in halves, barriers tested ahead, 16 epilogue warps and
