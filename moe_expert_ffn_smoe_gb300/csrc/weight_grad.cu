@@ -256,8 +256,13 @@ __global__ void __launch_bounds__(WG_THREADS, 1) weight_grad(const __grid_consta
             }
             const int y = (m * 2 + rank) * MT + q * 32, x0 = c * NT + h * 128;
             const uint32_t acc = tmem + (static_cast<uint32_t>(q * 32) << 16) + (d & 1) * NT + h * 128;
-#pragma unroll
-            for (int j = 0; j < 128 / COLS; ++j) {
+            // boxes of the tile that lie in the matrix at all
+            const int boxes = y < a.N && x0 < a.K ? min((a.K - x0 + COLS - 1) / COLS, 128 / COLS) : 0;
+            if (boxes == 0 && r.y != 0) {
+                __syncwarp();
+                if (lane == 0) mbar_arrive_cluster(lead + 8 * (d & 1));
+            }
+            for (int j = 0; j < boxes; ++j) {
                 float v[COLS];
                 if (r.y != 0) {
                     tmem_ld<COLS>(acc + j * COLS, v);
@@ -266,7 +271,7 @@ __global__ void __launch_bounds__(WG_THREADS, 1) weight_grad(const __grid_consta
 #pragma unroll
                     for (int i = 0; i < COLS; ++i) v[i] = 0.f;
                 }
-                if (j == 128 / COLS - 1 && r.y != 0) {
+                if (j == boxes - 1 && r.y != 0) {
                     tc_fence_before();
                     __syncwarp();
                     if (lane == 0) mbar_arrive_cluster(lead + 8 * (d & 1));
@@ -294,7 +299,7 @@ __global__ void __launch_bounds__(WG_THREADS, 1) weight_grad(const __grid_consta
                 fence_proxy_async_smem();
                 __syncwarp();
                 if (lane == 0) {
-                    if (y < a.N && x0 + j * COLS < a.K) store_box(&a.out, box, x0 + j * COLS, y, e, a.accumulate);
+                    store_box(&a.out, box, x0 + j * COLS, y, e, a.accumulate);
                     asm volatile("cp.async.bulk.commit_group;" ::: "memory");
                 }
             }
