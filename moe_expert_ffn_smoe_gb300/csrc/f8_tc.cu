@@ -170,19 +170,15 @@ __global__ void __launch_bounds__(TC_THREADS, 1) f8_tc(const __grid_constant__ T
     const int krank = nsplit > 1 ? static_cast<int>(blockIdx.x) % nsplit : 0;  // = the rank in the cluster
     const int first = static_cast<int>(blockIdx.x) / nsplit, stride = static_cast<int>(gridDim.x) / nsplit;
 
-    if (threadIdx.x == 0) {
-        for (int i = 0; i < ST; ++i) {
-            mbar_init(full + 8 * i, 1 + (a.order ? X_WARPS : 1));  // the loading warps
-            mbar_init(empty + 8 * i, 1);
-        }
-        for (int i = 0; i < SLOTS; ++i) {
-            mbar_init(sfull + 8 * i, 1);
-            mbar_init(sempty + 8 * i, EPI_WARPS);
-        }
-        for (int i = 0; i < D; ++i) {
-            mbar_init(dfull + 8 * i, 1);
-            mbar_init(dempty + 8 * i, EPI_WARPS);
-        }
+    static_assert(ST == SLOTS && ST == D, "a thread for each place of the rings");
+    if (threadIdx.x < ST) {
+        const uint32_t i = 8 * threadIdx.x;
+        mbar_init(full + i, 1 + (a.order ? X_WARPS : 1));  // the loading warps
+        mbar_init(empty + i, 1);
+        mbar_init(sfull + i, 1);
+        mbar_init(sempty + i, EPI_WARPS);
+        mbar_init(dfull + i, 1);
+        mbar_init(dempty + i, EPI_WARPS);
         fence_mbar_init();
     }
     if (warp == MMA_WARP) {
