@@ -43,6 +43,22 @@ _FLOATS = (torch.float32, torch.bfloat16, torch.float16, torch.float64)
 _INTS = (torch.int32, torch.int64, torch.int16, torch.int8, torch.uint8)
 
 
+@contextlib.contextmanager
+def _graph_of(*tensors):
+    """Around what builds an autograd graph of the tensors.  Refuses a CUDA graph's
+    capture on leaves that an eager graph still holds: torch would add to their
+    gradients on that graph's stream, and end the process."""
+    leaves = [t for t in tensors if t.requires_grad and t.is_leaf] if torch.is_grad_enabled() else []
+    # what adds to a leaf's gradient: the same one as long as any graph holds it
+    notes = lambda t: t.view_as(t).grad_fn.next_functions[0][0].metadata  # noqa: E731
+    capturing = torch.cuda.is_current_stream_capturing()
+    if capturing and any(notes(t).get("eager") for t in leaves):
+        raise RuntimeError("a captured step needs leaves that no eager graph holds: drop that graph, or detach copies")
+    yield
+    for t in leaves:
+        notes(t)["eager"] = not capturing
+
+
 def _bytes(n, device):
     return torch.empty(max(n, 16), dtype=torch.uint8, device=device)
 
@@ -348,7 +364,9 @@ def route(logits, k, bias=None, score=smoe.SMOE_SCORE_SOFTMAX, n_groups=1, top_g
     if bias is not None:
         _check("bias", bias, (logits.shape[1],), (torch.float32,))
         bias = bias.detach().contiguous()
-    return _Route.apply(logits.float(), bias, k, score, n_groups, top_groups, group_best, int(norm), scale)
+    with _graph_of(logits):
+        out = _Route.apply(logits.float(), bias, k, score, n_groups, top_groups, group_best, int(norm), scale)
+    return out
 
 
 def experts_f8(xs, w, offsets):
@@ -363,7 +381,9 @@ def experts_f8(xs, w, offsets):
     _check("offsets", offsets, (w.shape[0] + 1,), (torch.int32,))
     if w.shape[1] % 16 or w.shape[2] % 16:
         raise ValueError(f"matrices of {tuple(w.shape[1:])}: both sizes are to be multiples of 16")
-    return _ExpertsF8.apply(xs, w, offsets)
+    with _graph_of(xs, w):
+        ys = _ExpertsF8.apply(xs, w, offsets)
+    return ys
 
 
 def dispatch(x, idx, n_experts):
@@ -406,15 +426,18 @@ def moe_train(x, router, gate_up, down, k):
 def moe_train_f8(x, router, gate_up, down, k, bias=None, **how):
     """The layer in 8-bit floating point, routed by scores (how: as route takes
     it); nothing is read back, so that a step can be captured in a CUDA graph.
-    x bf16 or f32; every argument but bias may need a gradient."""
+    x bf16 or f32; every argument but bias may need a gradient.  A capture is refused
+    while an eager graph of the same leaves lives."""
     n, d_ff = router.shape[0], down.shape[2]
-    with torch.autocast(x.device.type, enabled=False):  # the selection is made on f32 logits
+    # (the selection is made on f32 logits)
+    with _graph_of(x, router, gate_up, down), torch.autocast(x.device.type, enabled=False):
         logits = x.float() @ router.float().t()
         idx, w = route(logits, k, bias, **how)
         xs, offsets, place = dispatch(x, idx, n)
         h = experts_f8(xs, gate_up, offsets)
         ys = experts_f8(torch.nn.functional.silu(h[:, :d_ff]) * h[:, d_ff:], down, offsets)
-        return combine(ys, place, w)
+        out = combine(ys, place, w)
+    return out
 
 
 def main():

@@ -346,6 +346,30 @@ def test_a_training_step_in_a_graph(ex, how):
 
 # ---------------------------------------------------------------- refusals
 
+def test_a_capture_on_leaves_of_a_living_graph_is_refused(ex):
+    """Torch's own additions to their gradients would end the process; refused before
+    anything is captured, and not once that graph is gone."""
+    leaves, bias, d_out = _train_inputs(torch.bfloat16)
+    s = torch.cuda.Stream()
+    living = ex.moe_train_f8(*leaves, 3, bias)
+    torch.cuda.synchronize()
+    with pytest.raises(RuntimeError, match="no eager graph holds"):
+        with torch.cuda.graph(torch.cuda.CUDAGraph(), stream=s):
+            ex.moe_train_f8(*leaves, 3, bias)
+    eager = torch.autograd.grad(living, leaves, d_out)
+    del living
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=s):
+        grads = torch.autograd.grad(ex.moe_train_f8(*leaves, 3, bias), leaves, d_out)
+    graph.replay()
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(grads, eager))
+    with torch.no_grad():  # without gradients there is nothing to refuse
+        out = ex.moe_train_f8(*leaves, 3, bias)
+    assert not out.requires_grad and ex.smoe.smoe_last_device_status() == ex.smoe.SMOE_OK
+
+
 def test_what_is_refused(ex):
     gate, gate_up, down, bias, r = _weights(6)
     for bad in ((gate.float(), gate_up, down), (gate[:-1], gate_up, down), (gate, gate_up[:, :-2], down),
