@@ -17,7 +17,7 @@
 // never meet this one's.
 //
 // Bound by what crosses between L2 and the SMs, whose reads (3.3 GB of them) wait
-// behind the writes of d_w: 128 experts, 32,768 rows, 1536 x 4096 in bf16 386 us (1.6 GB
+// behind the writes of d_w: 128 experts, 32,768 rows, 1536 x 4096 in bf16 386 to 396 us (1.6 GB
 // written; without the stores 297), with one stage less and two places for the outputs 4%
 // more (of few rows 2 to 5% less), with three stages 499.  8 experts of
 // 4096 rows each in f32 277 us, 1490 TFLOP/s.  Measured and not kept: two tiles an item
