@@ -744,11 +744,13 @@ int smoe_route_rows_backward(const float *logits, int n_tokens, int n_experts,
  * be short.
  *
  * Quantises rows of v = x (SMOE_Q8_PLAIN) or of v = SiLU(gate) * up (SMOE_Q8_SILU_MUL;
- * x: [rows x 2 cols]), as smoe_quantize_rows_q8 takes them:
+ * x: [rows x 2 cols], gate the first cols of a row and up the last):
  *
+ *   SiLU(g) = g / (1 + exp(-g)),  exp CUDA's expf       (g exp(g) from -88 down)
  *   top = max |v| of the block,  scale = top / 448,  q = e4m3(v (448 / top))
  *
- * (f32 operations rounded once each, the code to nearest, ties to even; where
+ * (f32 operations rounded once each, the code to nearest, ties to even; SiLU's
+ * quotient may be rounded to the other side, once in some two million; where
  * 448 / top is beyond f32, v and top are taken 2^64 times).  A block of zeros has
  * scale 0 and codes 0; one that holds a NaN or an infinity has scale NaN and codes 0,
  * so that every product of it is NaN.  cols <= SMOE_MAX_COLS; q: [rows x cols],
