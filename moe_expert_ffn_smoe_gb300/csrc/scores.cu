@@ -134,9 +134,9 @@ __device__ __noinline__ double inverse_sum64(const Row r)
     return 1.0 / sum;
 }
 
-// Whether all experts of the row that are on have one logit and one bias: then
-// equal sums of scores are equal, and no 64-bit look is needed (a router whose
-// weights are still zero).
+// Whether all experts of the row that are on have one logit and one bias: then sums
+// of as many scores are equal, and no 64-bit look is needed (a router whose weights
+// are still zero).
 __device__ __noinline__ bool all_alike(const Row r)
 {
     float lo = INFINITY, hi = -INFINITY, blo = INFINITY, bhi = -INFINITY;
@@ -449,8 +449,12 @@ __device__ __forceinline__ void route_row(const RouteArgs &a, int t, const float
         const float value = b1 + (two ? b2 : 0.f);
         Groups q = {value, BY == By::Logit ? 0.f : fmaf(fabsf(value), 0x1p-23f, 2.f * err)};
         take_groups(q, a);
-        if (BY != By::Logit && q.high >= q.low && !all_alike(r))
-            q.taken = take_groups64<BY, V, NEAR>(r, a, q, v, two ? b2 : b1, err, room.cands);
+        if (BY != By::Logit && q.high >= q.low) {
+            // groups of one expert that is on and groups of more differ however alike those are
+            const bool on = g < a.groups && value > -INFINITY;
+            const bool even = a.best == 1 || !__any_sync(FULL_MASK, on && two) || !__any_sync(FULL_MASK, on && !two);
+            if (!even || !all_alike(r)) q.taken = take_groups64<BY, V, NEAR>(r, a, q, v, two ? b2 : b1, err, room.cands);
+        }
         const uint32_t taken = NEAR ? 0u : __ballot_sync(FULL_MASK, q.taken);
 #pragma unroll
         for (int i = 0; i < V; ++i) {
