@@ -693,7 +693,9 @@ int smoe_experts_matmul_q8(const int8_t *xq, const float *x_scales, int n_src,
  *   top_w[t][r] = scale s_r                             (norm == 0)
  *
  * The order is that of the real numbers c: where f32 cannot tell two of them apart,
- * 64 bits decide (equal there: a tie).  An expert whose logit or bias is -infinity is
+ * 64 bits decide (equal there: a tie).  Without a bias the experts' order is that of
+ * their logits, which differ where scores have run out of digits; the 64 bits then
+ * decide on groups' sums of two alone.  An expert whose logit or bias is -infinity is
  * off: it is not chosen, and counts for nothing in its group (its logit stays in the
  * softmax's sum where only the bias is -infinity).  Slots for which no expert is left
  * have index -1 and weight 0.  A row that holds a NaN logit, a logit of +infinity

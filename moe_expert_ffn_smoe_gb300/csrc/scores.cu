@@ -6,8 +6,8 @@
 //   c_i = s_i + b_i                      (what the choice goes by)
 //   w_r = scale s_r / sum over the chosen   or   scale s_r
 //
-// The choice is the one that the real numbers c_i make.  Where no bias is added
-// and no two scores are summed, that is the order of the logits.  Elsewhere c_i
+// The choice is the one that the real numbers c_i make.  Where no bias is added that
+// is the order of the logits, but for groups that count two scores.  Elsewhere c_i
 // is taken in f32 with a bound of its error, and what lies closer than the bounds
 // (a row in some thousands) is decided by the same values in 64 bits: of the
 // candidates alone, one a lane, or, where the border between groups is in doubt,
@@ -366,8 +366,10 @@ struct WarpRoom {
     float row[NEAR ? 1 : 32 * V];
 };
 
-// One row: its logits and the biases of this lane's experts.
-template <By BY, int V, bool NEAR>
+// One row: its logits and the biases of this lane's experts.  BIAS: there are some, and
+// the choice among the experts goes by c, not by the logits.  (As a question to the
+// arguments: 28.3 us against 27.7 for 32,768 rows by groups.)
+template <By BY, bool BIAS, int V, bool NEAR>
 __device__ __forceinline__ void route_row(const RouteArgs &a, int t, const float (&l)[V], const float (&b)[V],
                                           WarpRoom<V, NEAR> &room)
 {
@@ -461,6 +463,14 @@ __device__ __forceinline__ void route_row(const RouteArgs &a, int t, const float
             const int of = static_cast<int>((static_cast<unsigned>(i * 32 + lane) * a.magic) >> 20) << a.shift;
             if (NEAR ? !q.taken : i * 32 + lane < a.n && !(taken >> of & 1u)) v[i] = -INFINITY;
         }
+        if (BY != By::Logit && !BIAS) {
+            // the scores' order is the logits', which have digits where scores have none left
+            float again[V];
+            load_row<V, NEAR>(r.l, a.n, a.wide, -INFINITY, again);
+#pragma unroll
+            for (int i = 0; i < V; ++i) v[i] = v[i] > -INFINITY ? again[i] : v[i];
+            err = 0.f;
+        }
     }
     uint32_t key[V];
 #pragma unroll
@@ -476,7 +486,7 @@ __device__ __forceinline__ void route_row(const RouteArgs &a, int t, const float
             return;
         }
         // what may be among the k best: within the bounds of the bound
-        if (BY != By::Logit && bound > kKeyNegInf) bound = value_key(value_of_key(bound) - 2.f * err);
+        if (BIAS && bound > kKeyNegInf) bound = value_key(value_of_key(bound) - 2.f * err);
         bound = max(bound, kKeyNegInf + 1u);
         Candidates &c = room.cands;
         c.key[lane] = 0u;
@@ -515,7 +525,7 @@ __device__ __forceinline__ void route_row(const RouteArgs &a, int t, const float
             int rank = 0;
             for (int o = 0; o < count; o += 4) {
                 const uint4 u = *reinterpret_cast<const uint4 *>(&c.key[o]);
-                if (BY == By::Logit) {
+                if (!BIAS) {
                     rank += u.x >= mine + (o >= lane ? 1u : 0u);
                     rank += u.y >= mine + (o + 1 >= lane ? 1u : 0u);
                     rank += u.z >= mine + (o + 2 >= lane ? 1u : 0u);
@@ -524,7 +534,7 @@ __device__ __forceinline__ void route_row(const RouteArgs &a, int t, const float
                     rank += (u.x > mine) + (u.y > mine) + (u.z > mine) + (u.w > mine);
                 }
             }
-            if (BY != By::Logit) {
+            if (BIAS) {
                 // One bound for all: two that it does not separate make neighbours that it does
                 // not.  Equal ones leave the ranks after the first empty (infinite).
                 float *by_rank = room.sorted;
@@ -559,7 +569,7 @@ __device__ __forceinline__ void route_row(const RouteArgs &a, int t, const float
 // 8 groups of which 4 stay, k = 8 24.6 us (8 warps a CTA 27; 690 instructions a row),
 // where reading and writing takes 2.8; CTAs that walk the rows, the next one's logits
 // loaded ahead, 29 us: the registers cost the warps that would have filled the gaps.
-template <By BY, int V, bool NEAR>
+template <By BY, bool BIAS, int V, bool NEAR>
 __global__ void __launch_bounds__(ROW_WARPS * 32) route_rows_warp(const RouteArgs a)
 {
     __shared__ WarpRoom<V, NEAR> rooms[ROW_WARPS];
@@ -571,8 +581,8 @@ __global__ void __launch_bounds__(ROW_WARPS * 32) route_rows_warp(const RouteArg
 #pragma unroll
     for (int i = 0; i < V; ++i) b[i] = 0.f;
     load_row<V, NEAR>(a.logits + static_cast<size_t>(t) * a.ld, a.n, a.wide, -INFINITY, l);
-    if (a.bias) load_row<V, NEAR>(a.bias, a.n, a.wide, 0.f, b);
-    route_row<BY, V, NEAR>(a, t, l, b, rooms[wi]);
+    if (BIAS) load_row<V, NEAR>(a.bias, a.n, a.wide, 0.f, b);
+    route_row<BY, BIAS, V, NEAR>(a, t, l, b, rooms[wi]);
 }
 
 // ---------------------------------------------------------------- gradient
@@ -693,15 +703,15 @@ cudaError_t grad_wide(const RouteGradArgs &a, cudaStream_t stream)
     return launch_pdl(route_rows_grad<32, WIDE>, grid, block, 0, stream, a);
 }
 
-template <By BY, int V>
+template <By BY, bool BIAS, int V>
 cudaError_t route_wide(const RouteArgs &a, bool near, cudaStream_t stream)
 {
     const dim3 grid(static_cast<unsigned>((a.T + ROW_WARPS - 1) / ROW_WARPS)), block(ROW_WARPS * 32);
-    return near ? launch_pdl(route_rows_warp<BY, V, true>, grid, block, 0, stream, a)
-                : launch_pdl(route_rows_warp<BY, V, false>, grid, block, 0, stream, a);
+    return near ? launch_pdl(route_rows_warp<BY, BIAS, V, true>, grid, block, 0, stream, a)
+                : launch_pdl(route_rows_warp<BY, BIAS, V, false>, grid, block, 0, stream, a);
 }
 
-template <By BY>
+template <By BY, bool BIAS>
 cudaError_t route_by(RouteArgs a, cudaStream_t stream)
 {
     const int V = a.n <= 128 ? 4 : a.n <= 256 ? 8 : a.n <= 512 ? 16 : 32;
@@ -715,10 +725,10 @@ cudaError_t route_by(RouteArgs a, cudaStream_t stream)
                       (stay >= 2 * a.k * V || stay <= 32);
     int lanes = near ? a.size / V : 32 / a.groups;  // the largest power of two that leaves every group its lanes
     for (a.shift = 0; lanes > 1; lanes /= 2) ++a.shift;
-    if (V == 4) return route_wide<BY, 4>(a, near, stream);
-    if (V == 8) return route_wide<BY, 8>(a, near, stream);
-    if (V == 16) return route_wide<BY, 16>(a, near, stream);
-    return route_wide<BY, 32>(a, near, stream);
+    if (V == 4) return route_wide<BY, BIAS, 4>(a, near, stream);
+    if (V == 8) return route_wide<BY, BIAS, 8>(a, near, stream);
+    if (V == 16) return route_wide<BY, BIAS, 16>(a, near, stream);
+    return route_wide<BY, BIAS, 32>(a, near, stream);
 }
 
 }  // namespace
@@ -732,8 +742,9 @@ cudaError_t launch_route_rows(const float *logits, int T, int n, int ld, const f
     const RouteArgs a = {logits, bias, idx, w, T, n, ld, k, groups, top_groups, best, size, 0,
                          static_cast<unsigned>(((1 << 20) + size - 1) / size), scale, softmax, norm,
                          ld % 4 == 0 && reinterpret_cast<uintptr_t>(logits) % 16 == 0 && reinterpret_cast<uintptr_t>(bias) % 16 == 0};
-    if (!bias && (groups == 1 || best == 1)) return route_by<By::Logit>(a, stream);
-    return softmax ? route_by<By::Softmax>(a, stream) : route_by<By::Sigmoid>(a, stream);
+    if (!bias && (groups == 1 || best == 1)) return route_by<By::Logit, false>(a, stream);
+    if (!bias) return softmax ? route_by<By::Softmax, false>(a, stream) : route_by<By::Sigmoid, false>(a, stream);
+    return softmax ? route_by<By::Softmax, true>(a, stream) : route_by<By::Sigmoid, true>(a, stream);
 }
 
 cudaError_t launch_route_rows_grad(const float *logits, int T, int n, int ld, bool softmax, int k, bool norm, float scale,

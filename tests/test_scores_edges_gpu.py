@@ -28,3 +28,36 @@ def test_alike_experts_in_groups_of_different_numbers(env, softmax, n, G, tg, k)
         for b in (0.0, -np.float32(s), np.nextafter(-np.float32(s), np.float32(1))):
             t.check(env, l, np.full(n, b, np.float32), softmax, G, tg, 2, k, False)
             t.check(env, l, np.full(n, b, np.float32), softmax, G, tg, 1, k, False)
+
+
+@pytest.mark.parametrize("softmax", [True, False])
+@pytest.mark.parametrize("n,G,tg,k", [(128, 8, 4, 8), (128, 8, 4, 20), (60, 6, 2, 5), (256, 4, 2, 16), (1024, 32, 7, 20)])
+def test_scores_that_64_bits_cannot_tell_apart(env, softmax, n, G, tg, k):
+    """Without a bias the experts of the groups that stay are ordered by their logits:
+    sigmoids of 40 and 41 are 1 in 64 bits, softmax terms far below the largest 0."""
+    rng = np.random.default_rng([n, G, k, 1])
+    T, size = 80, n // G
+    # (the groups themselves are told apart by their two best)
+    l = 40 + rng.integers(0, 64, size=(T, n)) * 0.125 if not softmax else -800 - rng.integers(0, 64, size=(T, n)) * 16.0
+    level = rng.random((T, G)).argsort(1)
+    head = np.repeat(level, size, axis=1) * 0.25 - (0 if softmax else 20)
+    first = np.tile(np.arange(n) % size, (T, 1)) < 1  # one of each group far from the rest
+    if softmax:
+        l = np.where(first, head, l)
+    else:
+        l = np.where(np.repeat(level, size, axis=1) >= G - tg, l, head)
+    l = l.astype(np.float32)
+    l[rng.random((T, n)) < 0.02] = -np.inf
+    p = u.scores(l, softmax)
+    c = np.where(l == -np.inf, -np.inf, p)
+    v = -np.sort(-c.reshape(T, G, size), axis=2)[:, :, :2]
+    of = np.where(v[:, :, 0] > -np.inf, np.where(v > -np.inf, v, 0).sum(2), -np.inf)
+    rank = np.argsort(np.argsort(-of, axis=1, kind="stable"), axis=1, kind="stable")
+    left = np.where(np.repeat(rank < tg, size, axis=1), l, -np.inf)
+    take = np.argsort(-left, axis=1, kind="stable")[:, :k]
+    ref = np.where(np.take_along_axis(left, take, 1) > -np.inf, take, -1)
+    _, idx, w = t.route(env, l, None, softmax, G, tg, 2, k, False, 1.0)
+    gi = idx.cpu().numpy()
+    assert (gi == ref).all(), np.argwhere(gi != ref)[:5]
+    rw = u.weights(l, ref, softmax, False, 1.0)
+    assert (np.abs(w.cpu().numpy() - rw) <= t.rtol(n) * rw + 1e-37).all()
