@@ -448,8 +448,10 @@ __device__ __forceinline__ void route_row(const RouteArgs &a, int t, const float
             b1 = fmaxf(b1, o1);
         }
         const bool two = a.best == 2 && b2 > -INFINITY;
-        const float value = b1 + (two ? b2 : 0.f);
+        float value = b1 + (two ? b2 : 0.f);
         Groups q = {value, BY == By::Logit ? 0.f : fmaf(fabsf(value), 0x1p-23f, 2.f * err)};
+        if (BY != By::Logit && two && fabsf(value) == INFINITY)  // two biases that leave f32 (a mask of its lowest value)
+            q = {value = copysignf(0x1.fffffep127f, value), INFINITY};
         take_groups(q, a);
         if (BY != By::Logit && q.high >= q.low) {
             // groups of one expert that is on and groups of more differ however alike those are

@@ -61,3 +61,19 @@ def test_scores_that_64_bits_cannot_tell_apart(env, softmax, n, G, tg, k):
     assert (gi == ref).all(), np.argwhere(gi != ref)[:5]
     rw = u.weights(l, ref, softmax, False, 1.0)
     assert (np.abs(w.cpu().numpy() - rw) <= t.rtol(n) * rw + 1e-37).all()
+
+
+@pytest.mark.parametrize("softmax", [True, False])
+@pytest.mark.parametrize("low", [-np.finfo(np.float32).max, -3e38, 3e38, np.finfo(np.float32).max])
+@pytest.mark.parametrize("n,G,tg,k", [(128, 8, 4, 8), (128, 8, 4, 20), (60, 6, 3, 7), (256, 4, 2, 16)])
+def test_biases_whose_sum_of_two_leaves_f32(env, softmax, low, n, G, tg, k):
+    """A mask of the type's lowest value is a bias like another: its experts come last,
+    and a group of them counts less than any other that is on, but is not off."""
+    rng = np.random.default_rng([n, G, k, 2])
+    size = n // G
+    l = t.logits(rng, 50, n, False)
+    for some in (np.arange(n) // size >= 2, np.arange(n) % size > 1, rng.random(n) < 0.7, np.full(n, True)):
+        b = np.where(some, np.float32(low), rng.normal(size=n) * 0.05).astype(np.float32)
+        b[size] = -np.inf
+        t.check(env, l, b, softmax, G, tg, 2, k, False)
+        t.check(env, l, b, softmax, G, tg, 1, k, False)
