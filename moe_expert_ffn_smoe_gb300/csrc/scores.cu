@@ -327,15 +327,16 @@ __device__ __forceinline__ void write_weights(const RouteArgs &a, const Row &r, 
     const float sa = ea >= 0 ? chosen_score(a, r, la, m) : 0.f;
     float sb = 0.f;
     if (a.k > 32 && eb >= 0) sb = chosen_score(a, r, lb, m);
-    // (the sum is never small: of a sigmoid at least a half, of a softmax 2^-11)
-    const float times = a.norm ? a.scale * rcp_approx(warp_sum(sa + sb)) : a.scale;
+    // (the sum is never small: of a sigmoid at least a half, of a softmax 2^-11; the
+    // scale over it may be beyond f32 where no weight is)
+    const float over = a.norm ? rcp_approx(warp_sum(sa + sb)) : 1.f;
     if (ra >= 0 && ra < a.k) {
         idx[ra] = ea;
-        w[ra] = ea >= 0 ? sa * times : 0.f;
+        w[ra] = ea >= 0 ? sa * over * a.scale : 0.f;
     }
     if (rb >= 0 && rb < a.k) {
         idx[rb] = eb;
-        w[rb] = eb >= 0 ? sb * times : 0.f;
+        w[rb] = eb >= 0 ? sb * over * a.scale : 0.f;
     }
 }
 
@@ -635,7 +636,8 @@ __global__ void __launch_bounds__(GRAD_WARPS * 32) route_rows_grad(const RouteGr
         w[h] = in ? a.w[at] : 0.f;
         g[h] = in ? a.dw[at] : 0.f;
         if (e[h] < 0 || e[h] >= a.n) e[h] = -1;  // no expert: counts for nothing
-        if (e[h] >= 0) dot = fmaf(w[h], g[h], dot);
+        // (weights over the scale are at most 1: a sum of the weights' own could leave f32)
+        if (e[h] >= 0) dot = fmaf(a.norm ? w[h] / a.scale : w[h], g[h], dot);
     }
     if (dense) {
         float top = p[0];
@@ -660,7 +662,7 @@ __global__ void __launch_bounds__(GRAD_WARPS * 32) route_rows_grad(const RouteGr
         twice = e[0] >= 0 && reinterpret_cast<const int *>(row)[e[0]] != lane;
         twice = __any_sync(FULL_MASK, twice);
     }
-    const float mean = a.norm ? dot / a.scale : 0.f;
+    const float mean = a.norm ? dot : 0.f;
 #pragma unroll
     for (int h = 0; h < H; ++h) {
         g[h] = w[h] * (g[h] - mean);

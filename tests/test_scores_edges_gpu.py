@@ -77,3 +77,30 @@ def test_biases_whose_sum_of_two_leaves_f32(env, softmax, low, n, G, tg, k):
         b[size] = -np.inf
         t.check(env, l, b, softmax, G, tg, 2, k, False)
         t.check(env, l, b, softmax, G, tg, 1, k, False)
+
+
+@pytest.mark.parametrize("softmax", [True, False])
+@pytest.mark.parametrize("scale", [3e38, -1e37, 2e-38])
+@pytest.mark.parametrize("n,k", [(128, 8), (1000, 64), (7, 3)])
+def test_scales_at_the_ends_of_f32(env, softmax, scale, n, k):
+    """Renormalised weights are at most the scale, whatever the sum that they are over."""
+    rng = np.random.default_rng([n, k])
+    scale = float(np.float32(scale))
+    l = np.concatenate([t.logits(rng, 20, n, False), t.logits(rng, 20, n, False) - 30]).astype(np.float32)
+    L, idx, w = t.route(env, l, None, softmax, 1, 1, 1, k, True, scale)
+    ref = u.choose(l, None, softmax, 1, 1, 1, k)
+    assert (idx.cpu().numpy() == ref).all()
+    rw = u.weights(l, ref, softmax, True, scale)
+    gw = w.cpu().numpy().astype(np.float64)
+    # below the normal numbers by a step of 2^-149
+    assert (np.abs(gw - rw) <= t.rtol(n) * np.abs(rw) + 2.0 ** -148).all()
+    torch, smoe, dev = env
+    dw = (rng.random((40, k)) + 1).astype(np.float32)
+    dl = torch.full((40, n), float("nan"), device=dev)
+    smoe.smoe_route_rows_backward(L, 40, n, n, smoe.SMOE_SCORE_SOFTMAX if softmax else smoe.SMOE_SCORE_SIGMOID, k, 1, scale,
+                                  idx, w, torch.from_numpy(dw).to(dev), dl)
+    d, mag = u.weights_gradient(l, ref, softmax, True, scale, dw.astype(np.float64))
+    got = dl.cpu().numpy().astype(np.float64)
+    # a weight below the normal numbers is off by 2^-149, as a share by that over the scale
+    share = (k + 2) * 2.0 ** -148 / abs(scale)
+    assert (np.abs(got - d) <= 4 * (t.rtol(n) + k * 2.0 ** -23) * mag + 4 * share * mag.max() + 2.0 ** -147).all()
