@@ -613,7 +613,7 @@ template <int V, bool WIDE>  // WIDE: k > 32, lane l holds the slots l and l + 3
 __global__ void __launch_bounds__(GRAD_WARPS * 32) route_rows_grad(const RouteGradArgs a)
 {
     constexpr int H = WIDE ? 2 : 1;
-    __shared__ float rows[GRAD_WARPS][32 * V];
+    __shared__ alignas(16) float rows[GRAD_WARPS][32 * V];  // (written out in 16 bytes a lane)
     const int wi = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int t = blockIdx.x * GRAD_WARPS + wi;
     pdl_launch_dependents();
