@@ -43,20 +43,37 @@ _FLOATS = (torch.float32, torch.bfloat16, torch.float16, torch.float64)
 _INTS = (torch.int32, torch.int64, torch.int16, torch.int8, torch.uint8)
 
 
+def _adder(t):
+    """The node that adds to the leaf t's gradient: one as long as anything holds it."""
+    return t.view_as(t).grad_fn.next_functions[0][0]
+
+
 @contextlib.contextmanager
 def _graph_of(*tensors):
-    """Around what builds an autograd graph of the tensors.  Refuses a CUDA graph's
-    capture on leaves that an eager graph still holds: torch would add to their
-    gradients on that graph's stream, and end the process."""
-    leaves = [t for t in tensors if t.requires_grad and t.is_leaf] if torch.is_grad_enabled() else []
-    # what adds to a leaf's gradient: the same one as long as any graph holds it
-    notes = lambda t: t.view_as(t).grad_fn.next_functions[0][0].metadata  # noqa: E731
-    capturing = torch.cuda.is_current_stream_capturing()
-    if capturing and any(notes(t).get("eager") for t in leaves):
-        raise RuntimeError("a captured step needs leaves that no eager graph holds: drop that graph, or detach copies")
-    yield
+    """Around what builds an autograd graph of the tensors.  Torch adds to a leaf's
+    gradient on the stream that was current when the leaf's node was made, and ends the
+    process where a CUDA graph's capture meets the default stream there.  A capture is
+    refused on leaves whose node is held (by an eager graph, whoever built it, or a hook)
+    and was made on the default stream, or on one that no backward pass has shown yet."""
+    leaves = [t for t in tensors if t.requires_grad and t.is_leaf and t.is_cuda] if torch.is_grad_enabled() else []
+    held, key = [], "made on"
     for t in leaves:
-        notes(t)["eager"] = not capturing
+        node = _adder(t)
+        if key not in node.metadata:
+            node.metadata["seen"] = True
+            del node  # gone, unless others hold it
+            node = _adder(t)
+            if not node.metadata.pop("seen", False):
+                node.metadata[key] = torch.cuda.current_stream(t.device).cuda_stream
+            elif not node.metadata.setdefault("asked", False) and not torch.cuda.is_current_stream_capturing():
+                notes, device = node.metadata, t.device
+                notes["asked"] = True
+                node.register_prehook(lambda _, n=notes, d=device: n.__setitem__(key, torch.cuda.current_stream(d).cuda_stream))
+        if not node.metadata.get(key) and torch.cuda.is_current_stream_capturing():
+            raise RuntimeError("a captured step needs leaves that no eager graph holds from the default stream (or from one that "
+                               "no backward pass has shown): drop that graph, build it on another stream, or detach copies")
+        held.append(node)  # until the graph does
+    yield
 
 
 def _bytes(n, device):
@@ -354,7 +371,9 @@ def top_k(logits, k):
     """(indices, weights) of each row's k experts, taken and summed in f32;
     differentiable in logits (of any float type)."""
     _check("logits", logits, (None, None), _FLOATS)
-    return _TopK.apply(logits.float(), k)
+    with _graph_of(logits):
+        out = _TopK.apply(logits.float(), k)
+    return out
 
 
 def route(logits, k, bias=None, score=smoe.SMOE_SCORE_SOFTMAX, n_groups=1, top_groups=1, group_best=1, norm=True, scale=1.0):
@@ -393,7 +412,9 @@ def dispatch(x, idx, n_experts):
     _check("idx", idx, (x.shape[0], None), _INTS)
     if idx.dtype != torch.int32:  # the library's type; clamped, so that none wraps into another expert
         idx = idx.long().clamp(-1, n_experts).int()
-    return _Dispatch.apply(x, idx, n_experts)
+    with _graph_of(x):
+        out = _Dispatch.apply(x, idx, n_experts)
+    return out
 
 
 def combine(ys, place, w):
@@ -402,7 +423,9 @@ def combine(ys, place, w):
     _check("w", w, (None, None), _FLOATS)
     _check("place", place, (w.numel(),), (torch.int32,))
     _check("ys", ys, (w.numel(), None), tuple(_CODE))
-    return _Combine.apply(ys, place, w.float())
+    with _graph_of(ys, w):
+        out = _Combine.apply(ys, place, w.float())
+    return out
 
 
 def moe_train(x, router, gate_up, down, k):
@@ -427,7 +450,7 @@ def moe_train_f8(x, router, gate_up, down, k, bias=None, **how):
     """The layer in 8-bit floating point, routed by scores (how: as route takes
     it); nothing is read back, so that a step can be captured in a CUDA graph.
     x bf16 or f32; every argument but bias may need a gradient.  A capture is refused
-    while an eager graph of the same leaves lives."""
+    while an eager graph that was built on the default stream holds the same leaves."""
     n, d_ff = router.shape[0], down.shape[2]
     # (the selection is made on f32 logits)
     with _graph_of(x, router, gate_up, down), torch.autocast(x.device.type, enabled=False):
