@@ -16,6 +16,7 @@
 ``python examples/moe_layer.py`` runs them on a GPU with seeded weights.
 """
 import contextlib
+import ctypes
 import os
 import sys
 
@@ -77,6 +78,8 @@ def _graph_of(*tensors):
 
 
 def _bytes(n, device):
+    if n == ctypes.c_size_t(-1).value:  # what the library answers to sizes that it refuses
+        raise ValueError("no workspace for these sizes: the library refuses them")
     return torch.empty(max(n, 16), dtype=torch.uint8, device=device)
 
 
@@ -114,6 +117,8 @@ class Q8Layer:
         _check("gate", gate, (n, d), (torch.int16, torch.bfloat16))
         _check("gate_up", gate_up, (n, 2 * d_ff, d), tuple(_CODE))
         _check("down", down, (n, d, d_ff), tuple(_CODE))
+        if d % 16 or d_ff % 16:
+            raise ValueError(f"d_model {d}, d_ff {d_ff}: both are to be multiples of 16")
         dev, gate, self.max_tokens = gate.device, gate.contiguous(), max_tokens
         self.gate, self.gate32, self.k = gate, gate.view(torch.bfloat16).float(), k
         self.n, self.d_ff, self.d = gate_up.shape[0], down.shape[2], down.shape[1]
@@ -189,6 +194,8 @@ class F8Layer:
         _check("gate", gate, (n, d), (torch.bfloat16,))
         _check("gate_up", gate_up, (n, 2 * ff, d), tuple(_CODE))
         _check("down", down, (n, d, ff), tuple(_CODE))
+        if d % 16 or ff % 16:
+            raise ValueError(f"d_model {d}, d_ff {ff}: both are to be multiples of 16")
         if bias is not None:
             _check("bias", bias, (n,), (torch.float32,))
         dev, self.n, self.d, self.d_ff, self.k, self.max_tokens = gate.device, n, d, ff, k, max_tokens

@@ -1,0 +1,45 @@
+"""Sizes and parameters that a user's model has: those that the layers do not take are
+refused in words, parameters that need a gradient are served."""
+import importlib.util
+import os
+
+import pytest
+
+torch = pytest.importorskip("torch")
+pytestmark = pytest.mark.gpu
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+
+
+@pytest.fixture(scope="module")
+def ex():
+    if not torch.cuda.is_available():
+        pytest.skip("no CUDA device")
+    import __graft_entry__
+    __graft_entry__.build_library()
+    spec = importlib.util.spec_from_file_location("moe_layer", os.path.join(ROOT, "examples", "moe_layer.py"))
+    m = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(m)
+    return m
+
+
+def weights(n, d, ff):
+    g = torch.Generator(device="cuda").manual_seed(n)
+    r = lambda *s: torch.randn(*s, generator=g, device="cuda")  # noqa: E731
+    return (r(n, d) / d ** 0.5).to(torch.bfloat16), r(n, 2 * ff, d) / d ** 0.5, r(n, d, ff) / ff ** 0.5, r
+
+
+@pytest.mark.parametrize("layer", ["Q8Layer", "F8Layer"])
+@pytest.mark.parametrize("d,ff", [(72, 64), (64, 72), (100, 36), (64, 8)])
+def test_sizes_that_are_no_multiples_of_16(ex, layer, d, ff):
+    gate, gate_up, down, _ = weights(4, d, ff)
+    with pytest.raises(ValueError, match="multiples of 16"):
+        getattr(ex, layer)(gate, gate_up, down, 2, 8)
+
+
+def test_sizes_that_the_library_refuses(ex):
+    gate, gate_up, down, r = weights(4, 64, 32)
+    with pytest.raises(ValueError, match="the library refuses"):
+        ex.F8Layer(gate, gate_up, down, 65, 1)  # more slots a token than there are
+    idx = torch.zeros(2, 65, dtype=torch.int32, device="cuda")
+    with pytest.raises((ValueError, ex.smoe.SmoeError)):
+        ex.dispatch(r(2, 64), idx, 4)
