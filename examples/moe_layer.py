@@ -90,7 +90,7 @@ def _logits(x, gate, gate32, logits, stream):
         smoe.matvec_bf16_batch([gate] * T, [x.data_ptr() + 4 * d * t for t in range(T)],
                                [logits.data_ptr() + 4 * n * t for t in range(T)], [n] * T, [d] * T, stream)
     else:  # a matvec a token would read the router's weights T times
-        with torch.cuda.stream(stream) if stream is not None else contextlib.nullcontext():
+        with torch.no_grad(), torch.cuda.stream(stream) if stream is not None else contextlib.nullcontext():
             torch.mm(x, gate32.t(), out=logits[:T])
 
 

@@ -43,3 +43,18 @@ def test_sizes_that_the_library_refuses(ex):
     idx = torch.zeros(2, 65, dtype=torch.int32, device="cuda")
     with pytest.raises((ValueError, ex.smoe.SmoeError)):
         ex.dispatch(r(2, 64), idx, 4)
+
+
+@pytest.mark.parametrize("layer", ["Q8Layer", "F8Layer"])
+@pytest.mark.parametrize("T", [3, 70])
+def test_parameters_and_rows_that_need_a_gradient(ex, layer, T):
+    """A trained model's parameters as they are: served as their values are."""
+    gate, gate_up, down, r = weights(8, 144, 80)
+    x = r(T, 144)
+    outs = []
+    for own in (lambda t: t, torch.nn.Parameter):
+        out = torch.full((T, 144), float("nan"), dtype=torch.bfloat16, device="cuda")
+        served = getattr(ex, layer)(own(gate), own(gate_up), own(down), 2, 70)
+        outs.append(served(own(x), out))
+    assert torch.equal(*outs) and not outs[0].isnan().any() and not outs[1].requires_grad
+    assert ex.smoe.smoe_last_device_status() == ex.smoe.SMOE_OK
