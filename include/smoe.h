@@ -754,9 +754,9 @@ int smoe_route_rows_backward(const float *logits, int n_tokens, int n_experts,
  * (f32 operations rounded once each, the code to nearest, ties to even; SiLU's
  * quotient may be rounded to the other side, once in some two million; where
  * 448 / top is beyond f32, v and top are taken 2^64 times).  A block of zeros has
- * scale 0 and codes 0; one that holds a NaN or an infinity has scale NaN and codes 0,
- * so that every product of it is NaN.  cols <= SMOE_MAX_COLS; q: [rows x cols],
- * 16-byte aligned.
+ * scale 0 and codes of zero, 0x00 or 0x80 by its sign (after the activation either);
+ * one that holds a NaN or an infinity has scale NaN and codes 0x00, so that every
+ * product of it is NaN.  cols <= SMOE_MAX_COLS; q: [rows x cols], 16-byte aligned.
  */
 int smoe_quantize_rows_f8(const void *x, int dtype, int act, int rows, int cols,
                           uint8_t *q, float *scales, void *stream);

@@ -7,9 +7,9 @@
 // each f32 operation rounded once, the code to nearest, ties to even: the codes of
 // a block are the same on any machine, and after the activation wherever expf is the
 // same.  448 / top is beyond f32 below 1.4e-36:
-// there top and v are taken 2^64 times.  A block of zeros has scale 0; one that
-// holds a NaN or an infinity has scale NaN and codes 0, so that every product of it
-// is NaN.
+// there top and v are taken 2^64 times.  A block of zeros has scale 0 and codes that
+// keep their sign; one that holds a NaN or an infinity has scale NaN and codes 0, so
+// that every product of it is NaN.
 #include "q8.cuh"
 #include "rowvec.cuh"
 #include "smoe.h"
