@@ -36,6 +36,8 @@ def _check(name, t, shape, dtypes):
         raise TypeError(f"{name} is {t.dtype}, not " + " or ".join(map(str, dtypes)))
     if not t.is_cuda:
         raise ValueError(f"{name} is on {t.device}, not on a GPU")
+    if t.device.index != torch.cuda.current_device():
+        raise ValueError(f"{name} is on {t.device}: the calls take the streams of the current device, {torch.cuda.current_device()}")
     if t.dim() != len(shape) or any(w is not None and w != n for n, w in zip(t.shape, shape)):
         raise ValueError(f"{name} has the shape {tuple(t.shape)}, not {shape}")
 

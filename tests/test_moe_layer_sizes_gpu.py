@@ -58,3 +58,23 @@ def test_parameters_and_rows_that_need_a_gradient(ex, layer, T):
         outs.append(served(own(x), out))
     assert torch.equal(*outs) and not outs[0].isnan().any() and not outs[1].requires_grad
     assert ex.smoe.smoe_last_device_status() == ex.smoe.SMOE_OK
+
+
+def test_tensors_of_another_device_than_the_current_one(ex, monkeypatch):
+    """The calls run on the current device's stream: refused before anything is launched."""
+    gate, gate_up, down, r = weights(4, 64, 32)
+    layer, out = ex.F8Layer(gate, gate_up, down, 2, 4), torch.full((3, 64), -7.0, dtype=torch.bfloat16, device="cuda")
+    x, idx, offsets = r(3, 64), torch.zeros(3, 2, dtype=torch.int32, device="cuda"), torch.zeros(5, dtype=torch.int32, device="cuda")
+    torch.cuda.synchronize()
+    with monkeypatch.context() as m:
+        m.setattr(torch.cuda, "current_device", lambda: 1)
+        for call in (lambda: layer(x, out), lambda: ex.F8Layer(gate, gate_up, down, 2, 4), lambda: ex.route(r(3, 4), 2),
+                     lambda: ex.top_k(r(3, 4), 2), lambda: ex.dispatch(x, idx, 4), lambda: ex.experts_f8(x, gate_up, offsets),
+                     lambda: ex.combine(r(6, 64), torch.zeros(6, dtype=torch.int32, device="cuda"), r(3, 2)),
+                     lambda: ex.quantize_weights(gate_up)):
+            with pytest.raises(ValueError, match="current device"):
+                call()
+    torch.cuda.synchronize()
+    assert (out == -7).all()
+    layer(x, out)
+    assert ex.smoe.smoe_last_device_status() == ex.smoe.SMOE_OK and (out != -7).any()
