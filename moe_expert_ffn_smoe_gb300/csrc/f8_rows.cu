@@ -17,12 +17,16 @@
 // against the 512 of its MMAs (1999 rows x 8192 x 4096 88 us).  Here a tile of fewer
 // than 128 rows costs as much as a full one.
 //
-// Bound by handing the accumulators over: a block takes 1190 clocks, of which its MMAs
-// are 440 to 512, the way to the epilogue and back some 750, reading and adding 450 (1999
-// rows x 8192 x 4096 74.5 us, 1.8 PFLOP/s).  Pairs of
-// CTAs on 256 rows need two thirds of the copies and took 73 us there, but cost 256 rows
-// a tile: through 128 experts, 2047 tokens of 8 221 us against 192, 4096 tokens 307
-// against 291.  Accumulators in halves, barriers tested ahead, 16 epilogue warps and
+// Bound by handing the accumulators over: a block takes 945 clocks (the slope of the time
+// over 16 to 64 blocks an item, 1 to 4 items a CTA), since each of the two accumulators
+// goes round in some 1900: 1130 from the issue of its MMAs, 512 of them their own, until
+// the epilogue sees them, 450 read and added, 350 handed back and issued again (stamps of
+// a launch).  An item costs some 8000 clocks more, its stores and the next one's first
+// copies: of 32 blocks a fifth of its time.  1999 rows x 8192 x 4096, 3.4 items a CTA run
+// as 4, 74.5 us, 1.8 PFLOP/s.
+// Pairs of CTAs on 256 rows need two thirds of the copies and took 73 us there, but cost
+// 256 rows a tile: through 128 experts, 2047 tokens of 8 221 us against 192, 4096 tokens
+// 307 against 291.  Accumulators in halves, barriers tested ahead, 16 epilogue warps and
 // spinning waits were no faster.
 //
 // Persistent: CTAs walk the items (tile of rows, 256 weights).  Roles (warps): 0-7

@@ -120,9 +120,9 @@ __device__ __forceinline__ void load_run(const T *row, int c, int cols, float (&
     }
 }
 
-// Eight threads a block of 128 columns, 16 each, a warp four blocks.  HBM-bound, with 82% of
+// Eight threads a block of 128 columns, 16 each, a warp four blocks.  HBM-bound, with 76% of
 // the issue slots taken where the activation is: 32,768 rows of 1536 in bf16 (253 MB)
-// 44.5 us, 5.7 TB/s (256 threads a CTA 45.2; 32 registers for all the warps 46.3).
+// 44.5 us, 5.7 TB/s (40 registers, for more warps, 44.4).
 template <typename T, bool VEC, bool ACT>
 __global__ void __launch_bounds__(ROWS_THREADS) quantize_rows_f8(const T *__restrict__ x, long long blocks, int nkb,
                                                                  unsigned long long magic, int cols, uint8_t *__restrict__ q,
