@@ -122,9 +122,11 @@ __device__ __forceinline__ void load_run(const T *row, int c, int cols, float (&
 
 // Eight threads a block of 128 columns, 16 each, a warp four blocks.  HBM-bound, with 76% of
 // the issue slots taken where the activation is: 32,768 rows of 1536 in bf16 (253 MB)
-// 44.5 us, 5.7 TB/s (40 registers, for more warps, 44.4).
+// 44.5 us, 5.7 TB/s (40 registers, for more warps, 44.4).  Rows that no vector fits, with
+// the activation, have the registers of seven CTAs an SM (left to itself the compiler
+// spills at 64): 8191 rows of 1001 in f32 37.1 us against 38.1, in bf16 26.4 against 27.3.
 template <typename T, bool VEC, bool ACT>
-__global__ void __launch_bounds__(ROWS_THREADS) quantize_rows_f8(const T *__restrict__ x, long long blocks, int nkb,
+__global__ void __launch_bounds__(ROWS_THREADS, ACT && !VEC ? 7 : 0) quantize_rows_f8(const T *__restrict__ x, long long blocks, int nkb,
                                                                  unsigned long long magic, int cols, uint8_t *__restrict__ q,
                                                                  float *__restrict__ scales)
 {
